@@ -78,7 +78,8 @@ typedef enum { TTC_ROW_MAJOR = 0, TTC_COL_MAJOR = 1 } ttc_layout;
 
 typedef enum { TTC_ACT_NONE = 0, TTC_ACT_RELU = 1, TTC_ACT_GELU_TANH = 2 } ttc_act;
 
-typedef enum { TTC_F16 = 0, TTC_BF16 = 1, TTC_I8 = 2 } ttc_dtype;
+/* TTC_F32 is the type of inputs and outputs of the calls that say so. */
+typedef enum { TTC_F16 = 0, TTC_BF16 = 1, TTC_I8 = 2, TTC_F32 = 3 } ttc_dtype;
 
 /*
  * D = act(alpha * A * B + beta * C + bias).  See the file comment for the
@@ -161,6 +162,126 @@ ttc_status ttc_conv2d_fprop(int64_t N, int64_t H, int64_t W, int64_t C, int64_t 
  */
 ttc_status ttc_transpose(int64_t rows, int64_t cols, const void* src, int64_t lds,
                          void* dst, int64_t ldd, int elem_bytes, void* stream);
+
+/*
+ * Products grouped by expert, with ragged groups of rows: for every group g
+ * and every row i with offsets[g] <= i < offsets[g + 1],
+ *   D[i, :] = act(alpha * A[i, :] * B_g + bias_g).
+ * A is M x K and D is M x N, both row-major (pitches lda >= K, ldd >= N), the
+ * rows of one group next to one another: the tokens sorted by the expert they
+ * were sent to.  B_g is K x N at B + g * strideB elements, row- or
+ * column-major (layoutB, ldb as in ttc_gemm; a stride of 0 shares one B).
+ * bias_g is fp32[N] at bias + g * strideBias, or bias is NULL.  fp16 or bf16
+ * in and out, fp32 sums.  With the other layoutB over the same weights this is
+ * the gradient of the rows: dA[i, :] = dD[i, :] * B_g^T.
+ *
+ * offsets is an array of groups + 1 int32 in DEVICE memory, ascending, read
+ * when the work runs: the host never waits for the router that wrote it.
+ * Groups may be empty.  Rows that no group covers are not written.  Offsets
+ * outside [0, M] count as the nearer end of that range, and a group that ends
+ * before it starts as empty, so that no offset leads outside A or D; where
+ * groups overlap, the shared rows of D are undefined.
+ *
+ * What lies in rows of other groups never reaches a group's result, NaN and
+ * infinity included.  GELU is computed to fp32 accuracy here.  Asynchronous on
+ * `stream`; allocates nothing; may be captured (ttc_gemm's notes apply).
+ * Operands TMA can read (16-byte aligned bases, pitches and strides of B in
+ * 16-byte multiples) run faster than others.
+ * TTC_ERR_INVALID_ARG: negative sizes or strides, a pitch below the contiguous
+ * extent, NULL or misaligned pointers, D overlapping A or B, an unknown enum
+ * value.  TTC_ERR_UNSUPPORTED: TTC_I8 or TTC_F32, more than 1024 groups, sizes
+ * beyond 2^31 - 2^24.  groups, M or N == 0 is a no-op; K == 0 gives act(bias_g).
+ */
+ttc_status ttc_gemm_grouped(int64_t groups, int64_t M, int64_t N, int64_t K,
+                            const void* A, int64_t lda, const int32_t* offsets,
+                            const void* B, int64_t ldb, int64_t strideB, ttc_layout layoutB,
+                            void* D, int64_t ldd, float alpha,
+                            const float* bias, int64_t strideBias,
+                            ttc_act act, ttc_dtype dtype, void* stream);
+
+/*
+ * The gradient of the grouped products' weights: for every group g,
+ *   D_g = alpha * A_g^T * B_g + beta * C_g   (K x N),
+ * A_g the rows offsets[g] .. offsets[g + 1] - 1 of A (M x K, row-major) and B_g
+ * those of B (M x N, row-major): with A the rows ttc_gemm_grouped read and B
+ * the gradient of its result, D_g is the gradient of a row-major B_g; with A
+ * and B exchanged, of a column-major one.  C_g and D_g are row-major at
+ * C + g * strideC and D + g * strideD (pitches ldc, ldd >= N).  out_dtype, the
+ * type of C and D, is dtype (fp16 or bf16) or TTC_F32; sums are fp32.  C is
+ * read only when beta != 0 and may be D itself (same pitch and stride), which
+ * adds up micro-batches in place.  offsets as in ttc_gemm_grouped.  An empty
+ * group gives D_g = beta * C_g (zeros with beta == 0).
+ * TTC_ERR_INVALID_ARG as ttc_gemm_grouped, plus NULL C with beta != 0, D
+ * overlapping C other than in place, and (groups > 1) a strideD below
+ * (K - 1) * ldd + N.  TTC_ERR_UNSUPPORTED as ttc_gemm_grouped, plus another
+ * out_dtype.  groups, N or K == 0 is a no-op; M == 0 leaves every group empty.
+ */
+ttc_status ttc_gemm_grouped_wgrad(int64_t groups, int64_t M, int64_t N, int64_t K,
+                                  const void* A, int64_t lda, const void* B, int64_t ldb,
+                                  const int32_t* offsets,
+                                  const void* C, int64_t ldc, int64_t strideC,
+                                  void* D, int64_t ldd, int64_t strideD,
+                                  float alpha, float beta,
+                                  ttc_dtype dtype, ttc_dtype out_dtype, void* stream);
+
+/*
+ * Rows of int8 with a scale each, the operands of ttc_gemm_i8_scaled:
+ *   scale[i] = max_j |X[i, j]| / 127,  Q[i, j] = round(X[i, j] * (1 / scale[i])),
+ * all in fp32, every operation rounded to nearest (the last one to the nearest
+ * integer, ties to even), so |Q| <= 127 and scale[i] * Q[i, j] is within about
+ * half a scale of X[i, j].  X is rows x cols, row-major with pitch ldx, of
+ * `dtype` (TTC_F16, TTC_BF16 or TTC_F32); Q has pitch ldq.  A row whose scale
+ * would be below 2^-126 counts as zeros: scale 0 and Q 0.  A row with a NaN or
+ * an infinity gets that as its scale and zeros in Q, so that its products are
+ * NaN.  Only Q's rows x cols elements are written.  Asynchronous on `stream`;
+ * allocates nothing.
+ * TTC_ERR_INVALID_ARG: negative sizes, pitches below cols, NULL or misaligned
+ * pointers, overlapping arrays, an unknown enum value.  TTC_ERR_UNSUPPORTED:
+ * TTC_I8, sizes beyond 2^31 - 2^24.  rows == 0 is a no-op; cols == 0 writes
+ * zero scales.
+ */
+ttc_status ttc_quantize_rows(int64_t rows, int64_t cols, const void* X, int64_t ldx, ttc_dtype dtype,
+                             int8_t* Q, int64_t ldq, float* scale, void* stream);
+
+/* The largest K of ttc_gemm_i8_scaled: K products of at most 2^14 stay inside int32. */
+#define TTC_I8_SCALED_MAX_K 131071
+
+/*
+ * Product of int8 rows with int8 weights, a scale for each token and each
+ * output channel:
+ *   D[i, j] = act(scaleA[i] * scaleB[j] * sum_k A[i, k] * B[j, k] + bias[j]).
+ * A is M x K and B is N x K, both row-major with pitches lda, ldb >= K: rows as
+ * ttc_quantize_rows writes them, one token or one output channel each.  The
+ * integer sum is exact (int32); it is converted to fp32 once, scaled, and the
+ * result rounded to out_dtype (TTC_F16, TTC_BF16 or TTC_F32), M x N with pitch
+ * ldd.  scaleA is fp32[M], scaleB and bias are fp32[N]; bias may be NULL.
+ * Asynchronous on `stream`; allocates nothing.
+ *
+ * workspace: 256-byte aligned device memory of
+ * ttc_gemm_i8_scaled_workspace_size() bytes, scratch until the work enqueued
+ * here has finished.  With a NULL, misaligned or smaller one the result is the
+ * same; products of many tokens then take longer.
+ * TTC_ERR_INVALID_ARG: negative sizes, pitches below the extent, NULL or
+ * misaligned pointers, D overlapping A or B, an unknown enum value.
+ * TTC_ERR_UNSUPPORTED: out_dtype TTC_I8, K above TTC_I8_SCALED_MAX_K, sizes
+ * beyond 2^31 - 2^24.  M or N == 0 is a no-op.
+ */
+ttc_status ttc_gemm_i8_scaled(int64_t M, int64_t N, int64_t K,
+                              const int8_t* A, int64_t lda, const float* scaleA,
+                              const int8_t* B, int64_t ldb, const float* scaleB,
+                              void* D, int64_t ldd, const float* bias,
+                              ttc_act act, ttc_dtype out_dtype,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Workspace bytes of ttc_gemm_i8_scaled for these operands: 0 for few tokens,
+ * whose weights are widened on their way through the SMs, and for invalid or
+ * empty arguments.  Pure host computation; the pointers are only looked at for
+ * their alignment.
+ */
+size_t ttc_gemm_i8_scaled_workspace_size(int64_t M, int64_t N, int64_t K,
+                                         const int8_t* A, int64_t lda, const int8_t* B, int64_t ldb,
+                                         const void* D, int64_t ldd, ttc_dtype out_dtype);
 
 /*
  * As ttc_gemm, with caller-provided device workspace.  An operand that TMA

@@ -23,7 +23,7 @@ from . import _build
 
 ROW_MAJOR, COL_MAJOR = 0, 1
 ACT = {"none": 0, "relu": 1, "gelu_tanh": 2}
-DTYPE = {"f16": 0, "bf16": 1, "i8": 2}
+DTYPE = {"f16": 0, "bf16": 1, "i8": 2, "f32": 3}
 STATUS = {0: "TTC_OK", 1: "TTC_ERR_INVALID_ARG", 2: "TTC_ERR_UNSUPPORTED", 3: "TTC_ERR_CUDA",
           4: "TTC_ERR_TIMEOUT", 5: "TTC_ERR_SCRATCH_TOO_SMALL"}
 STATIC_SCRATCH_BYTES = 16 * 1024 * 1024
@@ -35,6 +35,8 @@ KNOB = {"timeout_ns": 0, "inject_stall": 1, "force_generic_load": 2, "force_gene
 EXPORTS = ("ttc_gemm", "ttc_gemm_strided_batched", "ttc_gemm_ws", "ttc_gemm_workspace_size",
            "ttc_gemm_workspace_size_staged",
            "ttc_gemm_static_scratch", "ttc_transpose", "ttc_conv2d_fprop",
+           "ttc_gemm_grouped", "ttc_gemm_grouped_wgrad", "ttc_quantize_rows", "ttc_gemm_i8_scaled",
+           "ttc_gemm_i8_scaled_workspace_size",
            "ttc_get_device_error", "ttc_status_string", "ttc_set_knob", "ttc_launch_count", "ttc_gemm_plan")
 
 _lib = None
@@ -78,6 +80,18 @@ def load():
     L.ttc_gemm_workspace_size.restype = ctypes.c_size_t
     L.ttc_gemm_workspace_size_staged.argtypes = [i64, i64, i64, vp, i64, i, vp, i64, i, vp, i64, i]
     L.ttc_gemm_workspace_size_staged.restype = ctypes.c_size_t
+    L.ttc_gemm_grouped.argtypes = [i64, i64, i64, i64, vp, i64, vp, vp, i64, i64, i, vp, i64, f, vp, i64, i, i, vp]
+    L.ttc_gemm_grouped.restype = i
+    L.ttc_gemm_grouped_wgrad.argtypes = [i64, i64, i64, i64, vp, i64, vp, i64, vp, vp, i64, i64, vp, i64, i64, f, f,
+                                         i, i, vp]
+    L.ttc_gemm_grouped_wgrad.restype = i
+    L.ttc_quantize_rows.argtypes = [i64, i64, vp, i64, i, vp, i64, vp, vp]
+    L.ttc_quantize_rows.restype = i
+    L.ttc_gemm_i8_scaled.argtypes = [i64, i64, i64, vp, i64, vp, vp, i64, vp, vp, i64, vp, i, i, vp, ctypes.c_size_t,
+                                     vp]
+    L.ttc_gemm_i8_scaled.restype = i
+    L.ttc_gemm_i8_scaled_workspace_size.argtypes = [i64, i64, i64, vp, i64, vp, i64, vp, i64, i]
+    L.ttc_gemm_i8_scaled_workspace_size.restype = ctypes.c_size_t
     L.ttc_get_device_error.argtypes = [vp]
     L.ttc_get_device_error.restype = i
     L.ttc_status_string.argtypes = [i]
@@ -117,6 +131,33 @@ def ttc_conv2d_fprop(N, H, W, C, K, R, S, pad_h, pad_w, stride_h, stride_w, dil_
 
 def ttc_transpose(rows, cols, src, lds, dst, ldd, elem_bytes, stream) -> int:
     return load().ttc_transpose(rows, cols, src, lds, dst, ldd, elem_bytes, stream)
+
+
+def ttc_gemm_grouped(groups, M, N, K, A, lda, offsets, B, ldb, strideB, layoutB, D, ldd, alpha, bias, strideBias,
+                     act, dtype, stream) -> int:
+    """offsets: device address of groups + 1 int32."""
+    return load().ttc_gemm_grouped(groups, M, N, K, A, lda, offsets, B, ldb, strideB, layoutB, D, ldd, alpha, bias,
+                                   strideBias, act, dtype, stream)
+
+
+def ttc_gemm_grouped_wgrad(groups, M, N, K, A, lda, B, ldb, offsets, C, ldc, strideC, D, ldd, strideD, alpha, beta,
+                           dtype, out_dtype, stream) -> int:
+    return load().ttc_gemm_grouped_wgrad(groups, M, N, K, A, lda, B, ldb, offsets, C, ldc, strideC, D, ldd, strideD,
+                                         alpha, beta, dtype, out_dtype, stream)
+
+
+def ttc_quantize_rows(rows, cols, X, ldx, dtype, Q, ldq, scale, stream) -> int:
+    return load().ttc_quantize_rows(rows, cols, X, ldx, dtype, Q, ldq, scale, stream)
+
+
+def ttc_gemm_i8_scaled(M, N, K, A, lda, scaleA, B, ldb, scaleB, D, ldd, bias, act, out_dtype, workspace,
+                       workspace_bytes, stream) -> int:
+    return load().ttc_gemm_i8_scaled(M, N, K, A, lda, scaleA, B, ldb, scaleB, D, ldd, bias, act, out_dtype, workspace,
+                                     workspace_bytes, stream)
+
+
+def ttc_gemm_i8_scaled_workspace_size(M, N, K, A, lda, B, ldb, D, ldd, out_dtype) -> int:
+    return load().ttc_gemm_i8_scaled_workspace_size(M, N, K, A, lda, B, ldb, D, ldd, out_dtype)
 
 
 def ttc_gemm_ws(M, N, K, A, lda, layoutA, B, ldb, layoutB, C, ldc, D, ldd, alpha, beta, bias, act,

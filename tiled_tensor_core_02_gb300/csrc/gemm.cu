@@ -20,6 +20,7 @@
 #include "gemm2sm_kernel.cuh"
 #include "gemm_launch.cuh"
 #include "gemv.cuh"
+#include "host.cuh"
 #include "index_maps.hpp"
 #include "repack.cuh"
 #include "transpose.cuh"
@@ -51,11 +52,6 @@ std::atomic<int> g_pair_epi_warps{0};
 std::atomic<int64_t> g_launches{0};
 
 constexpr int kMaxDevices = 64;
-
-// Largest size or leading dimension accepted (elements): the kernels index
-// rows, columns and k in 32-bit integers and step past the end by up to a
-// grid's stride (well under 2^24) before a loop test, which must not wrap.
-constexpr int64_t kSizeLimit = (1ll << 31) - (1ll << 24);
 
 struct DeviceInfo {
   bool ready = false;
@@ -648,6 +644,36 @@ DStage plan_dstage(int64_t M, int64_t N, const void* D, int64_t ldd, int esize, 
 }  // namespace
 
 bool pdl_enabled() { return g_pdl_off.load() == 0; }
+
+ttc_status host_env(HostEnv& env) {
+  DeviceInfo* dev = nullptr;
+  const ttc_status st = device_info(&dev);
+  if (st != TTC_OK) return st;
+  env.sm_count = dev->sm_count;
+  env.err = dev->err;
+  env.timeout_ns = (uint64_t)g_timeout_ns.load();
+  env.inject_stall = g_inject_stall.load();
+  env.plain_loads = g_force_generic_load.load() != 0;
+  env.plain_stores = g_force_generic_store.load() != 0;
+  return TTC_OK;
+}
+
+bool encode_matrices(CUtensorMap* m, CUtensorMapDataType dt, int esize, const void* base, int64_t inner, int64_t outer,
+                     int64_t pitch, int64_t count, int64_t stride, int box_inner, int box_outer,
+                     CUtensorMapSwizzle sw) {
+  return encode_3d(m, dt, esize, base, (uint64_t)inner, (uint64_t)outer, (uint64_t)pitch, (uint32_t)box_inner,
+                   (uint32_t)box_outer, sw, BatchDim{(uint64_t)count, (uint64_t)stride});
+}
+
+bool tma_rows_ok(const void* p, int64_t ld, int esize) { return tma_ok(p, ld, esize); }
+
+bool tma_stride_ok(int64_t count, int64_t stride, int esize) { return tma_batch_ok(count, stride, esize); }
+
+bool byte_ranges_overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+  return ranges_overlap(a, a_bytes, b, b_bytes);
+}
+
+void count_launches(int n) { g_launches.fetch_add(n); }
 
 }  // namespace ttc
 

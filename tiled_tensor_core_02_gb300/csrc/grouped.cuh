@@ -1,0 +1,64 @@
+// Products grouped by expert: what the kernels and their launchers share.
+//
+//   forward   D[i, :] = act(alpha A[i, :] B_g + bias_g)   for every row i of group g
+//   wgrad     D_g     = alpha A[rows of g]^T B[rows of g] + beta C_g
+//
+// Group g's rows are offsets[g] .. offsets[g + 1] - 1 of A (and of D, or B).
+// The offsets live on the device and are read there, so that the host need
+// not wait for the router that wrote them: the kernels count the tiles
+// themselves.  Offsets out of [0, M] are clamped to it and a group that ends
+// before it starts is empty, so no offset leads out of the operands.
+#pragma once
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace ttc {
+
+// Largest number of groups: their tables fit in the shared memory that the
+// widest kernel has left.
+constexpr int kMaxGroups = 1024;
+
+struct GroupedParams {
+  CUtensorMap tmA;  // the kernels that load with TMA
+  CUtensorMap tmB;
+  CUtensorMap tmD;
+  const void* A;
+  int64_t lda;
+  const void* B;
+  int64_t ldb, strideB;
+  const int32_t* offsets;
+  int groups;
+  int M;  // rows of all groups together: the bound of every offset
+  int N, K;
+  int a_vec, b_vec;  // plain loads: groups of 8 elements may be read as one vector
+  int b_mn;          // forward: B_g is stored K x N (its columns contiguous)
+  // tiles: blocks of D's columns, blocks of its rows (wgrad: per group; forward:
+  // counted on the device), and how many row blocks share one column block
+  // before the walk moves on
+  int col_blocks, row_blocks, group_rows;
+  int k_blocks;  // forward: 64-wide blocks of K
+  float alpha, beta;
+  const float* bias;
+  int64_t stride_bias;
+  int act;
+  const void* C;
+  int64_t ldc, strideC;
+  void* D;
+  int64_t ldd, strideD;
+  int out_f32;  // wgrad: C and D are fp32
+  int c_vec, d_vec;  // rows of C, D start on 16-byte boundaries
+  int d_tma;
+  int one_buf;  // pair kernel: the second staging buffers hold the group tables
+  int ksplit;   // token-side kernel: CTAs of a cluster that share a tile's k-blocks
+  uint32_t* err;
+  uint64_t timeout_ns;
+  int inject_stall;
+};
+
+// Tile of the kernels that load with plain loads: 128 x 128.
+constexpr int kGroupedPlainTile = 128;
+cudaError_t launch_grouped_plain(bool bf16, bool wgrad, const GroupedParams& p, int ctas, cudaStream_t stream);
+
+}  // namespace ttc

@@ -1,0 +1,197 @@
+// Device side of the grouped products: the table of groups and tiles that
+// every CTA builds from the device's offsets, and the values of the epilogue.
+#pragma once
+#include "gemm_kernel.cuh"
+#include "grouped.cuh"
+
+namespace ttc {
+
+// offs[g] is the first row of group g, held to [0, M] (offs[groups] ends the
+// last one); start[g] the first tile of group g and start[groups] their
+// number.  ROWS: rows of a tile.  All threads of the CTA; `start` may be null
+// where every group has as many tiles as another.
+template <int ROWS>
+__device__ __forceinline__ void build_group_table(const GroupedParams& p, int* offs, int* start) {
+  for (int i = threadIdx.x; i <= p.groups; i += blockDim.x) offs[i] = min(max(__ldg(p.offsets + i), 0), p.M);
+  __syncthreads();
+  if (start == nullptr) return;
+  if (threadIdx.x < 32) {
+    int carry = 0;
+    for (int g0 = 0; g0 < p.groups; g0 += 32) {
+      const int g = g0 + (int)threadIdx.x;
+      int n = 0;
+      if (g < p.groups) n = (max(offs[g + 1] - offs[g], 0) + ROWS - 1) / ROWS * p.col_blocks;
+      int sum = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+        if ((int)threadIdx.x >= o) sum += v;
+      }
+      if (g < p.groups) start[g] = carry + sum - n;
+      carry += __shfl_sync(0xFFFFFFFFu, sum, 31);
+    }
+    if (threadIdx.x == 0) start[p.groups] = carry;
+  }
+  __syncthreads();
+}
+
+// The group of tile t: the last one that starts at or before it and has tiles.
+__device__ __forceinline__ int group_of_tile(const int* start, int groups, int t) {
+  int lo = 0, hi = groups - 1;  // the first g with start[g + 1] > t
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (start[mid + 1] > t)
+      hi = mid;
+    else
+      lo = mid + 1;
+  }
+  return lo;
+}
+
+struct GroupedTile {
+  int g;         // group
+  int lo, hi;    // its rows
+  int rb, cb;    // block of D's rows (forward: counted from the group's first row) and of its columns
+};
+
+// Tiles of a group walk `group_rows` row blocks of one column block before the
+// next column block, so that CTAs at work together share panels of A and B.
+template <int ROWS, bool WGRAD>
+__device__ __forceinline__ GroupedTile grouped_tile(const GroupedParams& p, const int* offs, const int* start, int t) {
+  GroupedTile x;
+  int r, rows;
+  if constexpr (WGRAD) {
+    const int per = p.row_blocks * p.col_blocks;
+    x.g = t / per;
+    r = t - x.g * per;
+    x.lo = offs[x.g];
+    x.hi = max(offs[x.g + 1], x.lo);
+    rows = p.row_blocks;
+  } else {
+    x.g = group_of_tile(start, p.groups, t);
+    r = t - start[x.g];
+    x.lo = offs[x.g];
+    x.hi = max(offs[x.g + 1], x.lo);
+    rows = (x.hi - x.lo + ROWS - 1) / ROWS;
+  }
+  const int band = p.group_rows * p.col_blocks;
+  const int b = r / band;
+  const int first = b * p.group_rows;
+  const int size = min(rows - first, p.group_rows);
+  r -= b * band;
+  x.rb = first + r % size;
+  x.cb = r / size;
+  return x;
+}
+
+// GELU in its tanh form as v / (1 + exp(-2 u)), u = sqrt(2/pi) (v + 0.044715 v^3):
+// 0.5 (1 + tanh u) is the logistic function of 2 u.  Unlike the sum 1 + tanh u
+// it keeps its relative accuracy where v is negative.
+__device__ __forceinline__ float gelu_logistic(float v) {
+  const float u2 = 1.5957691216057308f * fmaf(0.044715f * v, v * v, v);
+  return __fdividef(v, 1.0f + __expf(-u2));
+}
+
+__device__ __forceinline__ float act_value(int act, float v) {
+  if (act == kActRelu) return v < 0.0f ? 0.0f : v;  // a NaN stays one
+  if (act == kActGelu) return gelu_logistic(v);
+  return v;
+}
+
+// 32 values of a row (columns col0 .. col0 + 31, `n` of them inside D) from
+// their accumulator: alpha, C, bias, activation.
+template <bool BF16>
+__device__ __forceinline__ void grouped_values(const GroupedParams& p, const uint32_t (&r)[32], const void* c_row,
+                                               const float* bias, int n, float (&v)[32]) {
+#pragma unroll
+  for (int j = 0; j < 32; ++j) v[j] = p.alpha * __uint_as_float(r[j]);
+  if (c_row != nullptr) {
+    if (p.out_f32) {
+      const float* c = static_cast<const float*>(c_row);
+      if (p.c_vec && n == 32) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const float4 w = __ldg(reinterpret_cast<const float4*>(c) + u);
+          v[4 * u] = fmaf(p.beta, w.x, v[4 * u]);
+          v[4 * u + 1] = fmaf(p.beta, w.y, v[4 * u + 1]);
+          v[4 * u + 2] = fmaf(p.beta, w.z, v[4 * u + 2]);
+          v[4 * u + 3] = fmaf(p.beta, w.w, v[4 * u + 3]);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (j < n) v[j] = fmaf(p.beta, __ldg(c + j), v[j]);
+      }
+    } else {
+      const uint16_t* c = static_cast<const uint16_t*>(c_row);
+      if (p.c_vec && n == 32) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const uint4 w = __ldg(reinterpret_cast<const uint4*>(c) + u);
+          const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            v[8 * u + 2 * h] = fmaf(p.beta, half_bits_to_float<BF16>((uint16_t)(ws[h] & 0xFFFFu)), v[8 * u + 2 * h]);
+            v[8 * u + 2 * h + 1] = fmaf(p.beta, half_bits_to_float<BF16>((uint16_t)(ws[h] >> 16)), v[8 * u + 2 * h + 1]);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (j < n) v[j] = fmaf(p.beta, half_bits_to_float<BF16>(__ldg(c + j)), v[j]);
+      }
+    }
+  }
+  if (bias != nullptr) {
+    if (n == 32 && (reinterpret_cast<uintptr_t>(bias) & 15) == 0) {
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const float4 w = __ldg(reinterpret_cast<const float4*>(bias) + u);
+        v[4 * u] += w.x;
+        v[4 * u + 1] += w.y;
+        v[4 * u + 2] += w.z;
+        v[4 * u + 3] += w.w;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (j < n) v[j] += __ldg(bias + j);
+    }
+  }
+  if (p.act != kActNone) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = act_value(p.act, v[j]);
+  }
+}
+
+// Writes `n` of a row's 32 values to d_row, rounded to nearest even for 16-bit outputs.
+template <bool BF16>
+__device__ __forceinline__ void store_row(const GroupedParams& p, const float (&v)[32], void* d_row, int n) {
+  if (p.out_f32) {
+    float* d = static_cast<float*>(d_row);
+    if (p.d_vec && n == 32) {
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        reinterpret_cast<float4*>(d)[u] = make_float4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (j < n) d[j] = v[j];
+    }
+  } else {
+    uint16_t* d = static_cast<uint16_t*>(d_row);
+    if (p.d_vec && n == 32) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        reinterpret_cast<uint4*>(d)[u] =
+            make_uint4(pack2<BF16>(v[8 * u], v[8 * u + 1]), pack2<BF16>(v[8 * u + 2], v[8 * u + 3]),
+                       pack2<BF16>(v[8 * u + 4], v[8 * u + 5]), pack2<BF16>(v[8 * u + 6], v[8 * u + 7]));
+    } else {
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (j < n) d[j] = (uint16_t)(pack2<BF16>(v[j], 0.0f) & 0xFFFFu);
+    }
+  }
+}
+
+}  // namespace ttc

@@ -1,0 +1,258 @@
+// Host side of the grouped products, the quantization of rows and the scaled
+// int8 product: argument checks, the choice of a kernel, tensor maps, launch.
+// See include/ttc.h for the contract of each entry point.
+#include <cstring>
+
+#include "gemm_kernel.cuh"
+#include "grouped.cuh"
+#include "host.cuh"
+#include "i8_rows.cuh"
+#include "quantize.cuh"
+#include "ttc.h"
+
+using namespace ttc;
+
+namespace {
+
+bool is_16bit(ttc_dtype t) { return t == TTC_F16 || t == TTC_BF16; }
+bool is_dtype(ttc_dtype t) { return t == TTC_F16 || t == TTC_BF16 || t == TTC_I8 || t == TTC_F32; }
+bool is_act(ttc_act a) { return a == TTC_ACT_NONE || a == TTC_ACT_RELU || a == TTC_ACT_GELU_TANH; }
+bool aligned(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+int64_t at_least_1(int64_t x) { return x > 1 ? x : 1; }
+int64_t blocks_of(int64_t x, int64_t b) { return (x + b - 1) / b; }
+
+// Largest distance between two groups' matrices (elements).
+constexpr int64_t kStrideLimit = 1ll << 40;
+
+// Bytes from the first to the last element of `count` matrices `stride`
+// elements apart, each rows x cols with pitch ld; capped well inside int64.
+int64_t span_bytes(int64_t count, int64_t stride, int64_t rows, int64_t ld, int64_t cols, int esize) {
+  const __int128 n = ((__int128)(count - 1) * stride + (__int128)(rows - 1) * ld + cols) * esize;
+  return n > ((__int128)1 << 60) ? 1ll << 60 : (int64_t)n;
+}
+
+// Parameters both grouped products share.
+void common_params(GroupedParams& p, const HostEnv& env, int64_t groups, int64_t M, int64_t N, int64_t K, const void* A,
+                   int64_t lda, const void* B, int64_t ldb, const int32_t* offsets) {
+  std::memset(&p, 0, sizeof p);
+  p.A = A;
+  p.lda = lda;
+  p.B = B;
+  p.ldb = ldb;
+  p.offsets = offsets;
+  p.groups = (int)groups;
+  p.M = (int)M;
+  p.N = (int)N;
+  p.K = (int)K;
+  p.a_vec = aligned(A, 16) && lda % 8 == 0;
+  p.b_vec = aligned(B, 16) && ldb % 8 == 0;
+  p.group_rows = 16;
+  p.ksplit = 1;
+  p.err = env.err;
+  p.timeout_ns = env.timeout_ns;
+  p.inject_stall = env.inject_stall;
+}
+
+}  // namespace
+
+extern "C" {
+
+ttc_status ttc_gemm_grouped(int64_t groups, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,
+                            const int32_t* offsets, const void* B, int64_t ldb, int64_t strideB, ttc_layout layoutB,
+                            void* D, int64_t ldd, float alpha, const float* bias, int64_t strideBias, ttc_act act,
+                            ttc_dtype dtype, void* stream) {
+  if (groups < 0 || M < 0 || N < 0 || K < 0 || strideB < 0 || strideBias < 0) return TTC_ERR_INVALID_ARG;
+  if (layoutB != TTC_ROW_MAJOR && layoutB != TTC_COL_MAJOR) return TTC_ERR_INVALID_ARG;
+  if (!is_act(act) || !is_dtype(dtype)) return TTC_ERR_INVALID_ARG;
+  if (!is_16bit(dtype)) return TTC_ERR_UNSUPPORTED;
+  if (groups == 0 || M == 0 || N == 0) return TTC_OK;
+  if (lda < at_least_1(K) || ldb < at_least_1(layoutB == TTC_ROW_MAJOR ? N : K) || ldd < N) return TTC_ERR_INVALID_ARG;
+  if (offsets == nullptr || D == nullptr || (K > 0 && (A == nullptr || B == nullptr))) return TTC_ERR_INVALID_ARG;
+  if (!aligned(offsets, 4) || !aligned(D, 2) || !aligned(bias, 4) || (K > 0 && (!aligned(A, 2) || !aligned(B, 2))))
+    return TTC_ERR_INVALID_ARG;
+  if (groups > kMaxGroups || M > kSizeLimit || N > kSizeLimit || K > kSizeLimit || lda > kSizeLimit ||
+      ldb > kSizeLimit || ldd > kSizeLimit || strideB > kStrideLimit || strideBias > kStrideLimit)
+    return TTC_ERR_UNSUPPORTED;
+  const int64_t d_bytes = span_bytes(1, 0, M, ldd, N, 2);
+  if (K > 0) {
+    const int64_t b_rows = layoutB == TTC_ROW_MAJOR ? K : N, b_cols = layoutB == TTC_ROW_MAJOR ? N : K;
+    if (byte_ranges_overlap(D, d_bytes, A, span_bytes(1, 0, M, lda, K, 2)) ||
+        byte_ranges_overlap(D, d_bytes, B, span_bytes(groups, strideB, b_rows, ldb, b_cols, 2)))
+      return TTC_ERR_INVALID_ARG;
+  }
+  const int64_t col_blocks = blocks_of(N, kGroupedPlainTile);
+  if ((blocks_of(M, kGroupedPlainTile) + groups) * col_blocks > kSizeLimit) return TTC_ERR_UNSUPPORTED;
+
+  HostEnv env;
+  const ttc_status st = host_env(env);
+  if (st != TTC_OK) return st;
+  GroupedParams p;
+  common_params(p, env, groups, M, N, K, A, lda, B, ldb, offsets);
+  p.strideB = strideB;
+  p.b_vec = p.b_vec && (groups == 1 || strideB % 8 == 0);
+  p.b_mn = layoutB == TTC_ROW_MAJOR;
+  p.col_blocks = (int)col_blocks;
+  p.k_blocks = (int)blocks_of(K, kBK);
+  p.alpha = alpha;
+  p.bias = bias;
+  p.stride_bias = strideBias;
+  p.act = (int)act;
+  p.D = D;
+  p.ldd = ldd;
+  p.d_vec = aligned(D, 16) && ldd % 8 == 0;
+  const int64_t tiles = (blocks_of(M, kGroupedPlainTile) + (groups < M ? groups : M)) * col_blocks;
+  const int ctas = (int)(tiles < env.sm_count ? tiles : env.sm_count);
+  if (launch_grouped_plain(dtype == TTC_BF16, false, p, ctas, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return TTC_ERR_CUDA;
+  count_launches(1);
+  return TTC_OK;
+}
+
+ttc_status ttc_gemm_grouped_wgrad(int64_t groups, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,
+                                  const void* B, int64_t ldb, const int32_t* offsets, const void* C, int64_t ldc,
+                                  int64_t strideC, void* D, int64_t ldd, int64_t strideD, float alpha, float beta,
+                                  ttc_dtype dtype, ttc_dtype out_dtype, void* stream) {
+  if (groups < 0 || M < 0 || N < 0 || K < 0 || strideC < 0 || strideD < 0) return TTC_ERR_INVALID_ARG;
+  if (!is_dtype(dtype) || !is_dtype(out_dtype)) return TTC_ERR_INVALID_ARG;
+  if (!is_16bit(dtype) || (out_dtype != dtype && out_dtype != TTC_F32)) return TTC_ERR_UNSUPPORTED;
+  if (groups == 0 || N == 0 || K == 0) return TTC_OK;
+  if (lda < K || ldb < N || ldd < N || (beta != 0.0f && (C == nullptr || ldc < N))) return TTC_ERR_INVALID_ARG;
+  if (offsets == nullptr || D == nullptr || (M > 0 && (A == nullptr || B == nullptr))) return TTC_ERR_INVALID_ARG;
+  const int esize = out_dtype == TTC_F32 ? 4 : 2;
+  if (!aligned(offsets, 4) || !aligned(D, esize) || (beta != 0.0f && !aligned(C, esize)) ||
+      (M > 0 && (!aligned(A, 2) || !aligned(B, 2))))
+    return TTC_ERR_INVALID_ARG;
+  // the groups' D may not overlap
+  if (groups > 1 && (__int128)strideD < (__int128)(K - 1) * ldd + N) return TTC_ERR_INVALID_ARG;
+  if (groups > kMaxGroups || M > kSizeLimit || N > kSizeLimit || K > kSizeLimit || lda > kSizeLimit ||
+      ldb > kSizeLimit || ldd > kSizeLimit || strideD > kStrideLimit ||
+      (beta != 0.0f && (ldc > kSizeLimit || strideC > kStrideLimit)))
+    return TTC_ERR_UNSUPPORTED;
+  const int64_t d_bytes = span_bytes(groups, strideD, K, ldd, N, esize);
+  if (beta != 0.0f && !(C == D && ldc == ldd && (strideC == strideD || groups == 1)) &&
+      byte_ranges_overlap(D, d_bytes, C, span_bytes(groups, strideC, K, ldc, N, esize)))
+    return TTC_ERR_INVALID_ARG;
+  if (M > 0 && (byte_ranges_overlap(D, d_bytes, A, span_bytes(1, 0, M, lda, K, 2)) ||
+                byte_ranges_overlap(D, d_bytes, B, span_bytes(1, 0, M, ldb, N, 2))))
+    return TTC_ERR_INVALID_ARG;
+  const int64_t row_blocks = blocks_of(K, kGroupedPlainTile), col_blocks = blocks_of(N, kGroupedPlainTile);
+  if (row_blocks * col_blocks > kSizeLimit / groups) return TTC_ERR_UNSUPPORTED;
+
+  HostEnv env;
+  const ttc_status st = host_env(env);
+  if (st != TTC_OK) return st;
+  GroupedParams p;
+  common_params(p, env, groups, M, N, K, A, lda, B, ldb, offsets);
+  p.b_mn = 1;
+  p.row_blocks = (int)row_blocks;
+  p.col_blocks = (int)col_blocks;
+  p.alpha = alpha;
+  p.beta = beta;
+  p.out_f32 = out_dtype == TTC_F32;
+  if (beta != 0.0f) {
+    p.C = C;
+    p.ldc = ldc;
+    p.strideC = strideC;
+    p.c_vec = aligned(C, 16) && ldc * esize % 16 == 0 && (groups == 1 || strideC * esize % 16 == 0);
+  }
+  p.D = D;
+  p.ldd = ldd;
+  p.strideD = strideD;
+  p.d_vec = aligned(D, 16) && ldd * esize % 16 == 0 && (groups == 1 || strideD * esize % 16 == 0);
+  const int64_t tiles = groups * row_blocks * col_blocks;
+  const int ctas = (int)(tiles < env.sm_count ? tiles : env.sm_count);
+  if (launch_grouped_plain(dtype == TTC_BF16, true, p, ctas, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return TTC_ERR_CUDA;
+  count_launches(1);
+  return TTC_OK;
+}
+
+ttc_status ttc_quantize_rows(int64_t rows, int64_t cols, const void* X, int64_t ldx, ttc_dtype dtype, int8_t* Q,
+                             int64_t ldq, float* scale, void* stream) {
+  if (rows < 0 || cols < 0 || !is_dtype(dtype)) return TTC_ERR_INVALID_ARG;
+  if (dtype == TTC_I8) return TTC_ERR_UNSUPPORTED;
+  if (rows == 0) return TTC_OK;
+  const int esize = dtype == TTC_F32 ? 4 : 2;
+  if (scale == nullptr || !aligned(scale, 4)) return TTC_ERR_INVALID_ARG;
+  if (cols > 0 && (X == nullptr || Q == nullptr || !aligned(X, esize))) return TTC_ERR_INVALID_ARG;
+  if (ldx < cols || ldq < cols) return TTC_ERR_INVALID_ARG;
+  if (rows > kSizeLimit || cols > kSizeLimit || ldx > kSizeLimit || ldq > kSizeLimit) return TTC_ERR_UNSUPPORTED;
+  if (cols > 0) {
+    const int64_t x_bytes = span_bytes(1, 0, rows, ldx, cols, esize), q_bytes = span_bytes(1, 0, rows, ldq, cols, 1);
+    if (byte_ranges_overlap(X, x_bytes, Q, q_bytes) || byte_ranges_overlap(scale, rows * 4, Q, q_bytes) ||
+        byte_ranges_overlap(scale, rows * 4, X, x_bytes))
+      return TTC_ERR_INVALID_ARG;
+  }
+  HostEnv env;
+  const ttc_status st = host_env(env);
+  if (st != TTC_OK) return st;
+  QuantParams p{X, ldx, Q, ldq, scale, (int)rows, (int)cols};
+  const QuantIn in = dtype == TTC_F32 ? kQuantF32 : dtype == TTC_BF16 ? kQuantBF16 : kQuantF16;
+  if (launch_quantize_rows(p, in, env.sm_count, static_cast<cudaStream_t>(stream)) != cudaSuccess) return TTC_ERR_CUDA;
+  count_launches(1);
+  return TTC_OK;
+}
+
+size_t ttc_gemm_i8_scaled_workspace_size(int64_t M, int64_t N, int64_t K, const int8_t* A, int64_t lda, const int8_t* B,
+                                         int64_t ldb, const void* D, int64_t ldd, ttc_dtype out_dtype) {
+  (void)M, (void)N, (void)K, (void)A, (void)lda, (void)B, (void)ldb, (void)D, (void)ldd, (void)out_dtype;
+  return 0;
+}
+
+ttc_status ttc_gemm_i8_scaled(int64_t M, int64_t N, int64_t K, const int8_t* A, int64_t lda, const float* scaleA,
+                              const int8_t* B, int64_t ldb, const float* scaleB, void* D, int64_t ldd,
+                              const float* bias, ttc_act act, ttc_dtype out_dtype, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  (void)workspace, (void)workspace_bytes;
+  if (M < 0 || N < 0 || K < 0 || !is_act(act) || !is_dtype(out_dtype)) return TTC_ERR_INVALID_ARG;
+  if (out_dtype == TTC_I8) return TTC_ERR_UNSUPPORTED;
+  if (M == 0 || N == 0) return TTC_OK;
+  if (lda < at_least_1(K) || ldb < at_least_1(K) || ldd < N) return TTC_ERR_INVALID_ARG;
+  if (scaleA == nullptr || scaleB == nullptr || D == nullptr || (K > 0 && (A == nullptr || B == nullptr)))
+    return TTC_ERR_INVALID_ARG;
+  const int esize = out_dtype == TTC_F32 ? 4 : 2;
+  if (!aligned(scaleA, 4) || !aligned(scaleB, 4) || !aligned(bias, 4) || !aligned(D, esize)) return TTC_ERR_INVALID_ARG;
+  if (M > kSizeLimit || N > kSizeLimit || lda > kSizeLimit || ldb > kSizeLimit || ldd > kSizeLimit ||
+      K > TTC_I8_SCALED_MAX_K)
+    return TTC_ERR_UNSUPPORTED;
+  const int64_t d_bytes = span_bytes(1, 0, M, ldd, N, esize);
+  if (K > 0 && (byte_ranges_overlap(D, d_bytes, A, span_bytes(1, 0, M, lda, K, 1)) ||
+                byte_ranges_overlap(D, d_bytes, B, span_bytes(1, 0, N, ldb, K, 1))))
+    return TTC_ERR_INVALID_ARG;
+
+  HostEnv env;
+  const ttc_status st = host_env(env);
+  if (st != TTC_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const I8Out out = out_dtype == TTC_F32 ? kI8OutF32 : out_dtype == TTC_BF16 ? kI8OutBF16 : kI8OutF16;
+  I8ScaledParams p;
+  std::memset(&p, 0, sizeof p);
+  p.A = A;
+  p.lda = lda;
+  p.B = B;
+  p.ldb = ldb;
+  p.scaleA = scaleA;
+  p.scaleB = scaleB;
+  p.bias = bias;
+  p.D = D;
+  p.ldd = ldd;
+  p.M = (int)M;
+  p.N = (int)N;
+  p.K = (int)K;
+  p.act = (int)act;
+  p.a_vec = aligned(A, 16) && lda % 16 == 0;
+  p.b_vec = aligned(B, 16) && ldb % 16 == 0;
+  // The CTAs of two per SM, where a cluster of up to eight leaves each CTA two
+  // chunks of K at least.
+  p.chunks = (int)blocks_of(K, kI8RowsChunk);
+  const int64_t blocks = blocks_of(N, kI8RowsFeatures) * blocks_of(M, kI8RowsTokens);
+  int64_t split = 2ll * env.sm_count / blocks;
+  if (split > p.chunks / 2) split = p.chunks / 2;
+  p.split = (int)(split < 1 ? 1 : split > 8 ? 8 : split);
+  p.chunks_per_cta = (int)blocks_of(p.chunks, p.split);
+  if (launch_i8_rows(p, out, s) != cudaSuccess) return TTC_ERR_CUDA;
+  count_launches(1);
+  return TTC_OK;
+}
+
+}  // extern "C"
