@@ -35,6 +35,18 @@ __device__ __forceinline__ void build_group_table(const GroupedParams& p, int* o
   __syncthreads();
 }
 
+// Rows of group g: from the table, or (null) from the device's offsets themselves.
+__device__ __forceinline__ void group_rows(const GroupedParams& p, const int* offs, int g, int& lo, int& hi) {
+  if (offs != nullptr) {
+    lo = offs[g];
+    hi = offs[g + 1];
+  } else {
+    lo = min(max(__ldg(p.offsets + g), 0), p.M);
+    hi = min(max(__ldg(p.offsets + g + 1), 0), p.M);
+  }
+  hi = max(lo, hi);
+}
+
 // The group of tile t: the last one that starts at or before it and has tiles.
 __device__ __forceinline__ int group_of_tile(const int* start, int groups, int t) {
   int lo = 0, hi = groups - 1;  // the first g with start[g + 1] > t
@@ -64,14 +76,12 @@ __device__ __forceinline__ GroupedTile grouped_tile(const GroupedParams& p, cons
     const int per = p.row_blocks * p.col_blocks;
     x.g = t / per;
     r = t - x.g * per;
-    x.lo = offs[x.g];
-    x.hi = max(offs[x.g + 1], x.lo);
+    group_rows(p, offs, x.g, x.lo, x.hi);
     rows = p.row_blocks;
   } else {
     x.g = group_of_tile(start, p.groups, t);
     r = t - start[x.g];
-    x.lo = offs[x.g];
-    x.hi = max(offs[x.g + 1], x.lo);
+    group_rows(p, offs, x.g, x.lo, x.hi);
     rows = (x.hi - x.lo + ROWS - 1) / ROWS;
   }
   const int band = p.group_rows * p.col_blocks;
