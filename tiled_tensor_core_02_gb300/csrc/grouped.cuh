@@ -23,7 +23,6 @@ constexpr int kMaxGroups = 1024;
 struct GroupedParams {
   CUtensorMap tmA;  // the kernels that load with TMA
   CUtensorMap tmB;
-  CUtensorMap tmD;
   const void* A;
   int64_t lda;
   const void* B;
@@ -49,8 +48,6 @@ struct GroupedParams {
   int64_t ldd, strideD;
   int out_f32;  // wgrad: C and D are fp32
   int c_vec, d_vec;  // rows of C, D start on 16-byte boundaries
-  int d_tma;
-  int table;  // pair kernel: where the group tables lie (GroupTablePlace)
   int b_stream;  // forward: a group's weights are read by one block of rows as a rule
   int ksplit;   // token-side kernel: CTAs of a cluster that share a tile's k-blocks
   uint32_t* err;
@@ -58,14 +55,9 @@ struct GroupedParams {
   int inject_stall;
 };
 
-// The pair kernel's shared memory is nearly full: short tables fit behind the
-// barriers; longer ones take the second staging buffers of a 16-bit forward
-// output; the gradient of the weights, which needs no count of tiles, then reads
-// the offsets from global memory.
-enum GroupTablePlace : int { kTableBehind = 0, kTableInStaging = 1, kTableGlobal = 2 };
+// Tile of the kernel of CTA pairs: 256 x 256.
 constexpr int kGroupedPairTile = 256;
-constexpr int kPairTableBytes = 1536;
-int grouped_pair_clusters(bool bf16, bool wgrad, bool f32);
+int grouped_pair_clusters();
 cudaError_t launch_grouped_pair(bool bf16, bool wgrad, const GroupedParams& p, int clusters, cudaStream_t stream);
 
 // Tile of the kernels that load with plain loads: 128 x 128.

@@ -6,58 +6,87 @@
 
 namespace ttc {
 
-// offs[g] is the first row of group g, held to [0, M] (offs[groups] ends the
-// last one); start[g] the first tile of group g and start[groups] their
-// number.  ROWS: rows of a tile.  All threads of the CTA; `start` may be null
-// where every group has as many tiles as another.
+// The group table of a CTA in shared memory.  offs[g] is the first row of group
+// g, held to [0, M] (offs[groups] ends the last one); null where shared memory
+// has no room for it and the device's offsets are read instead.  start[i] is
+// the first tile of group i * step, its last entry the number of tiles; null in
+// the weights' gradient, where every group has as many tiles as another.
+struct GroupTable {
+  int* offs;
+  int* start;
+  int step;
+};
+
+__device__ __forceinline__ int offset_of(const GroupedParams& p, const GroupTable& tb, int g) {
+  return tb.offs != nullptr ? tb.offs[g] : min(max(__ldg(p.offsets + g), 0), p.M);
+}
+
+__device__ __forceinline__ void group_rows(const GroupedParams& p, const GroupTable& tb, int g, int& lo, int& hi) {
+  lo = offset_of(p, tb, g);
+  hi = max(lo, offset_of(p, tb, g + 1));
+}
+
 template <int ROWS>
-__device__ __forceinline__ void build_group_table(const GroupedParams& p, int* offs, int* start) {
-  for (int i = threadIdx.x; i <= p.groups; i += blockDim.x) offs[i] = min(max(__ldg(p.offsets + i), 0), p.M);
-  __syncthreads();
-  if (start == nullptr) return;
+__device__ __forceinline__ int group_tiles(const GroupedParams& p, const GroupTable& tb, int g) {
+  int lo, hi;
+  group_rows(p, tb, g, lo, hi);
+  return (hi - lo + ROWS - 1) / ROWS * p.col_blocks;
+}
+
+// Fills the table; all threads of the CTA.  ROWS: rows of a tile.
+template <int ROWS>
+__device__ __forceinline__ void build_group_table(const GroupedParams& p, const GroupTable& tb) {
+  if (tb.offs != nullptr) {
+    for (int i = threadIdx.x; i <= p.groups; i += blockDim.x) tb.offs[i] = min(max(__ldg(p.offsets + i), 0), p.M);
+    __syncthreads();
+  }
+  if (tb.start == nullptr) return;
   if (threadIdx.x < 32) {
+    const int entries = (p.groups + tb.step - 1) / tb.step;
     int carry = 0;
-    for (int g0 = 0; g0 < p.groups; g0 += 32) {
-      const int g = g0 + (int)threadIdx.x;
+    for (int i0 = 0; i0 < entries; i0 += 32) {
+      const int i = i0 + (int)threadIdx.x;
       int n = 0;
-      if (g < p.groups) n = (max(offs[g + 1] - offs[g], 0) + ROWS - 1) / ROWS * p.col_blocks;
+      for (int g = i * tb.step; g < min((i + 1) * tb.step, p.groups); ++g) n += group_tiles<ROWS>(p, tb, g);
       int sum = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
         if ((int)threadIdx.x >= o) sum += v;
       }
-      if (g < p.groups) start[g] = carry + sum - n;
+      if (i < entries) tb.start[i] = carry + sum - n;
       carry += __shfl_sync(0xFFFFFFFFu, sum, 31);
     }
-    if (threadIdx.x == 0) start[p.groups] = carry;
+    if (threadIdx.x == 0) tb.start[entries] = carry;
   }
   __syncthreads();
 }
 
-// Rows of group g: from the table, or (null) from the device's offsets themselves.
-__device__ __forceinline__ void group_rows(const GroupedParams& p, const int* offs, int g, int& lo, int& hi) {
-  if (offs != nullptr) {
-    lo = offs[g];
-    hi = offs[g + 1];
-  } else {
-    lo = min(max(__ldg(p.offsets + g), 0), p.M);
-    hi = min(max(__ldg(p.offsets + g + 1), 0), p.M);
-  }
-  hi = max(lo, hi);
+__device__ __forceinline__ int table_tiles(const GroupedParams& p, const GroupTable& tb) {
+  return tb.start[(p.groups + tb.step - 1) / tb.step];
 }
 
-// The group of tile t: the last one that starts at or before it and has tiles.
-__device__ __forceinline__ int group_of_tile(const int* start, int groups, int t) {
-  int lo = 0, hi = groups - 1;  // the first g with start[g + 1] > t
+// The group of tile t, which has tiles, and its first tile.
+template <int ROWS>
+__device__ __forceinline__ int group_of_tile(const GroupedParams& p, const GroupTable& tb, int t, int& first) {
+  int lo = 0, hi = (p.groups + tb.step - 1) / tb.step - 1;  // the first i with start[i + 1] > t
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
-    if (start[mid + 1] > t)
+    if (tb.start[mid + 1] > t)
       hi = mid;
     else
       lo = mid + 1;
   }
-  return lo;
+  first = tb.start[lo];
+  if (tb.step == 1) return lo;
+  int g = lo * tb.step;
+  const int last = min(g + tb.step, p.groups) - 1;
+  for (; g < last; ++g) {
+    const int n = group_tiles<ROWS>(p, tb, g);
+    if (first + n > t) break;
+    first += n;
+  }
+  return g;
 }
 
 struct GroupedTile {
@@ -69,27 +98,27 @@ struct GroupedTile {
 // Tiles of a group walk `group_rows` row blocks of one column block before the
 // next column block, so that CTAs at work together share panels of A and B.
 template <int ROWS, bool WGRAD>
-__device__ __forceinline__ GroupedTile grouped_tile(const GroupedParams& p, const int* offs, const int* start, int t) {
+__device__ __forceinline__ GroupedTile grouped_tile(const GroupedParams& p, const GroupTable& tb, int t) {
   GroupedTile x;
-  int r, rows;
+  int first, rows;
   if constexpr (WGRAD) {
     const int per = p.row_blocks * p.col_blocks;
     x.g = t / per;
-    r = t - x.g * per;
-    group_rows(p, offs, x.g, x.lo, x.hi);
+    first = x.g * per;
+    group_rows(p, tb, x.g, x.lo, x.hi);
     rows = p.row_blocks;
   } else {
-    x.g = group_of_tile(start, p.groups, t);
-    r = t - start[x.g];
-    group_rows(p, offs, x.g, x.lo, x.hi);
+    x.g = group_of_tile<ROWS>(p, tb, t, first);
+    group_rows(p, tb, x.g, x.lo, x.hi);
     rows = (x.hi - x.lo + ROWS - 1) / ROWS;
   }
+  int r = t - first;
   const int band = p.group_rows * p.col_blocks;
   const int b = r / band;
-  const int first = b * p.group_rows;
-  const int size = min(rows - first, p.group_rows);
+  const int above = b * p.group_rows;
+  const int size = min(rows - above, p.group_rows);
   r -= b * band;
-  x.rb = first + r % size;
+  x.rb = above + r % size;
   x.cb = r / size;
   return x;
 }

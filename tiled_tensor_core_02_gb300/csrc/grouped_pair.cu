@@ -12,9 +12,7 @@
 // * A tile's rows start at the group's first row wherever that is, which TMA
 //   allows (only the contiguous coordinate has an alignment).  The box of the
 //   last tile reaches into the next group's rows; they fill accumulator rows
-//   that are not stored.  A warp whose 32 rows all belong to the group stores
-//   them with TMA, the others row by row.  A half tile with no row in the group
-//   loads no A.
+//   that are not stored.  A half tile with no row in the group loads no A.
 // * In wgrad the next group's rows would be added to the sums.  The last
 //   k-block therefore issues MMAs for ceil(rows / 16) steps of 16 only, and where
 //   the group ends inside a step the rows behind it are set to zero in shared
@@ -28,7 +26,17 @@
 //   of the result after 2000 to 5600 tokens).  Every kChunkKBlocks k-blocks a fresh
 //   accumulator is started and the epilogue warps add up the partial sums in
 //   registers, rounded to nearest.
+//
+// Results leave through a 4 KB block of shared memory per epilogue warp, 32 rows
+// of 128 bytes: written a row per lane, read back and stored four whole rows an
+// instruction, with no asynchronous copy to wait for and any row left out.
+//
+// An operand with its rows contiguous ("MN-major") comes as two boxes of 64
+// rows by the stage's 128 k, so that a stage takes as few TMA instructions as
+// one with K contiguous: with a box per k-block the issuing thread, at about 70 ns
+// an instruction, set the pace.
 #include <atomic>
+#include <type_traits>
 
 #include "gemm2sm_kernel.cuh"
 #include "grouped_common.cuh"
@@ -40,20 +48,28 @@ namespace {
 constexpr int kTile = kGroupedPairTile;
 constexpr int kKPS = 2;  // k-blocks of a stage
 constexpr int kStages = 3;
-constexpr int kHalfBytes = 128 * kBK * 2;             // a CTA's share of one operand's k-block
-constexpr int kKBlockBytes = 2 * kHalfBytes;          // of both
-constexpr int kEpiWarps8 = 8;
-constexpr int kStagingBytes = kEpiWarps8 * 4096;      // 2 x 2 KB a warp (16-bit), or 4 KB (fp32)
+constexpr int kHalfBytes = 128 * kBK * 2;      // a CTA's share of one operand's k-block
+constexpr int kShareBytes = kKPS * kHalfBytes;  // ... of its stage
+constexpr int kEpiWarpCount = 8;
+constexpr int kStagingBytes = kEpiWarpCount * 4096;
 constexpr int kBarBytes = 256;
-constexpr int kSmemBytes = 1024 + kStages * kKPS * kKBlockBytes + kStagingBytes + kBarBytes + kPairTableBytes;
-constexpr int kChunkKBlocks = 8;                      // fp32 results: 512 tokens to an accumulator
+constexpr int kTableInts = 384;
+constexpr int kSmemBytes = 1024 + kStages * 2 * kShareBytes + kStagingBytes + kBarBytes + kTableInts * 4;
+constexpr int kChunkKBlocks = 12;  // fp32 results: 768 tokens to an accumulator
 static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 static_assert(kChunkKBlocks % kKPS == 0, "accumulator chunks hold whole stages");
+static_assert((kMaxGroups + 3) / 4 + 1 <= kTableInts, "a table of every fourth group's tiles has room");
 
-// threads: producer, MMA issuer, eight epilogue warps, and in wgrad the warp
-// that clears the rows behind a group's end
-template <bool WGRAD>
-constexpr int kThreadsOf = 32 * (2 + kEpiWarps8 + (WGRAD ? 1 : 0));
+// Warps: producer, MMA issuer, in wgrad the one that clears the rows behind a
+// group's end, a spare; then eight of the epilogue.
+constexpr int kEpiWarp0 = 4;
+constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarpCount);
+
+// A stage's k-blocks (0 to 2), the steps of 16 in its last one where that is
+// the tile's last, and whether it is.
+__device__ __forceinline__ int stage_word(int nkb, int last_steps, bool last) {
+  return nkb | (last ? last_steps << 4 | 256 : (kBK / kUmmaK) << 4);
+}
 
 struct PairLoop {
   int k_blocks;  // of the tile
@@ -78,56 +94,180 @@ __device__ __forceinline__ PairLoop pair_loop(const GroupedParams& p, const Grou
   return l;
 }
 
-// `boxes` boxes of one operand's share of a k-block: one 64 x 128 box with K
-// contiguous, or two 64 x 64 ones of 64 contiguous rows (columns) each.
+// A CTA's share of one operand's stage: with K contiguous a box of 64 k by 128
+// rows for each of `nkb` k-blocks, else two boxes of 64 rows by 128 k.
+__device__ __forceinline__ int share_bytes(bool mn, int nkb) { return mn ? kShareBytes : nkb * kHalfBytes; }
+
 template <bool PAIR>
-__device__ __forceinline__ void load_share(uint8_t* dst, const CUtensorMap* m, bool mn, int r0, int k0, int z,
+__device__ __forceinline__ void load_share(uint8_t* dst, const CUtensorMap* m, bool mn, int nkb, int r0, int k0, int z,
                                            uint64_t* bar, uint32_t bar_leader, uint64_t pol) {
-  const int x = mn ? r0 : k0, y = mn ? k0 : r0;
+  const int x0 = mn ? r0 : k0, y = mn ? k0 : r0;
+  const int x1 = x0 + 64;
   if constexpr (PAIR) {
-    tma_load_3d_pair(dst, m, x, y, z, bar_leader, pol);
-    if (mn) tma_load_3d_pair(dst + kHalfBytes / 2, m, x + 64, y, z, bar_leader, pol);
+    tma_load_3d_pair(dst, m, x0, y, z, bar_leader, pol);
+    if (mn || nkb > 1) tma_load_3d_pair(dst + kHalfBytes, m, x1, y, z, bar_leader, pol);
   } else {
-    tma_load_3d(dst, m, x, y, z, bar, pol);
-    if (mn) tma_load_3d(dst + kHalfBytes / 2, m, x + 64, y, z, bar, pol);
+    tma_load_3d(dst, m, x0, y, z, bar, pol);
+    if (mn || nkb > 1) tma_load_3d(dst + kHalfBytes, m, x1, y, z, bar, pol);
   }
 }
 
-// Stores 32 columns of the warp's 32 rows through the staging buffer by TMA.
-template <bool BF16, bool F32>
-__device__ __forceinline__ void store_block_tma(const GroupedParams& p, const float (&v)[32], uint8_t* sb, int col0,
-                                                int row0, int z, int lane) {
-  if constexpr (F32) {
-    constexpr layout::SwizzleBytes128 swz{};
+// The warp's staging block: 32 rows of 4 W bytes in 16-byte pieces, turned so
+// that neither a row per lane nor whole rows meet a bank twice (eight lanes take
+// a row of 128 bytes, four lanes one of 64).
+template <int W>
+__device__ __forceinline__ int staged(int r, int piece) {
+  return W == 32 ? r * 128 + ((piece ^ (r & 7)) << 4) : r * 64 + ((piece ^ ((r >> 1) & 3)) << 4);
+}
+
+// Writes 32 staged rows to D: `rows` of them, from d0 on with pitch ldd, and `n`
+// columns are inside D.  Whole 128-byte lines where D allows it: stores of half
+// lines took 1.6 times as long (gradient to fp32 of 8 x 4096 x 4096, 128 tokens
+// a group: 172 us against 109).
+template <typename T>
+__device__ __forceinline__ void copy_out(const GroupedParams& p, const uint8_t* sb, T* d0, int rows, int n, int lane) {
+  constexpr int kElems = 16 / (int)sizeof(T), kCols = 128 / (int)sizeof(T);
+  const int whole = p.d_vec ? min(n, kCols) & ~(kElems - 1) : 0;  // columns stored as 16-byte pieces
+  const int piece = lane & 7, r0 = lane >> 3;
+  if (piece * kElems < whole) {
+    T* d = d0 + (int64_t)r0 * p.ldd + piece * kElems;
 #pragma unroll
-    for (int ch = 0; ch < 8; ++ch)
-      *reinterpret_cast<float4*>(sb + swz((uint32_t)(lane * 128 + ch * 16))) =
-          make_float4(v[4 * ch], v[4 * ch + 1], v[4 * ch + 2], v[4 * ch + 3]);
-  } else {
-    constexpr layout::SwizzleBytes64 swz{};
-#pragma unroll
-    for (int ch = 0; ch < 4; ++ch)
-      *reinterpret_cast<uint4*>(sb + swz((uint32_t)(lane * 64 + ch * 16))) =
-          make_uint4(pack2<BF16>(v[8 * ch], v[8 * ch + 1]), pack2<BF16>(v[8 * ch + 2], v[8 * ch + 3]),
-                     pack2<BF16>(v[8 * ch + 4], v[8 * ch + 5]), pack2<BF16>(v[8 * ch + 6], v[8 * ch + 7]));
+    for (int i = 0; i < 8; ++i) {
+      const uint4 v = *reinterpret_cast<const uint4*>(sb + staged<32>(i * 4 + r0, piece));
+      if (i * 4 + r0 < rows) *reinterpret_cast<uint4*>(d + (int64_t)(i * 4) * p.ldd) = v;
+    }
   }
-  fence_proxy_async_smem();
+  if (whole < min(n, kCols)) {
+#pragma unroll 1
+    for (int r = 0; r < rows; ++r)
+#pragma unroll 1
+      for (int c = whole + lane; c < min(n, kCols); c += 32)
+        d0[(int64_t)r * p.ldd + c] = *reinterpret_cast<const T*>(sb + staged<32>(r, c / kElems) + (c % kElems) * sizeof(T));
+  }
+}
+
+// The reverse for C, in two steps so that the loads are in flight meanwhile: 32
+// rows of 4 W bytes by whole rows into registers, zeros outside `rows` and `n`
+// columns, and through the staging block to a row per lane.
+template <int W, typename T>
+__device__ __forceinline__ void copy_in(const GroupedParams& p, const T* c0, int rows, int n, int lane,
+                                        uint32_t (&w)[W]) {
+  constexpr int kElems = 16 / (int)sizeof(T);
+  constexpr int kLanes = W / 4;  // of a row
+  const int r0 = lane / kLanes, c = (lane % kLanes) * kElems;
+#pragma unroll
+  for (int i = 0; i < kLanes; ++i) {
+    const int r = i * (32 / kLanes) + r0;
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (r < rows) {
+      const T* src = c0 + (int64_t)r * p.ldc + c;
+      if (p.c_vec && c + kElems <= n) {
+        v = *reinterpret_cast<const uint4*>(src);
+      } else if (c < n) {
+        uint32_t ws[4] = {0u, 0u, 0u, 0u};
+#pragma unroll 1
+        for (int e = 0; e < min(kElems, n - c); ++e) {
+          uint32_t x;
+          if constexpr (sizeof(T) == 4)
+            x = __float_as_uint(src[e]);
+          else
+            x = (uint32_t)src[e] << ((e & 1) * 16);
+          const int at = sizeof(T) == 4 ? e : e >> 1;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) ws[k] |= k == at ? x : 0u;
+        }
+        v = make_uint4(ws[0], ws[1], ws[2], ws[3]);
+      }
+    }
+    w[4 * i] = v.x;
+    w[4 * i + 1] = v.y;
+    w[4 * i + 2] = v.z;
+    w[4 * i + 3] = v.w;
+  }
+}
+
+template <int W>
+__device__ __forceinline__ void stage_rows(uint8_t* sb, int lane, const uint32_t (&w)[W]) {
+  constexpr int kLanes = W / 4;
+#pragma unroll
+  for (int i = 0; i < kLanes; ++i)
+    *reinterpret_cast<uint4*>(sb + staged<W>(i * (32 / kLanes) + lane / kLanes, lane % kLanes)) =
+        make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
   __syncwarp();
-  if (lane == 0) {
-    tma_store_3d(&p.tmD, col0, row0, z, sb);
-    bulk_commit();
+}
+
+// Both steps for 32 fp32 columns without a register, asynchronously where C
+// allows it: the sums' 128 registers leave none (any that is spilled goes to L2,
+// nearly all of L1 being shared memory here; with C held in registers ahead of
+// its use the 1024-token case above took 320 to 370 us).  copy_async_wait and a
+// __syncwarp come before the rows' use.
+__device__ __forceinline__ void stage_rows_async(const GroupedParams& p, const float* c0, int rows, int n, int lane,
+                                                 uint8_t* sb) {
+  const int whole = p.c_vec ? min(n, 32) & ~3 : 0;
+  const int piece = lane & 7, r0 = lane >> 3;
+  if (piece * 4 < whole) {
+    const float* src = c0 + (int64_t)r0 * p.ldc + piece * 4;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i * 4 + r0 < rows) copy_async_16(sb + staged<32>(i * 4 + r0, piece), src + (int64_t)(i * 4) * p.ldc);
+  }
+  if (whole < min(n, 32)) {
+#pragma unroll 1
+    for (int r = 0; r < rows; ++r)
+      if (lane >= whole && lane < n)
+        *reinterpret_cast<float*>(sb + staged<32>(r, lane / 4) + (lane & 3) * 4) = c0[(int64_t)r * p.ldc + lane];
   }
 }
 
-template <bool BF16, bool WGRAD, bool F32>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<WGRAD>, 1)
+// What an epilogue warp has of a tile: 32 rows by 128 columns.
+template <typename T>
+struct EpiTile {
+  T* d;        // its first element of D, and of C (null without C)
+  const T* c;
+  int g, col0;
+  int rows, cols;  // rows inside the group (wgrad: inside D); columns of D from col0 on
+  int k_blocks;
+};
+
+template <bool WGRAD, typename T>
+__device__ __forceinline__ EpiTile<T> epi_tile(const GroupedParams& p, const GroupedTile& x, uint32_t rank, int q,
+                                               int part) {
+  EpiTile<T> e;
+  const int r0 = x.rb * kTile + (int)rank * 128 + q * 32;
+  const int64_t row0 = WGRAD ? r0 : (int64_t)x.lo + r0;
+  e.g = x.g;
+  e.col0 = x.cb * kTile + part * (kTile / 2);
+  e.rows = max(0, min(32, WGRAD ? p.K - r0 : x.hi - x.lo - r0));
+  e.cols = p.N - e.col0;
+  e.d = static_cast<T*>(p.D) + (WGRAD ? (int64_t)x.g * p.strideD : 0) + row0 * p.ldd + e.col0;
+  e.c = WGRAD && p.C != nullptr ? static_cast<const T*>(p.C) + (int64_t)x.g * p.strideC + row0 * p.ldc + e.col0 : nullptr;
+  e.k_blocks = pair_loop<WGRAD>(p, x).k_blocks;
+  return e;
+}
+
+// Asks L2 for the tile's C, line by line and not as bulk copies: those go through
+// the unit that brings the operands.
+template <typename T>
+__device__ __forceinline__ void prefetch_c(const GroupedParams& p, const EpiTile<T>& e, int lane) {
+  if (lane >= e.rows) return;
+  const T* row = e.c + (int64_t)lane * p.ldc;
+  constexpr int kLine = 128 / (int)sizeof(T);
+#pragma unroll
+  for (int c = 0; c < kTile / 2; c += kLine)
+    if (c < e.cols) prefetch_l2_line(row + c);
+}
+
+// ADD: C is read (wgrad); a parameter of its own because the fp32 sums leave
+// few registers for it.
+template <bool BF16, bool WGRAD, bool F32, bool ADD>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     grouped_pair_kernel(const __grid_constant__ GroupedParams p) {
-  static_assert(WGRAD || !F32, "forward results are 16-bit");
+  static_assert(WGRAD || (!F32 && !ADD), "forward results are 16-bit and added to nothing");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sA = smem;  // [stage][k-block of the stage]
-  uint8_t* sB = sA + kStages * kKPS * kHalfBytes;
-  uint8_t* staging = sB + kStages * kKPS * kHalfBytes;
+  uint8_t* sA = smem;  // [stage][k-block of the stage, or 64 rows]
+  uint8_t* sB = sA + kStages * kShareBytes;
+  uint8_t* staging = sB + kStages * kShareBytes;
   uint64_t* bars = reinterpret_cast<uint64_t*>(staging + kStagingBytes);
   uint64_t* full = bars;
   uint64_t* empty = bars + kStages;
@@ -137,10 +277,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<WGRAD>, 1
   uint64_t* stall_bar = bars + 3 * kStages + 4;
   uint64_t* drain_bar = bars + 3 * kStages + 5;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 3 * kStages + 6);
-  int* table = reinterpret_cast<int*>(p.table == kTableInStaging ? staging + kStagingBytes / 2
-                                                                 : reinterpret_cast<uint8_t*>(bars) + kBarBytes);
-  int* offs = p.table == kTableGlobal ? nullptr : table;
-  int* start = WGRAD ? nullptr : table + p.groups + 1;
+  // what the producer tells the MMA issuer about a stage
+  int* stage_info = reinterpret_cast<int*>(bars + 3 * kStages + 7);
+  int* table = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + kBarBytes);
+  // the whole table where it has room, else only every fourth group's first tile
+  GroupTable tb{nullptr, nullptr, 1};
+  if constexpr (WGRAD) {
+    if (p.groups + 1 <= kTableInts) tb.offs = table;
+  } else if (2 * (p.groups + 1) <= kTableInts) {
+    tb.offs = table;
+    tb.start = table + p.groups + 1;
+  } else {
+    tb.start = table;
+    tb.step = 4;
+  }
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -156,14 +306,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<WGRAD>, 1
     }
     if (lane < 2) {
       mbar_init(&tmem_full[lane], 1);
-      mbar_init(&tmem_empty[lane], 2 * kEpiWarps8);
+      mbar_init(&tmem_empty[lane], 2 * kEpiWarpCount);
     }
     if (lane == 0) {
       mbar_init(stall_bar, 1);
       mbar_init(drain_bar, 1);
       prefetch_tmap(&p.tmA);
       prefetch_tmap(&p.tmB);
-      if (p.d_tma) prefetch_tmap(&p.tmD);
     }
     fence_barrier_init();
   }
@@ -177,8 +326,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<WGRAD>, 1
   const uint32_t tmem_base = *tmem_slot;
   grid_dependency_wait();
   grid_dependents_launch();
-  if (offs != nullptr) build_group_table<kTile>(p, offs, start);
-  const int tiles = WGRAD ? p.groups * p.row_blocks * p.col_blocks : start[p.groups];
+  build_group_table<kTile>(p, tb);
+  const int tiles = WGRAD ? p.groups * p.row_blocks * p.col_blocks : table_tiles(p, tb);
 
   if (warp == 0) {
     // ---------------------------------------------------------------- producer (both CTAs)
@@ -191,7 +340,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<WGRAD>, 1
       uint32_t fixed = 0, fix_parity = 0, fix_phase = 0;  // stages armed on `fix`
       bool ok = true;
       for (int t = pair; ok && t < tiles; t += num_pairs) {
-        const GroupedTile x = grouped_tile<kTile, WGRAD>(p, offs, start, t);
+        const GroupedTile x = grouped_tile<kTile, WGRAD>(p, tb, t);
         const PairLoop l = pair_loop<WGRAD>(p, x);
         const int n0 = x.cb * kTile + (int)rank * 128;
         const int m0 = (WGRAD ? 0 : x.lo) + x.rb * kTile + (int)rank * 128;
@@ -199,43 +348,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<WGRAD>, 1
         const bool a_on = WGRAD || m0 < x.hi;
         const int halves = WGRAD || x.lo + x.rb * kTile + 128 < x.hi ? 2 : 1;
         const int zb = WGRAD ? 0 : (p.strideB != 0 ? x.g : 0);
-        for (int kb0 = 0; kb0 < l.k_blocks; kb0 += kKPS) {
+        int kb0 = 0;
+        do {  // a tile without k-blocks takes a stage without loads
           const int nkb = min(kKPS, l.k_blocks - kb0);
           if (!mbar_wait(&empty[stage], phase ^ 1u, wc)) {
             ok = false;
             break;
           }
+          if (leader) stage_info[stage] = stage_word(nkb, l.last_steps, kb0 + nkb >= l.k_blocks);
+          const bool b_mn = WGRAD || p.b_mn;
+          const int bytes_a = nkb > 0 ? share_bytes(WGRAD, nkb) : 0, bytes_b = nkb > 0 ? share_bytes(b_mn, nkb) : 0;
           const bool clear = WGRAD && l.fix_rows != 0 && kb0 + nkb == l.k_blocks;
           const uint32_t full_leader = mapa_shared(smem_u32(&full[stage]), 0);
           if (clear) {
-            mbar_arrive_expect_tx(&fix[stage], nkb * kKBlockBytes);
+            mbar_arrive_expect_tx(&fix[stage], bytes_a + bytes_b);
             fixed |= 1u << stage;
             fix_parity = (fix_parity & ~(1u << stage)) | (fix_phase & (1u << stage));
             fix_phase ^= 1u << stage;
           } else if (leader) {
-            mbar_arrive_expect_tx(&full[stage], nkb * (halves + 2) * kHalfBytes);
+            mbar_arrive_expect_tx(&full[stage], halves * bytes_a + 2 * bytes_b);
             armed |= 1u << stage;
             armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
           } else if (WGRAD) {
             mbar_arrive_cluster_relaxed(full_leader);
           }
-          for (int j = 0; j < nkb; ++j) {
-            uint8_t* a = sA + (stage * kKPS + j) * kHalfBytes;
-            uint8_t* b = sB + (stage * kKPS + j) * kHalfBytes;
-            const int k0 = (WGRAD ? x.lo : 0) + (kb0 + j) * kBK;
-            if (clear) {
-              load_share<false>(a, &p.tmA, WGRAD, m0, k0, 0, &fix[stage], 0, keep);
-              load_share<false>(b, &p.tmB, WGRAD || p.b_mn, n0, k0, zb, &fix[stage], 0, pol_b);
-            } else {
-              if (a_on) load_share<true>(a, &p.tmA, WGRAD, m0, k0, 0, nullptr, full_leader, keep);
-              load_share<true>(b, &p.tmB, WGRAD || p.b_mn, n0, k0, zb, nullptr, full_leader, pol_b);
-            }
+          uint8_t* a = sA + stage * kShareBytes;
+          uint8_t* b = sB + stage * kShareBytes;
+          const int k0 = (WGRAD ? x.lo : 0) + kb0 * kBK;
+          if (nkb == 0) {
+            // nothing to load
+          } else if (clear) {
+            load_share<false>(a, &p.tmA, WGRAD, nkb, m0, k0, 0, &fix[stage], 0, keep);
+            load_share<false>(b, &p.tmB, b_mn, nkb, n0, k0, zb, &fix[stage], 0, pol_b);
+          } else {
+            if (a_on) load_share<true>(a, &p.tmA, WGRAD, nkb, m0, k0, 0, nullptr, full_leader, keep);
+            load_share<true>(b, &p.tmB, b_mn, nkb, n0, k0, zb, nullptr, full_leader, pol_b);
           }
           if (++stage == kStages) {
             stage = 0;
             phase ^= 1u;
           }
-        }
+          kb0 += kKPS;
+        } while (kb0 < l.k_blocks);
       }
       if (!ok) {
         // loads in flight land before the pair may exit
@@ -250,64 +404,63 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<WGRAD>, 1
     if (leader && lane == 0) {
       const bool b_mn = WGRAD || p.b_mn != 0;
       const uint32_t idesc = idesc_f16(BF16, WGRAD, b_mn, kTile, kTile);
-      const uint64_t a0 = smem_desc_sw128(smem_u32(sA), WGRAD ? 8192u : 16u, 1024);
-      const uint64_t b0 = smem_desc_sw128(smem_u32(sB), b_mn ? 8192u : 16u, 1024);
+      const uint64_t a0 = smem_desc_sw128(smem_u32(sA), WGRAD ? (uint32_t)kHalfBytes : 16u, 1024);
+      const uint64_t b0 = smem_desc_sw128(smem_u32(sB), b_mn ? (uint32_t)kHalfBytes : 16u, 1024);
       const uint64_t a_step = WGRAD ? 2048u >> 4 : 32u >> 4, b_step = b_mn ? 2048u >> 4 : 32u >> 4;
+      // from one k-block of a stage to the next
+      const uint32_t a_kb = (WGRAD ? kHalfBytes / 2 : kHalfBytes) >> 4, b_kb = (b_mn ? kHalfBytes / 2 : kHalfBytes) >> 4;
       bool ok = true, any = false;
       if (p.inject_stall) ok = mbar_wait(stall_bar, 0, wc);  // nothing arrives here
       int stage = 0, it = 0;
       uint32_t phase = 0;
+      bool ready = true;  // whether the next accumulator is known to be free
+      // the first use of each accumulator passes at once
       for (int t = pair; ok && t < tiles; t += num_pairs) {
-        const GroupedTile x = grouped_tile<kTile, WGRAD>(p, offs, start, t);
-        const PairLoop l = pair_loop<WGRAD>(p, x);
-        const int chunk = F32 ? kChunkKBlocks : l.k_blocks;
-        int kbeg = 0;
-        do {  // once, too, for a tile without k-blocks
-          const int kend = min(l.k_blocks, kbeg + chunk);
+        bool last = false;
+        do {  // an accumulator: the tile's, or a chunk of it
           const int acc = it & 1;
-          if (!mbar_wait_cluster(&tmem_empty[acc], ((it >> 1) & 1) ^ 1u, wc)) {
+          if (!ready && !mbar_wait_cluster(&tmem_empty[acc], ((it >> 1) & 1) ^ 1u, wc)) {
             ok = false;
             break;
           }
+          ready = false;
           tc_fence_after();
           const uint32_t d_tmem = tmem_base + acc * kTile;
-          for (int kb0 = kbeg; kb0 < kend; kb0 += kKPS) {
-            const int nkb = min(kKPS, kend - kb0);
+          int done = 0;  // k-blocks in this accumulator
+          do {
             // zeros written by the other CTA's threads are behind this barrier in wgrad
             if (!(WGRAD ? mbar_wait_cluster(&full[stage], phase, wc) : mbar_wait(&full[stage], phase, wc))) {
               ok = false;
               break;
             }
+            const int info = stage_info[stage];
+            const int nkb = info & 15, steps = (info >> 4) & 15;
+            last = (info & 256) != 0;
             tc_fence_after();
 #pragma unroll
             for (int j = 0; j < kKPS; ++j) {
               if (j < nkb) {
-                const uint64_t ad = a0 + (uint32_t)(stage * kKPS + j) * (kHalfBytes >> 4);
-                const uint64_t bd = b0 + (uint32_t)(stage * kKPS + j) * (kHalfBytes >> 4);
-                const int steps = WGRAD && kb0 + j == l.k_blocks - 1 ? l.last_steps : kBK / kUmmaK;
-                mma_f16_pair(d_tmem, ad, bd, idesc, kb0 + j != kbeg);
+                const uint64_t ad = a0 + (uint32_t)stage * (kShareBytes >> 4) + j * a_kb;
+                const uint64_t bd = b0 + (uint32_t)stage * (kShareBytes >> 4) + j * b_kb;
+                mma_f16_pair(d_tmem, ad, bd, idesc, (done | j) != 0);
 #pragma unroll
                 for (int k = 1; k < kBK / kUmmaK; ++k)
-                  if (!WGRAD || k < steps) mma_f16_pair(d_tmem, ad + k * a_step, bd + k * b_step, idesc, 1u);
+                  if (!WGRAD || k < steps || j + 1 < nkb) mma_f16_pair(d_tmem, ad + k * a_step, bd + k * b_step, idesc, 1u);
               }
             }
-            any = true;
+            done += nkb;
+            any = any || nkb > 0;
             mma_commit_pair(&empty[stage], 0x3);
             if (++stage == kStages) {
               stage = 0;
               phase ^= 1u;
             }
-          }
+            if (!ready) ready = mbar_test_cluster(&tmem_empty[acc ^ 1], (((it + 1) >> 1) & 1) ^ 1u);
+          } while (!last && (!F32 || done < kChunkKBlocks));
           if (!ok) break;
-          if (kend == kbeg) {
-            mbar_arrive(&tmem_full[acc]);
-            mbar_arrive_cluster(mapa_shared(smem_u32(&tmem_full[acc]), 1));
-          } else {
-            mma_commit_pair(&tmem_full[acc], 0x3);
-          }
+          mma_commit_pair(&tmem_full[acc], 0x3);
           ++it;
-          kbeg = kend;
-        } while (kbeg < l.k_blocks);
+        } while (!last);
       }
       if (any) {
         // every MMA must have finished with both CTAs' TMEM before it is freed
@@ -315,64 +468,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<WGRAD>, 1
         drain_wait(drain_bar, 0, 100000000ull);
       }
     }
-  } else if (warp < 2 + kEpiWarps8) {
+  } else if (warp >= kEpiWarp0) {
     // ---------------------------------------------------------------- epilogue (both CTAs)
-    const int ew = warp - 2, q = warp & 3, part = ew >> 2;
-    constexpr int esize = F32 ? 4 : 2;
-    constexpr int kChunks = kTile / 64;  // 32-column chunks of this warp: one half of the tile's columns
-    uint8_t* sbuf = staging + ew * (F32 ? 4096 : 2048);
-    const bool two_bufs = !F32 && p.table != kTableInStaging;
-    const int gran = 16 / esize;
-    int buf = 0, it = 0;
+    const int ew = warp - kEpiWarp0, q = warp & 3, part = ew >> 2;  // quarter of the rows, half of the columns
+    using T = typename std::conditional<F32, float, uint16_t>::type;
+    constexpr int kUnit = 128 / (int)sizeof(T);    // columns that 128 bytes hold
+    constexpr int kUnits = kTile / 2 / kUnit;      // of this warp
+    uint8_t* sb = staging + ew * 4096;
+    const uint32_t tmem_mine = tmem_base + ((uint32_t)(q * 32) << 16) + part * (kTile / 2);
+    int it = 0;
     bool ok = true;
     for (int t = pair; ok && t < tiles; t += num_pairs) {
-      const GroupedTile x = grouped_tile<kTile, WGRAD>(p, offs, start, t);
-      const PairLoop l = pair_loop<WGRAD>(p, x);
-      const int r0 = x.rb * kTile + (int)rank * 128 + q * 32;  // the warp's first row, of the group in forward
-      const int64_t row0 = WGRAD ? r0 : (int64_t)x.lo + r0;
-      const int64_t row = row0 + lane;
-      const bool row_ok = WGRAD ? row < p.K : row < x.hi;
-      const int z = WGRAD ? x.g : 0;
-      const int colp = x.cb * kTile + part * (kTile / 2);
-      char* d_row = static_cast<char*>(p.D) + ((int64_t)z * p.strideD + row * p.ldd) * esize;
-      const char* c_row = p.C != nullptr && row_ok
-                              ? static_cast<const char*>(p.C) + ((int64_t)z * p.strideC + row * p.ldc) * esize
-                              : nullptr;
-      const float* bias = p.bias != nullptr ? p.bias + (int64_t)x.g * p.stride_bias : nullptr;
-      if (c_row != nullptr && p.c_vec && colp < p.N) {
-        // this row's part of C toward L2 while the sums are made
-        const int n = min(kTile / 2, p.N - colp) * esize & ~15;
-        if (n > 0) prefetch_l2_bulk(c_row + (int64_t)colp * esize, (uint32_t)n);
+      const EpiTile<T> e0 = epi_tile<WGRAD, T>(p, grouped_tile<kTile, WGRAD>(p, tb, t), rank, q, part);
+      if constexpr (ADD && !F32) {
+        // C of the pair's next tile toward L2
+        if (t == pair) prefetch_c(p, e0, lane);
+        if (t + num_pairs < tiles)
+          prefetch_c(p, epi_tile<WGRAD, T>(p, grouped_tile<kTile, WGRAD>(p, tb, t + num_pairs), rank, q, part), lane);
       }
-      auto finish = [&](const uint32_t(&w)[32], int c) {
-        const int col0 = colp + c * 32;
-        const int n = min(32, p.N - col0);
-        float v[32];
-        grouped_values<BF16>(p, w, c_row != nullptr && n > 0 ? c_row + (int64_t)col0 * esize : nullptr,
-                             bias != nullptr && n > 0 ? bias + col0 : nullptr, n, v);
-        // a TMA store ends at whole 16-byte granules of a row: a chunk that
-        // holds fewer is stored by its threads
-        const bool by_tma = p.d_tma && n > 0 && n % gran == 0 && (WGRAD ? row0 < p.K : row0 + 32 <= x.hi);
-        if (by_tma) {
-          if (lane == 0) {
-            if (two_bufs)
-              bulk_wait_read<1>();
-            else
-              bulk_wait_read<0>();
-          }
-          __syncwarp();
-          store_block_tma<BF16, F32>(p, v, sbuf + (two_bufs ? buf * (kStagingBytes / 2) : 0), col0, (int)row0, z, lane);
-          buf ^= 1;
-        } else if (row_ok && n > 0) {
-          store_row<BF16>(p, v, d_row + (int64_t)col0 * esize, n);
-        }
-      };
       if constexpr (F32) {
-        uint32_t sums[kChunks][32];  // floats
+        uint32_t sums[kTile / 32][16];  // floats: this thread's row of the warp's 128 columns
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c)
+        for (int c = 0; c < kTile / 32; ++c)
 #pragma unroll
-          for (int j = 0; j < 32; ++j) sums[c][j] = 0u;
+          for (int j = 0; j < 16; ++j) sums[c][j] = 0u;
+        const int k_blocks = e0.k_blocks;
+        if constexpr (ADD) stage_rows_async(p, reinterpret_cast<const float*>(e0.c), e0.rows, e0.cols, lane, sb);
         int kbeg = 0;
         do {
           const int acc = it & 1;
@@ -381,15 +502,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<WGRAD>, 1
             break;
           }
           tc_fence_after();
-          if (l.k_blocks > 0) {
+          if (k_blocks > 0) {
 #pragma unroll
-            for (int c = 0; c < kChunks; ++c) {
-              uint32_t w[32];
-              tmem_ld_32x32b_x32(tmem_base + ((uint32_t)(q * 32) << 16) + acc * kTile + part * (kTile / 2) + c * 32, w);
+            for (int c = 0; c < kTile / 32; ++c) {
+              uint32_t w[16];
+              tmem_ld_32x32b_x16<0>(tmem_mine + acc * kTile + c * 16, w);
               tmem_ld_wait();
 #pragma unroll
-              for (int j = 0; j < 32; ++j)
+              for (int j = 0; j < 16; ++j) {
                 sums[c][j] = __float_as_uint(__uint_as_float(sums[c][j]) + __uint_as_float(w[j]));
+              }
             }
           }
           tc_fence_before();
@@ -397,44 +519,112 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<WGRAD>, 1
           if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&tmem_empty[acc]), 0));
           ++it;
           kbeg += kChunkKBlocks;
-        } while (kbeg < l.k_blocks);
+        } while (kbeg < k_blocks);
         if (!ok) break;
+        // found again rather than kept: the sums leave no registers for it
+        int t_again = t;
+        asm volatile("" : "+r"(t_again));
+        const EpiTile<T> e = epi_tile<WGRAD, T>(p, grouped_tile<kTile, WGRAD>(p, tb, t_again), rank, q, part);
+        float* df = reinterpret_cast<float*>(e.d);
+        const float* cf = reinterpret_cast<const float*>(e.c);
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c) finish(sums[c], c);
+        for (int c = 0; c < kTile / 64; ++c) {
+          if constexpr (ADD) {
+            copy_async_wait();
+            __syncwarp();
+          }
+          // a lane's own row: C there, if any, gives way to D
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t(&sum)[16] = sums[2 * c + (i >> 2)];
+            const int j = 4 * (i & 3);
+            float4* at = reinterpret_cast<float4*>(sb + staged<32>(lane, i));
+            float4 v = make_float4(p.alpha * __uint_as_float(sum[j]), p.alpha * __uint_as_float(sum[j + 1]),
+                                   p.alpha * __uint_as_float(sum[j + 2]), p.alpha * __uint_as_float(sum[j + 3]));
+            if constexpr (ADD) {
+              const float4 w = *at;
+              v = make_float4(fmaf(p.beta, w.x, v.x), fmaf(p.beta, w.y, v.y), fmaf(p.beta, w.z, v.z),
+                              fmaf(p.beta, w.w, v.w));
+            }
+            *at = v;
+          }
+          __syncwarp();
+          copy_out(p, sb, df + c * 32, e.rows, e.cols - c * 32, lane);
+          __syncwarp();
+          if (ADD && c + 1 < kTile / 64)
+            stage_rows_async(p, cf + c * 32 + 32, e.rows, e.cols - c * 32 - 32, lane, sb);
+        }
       } else {
         const int acc = it & 1;
+        uint32_t cw[32];  // C of the next unit
+        if (ADD) copy_in(p, e0.c, e0.rows, e0.cols, lane, cw);
         if (!mbar_wait(&tmem_full[acc], (it >> 1) & 1, wc)) break;
         ++it;
         tc_fence_after();
+        const float* bias = !WGRAD && p.bias != nullptr ? p.bias + (int64_t)e0.g * p.stride_bias + e0.col0 : nullptr;
 #pragma unroll 1
-        for (int c = 0; c < kChunks; ++c) {
-          uint32_t w[32];
-          if (l.k_blocks > 0) {
-            tmem_ld_32x32b_x32(tmem_base + ((uint32_t)(q * 32) << 16) + acc * kTile + part * (kTile / 2) + c * 32, w);
+        for (int u = 0; u < kUnits; ++u) {
+          uint32_t w[2][32];
+          if (e0.k_blocks > 0) {
+            tmem_ld_32x32b_x32(tmem_mine + acc * kTile + u * kUnit, w[0]);
+            tmem_ld_32x32b_x32(tmem_mine + acc * kTile + u * kUnit + 32, w[1]);
             tmem_ld_wait();
           } else {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) w[j] = 0u;
+            for (int j = 0; j < 32; ++j) w[0][j] = w[1][j] = 0u;
           }
-          if (c == kChunks - 1) {
+          if (u == kUnits - 1) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&tmem_empty[acc]), 0));
           }
-          finish(w, c);
+          if (e0.cols <= u * kUnit) continue;
+          if constexpr (ADD) {
+            stage_rows(sb, lane, cw);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const uint4 v = *reinterpret_cast<const uint4*>(sb + staged<32>(lane, i));
+              cw[4 * i] = v.x;
+              cw[4 * i + 1] = v.y;
+              cw[4 * i + 2] = v.z;
+              cw[4 * i + 3] = v.w;
+            }
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int at = u * kUnit + h * 32, n = min(32, e0.cols - at);
+            float v[32];
+            grouped_values<BF16>(p, w[h], nullptr, bias != nullptr && n > 0 ? bias + at : nullptr, n, v);
+            if (ADD) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                v[2 * j] = fmaf(p.beta, half_bits_to_float<BF16>((uint16_t)(cw[h * 16 + j] & 0xFFFFu)), v[2 * j]);
+                v[2 * j + 1] = fmaf(p.beta, half_bits_to_float<BF16>((uint16_t)(cw[h * 16 + j] >> 16)), v[2 * j + 1]);
+              }
+            }
+#pragma unroll
+            for (int ch = 0; ch < 4; ++ch)
+              *reinterpret_cast<uint4*>(sb + staged<32>(lane, h * 4 + ch)) =
+                  make_uint4(pack2<BF16>(v[8 * ch], v[8 * ch + 1]), pack2<BF16>(v[8 * ch + 2], v[8 * ch + 3]),
+                             pack2<BF16>(v[8 * ch + 4], v[8 * ch + 5]), pack2<BF16>(v[8 * ch + 6], v[8 * ch + 7]));
+          }
+          if (ADD && u + 1 < kUnits)
+            copy_in(p, e0.c + (u + 1) * kUnit, e0.rows, e0.cols - (u + 1) * kUnit, lane, cw);
+          __syncwarp();
+          copy_out(p, sb, e0.d + u * kUnit, e0.rows, e0.cols - u * kUnit, lane);
+          __syncwarp();
         }
       }
     }
-    if (p.d_tma && lane == 0) bulk_wait_all();
-  } else {
+  } else if (WGRAD && warp == 2) {
     // ---------------------------------------------------------------- wgrad: rows behind a group's end (both CTAs)
     int stage = 0;
     uint32_t fix_phase = 0;
     bool ok = true;
     for (int t = pair; ok && t < tiles; t += num_pairs) {
-      const GroupedTile x = grouped_tile<kTile, WGRAD>(p, offs, start, t);
+      const GroupedTile x = grouped_tile<kTile, WGRAD>(p, tb, t);
       const PairLoop l = pair_loop<WGRAD>(p, x);
-      const int stages = (l.k_blocks + kKPS - 1) / kKPS;
+      const int stages = max(1, (l.k_blocks + kKPS - 1) / kKPS);
       if (l.fix_rows != 0) {
         const int s = (stage + stages - 1) % kStages;
         if (!mbar_wait(&fix[s], (fix_phase >> s) & 1u, wc)) {
@@ -445,12 +635,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<WGRAD>, 1
         const int j = (l.k_blocks - 1) % kKPS;  // the last k-block's place in its stage
         const int r_end = (l.fix_rows + kUmmaK - 1) / kUmmaK * kUmmaK;
         const int n16 = (r_end - l.fix_rows) * 8;  // 16-byte pieces of a 64-wide slab's rows
-        uint8_t* ops[2] = {sA + (s * kKPS + j) * kHalfBytes, sB + (s * kKPS + j) * kHalfBytes};
+        // the k-block's rows of a 64-wide slab, 128 bytes each; two slabs an operand
+        uint8_t* ops[2] = {sA + s * kShareBytes + j * (kHalfBytes / 2), sB + s * kShareBytes + j * (kHalfBytes / 2)};
 #pragma unroll
         for (int o = 0; o < 2; ++o)
           for (int i = lane; i < 2 * n16; i += 32) {
             const int slab = i >= n16 ? 1 : 0;
-            *reinterpret_cast<uint4*>(ops[o] + slab * (kHalfBytes / 2) + l.fix_rows * 128 + (i - slab * n16) * 16) =
+            *reinterpret_cast<uint4*>(ops[o] + slab * kHalfBytes + l.fix_rows * 128 + (i - slab * n16) * 16) =
                 make_uint4(0u, 0u, 0u, 0u);
           }
         fence_proxy_async_smem();
@@ -470,7 +661,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<WGRAD>, 1
   }
 }
 
-template <bool BF16, bool WGRAD, bool F32>
+template <bool BF16, bool WGRAD, bool F32, bool ADD>
 cudaError_t prepare() {
   static std::atomic<bool> done[64];
   int dev = 0;
@@ -478,7 +669,7 @@ cudaError_t prepare() {
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!done[dev].load()) {
-    e = cudaFuncSetAttribute(grouped_pair_kernel<BF16, WGRAD, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(grouped_pair_kernel<BF16, WGRAD, F32, ADD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kSmemBytes);
     if (e != cudaSuccess) return e;
     done[dev].store(true);
@@ -486,51 +677,52 @@ cudaError_t prepare() {
   return cudaSuccess;
 }
 
-template <bool BF16, bool WGRAD, bool F32>
+template <bool BF16, bool WGRAD, bool F32, bool ADD>
 int clusters_of() {
   static std::atomic<int> known[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
   int n = known[dev].load();
   if (n > 0) return n;
-  if (prepare<BF16, WGRAD, F32>() != cudaSuccess) return 0;
+  if (prepare<BF16, WGRAD, F32, ADD>() != cudaSuccess) return 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2, 1, 1);
-  cfg.blockDim = dim3(kThreadsOf<WGRAD>, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = kSmemBytes;
-  if (cudaOccupancyMaxActiveClusters(&n, grouped_pair_kernel<BF16, WGRAD, F32>, &cfg) != cudaSuccess) return 0;
+  if (cudaOccupancyMaxActiveClusters(&n, grouped_pair_kernel<BF16, WGRAD, F32, ADD>, &cfg) != cudaSuccess) return 0;
   known[dev].store(n);
   return n;
 }
 
-template <bool BF16, bool WGRAD, bool F32>
+template <bool BF16, bool WGRAD, bool F32, bool ADD>
 cudaError_t launch(const GroupedParams& p, int clusters, cudaStream_t stream) {
-  cudaError_t e = prepare<BF16, WGRAD, F32>();
+  cudaError_t e = prepare<BF16, WGRAD, F32, ADD>();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * clusters, 1, 1);
-  cfg.blockDim = dim3(kThreadsOf<WGRAD>, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   add_pdl_attribute(cfg, attr);
-  e = cudaLaunchKernelEx(&cfg, grouped_pair_kernel<BF16, WGRAD, F32>, p);
+  e = cudaLaunchKernelEx(&cfg, grouped_pair_kernel<BF16, WGRAD, F32, ADD>, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
 
-// Pairs that can be resident at once (0 on error).
-int grouped_pair_clusters(bool bf16, bool wgrad, bool f32) {
-  if (!wgrad) return bf16 ? clusters_of<true, false, false>() : clusters_of<false, false, false>();
-  if (f32) return bf16 ? clusters_of<true, true, true>() : clusters_of<false, true, true>();
-  return bf16 ? clusters_of<true, true, false>() : clusters_of<false, true, false>();
-}
+// Pairs that can be resident at once (0 on error): one CTA fits an SM whatever
+// the variant.
+int grouped_pair_clusters() { return clusters_of<true, false, false, false>(); }
 
 cudaError_t launch_grouped_pair(bool bf16, bool wgrad, const GroupedParams& p, int clusters, cudaStream_t stream) {
-  if (!wgrad) return bf16 ? launch<true, false, false>(p, clusters, stream) : launch<false, false, false>(p, clusters, stream);
-  if (p.out_f32) return bf16 ? launch<true, true, true>(p, clusters, stream) : launch<false, true, true>(p, clusters, stream);
-  return bf16 ? launch<true, true, false>(p, clusters, stream) : launch<false, true, false>(p, clusters, stream);
+  const bool add = p.C != nullptr;
+#define TTC_PAIR(W, F, C) \
+  (bf16 ? launch<true, W, F, C>(p, clusters, stream) : launch<false, W, F, C>(p, clusters, stream))
+  if (!wgrad) return TTC_PAIR(false, false, false);
+  if (p.out_f32) return add ? TTC_PAIR(true, true, true) : TTC_PAIR(true, true, false);
+  return add ? TTC_PAIR(true, false, true) : TTC_PAIR(true, false, false);
+#undef TTC_PAIR
 }
 
 }  // namespace ttc

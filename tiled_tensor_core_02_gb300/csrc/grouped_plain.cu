@@ -66,8 +66,9 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_plain_kernel(const __grid
   const uint32_t tmem_base = *tmem_slot;
   grid_dependency_wait();
   grid_dependents_launch();
-  build_group_table<kTile>(p, offs, WGRAD ? nullptr : start);
-  const int tiles = WGRAD ? p.groups * p.row_blocks * p.col_blocks : start[p.groups];
+  const GroupTable tb{offs, WGRAD ? nullptr : start, 1};
+  build_group_table<kTile>(p, tb);
+  const int tiles = WGRAD ? p.groups * p.row_blocks * p.col_blocks : table_tiles(p, tb);
 
   if (warp < 4) {
     // ---------------------------------------------------------------- producers
@@ -75,7 +76,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_plain_kernel(const __grid
     uint32_t phase = 0;
     bool ok = true;
     for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-      const GroupedTile x = grouped_tile<kTile, WGRAD>(p, offs, start, t);
+      const GroupedTile x = grouped_tile<kTile, WGRAD>(p, tb, t);
       const int nkb = WGRAD ? (x.hi - x.lo + kBK - 1) / kBK : p.k_blocks;
       const int n0 = x.cb * kTile;
       for (int kb = 0; kb < nkb; ++kb) {
@@ -119,7 +120,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_plain_kernel(const __grid
       int stage = 0, it = 0;
       uint32_t phase = 0;
       for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x, ++it) {
-        const GroupedTile x = grouped_tile<kTile, WGRAD>(p, offs, start, t);
+        const GroupedTile x = grouped_tile<kTile, WGRAD>(p, tb, t);
         const int nkb = WGRAD ? (x.hi - x.lo + kBK - 1) / kBK : p.k_blocks;
         const int acc = it & 1;
         if (!mbar_wait(&tmem_empty[acc], ((it >> 1) & 1) ^ 1u, wc)) break;
@@ -159,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_plain_kernel(const __grid
     const int esize = p.out_f32 ? 4 : 2;
     int it = 0;
     for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++it) {
-      const GroupedTile x = grouped_tile<kTile, WGRAD>(p, offs, start, t);
+      const GroupedTile x = grouped_tile<kTile, WGRAD>(p, tb, t);
       const bool has_k = WGRAD ? x.hi > x.lo : p.k_blocks > 0;
       const int acc = it & 1;
       // D's row of this thread, and the group's first element of C and D

@@ -53,35 +53,21 @@ void common_params(GroupedParams& p, const HostEnv& env, int64_t groups, int64_t
   p.inject_stall = env.inject_stall;
 }
 
-// Tensor maps of the pair kernel's operands and result.  False where TMA cannot
-// read the operands; d_tma stays 0 where it cannot write D.
+// Tensor maps of the pair kernel's operands; false where TMA cannot read them.
 bool pair_maps(GroupedParams& p, bool wgrad, ttc_dtype dtype, const HostEnv& env) {
   if (env.plain_loads || p.M == 0 || p.K == 0) return false;
   if (!tma_rows_ok(p.A, p.lda, 2) || !tma_rows_ok(p.B, p.ldb, 2)) return false;
   if (!wgrad && !tma_stride_ok(p.groups, p.strideB, 2)) return false;
   const CUtensorMapDataType dt = dtype == TTC_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
-  // K contiguous: boxes of 64 k by 128 rows; rows contiguous: 64 rows by 64 k
-  if (wgrad) {
-    if (!encode_matrices(&p.tmA, dt, 2, p.A, p.K, p.M, p.lda, 1, 0, kBK, 64, sw) ||
-        !encode_matrices(&p.tmB, dt, 2, p.B, p.N, p.M, p.ldb, 1, 0, kBK, 64, sw))
-      return false;
-  } else {
-    const int64_t mats = p.strideB != 0 ? p.groups : 1;
-    if (!encode_matrices(&p.tmA, dt, 2, p.A, p.K, p.M, p.lda, 1, 0, kBK, 128, sw)) return false;
-    if (p.b_mn ? !encode_matrices(&p.tmB, dt, 2, p.B, p.N, p.K, p.ldb, mats, p.strideB, kBK, 64, sw)
-               : !encode_matrices(&p.tmB, dt, 2, p.B, p.K, p.N, p.ldb, mats, p.strideB, kBK, 128, sw))
-      return false;
-  }
-  // a TMA store ends at whole 16-byte granules of a row; what is behind the last one the threads store
-  const int esize = p.out_f32 ? 4 : 2;
-  const int64_t cols = p.N & ~(int64_t)(16 / esize - 1);
-  p.d_tma = !env.plain_stores && cols > 0 && tma_rows_ok(p.D, p.ldd, esize) &&
-            (!wgrad || tma_stride_ok(p.groups, p.strideD, esize)) &&
-            encode_matrices(&p.tmD, p.out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : dt, esize, p.D, cols,
-                            wgrad ? p.K : p.M, p.ldd, wgrad ? p.groups : 1, p.strideD, 32, 32,
-                            p.out_f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
-  return true;
+  // K contiguous: boxes of 64 k by 128 rows; rows contiguous: 64 rows by the 128 k of a stage
+  if (wgrad)
+    return encode_matrices(&p.tmA, dt, 2, p.A, p.K, p.M, p.lda, 1, 0, 64, 128, sw) &&
+           encode_matrices(&p.tmB, dt, 2, p.B, p.N, p.M, p.ldb, 1, 0, 64, 128, sw);
+  const int64_t mats = p.strideB != 0 ? p.groups : 1;
+  return encode_matrices(&p.tmA, dt, 2, p.A, p.K, p.M, p.lda, 1, 0, kBK, 128, sw) &&
+         (p.b_mn ? encode_matrices(&p.tmB, dt, 2, p.B, p.N, p.K, p.ldb, mats, p.strideB, 64, 128, sw)
+                 : encode_matrices(&p.tmB, dt, 2, p.B, p.K, p.N, p.ldb, mats, p.strideB, kBK, 128, sw));
 }
 
 }  // namespace
@@ -132,11 +118,10 @@ ttc_status ttc_gemm_grouped(int64_t groups, int64_t M, int64_t N, int64_t K, con
   p.ldd = ldd;
   p.d_vec = aligned(D, 16) && ldd % 8 == 0;
   if (pair_maps(p, false, dtype, env)) {
-    const int clusters = grouped_pair_clusters(dtype == TTC_BF16, false, false);
+    const int clusters = grouped_pair_clusters();
     if (clusters <= 0) return TTC_ERR_CUDA;
     p.col_blocks = (int)blocks_of(N, kGroupedPairTile);
     p.group_rows = 8;
-    p.table = 2 * (groups + 1) * 4 <= kPairTableBytes ? kTableBehind : kTableInStaging;
     p.b_stream = M <= groups * kGroupedPairTile;
     const int64_t tiles = (blocks_of(M, kGroupedPairTile) + (groups < M ? groups : M)) * p.col_blocks;
     if (launch_grouped_pair(dtype == TTC_BF16, false, p, (int)(tiles < clusters ? tiles : clusters),
@@ -205,12 +190,11 @@ ttc_status ttc_gemm_grouped_wgrad(int64_t groups, int64_t M, int64_t N, int64_t 
   p.strideD = strideD;
   p.d_vec = aligned(D, 16) && ldd * esize % 16 == 0 && (groups == 1 || strideD * esize % 16 == 0);
   if (pair_maps(p, true, dtype, env)) {
-    const int clusters = grouped_pair_clusters(dtype == TTC_BF16, true, p.out_f32 != 0);
+    const int clusters = grouped_pair_clusters();
     if (clusters <= 0) return TTC_ERR_CUDA;
     p.row_blocks = (int)blocks_of(K, kGroupedPairTile);
     p.col_blocks = (int)blocks_of(N, kGroupedPairTile);
     p.group_rows = 8;
-    p.table = (groups + 1) * 4 <= kPairTableBytes ? kTableBehind : kTableGlobal;
     const int64_t tiles = groups * p.row_blocks * p.col_blocks;
     if (launch_grouped_pair(dtype == TTC_BF16, true, p, (int)(tiles < clusters ? tiles : clusters),
                             static_cast<cudaStream_t>(stream)) != cudaSuccess)
