@@ -164,6 +164,10 @@ struct GemmParams {
   // (b_half_map == 1; otherwise they load the whole box and read half of it)
   int b_half_map;
   CUtensorMap tmBh;
+  // CTA-pair int8 kernel with a scaled result: a scale for each row of A and
+  // for each column of B (fp32)
+  const float* scale_a;
+  const float* scale_b;
 };
 
 // Loads the k-block tile of an operand whose rows start at r0 and whose K
@@ -256,6 +260,22 @@ __device__ __forceinline__ float apply_act(int act, float x) {
     return 0.5f * x * (1.0f + tanh_approx(inner));
   }
   return x;
+}
+
+// GELU in its tanh form as v / (1 + exp(-2 u)), u = sqrt(2/pi) (v + 0.044715 v^3):
+// 0.5 (1 + tanh u) is the logistic function of 2 u.  Unlike the sum 1 + tanh u
+// it keeps its relative accuracy where v is negative, and it is accurate enough
+// for fp32 results.
+__device__ __forceinline__ float gelu_logistic(float v) {
+  const float u2 = 1.5957691216057308f * fmaf(0.044715f * v, v * v, v);
+  return __fdividef(v, 1.0f + __expf(-u2));
+}
+
+// apply_act to fp32 accuracy; ReLU keeps a NaN.
+__device__ __forceinline__ float act_value(int act, float v) {
+  if (act == kActRelu) return v < 0.0f ? 0.0f : v;
+  if (act == kActGelu) return gelu_logistic(v);
+  return v;
 }
 
 template <bool BF16>

@@ -123,20 +123,6 @@ __device__ __forceinline__ GroupedTile grouped_tile(const GroupedParams& p, cons
   return x;
 }
 
-// GELU in its tanh form as v / (1 + exp(-2 u)), u = sqrt(2/pi) (v + 0.044715 v^3):
-// 0.5 (1 + tanh u) is the logistic function of 2 u.  Unlike the sum 1 + tanh u
-// it keeps its relative accuracy where v is negative.
-__device__ __forceinline__ float gelu_logistic(float v) {
-  const float u2 = 1.5957691216057308f * fmaf(0.044715f * v, v * v, v);
-  return __fdividef(v, 1.0f + __expf(-u2));
-}
-
-__device__ __forceinline__ float act_value(int act, float v) {
-  if (act == kActRelu) return v < 0.0f ? 0.0f : v;  // a NaN stays one
-  if (act == kActGelu) return gelu_logistic(v);
-  return v;
-}
-
 // 32 values of a row (columns col0 .. col0 + 31, `n` of them inside D) from
 // their accumulator: alpha, C, bias, activation.
 template <bool BF16>

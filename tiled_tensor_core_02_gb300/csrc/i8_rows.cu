@@ -23,7 +23,6 @@
 #include <cuda_fp16.h>
 
 #include "gemm_kernel.cuh"
-#include "grouped_common.cuh"
 #include "i8_rows.cuh"
 
 namespace ttc {

@@ -70,6 +70,13 @@ bool pair_maps(GroupedParams& p, bool wgrad, ttc_dtype dtype, const HostEnv& env
                  : encode_matrices(&p.tmB, dt, 2, p.B, p.K, p.N, p.ldb, mats, p.strideB, kBK, 128, sw));
 }
 
+// int8 products that take the CTA-pair kernel on fp16 copies.
+bool takes_i8_pair(int64_t M, int64_t N, int64_t K) {
+  // the copies' 16-byte pieces and the tiles are counted in 32 bits
+  return M > 64 && N > 0 && K > 0 && blocks_of(K, 16) * (M > N ? M : N) < (1ll << 31) &&
+         blocks_of(M, 256) * blocks_of(N, 256) < (1ll << 30);
+}
+
 }  // namespace
 
 extern "C" {
@@ -238,15 +245,17 @@ ttc_status ttc_quantize_rows(int64_t rows, int64_t cols, const void* X, int64_t 
 
 size_t ttc_gemm_i8_scaled_workspace_size(int64_t M, int64_t N, int64_t K, const int8_t* A, int64_t lda, const int8_t* B,
                                          int64_t ldb, const void* D, int64_t ldd, ttc_dtype out_dtype) {
-  (void)M, (void)N, (void)K, (void)A, (void)lda, (void)B, (void)ldb, (void)D, (void)ldd, (void)out_dtype;
-  return 0;
+  (void)A, (void)B, (void)D;
+  if (M <= 0 || N <= 0 || K <= 0 || K > TTC_I8_SCALED_MAX_K || lda < K || ldb < K || ldd < N || M > kSizeLimit ||
+      N > kSizeLimit || !(is_16bit(out_dtype) || out_dtype == TTC_F32))
+    return 0;
+  return takes_i8_pair(M, N, K) ? i8_pair_workspace(M, N, K) : 0;
 }
 
 ttc_status ttc_gemm_i8_scaled(int64_t M, int64_t N, int64_t K, const int8_t* A, int64_t lda, const float* scaleA,
                               const int8_t* B, int64_t ldb, const float* scaleB, void* D, int64_t ldd,
                               const float* bias, ttc_act act, ttc_dtype out_dtype, void* workspace,
                               size_t workspace_bytes, void* stream) {
-  (void)workspace, (void)workspace_bytes;
   if (M < 0 || N < 0 || K < 0 || !is_act(act) || !is_dtype(out_dtype)) return TTC_ERR_INVALID_ARG;
   if (out_dtype == TTC_I8) return TTC_ERR_UNSUPPORTED;
   if (M == 0 || N == 0) return TTC_OK;
@@ -263,6 +272,11 @@ ttc_status ttc_gemm_i8_scaled(int64_t M, int64_t N, int64_t K, const int8_t* A, 
                 byte_ranges_overlap(D, d_bytes, B, span_bytes(1, 0, N, ldb, K, 1))))
     return TTC_ERR_INVALID_ARG;
 
+  if (workspace != nullptr && aligned(workspace, 256) && takes_i8_pair(M, N, K) &&
+      workspace_bytes >= i8_pair_workspace(M, N, K)) {
+    const I8Scale scale{scaleA, scaleB, bias, (int)act, out_dtype};
+    return i8_pair_scaled(M, N, K, A, lda, B, ldb, D, ldd, scale, workspace, stream);
+  }
   HostEnv env;
   const ttc_status st = host_env(env);
   if (st != TTC_OK) return st;

@@ -182,6 +182,8 @@ struct WidenChunk {
   int n;  // values of the row in this chunk (1..16)
 };
 
+// kAny: rows that start anywhere, read as repack_load reads them.
+template <bool kAny>
 __device__ __forceinline__ void widen_load(const WidenParams& p, int64_t idx, WidenChunk& c) {
   const WidenJob& j = (p.jobs > 1 && idx >= p.job[1].first) ? p.job[1] : p.job[0];
   const uint32_t q = (uint32_t)(idx - j.first);
@@ -189,7 +191,18 @@ __device__ __forceinline__ void widen_load(const WidenParams& p, int64_t idx, Wi
   const uint32_t r = q / cpr;
   const int64_t c0 = (int64_t)(q - r * cpr) * 16;
   c.n = j.cols - c0 < 16 ? (int)(j.cols - c0) : 16;
-  c.v = __ldg(reinterpret_cast<const uint4*>(j.src + (int64_t)r * j.src_ld + c0));
+  const uint8_t* s = j.src + (int64_t)r * j.src_ld + c0;
+  if constexpr (kAny) {
+    const uint32_t phase = (uint32_t)(reinterpret_cast<uintptr_t>(s) & 15u);
+    const uint4* blk = reinterpret_cast<const uint4*>(s - phase);
+    const uint4 b0 = __ldg(blk);
+    const uint4 b1 = (int)phase + c.n > 16 ? __ldg(blk + 1) : make_uint4(0u, 0u, 0u, 0u);
+    uint32_t x[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+    window8_shift_down(x, phase);
+    c.v = make_uint4(x[0], x[1], x[2], x[3]);
+  } else {
+    c.v = __ldg(reinterpret_cast<const uint4*>(s));
+  }
   c.dst = j.dst + (int64_t)r * j.dst_ld + c0;
 }
 
@@ -219,6 +232,7 @@ __device__ __forceinline__ void widen_store(const WidenChunk& c) {
 
 // Two chunks per thread per iteration, both loads in flight before either
 // store; programmatic dependent launch as repack_rows_kernel.
+template <bool kAny>
 __global__ void __launch_bounds__(256, 8) widen_i8_kernel(const __grid_constant__ WidenParams p) {
   grid_dependency_wait();
   grid_dependents_launch();
@@ -226,14 +240,14 @@ __global__ void __launch_bounds__(256, 8) widen_i8_kernel(const __grid_constant_
   int64_t idx = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   for (; idx + stride < p.total; idx += 2 * stride) {
     WidenChunk c0, c1;
-    widen_load(p, idx, c0);
-    widen_load(p, idx + stride, c1);
+    widen_load<kAny>(p, idx, c0);
+    widen_load<kAny>(p, idx + stride, c1);
     widen_store(c0);
     widen_store(c1);
   }
   if (idx < p.total) {
     WidenChunk c0;
-    widen_load(p, idx, c0);
+    widen_load<kAny>(p, idx, c0);
     widen_store(c0);
   }
 }
@@ -243,6 +257,7 @@ cudaError_t launch_widen_i8(const WidenSpec* specs, int count, int sm_count, cud
   WidenParams p{};
   p.jobs = count;
   int64_t total = 0;
+  bool any = false;
   for (int i = 0; i < count; ++i) {
     const WidenSpec& sp = specs[i];
     WidenJob& j = p.job[i];
@@ -253,8 +268,8 @@ cudaError_t launch_widen_i8(const WidenSpec* specs, int count, int sm_count, cud
     j.dst = static_cast<uint16_t*>(sp.dst);
     j.dst_ld = sp.dst_ld;
     j.chunks_per_row = (j.cols + 15) / 16;
-    if (reinterpret_cast<uintptr_t>(j.src) % 16 || j.src_ld % 16 || reinterpret_cast<uintptr_t>(j.dst) % 16 ||
-        j.dst_ld % 16 || j.dst_ld < j.chunks_per_row * 16 || j.rows * j.chunks_per_row >= (int64_t(1) << 31))
+    any = any || reinterpret_cast<uintptr_t>(j.src) % 16 || j.src_ld % 16;
+    if (reinterpret_cast<uintptr_t>(j.dst) % 16 || j.dst_ld % 16 || j.dst_ld < j.chunks_per_row * 16 || j.rows * j.chunks_per_row >= (int64_t(1) << 31))
       return cudaErrorInvalidValue;
     j.first = total;
     total += j.rows * j.chunks_per_row;
@@ -270,7 +285,8 @@ cudaError_t launch_widen_i8(const WidenSpec* specs, int count, int sm_count, cud
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   add_pdl_attribute(cfg, attr);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, widen_i8_kernel, p);
+  const cudaError_t e = any ? cudaLaunchKernelEx(&cfg, widen_i8_kernel<true>, p)
+                            : cudaLaunchKernelEx(&cfg, widen_i8_kernel<false>, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

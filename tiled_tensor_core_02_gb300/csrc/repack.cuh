@@ -23,8 +23,8 @@ cudaError_t launch_repack2(const RepackSpec* specs, int count, int sm_count, cud
 cudaError_t launch_repack(const void* src, int64_t src_ld, int64_t rows, int64_t cols, void* dst, int64_t dst_ld,
                           int elem_bytes, int sm_count, cudaStream_t stream);
 
-// Widens `rows` rows of `cols` int8 values (`src` and `src_ld` in bytes, both
-// 16-byte aligned) into fp16 rows at `dst` with pitch `dst_ld` elements (a
+// Widens `rows` rows of `cols` int8 values (`src` and `src_ld` in bytes, of any
+// alignment; faster with both 16-byte aligned) into fp16 rows at `dst` with pitch `dst_ld` elements (a
 // multiple of 16; `dst` 16-byte aligned).  Every int8 value is exact in fp16.
 struct WidenSpec {
   const void* src;
