@@ -154,6 +154,16 @@ def test_shapes(shape, workspace):
     verify(*shape, out="f32", workspace=workspace, seed=sum(shape))
 
 
+@pytest.mark.parametrize("shape", [(96, 8192, 8192), (128, 520, 4096), (250, 1000, 2048), (48, 776, 16384), (20, 264, 16400),
+                                   (10, 136, 32768), (65, 2000, 16384), (3, 14336, 256), (33, 40, 2064)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_token_blocks_and_long_reductions(shape):
+    """Every block of tokens, K from one stage to many, tiles that fill several
+    waves; sums exact, bit for bit."""
+    got, _, _, s = scaled(*shape, out="f32", bias=False, unit=True, seed=sum(shape), workspace="none")
+    assert np.array_equal(got, s.astype(np.float32).astype(np.float64))
+
+
 @pytest.mark.parametrize("act", ["none", "relu", "gelu_tanh"])
 @pytest.mark.parametrize("out", ["f16", "bf16", "f32"])
 @pytest.mark.parametrize("M", [5, 200])

@@ -298,6 +298,18 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   }
 }
 
+// Four int8 in a word to two words of two fp16: x + 128 in the low bits of
+// 1024's pattern is 1152 + x.
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  const uint32_t u = w ^ 0x80808080u;
+  const __half2 off = __halves2half2(__ushort_as_half(0x6480u), __ushort_as_half(0x6480u));  // 1152
+  uint32_t l = __byte_perm(u, 0x64646464u, 0x4140), h = __byte_perm(u, 0x64646464u, 0x4342);
+  const __half2 l2 = __hsub2(*reinterpret_cast<__half2*>(&l), off);
+  const __half2 h2 = __hsub2(*reinterpret_cast<__half2*>(&h), off);
+  lo = *reinterpret_cast<const uint32_t*>(&l2);
+  hi = *reinterpret_cast<const uint32_t*>(&h2);
+}
+
 // Waits for a barrier phase during shutdown, ignoring errors raised by other
 // threads: used only to let copies this thread started land before exit.
 __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, uint64_t budget_ns) {

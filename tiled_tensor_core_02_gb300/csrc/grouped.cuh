@@ -49,7 +49,7 @@ struct GroupedParams {
   int out_f32;  // wgrad: C and D are fp32
   int c_vec, d_vec;  // rows of C, D start on 16-byte boundaries
   int b_stream;  // forward: a group's weights are read by one block of rows as a rule
-  int ksplit;   // token-side kernel: CTAs of a cluster that share a tile's k-blocks
+  int tile_cols, stages;  // few-token kernel: output columns of a tile, its pipeline's stages
   uint32_t* err;
   uint64_t timeout_ns;
   int inject_stall;
@@ -59,6 +59,11 @@ struct GroupedParams {
 constexpr int kGroupedPairTile = 256;
 int grouped_pair_clusters();
 cudaError_t launch_grouped_pair(bool bf16, bool wgrad, const GroupedParams& p, int clusters, cudaStream_t stream);
+
+// The kernel for few tokens: token tiles of 16, 32, 64 and 128, tiles of 8 to 128
+// output columns.  Stages that fit for these tiles:
+int few_tokens_stages(int tokens, int tile_cols, int groups);
+cudaError_t launch_few_tokens(bool bf16, int tokens, const GroupedParams& p, int ctas, cudaStream_t stream);
 
 // Tile of the kernels that load with plain loads: 128 x 128.
 constexpr int kGroupedPlainTile = 128;

@@ -32,6 +32,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kPitch = kI8RowsChunk * 2 + 16;  // bytes of a widened token row in shared memory
 constexpr int kDrainChunks = 1024 / kI8RowsChunk;
+constexpr int kAhead = 2;  // chunks of weights that L2 is asked for ahead of the next one
 
 // m16n8k16: A sixteen rows by sixteen k, B eight columns, fp32 sums
 __device__ __forceinline__ void mma_m16n8k16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -41,18 +42,6 @@ __device__ __forceinline__ void mma_m16n8k16(float (&c)[4], uint32_t a0, uint32_
       "{%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// Four int8 in a word to two words of two fp16: x + 128 in the low bits of
-// 1024's pattern is 1152 + x.
-__device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  const uint32_t u = w ^ 0x80808080u;
-  const __half2 off = __halves2half2(__ushort_as_half(0x6480u), __ushort_as_half(0x6480u));  // 1152
-  uint32_t l = __byte_perm(u, 0x64646464u, 0x4140), h = __byte_perm(u, 0x64646464u, 0x4342);
-  const __half2 l2 = __hsub2(*reinterpret_cast<__half2*>(&l), off);
-  const __half2 h2 = __hsub2(*reinterpret_cast<__half2*>(&h), off);
-  lo = *reinterpret_cast<const uint32_t*>(&l2);
-  hi = *reinterpret_cast<const uint32_t*>(&h2);
 }
 
 // Bytes k .. k + 15 of a row of K (k < K); those past its end are whatever
@@ -120,6 +109,11 @@ __global__ void __launch_bounds__(kThreads, 2) i8_rows_kernel(const I8ScaledPara
     w[j][0] = in ? row16(w0, k, p.K, p.b_vec != 0) : make_uint4(0u, 0u, 0u, 0u);
     w[j][1] = in ? row16(w1, k, p.K, p.b_vec != 0) : make_uint4(0u, 0u, 0u, 0u);
   };
+  // two lines of each of the warp's sixteen rows, one a lane
+  const int8_t* ahead = p.B + (int64_t)min(feature0 + (lane >> 1), p.N - 1) * p.ldb + (lane & 1) * 128;
+  auto prefetch_w = [&](int c) {
+    if (c < c_hi && c * kI8RowsChunk + (lane & 1) * 128 < p.K) prefetch_l2_line(ahead + c * kI8RowsChunk);
+  };
   auto load_x = [&](int c) {
 #pragma unroll
     for (int i = 0; i < kXIters; ++i) {
@@ -166,12 +160,15 @@ __global__ void __launch_bounds__(kThreads, 2) i8_rows_kernel(const I8ScaledPara
   grid_dependents_launch();
 #pragma unroll
   for (int j = 0; j < 4; ++j) load_w(c_lo, j);
+#pragma unroll
+  for (int c = 1; c <= kAhead; ++c) prefetch_w(c_lo + c);
   load_x(c_lo);
   store_x(smem);
   __syncthreads();
   int buf = 0, until_drain = kDrainChunks;
   for (int c = c_lo; c < c_hi; ++c) {
     load_x(c + 1);
+    prefetch_w(c + 1 + kAhead);
     const uint8_t* xb = smem + buf * kXBytes + g * kPitch + t * 32;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -236,10 +233,10 @@ __global__ void __launch_bounds__(kThreads, 2) i8_rows_kernel(const I8ScaledPara
     if (p.bias != nullptr) v += __ldg(p.bias + col);
     v = act_value(p.act, v);
     const int64_t o = (int64_t)row * p.ldd + col;
-    if constexpr (OUT == kI8OutF32)
+    if constexpr (OUT == kI8ResultF32)
       static_cast<float*>(p.D)[o] = v;
     else
-      static_cast<uint16_t*>(p.D)[o] = (uint16_t)(pack2<OUT == kI8OutBF16>(v, 0.0f) & 0xFFFFu);
+      static_cast<uint16_t*>(p.D)[o] = (uint16_t)(pack2<OUT == kI8ResultBF16>(v, 0.0f) & 0xFFFFu);
   }
   if (split > 1) cluster_sync();  // no CTA leaves while another may read its sums
 }
@@ -274,11 +271,11 @@ cudaError_t launch_out(const I8ScaledParams& p, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_i8_rows(const I8ScaledParams& p, I8Out out, cudaStream_t stream) {
+cudaError_t launch_i8_rows(const I8ScaledParams& p, I8ResultType out, cudaStream_t stream) {
   switch (out) {
-    case kI8OutF16: return launch_out<kI8OutF16>(p, stream);
-    case kI8OutBF16: return launch_out<kI8OutBF16>(p, stream);
-    case kI8OutF32: return launch_out<kI8OutF32>(p, stream);
+    case kI8ResultF16: return launch_out<kI8ResultF16>(p, stream);
+    case kI8ResultBF16: return launch_out<kI8ResultBF16>(p, stream);
+    case kI8ResultF32: return launch_out<kI8ResultF32>(p, stream);
   }
   return cudaErrorInvalidValue;
 }

@@ -1,0 +1,378 @@
+// int8 products for up to a few hundred tokens on the tensor cores:
+//   D[i, f] = act(scaleA[i] scaleB[f] sum_k A[i, k] B[f, k] + bias[f]).
+//
+// There is no int8 tcgen05.mma on this device (and the warp-level one does 262
+// multiply-adds a clock and SM: 113 us for 64 x 8192 x 8192), so the operands are
+// widened to fp16 on their way through the SM, exactly.  The weights B take the
+// MMA's 128-row side and are widened straight into tensor memory, from where the
+// MMA reads that operand: through shared memory their fp16 copy would be written
+// once and read once more at twice the size, and with the raw bytes' two passes
+// shared memory would set the pace (0.57 us for a stage of 56 rows).  The tokens,
+// the MMA's columns, are widened into shared memory.
+//
+// A CTA takes `tile_cols` channels by one block of tokens by its share of K, and
+// ends; the CTAs of a cluster share a tile's K.  The host picks both so that the
+// CTAs fill one wave of SMs.  One thread brings stages of 128 of K with TMA, as
+// many as fit; sixteen warps in four groups widen stages in turn, warp q of a
+// group the 32 rows of tensor memory it may write, a row a thread; one warp issues
+// the MMAs.
+//
+// Exactness: products of int8 values and sums of 1024 of them are exact in fp32.
+// Each 1024 of a CTA's K has an accumulator of its own (256 columns of tensor
+// memory hold them all), so nothing is drained on the way; at the end the same
+// sixteen warps add them up as int32, the cluster's CTAs exchange their sums
+// through shared memory, and one conversion, two scales, the bias and the
+// activation follow.
+#include <atomic>
+
+#include "gemm_kernel.cuh"
+#include "i8_rows.cuh"
+
+namespace ttc {
+
+namespace {
+
+constexpr int kWarp0 = 4;       // the first widening warp; 0 producer, 1 MMA issuer
+constexpr int kWidenWarps = 16;
+constexpr int kThreads = 32 * (kWarp0 + kWidenWarps);
+// Groups of widening warps, which take stages in turn.  A group waits for its slot
+// before it waits for its stage's bytes: the slot is free once the MMAs of
+// kGroups stages before are done, and with them, in order, of all earlier ones.
+// In a ring of at least kGroups stages the place's previous use is then over, and
+// cannot be taken for the one the group waits for.
+constexpr int groups_of(int block) { return block >= 128 ? 2 : 4; }
+constexpr int kMaxStages = 16;
+constexpr int kSmemLimit = 227 * 1024;
+constexpr int kAccStages = 1024 / kI8TokenStage;  // stages of an accumulator
+
+constexpr int kAlign = 1024;
+int ring_stage_bytes(int block, int tile_cols) { return (block + tile_cols) * kI8TokenStage; }
+int fixed_bytes(int block) { return kAlign + 1024 + groups_of(block) * block * kI8TokenStage * 2; }
+int total_bytes(int block, int tile_cols, int stages) {
+  const int n = fixed_bytes(block) + stages * ring_stage_bytes(block, tile_cols);
+  const int sums = kAlign + 1024 + block * 128 * 4;  // the exchange reuses the slots and the ring
+  return n > sums ? n : sums;
+}
+
+template <int BT, int OUT>
+__global__ void __launch_bounds__(kThreads, 1) i8_tokens_kernel(const __grid_constant__ I8TokensParams q) {
+  constexpr int kSlotBytes = BT * kI8TokenStage * 2;
+  constexpr int kGroups = groups_of(BT), kGroupWarps = kWidenWarps / kGroups;
+  constexpr int kHalves = kGroupWarps / 4;  // warps that share a row of the weights
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem);  // in front: the exchange at the end leaves them alone
+  uint8_t* slots = smem + 1024;                        // [group][k-block][token][64 fp16]
+  uint8_t* ring = slots + kGroups * kSlotBytes;        // [stage][weights, tokens]
+  const I8ScaledParams& p = q.p;
+  const int w_bytes = q.tile_cols * kI8TokenStage, stage_bytes = w_bytes + BT * kI8TokenStage, S = q.stages;  // at least the groups
+  uint64_t* full = bars;
+  uint64_t* empty = bars + kMaxStages;
+  uint64_t* wide_full = bars + 2 * kMaxStages;
+  uint64_t* wide_empty = wide_full + kGroups;
+  uint64_t* done_bar = wide_empty + kGroups;
+  uint64_t* stall_bar = done_bar + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(stall_bar + 1);
+  static_assert((2 * kMaxStages + 2 * kGroups + 2) * 8 + 4 <= 1024, "barrier area");
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const WaitCtx wc{q.err, q.timeout_ns};
+  const int rank = blockIdx.x % p.split, tile = blockIdx.x / p.split;
+  const int f0 = tile * q.tile_cols, token0 = blockIdx.y * BT;
+  const int s_lo = min(p.chunks, rank * p.chunks_per_cta), n_stages = min(p.chunks, s_lo + p.chunks_per_cta) - s_lo;
+
+  if (warp == 0) {
+    if (lane < S) {
+      mbar_init(&full[lane], 1);
+      mbar_init(&empty[lane], kGroupWarps);  // the widening group's warps
+    }
+    if (lane < kGroups) {
+      mbar_init(&wide_full[lane], kGroupWarps);
+      mbar_init(&wide_empty[lane], 1);
+    }
+    if (lane == 0) {
+      mbar_init(done_bar, 1);
+      mbar_init(stall_bar, 1);
+      prefetch_tmap(&q.tmA);
+      prefetch_tmap(&q.tmB);
+    }
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);  // accumulators in columns 0 .. 255, widened weights from 256 on
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  grid_dependency_wait();
+  grid_dependents_launch();
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- producer
+    if (lane == 0) {
+      const uint64_t keep = policy_evict_last();
+      const uint64_t pol_w = gridDim.y == 1 ? policy_evict_first() : keep;
+      int stage = 0;
+      uint32_t phase = 0, armed = 0, armed_parity = 0;
+      bool ok = true;
+      for (int n = 0; n < n_stages; ++n) {
+        if (!mbar_wait(&empty[stage], phase ^ 1u, wc)) {
+          ok = false;
+          break;
+        }
+        uint8_t* w = ring + stage * stage_bytes;
+        mbar_arrive_expect_tx(&full[stage], stage_bytes);
+        armed |= 1u << stage;
+        armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+        tma_load_3d(w, &q.tmB, (s_lo + n) * kI8TokenStage, f0, 0, &full[stage], pol_w);
+        tma_load_3d(w + w_bytes, &q.tmA, (s_lo + n) * kI8TokenStage, token0, 0, &full[stage], keep);
+        if (++stage == S) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      if (!ok) {
+        // loads in flight land before the CTA may exit
+        for (int s = 0; s < S; ++s)
+          if (armed & (1u << s)) drain_wait(&full[s], (armed_parity >> s) & 1u, 100000000ull);
+      }
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA issuer
+    const uint32_t lead = elect_lead();
+    const uint32_t idesc = idesc_f16(false, false, false, 128, BT);
+    const uint64_t x0 = smem_desc_sw128(smem_u32(slots), 16u, 1024);
+    constexpr uint32_t kTokenKb = BT * 128 >> 4;
+    bool ok = true;
+    if (q.inject_stall) ok = mbar_wait_warp(stall_bar, 0, wc);  // nothing arrives here
+    int g = 0;
+    uint32_t phase = 0;
+    for (int n = 0; ok && n < n_stages; ++n) {
+      const int steps = min(kI8TokenStage / kUmmaK, (p.K - (s_lo + n) * kI8TokenStage + kUmmaK - 1) / kUmmaK);
+      if (!mbar_wait_warp(&wide_full[g], phase, wc)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t d = tmem_base + (n / kAccStages) * BT;
+      const uint32_t w = tmem_base + kI8TokenCols + g * (kI8TokenStage / 2);
+      const uint64_t x = x0 + (uint32_t)(g * kSlotBytes >> 4);
+#pragma unroll
+      for (int k = 0; k < kI8TokenStage / kUmmaK; ++k)
+        if (k < steps)
+          mma_f16_ta_lead(lead, d, w + 8 * k, x + (k >> 2) * kTokenKb + (k & 3) * 2u, idesc,
+                          (n % kAccStages != 0) || k != 0);
+      mma_commit_lead(lead, &wide_empty[g]);
+      if (++g == kGroups) {
+        g = 0;
+        phase ^= 1u;
+      }
+    }
+    // every MMA issued is done when this completes, whether or not all were
+    mma_commit_lead(lead, done_bar);
+    drain_wait(done_bar, 0, 100000000ull);
+  } else if (warp >= kWarp0) {
+    // ---------------------------------------------------------------- widening
+    const int group = (warp - kWarp0) / kGroupWarps, quarter = warp & 3;
+    const int half = ((warp - kWarp0) >> 2) % kHalves, tid = (int)threadIdx.x % (kGroupWarps * 32);
+    const int row = quarter * 32 + lane;  // of the weights' tile, and of tensor memory
+    uint8_t* slot = slots + group * kSlotBytes;
+    const uint32_t tmem_w =
+        tmem_base + ((uint32_t)(quarter * 32) << 16) + kI8TokenCols + group * (kI8TokenStage / 2);
+    uint32_t wide_phase = 0;
+    for (int n = group; n < n_stages; n += kGroups) {
+      const int stage = n % S;
+      if (!mbar_wait(&wide_empty[group], wide_phase ^ 1u, wc)) break;  // first: see groups_of
+      if (!mbar_wait(&full[stage], (uint32_t)(n / S) & 1u, wc)) break;
+      tc_fence_after();
+      const uint8_t* w8 = ring + stage * stage_bytes;
+      const uint8_t* x8 = w8 + w_bytes;
+      if (quarter * 32 < q.tile_cols) {
+        const bool in = row < q.tile_cols;
+#pragma unroll
+        for (int h = half * (2 / kHalves); h < (half + 1) * (2 / kHalves); ++h) {
+          uint4 v[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            v[c] = in ? *reinterpret_cast<const uint4*>(w8 + row * 128 + (((h * 4 + c) ^ (row & 7)) << 4))
+                      : make_uint4(0u, 0u, 0u, 0u);
+          uint32_t w[32];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            widen4(v[c].x, w[8 * c], w[8 * c + 1]);
+            widen4(v[c].y, w[8 * c + 2], w[8 * c + 3]);
+            widen4(v[c].z, w[8 * c + 4], w[8 * c + 5]);
+            widen4(v[c].w, w[8 * c + 6], w[8 * c + 7]);
+          }
+          tmem_st_32x32b_x32(tmem_w + h * 32, w);
+        }
+      }
+      // the tokens: sixteen bytes a piece
+      constexpr int kPieces = BT * 8 / (kGroupWarps * 32);
+      constexpr int kBatch = kPieces < 4 ? kPieces : 4;  // loads before the first store: they do not move above one
+#pragma unroll
+      for (int i0 = 0; i0 < kPieces; i0 += kBatch) {
+        uint4 v[kBatch];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+          const int r = (tid + kGroupWarps * 32 * (i0 + b)) >> 3, c = tid & 7;
+          v[b] = *reinterpret_cast<const uint4*>(x8 + r * 128 + ((c ^ (r & 7)) << 4));
+        }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+          const int r = (tid + kGroupWarps * 32 * (i0 + b)) >> 3, c = tid & 7;
+          uint32_t h[8];
+          widen4(v[b].x, h[0], h[1]);
+          widen4(v[b].y, h[2], h[3]);
+          widen4(v[b].z, h[4], h[5]);
+          widen4(v[b].w, h[6], h[7]);
+          uint8_t* dst = slot + (c >> 2) * (BT * 128) + r * 128;
+          const int ch = (c & 3) * 2;
+          *reinterpret_cast<uint4*>(dst + ((ch ^ (r & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4*>(dst + (((ch + 1) ^ (r & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+        }
+      }
+      tmem_st_wait();
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&empty[stage]);
+        mbar_arrive(&wide_full[group]);
+      }
+      wide_phase ^= 1u;
+    }
+  }
+  // every MMA is done (the issuer waited) and every byte is read
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+
+  // ------------------------------------------------------------------ sums and result
+  // four sets of four warps; set g takes the tokens from g * kCols on, a thread a channel
+  constexpr int kCols = BT >= 64 ? BT / 4 : 16;
+  int32_t* red = reinterpret_cast<int32_t*>(slots);  // [token][128 channels]
+  const int tokens = min(BT, p.M - token0);
+  auto result = [&](int32_t s, int token, int f) {
+    float v = __int2float_rn(s) * __ldg(p.scaleA + token) * __ldg(p.scaleB + f);
+    if (p.bias != nullptr) v += __ldg(p.bias + f);
+    v = act_value(p.act, v);
+    const int64_t o = (int64_t)token * p.ldd + f;
+    if constexpr (OUT == kI8ResultF32)
+      static_cast<float*>(p.D)[o] = v;
+    else
+      static_cast<uint16_t*>(p.D)[o] = (uint16_t)(pack2<OUT == kI8ResultBF16>(v, 0.0f) & 0xFFFFu);
+  };
+  if (warp >= kWarp0) {
+    const int group = (warp - kWarp0) >> 2, quarter = warp & 3;
+    const int c0 = group * kCols, col = quarter * 32 + lane;
+    if (c0 < BT && quarter * 32 < q.tile_cols) {
+      const int parts = (n_stages + kAccStages - 1) / kAccStages;
+#pragma unroll
+      for (int c = 0; c < kCols; c += 16) {
+        int32_t sum[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) sum[j] = 0;
+        for (int a = 0; a < parts; ++a) {
+          uint32_t w[16];
+          tmem_ld_32x32b_x16<0>(tmem_base + ((uint32_t)(quarter * 32) << 16) + a * BT + c0 + c, w);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) sum[j] += __float2int_rn(__uint_as_float(w[j]));
+        }
+        const int f = f0 + col;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const int i = c0 + c + j;
+          if (p.split > 1)
+            red[i * 128 + col] = sum[j];
+          else if (i < tokens && col < q.tile_cols && f < p.N)
+            result(sum[j], token0 + i, f);
+        }
+      }
+    }
+  }
+  if (p.split > 1) {
+    cluster_sync();
+    // each CTA of the cluster adds up and stores its share
+    for (int e = rank * kThreads + threadIdx.x; e < tokens * 128; e += p.split * kThreads) {
+      const int col = e & 127, f = f0 + col;
+      if (col >= q.tile_cols || f >= p.N) continue;
+      const uint32_t at = smem_u32(red + e);
+      int32_t s = 0;
+      for (int r = 0; r < p.split; ++r) {
+        uint32_t v;
+        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(mapa_shared(at, (uint32_t)r)) : "memory");
+        s += (int32_t)v;
+      }
+      result(s, token0 + (e >> 7), f);
+    }
+    cluster_sync();  // no CTA leaves while another may read its sums
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, 512);
+  }
+}
+
+template <int BT, int OUT>
+cudaError_t launch(const I8TokensParams& q, cudaStream_t stream) {
+  static std::atomic<bool> done[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!done[dev].load()) {
+    e = cudaFuncSetAttribute(i8_tokens_kernel<BT, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+    if (e != cudaSuccess) return e;
+    done[dev].store(true);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(q.p.split * ((q.p.N + q.tile_cols - 1) / q.tile_cols)), (unsigned)((q.p.M + BT - 1) / BT), 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = total_bytes(BT, q.tile_cols, q.stages);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)q.p.split;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  add_pdl_attribute(cfg, attr);
+  e = cudaLaunchKernelEx(&cfg, i8_tokens_kernel<BT, OUT>, q);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <int BT>
+cudaError_t launch_block(const I8TokensParams& q, I8ResultType out, cudaStream_t stream) {
+  switch (out) {
+    case kI8ResultF16: return launch<BT, kI8ResultF16>(q, stream);
+    case kI8ResultBF16: return launch<BT, kI8ResultBF16>(q, stream);
+    case kI8ResultF32: return launch<BT, kI8ResultF32>(q, stream);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+int i8_tokens_stages(int block, int tile_cols) {
+  const int n = (kSmemLimit - fixed_bytes(block)) / ring_stage_bytes(block, tile_cols);
+  return n > kMaxStages ? kMaxStages : n < groups_of(block) ? 0 : n;
+}
+
+cudaError_t launch_i8_tokens(const I8TokensParams& q, int block, I8ResultType out, cudaStream_t stream) {
+  switch (block) {
+    case 16: return launch_block<16>(q, out, stream);
+    case 32: return launch_block<32>(q, out, stream);
+    case 64: return launch_block<64>(q, out, stream);
+    case 128: return launch_block<128>(q, out, stream);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace ttc

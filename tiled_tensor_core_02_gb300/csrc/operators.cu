@@ -47,7 +47,6 @@ void common_params(GroupedParams& p, const HostEnv& env, int64_t groups, int64_t
   p.a_vec = aligned(A, 16) && lda % 8 == 0;
   p.b_vec = aligned(B, 16) && ldb % 8 == 0;
   p.group_rows = 16;
-  p.ksplit = 1;
   p.err = env.err;
   p.timeout_ns = env.timeout_ns;
   p.inject_stall = env.inject_stall;
@@ -70,10 +69,97 @@ bool pair_maps(GroupedParams& p, bool wgrad, ttc_dtype dtype, const HostEnv& env
                  : encode_matrices(&p.tmB, dt, 2, p.B, p.K, p.N, p.ldb, mats, p.strideB, kBK, 128, sw));
 }
 
+// Output columns of a few-token tile: as many as make the tiles of `rows` weights'
+// rows fill whole waves of SMs, in steps of 8 up to 128; with the columns
+// contiguous in memory (TMA boxes of 64) 64 or 128.
+int few_tile_cols(int64_t rows, int sm_count, bool cols_contiguous) {
+  const int64_t waves = blocks_of(rows, 128ll * sm_count);
+  const int64_t c = blocks_of(blocks_of(rows, waves * sm_count), 8) * 8;
+  if (cols_contiguous) return c > 64 ? 128 : 64;
+  return (int)(c < 8 ? 8 : c > 128 ? 128 : c);
+}
+
+// Sets up the few-token kernel's tiles and tensor maps; false where TMA cannot
+// read the operands or no pipeline fits.  `matrices`: how many weight matrices
+// are likely to be read.
+bool few_maps(GroupedParams& p, ttc_dtype dtype, int tokens, int64_t matrices, const HostEnv& env) {
+  if (env.plain_loads || p.M == 0 || p.K == 0) return false;
+  if (!tma_rows_ok(p.A, p.lda, 2) || !tma_rows_ok(p.B, p.ldb, 2) || !tma_stride_ok(p.groups, p.strideB, 2)) return false;
+  p.tile_cols = few_tile_cols(matrices * p.N, env.sm_count, p.b_mn != 0);
+  p.col_blocks = (int)blocks_of(p.N, p.tile_cols);
+  p.group_rows = 64;  // a tile's blocks of tokens next to one another: the weights come from L2 after the first
+  p.b_stream = p.M <= matrices * tokens;
+  p.stages = few_tokens_stages(tokens, p.tile_cols, p.groups);
+  if (p.stages < 2) return false;
+  const CUtensorMapDataType dt = dtype == TTC_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
+  const int64_t mats = p.strideB != 0 ? p.groups : 1;
+  return encode_matrices(&p.tmA, dt, 2, p.A, p.K, p.M, p.lda, 1, 0, kBK, tokens, sw) &&
+         (p.b_mn ? encode_matrices(&p.tmB, dt, 2, p.B, p.N, p.K, p.ldb, mats, p.strideB, 64, 128, sw)
+                 : encode_matrices(&p.tmB, dt, 2, p.B, p.K, p.N, p.ldb, mats, p.strideB, kBK, p.tile_cols, sw));
+}
+
+// Block of tokens for groups of `mean` rows on average, `most` at most; 0: not few.
+int few_block(int64_t mean, int64_t most) {
+  if (most <= 16 || mean <= 8) return 16;
+  if (most <= 32 || mean <= 16) return 32;
+  if (mean <= 40) return 64;
+  return mean <= 80 ? 128 : 0;
+}
+
+// The tensor-core kernel for up to kI8FewTokens tokens: the tile's channels and
+// the split of K whose CTAs are done soonest.  A stage takes the widening groups
+// 0.33 us or HBM's share of an SM its bytes, whichever is more; an exchange of
+// sums about two microseconds.  False where TMA cannot read the operands or K is
+// too long for its accumulators.
+bool i8_tokens_plan(I8TokensParams& q, int block, const HostEnv& env) {
+  I8ScaledParams& p = q.p;
+  if (env.plain_loads || p.K == 0 || !tma_rows_ok(p.A, p.lda, 1) || !tma_rows_ok(p.B, p.ldb, 1)) return false;
+  const int64_t stages = blocks_of(p.K, kI8TokenStage), most = kI8TokenCols / block * (1024 / kI8TokenStage);
+  const int64_t blocks = blocks_of(p.M, block);
+  double best = 0.0;
+  const int splits[6] = {1, 2, 3, 4, 6, 8};
+  for (int split : splits) {
+    const int64_t per = blocks_of(stages, split);
+    if (per > most || split > stages) continue;
+    // larger clusters leave SMs of a processor group over (36 clusters of 4 fit 152 SMs)
+    const int64_t sms = env.sm_count * (split <= 2 ? 152 : split < 8 ? 144 : 128) / 152;
+    for (int64_t waves = 1; waves <= 64; ++waves) {
+      const int64_t room = waves * sms / (split * blocks);  // tiles
+      if (room < 1) continue;
+      const int64_t cols = blocks_of(blocks_of(p.N, room), 8) * 8;
+      if (cols > 128 && waves < 64) continue;
+      const int64_t c = cols > 128 ? 128 : cols;
+      const int64_t ctas = blocks_of(p.N, c) * split * blocks;
+      const double hbm = (double)c * kI8TokenStage / 44500.0, widen = block >= 128 ? 0.5 : 0.33;
+      const double cost = (double)blocks_of(ctas, sms > 0 ? sms : 1) * ((double)per * (hbm > widen ? hbm : widen) + 1.5) +
+                          (split > 1 ? 2.0 : 0.0);
+      if (best == 0.0 || cost < best) {
+        best = cost;
+        q.tile_cols = (int)c;
+        p.split = split;
+        p.chunks = (int)stages;
+        p.chunks_per_cta = (int)per;
+      }
+      break;
+    }
+  }
+  if (best == 0.0) return false;
+  q.stages = i8_tokens_stages(block, q.tile_cols);
+  if (q.stages < 1) return false;
+  q.err = env.err;
+  q.timeout_ns = env.timeout_ns;
+  q.inject_stall = env.inject_stall;
+  const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  return encode_matrices(&q.tmA, u8, 1, p.A, p.K, p.M, p.lda, 1, 0, 128, block, CU_TENSOR_MAP_SWIZZLE_128B) &&
+         encode_matrices(&q.tmB, u8, 1, p.B, p.K, p.N, p.ldb, 1, 0, 128, q.tile_cols, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
 // int8 products that take the CTA-pair kernel on fp16 copies.
+constexpr int64_t kI8FewTokens = 256;
 bool takes_i8_pair(int64_t M, int64_t N, int64_t K) {
   // the copies' 16-byte pieces and the tiles are counted in 32 bits
-  return M > 64 && N > 0 && K > 0 && blocks_of(K, 16) * (M > N ? M : N) < (1ll << 31) &&
+  return M > kI8FewTokens && N > 0 && K > 0 && blocks_of(K, 16) * (M > N ? M : N) < (1ll << 31) &&
          blocks_of(M, 256) * blocks_of(N, 256) < (1ll << 30);
 }
 
@@ -124,6 +210,16 @@ ttc_status ttc_gemm_grouped(int64_t groups, int64_t M, int64_t N, int64_t K, con
   p.D = D;
   p.ldd = ldd;
   p.d_vec = aligned(D, 16) && ldd % 8 == 0;
+  const int64_t likely = groups < M ? groups : M;  // groups with rows, as far as the host knows
+  const int block = few_block(blocks_of(M, likely), M);
+  if (block != 0 && few_maps(p, dtype, block, likely, env)) {
+    const int64_t tiles = (blocks_of(M, block) + likely) * p.col_blocks;
+    if (launch_few_tokens(dtype == TTC_BF16, block, p, (int)(tiles < env.sm_count ? tiles : env.sm_count),
+                          static_cast<cudaStream_t>(stream)) != cudaSuccess)
+      return TTC_ERR_CUDA;
+    count_launches(1);
+    return TTC_OK;
+  }
   if (pair_maps(p, false, dtype, env)) {
     const int clusters = grouped_pair_clusters();
     if (clusters <= 0) return TTC_ERR_CUDA;
@@ -281,9 +377,10 @@ ttc_status ttc_gemm_i8_scaled(int64_t M, int64_t N, int64_t K, const int8_t* A, 
   const ttc_status st = host_env(env);
   if (st != TTC_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const I8Out out = out_dtype == TTC_F32 ? kI8OutF32 : out_dtype == TTC_BF16 ? kI8OutBF16 : kI8OutF16;
-  I8ScaledParams p;
-  std::memset(&p, 0, sizeof p);
+  const I8ResultType out = out_dtype == TTC_F32 ? kI8ResultF32 : out_dtype == TTC_BF16 ? kI8ResultBF16 : kI8ResultF16;
+  I8TokensParams q;
+  std::memset(&q, 0, sizeof q);
+  I8ScaledParams& p = q.p;
   p.A = A;
   p.lda = lda;
   p.B = B;
@@ -299,7 +396,13 @@ ttc_status ttc_gemm_i8_scaled(int64_t M, int64_t N, int64_t K, const int8_t* A, 
   p.act = (int)act;
   p.a_vec = aligned(A, 16) && lda % 16 == 0;
   p.b_vec = aligned(B, 16) && ldb % 16 == 0;
-  // The CTAs of two per SM, where a cluster of up to eight leaves each CTA two
+  const int block = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+  if (M > 16 && M <= kI8FewTokens && i8_tokens_plan(q, block, env)) {
+    if (launch_i8_tokens(q, block, out, s) != cudaSuccess) return TTC_ERR_CUDA;
+    count_launches(1);
+    return TTC_OK;
+  }
+  // CTAs for two on each SM, where a cluster of up to eight leaves each CTA two
   // chunks of K at least.
   p.chunks = (int)blocks_of(K, kI8RowsChunk);
   const int64_t blocks = blocks_of(N, kI8RowsFeatures) * blocks_of(M, kI8RowsTokens);
