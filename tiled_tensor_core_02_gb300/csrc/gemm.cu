@@ -390,8 +390,13 @@ struct I8Wide {
   size_t a_off = 0, b_off = 0, bytes = 0;
 };
 
-// Places of the fp16 copies in the workspace.
-void place_i8_copies(I8Wide& w, int64_t M, int64_t N, int64_t K, ttc_layout layoutA, ttc_layout layoutB) {
+I8Wide plan_i8_wide(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, ttc_layout layoutA, const void* B,
+                    int64_t ldb, ttc_layout layoutB, const void* D, int64_t ldd) {
+  I8Wide w;
+  const int mode = g_i8_wide.load();
+  if (mode == 2 || K <= 0 || M < kPairBM || N < 256) return w;
+  if (mode == 0 && ((M + kPairBM - 1) / kPairBM) * ((N + 255) / 256) < kI8WideMinTiles) return w;
+  if (!tma_ok(A, lda, 1) || !tma_ok(B, ldb, 1) || !tma_ok(D, ldd, 4)) return w;
   w.a_rows = layoutA == TTC_ROW_MAJOR ? M : K;
   w.a_cols = layoutA == TTC_ROW_MAJOR ? K : M;
   w.b_rows = layoutB == TTC_ROW_MAJOR ? K : N;
@@ -402,25 +407,14 @@ void place_i8_copies(I8Wide& w, int64_t M, int64_t N, int64_t K, ttc_layout layo
   w.b_off = (size_t)round_up(w.a_rows * w.a_ld * 2, 256);
   w.bytes = w.b_off + (size_t)round_up(w.b_rows * w.b_ld * 2, 256);
   w.on = true;
-}
-
-I8Wide plan_i8_wide(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, ttc_layout layoutA, const void* B,
-                    int64_t ldb, ttc_layout layoutB, const void* D, int64_t ldd) {
-  I8Wide w;
-  const int mode = g_i8_wide.load();
-  if (mode == 2 || K <= 0 || M < kPairBM || N < 256) return w;
-  if (mode == 0 && ((M + kPairBM - 1) / kPairBM) * ((N + 255) / 256) < kI8WideMinTiles) return w;
-  if (!tma_ok(A, lda, 1) || !tma_ok(B, ldb, 1) || !tma_ok(D, ldd, 4)) return w;
-  place_i8_copies(w, M, N, K, layoutA, layoutB);
   return w;
 }
 
 ttc_status gemm_i8_wide(DeviceInfo* dev, const I8Wide& w, int64_t M, int64_t N, int64_t K, const void* A,
                         int64_t lda, ttc_layout layoutA, const void* B, int64_t ldb, ttc_layout layoutB,
                         const void* C, int64_t ldc, void* D, int64_t ldd, float beta, void* workspace,
-                        void* stream, const I8Scale* scale = nullptr) {
+                        void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int out_esize = scale == nullptr || scale->out == TTC_F32 ? 4 : 2;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const bool a_mn = layoutA == TTC_COL_MAJOR;
   const bool b_mn = layoutB == TTC_ROW_MAJOR;
@@ -442,22 +436,10 @@ ttc_status gemm_i8_wide(DeviceInfo* dev, const I8Wide& w, int64_t M, int64_t N, 
   const void* B16 = ws + w.b_off;
   const CUtensorMapDataType f16 = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   if (!encode_operand(&prm.tmA, f16, 2, A16, M, K, w.a_ld, prm.maps.a, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !encode_operand(&prm.tmB, f16, 2, B16, N, K, w.b_ld, prm.maps.b, CU_TENSOR_MAP_SWIZZLE_128B))
+      !encode_operand(&prm.tmB, f16, 2, B16, N, K, w.b_ld, prm.maps.b, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_3d(&prm.tmD, CU_TENSOR_MAP_DATA_TYPE_INT32, 4, D, tma_store_cols(N, 4), M, ldd, kEpiCols, 32,
+                 CU_TENSOR_MAP_SWIZZLE_128B))
     return TTC_ERR_CUDA;
-  // a scaled result may have rows TMA cannot store
-  prm.d_tma = scale == nullptr || (tma_ok(D, ldd, out_esize) && tma_store_cols(N, out_esize) > 0 &&
-                                   !g_force_generic_store.load());
-  if (prm.d_tma &&
-      !encode_3d(&prm.tmD, out_esize == 4 ? CU_TENSOR_MAP_DATA_TYPE_INT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, out_esize, D,
-                 tma_store_cols(N, out_esize), M, ldd, kEpiCols, 32,
-                 out_esize == 4 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
-    return TTC_ERR_CUDA;
-  if (scale != nullptr) {
-    prm.scale_a = scale->a;
-    prm.scale_b = scale->b;
-    prm.bias = scale->bias;
-    prm.act = scale->act;
-  }
   prm.A = A16;
   prm.B = B16;
   prm.lda = w.a_ld;
@@ -483,6 +465,7 @@ ttc_status gemm_i8_wide(DeviceInfo* dev, const I8Wide& w, int64_t M, int64_t N, 
   prm.ldc = ldc;
   prm.D = D;
   prm.ldd = ldd;
+  prm.d_tma = 1;
   prm.err = dev->err;
   prm.timeout_ns = (uint64_t)g_timeout_ns.load();
   prm.inject_stall = g_inject_stall.load();
@@ -502,12 +485,6 @@ ttc_status gemm_i8_wide(DeviceInfo* dev, const I8Wide& w, int64_t M, int64_t N, 
       launch_widen_i8(specs, 2, dev->sm_count, s) != cudaSuccess)
     return TTC_ERR_CUDA;
   g_launches.fetch_add(1);
-  if (scale != nullptr) {
-    const I8Result out = scale->out == TTC_F32 ? kI8ToF32 : scale->out == TTC_BF16 ? kI8ToBF16 : kI8ToF16;
-    if (launch_pair_i8_scaled(out, prm, nclus, s) != cudaSuccess) return TTC_ERR_CUDA;
-    g_launches.fetch_add(1);
-    return TTC_OK;
-  }
   if (!plan_note("pair_i8 bn=256 clusters=%d tiles=%d units=%d", nclus, prm.num_tiles, prm.num_units) &&
       launch_pair_i8(prm, nclus, s) != cudaSuccess)
     return TTC_ERR_CUDA;
@@ -694,23 +671,6 @@ bool tma_stride_ok(int64_t count, int64_t stride, int esize) { return tma_batch_
 
 bool byte_ranges_overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
   return ranges_overlap(a, a_bytes, b, b_bytes);
-}
-
-size_t i8_pair_workspace(int64_t M, int64_t N, int64_t K) {
-  I8Wide w;
-  place_i8_copies(w, M, N, K, TTC_ROW_MAJOR, TTC_COL_MAJOR);
-  return w.bytes;
-}
-
-ttc_status i8_pair_scaled(int64_t M, int64_t N, int64_t K, const int8_t* A, int64_t lda, const int8_t* B, int64_t ldb,
-                          void* D, int64_t ldd, const I8Scale& scale, void* workspace, void* stream) {
-  DeviceInfo* dev = nullptr;
-  const ttc_status st = device_info(&dev);
-  if (st != TTC_OK) return st;
-  I8Wide w;
-  place_i8_copies(w, M, N, K, TTC_ROW_MAJOR, TTC_COL_MAJOR);
-  return gemm_i8_wide(dev, w, M, N, K, A, lda, TTC_ROW_MAJOR, B, ldb, TTC_COL_MAJOR, nullptr, 0, D, ldd, 0.0f, workspace,
-                      stream, &scale);
 }
 
 void count_launches(int n) { g_launches.fetch_add(n); }

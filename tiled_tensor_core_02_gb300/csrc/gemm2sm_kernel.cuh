@@ -40,9 +40,7 @@
 // is an integer below 2^24 in magnitude and exact in fp32; the epilogue warps
 // add the partials as int32 into running sums held in their registers (a
 // thread's row, its half of the tile's columns) and store the int32 tile once
-// per unit, after the last partial.  With kScaled (see I8Result) the int32 sums
-// are converted to fp32 there, multiplied by their row's and column's scale,
-// given the bias and the activation, and stored in the type it names.
+// per unit, after the last partial.
 #pragma once
 #include "gemm_kernel.cuh"
 
@@ -97,57 +95,10 @@ __device__ __forceinline__ void tma_load_boxes_pair(uint8_t* dst, const CUtensor
   if (bm.boxes > 1) tma_load_3d_pair(dst + bm.smem_step, m, x + bm.box_step, y, z, bar_leader, pol);
 }
 
-// What the int8 kernel makes of its sums.
-enum I8Result : int { kI8Sums = 0, kI8ToF16 = 1, kI8ToBF16 = 2, kI8ToF32 = 3 };
-
-// 32 of a row's sums (columns gcol0 ..), scaled: the product of the two scales'
-// factors is rounded after each, then bias and activation.
-__device__ __forceinline__ void i8_scaled_values(const GemmParams& p, const int32_t (&sums)[32], float row_scale,
-                                                 int gcol0, float (&v)[32]) {
-#pragma unroll
-  for (int j = 0; j < 32; ++j) v[j] = __int2float_rn(sums[j]) * row_scale;
-  const float* sb = p.scale_b + gcol0;
-  const float* bias = p.bias != nullptr ? p.bias + gcol0 : nullptr;
-  const bool vec = gcol0 + 32 <= p.N && ((reinterpret_cast<uintptr_t>(sb) | reinterpret_cast<uintptr_t>(bias)) & 15) == 0;
-  if (vec) {
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const float4 w = __ldg(reinterpret_cast<const float4*>(sb) + u);
-      v[4 * u] *= w.x;
-      v[4 * u + 1] *= w.y;
-      v[4 * u + 2] *= w.z;
-      v[4 * u + 3] *= w.w;
-    }
-    if (bias != nullptr) {
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const float4 w = __ldg(reinterpret_cast<const float4*>(bias) + u);
-        v[4 * u] += w.x;
-        v[4 * u + 1] += w.y;
-        v[4 * u + 2] += w.z;
-        v[4 * u + 3] += w.w;
-      }
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      if (gcol0 + j < p.N) {
-        v[j] *= __ldg(sb + j);
-        if (bias != nullptr) v[j] += __ldg(bias + j);
-      }
-    }
-  }
-  if (p.act != kActNone) {
-#pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = act_value(p.act, v[j]);
-  }
-}
-
-template <int BN, bool kBF16, bool kI8 = false, int kEW = 8, int kScaled = kI8Sums>
+template <int BN, bool kBF16, bool kI8 = false, int kEW = 8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * kEW, 1)
     gemm_pair_kernel(const __grid_constant__ GemmParams p) {
   static_assert(!(kI8 && kBF16), "int8 runs on fp16 copies");
-  static_assert(kI8 || kScaled == kI8Sums, "scales belong to int8 sums");
   using PairCfg = ttc::PairCfg<BN, kI8, kEW>;
   constexpr int kPairBN = BN;
   constexpr int S = PairCfg::kStages;
@@ -444,51 +395,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * kEW, 1)
         }
         if (!ok) break;
         RowCarry carry{};
-        if constexpr (kScaled != kI8Sums) {
-          const float row_scale = row_ok ? __ldg(p.scale_a + grow) : 0.0f;
-          const EpiPtrs es = epi_ptrs(p, bz, kScaled == kI8ToF32 ? 4 : 2);
-#pragma unroll
-          for (int cc = 0; cc < 4; ++cc) {
-            const int c = c_lo + cc;
-            if (c < c_hi) {
-              const int gcol0 = n0 + c * chunk;
-              float v[32];
-              i8_scaled_values(p, sums[cc], row_scale, gcol0, v);
-              if (lane == 0) bulk_wait_read<0>();
-              __syncwarp();
-              if (kScaled == kI8ToF32 && !p.d_tma) {
-                // rows TMA cannot store: staged a row a lane, stored a row an instruction
-                // (epi_store_chunk's padded staging would not fit the one 4 KB buffer)
-                constexpr layout::SwizzleBytes128 swz{};
-#pragma unroll
-                for (int ch = 0; ch < 8; ++ch)
-                  *reinterpret_cast<float4*>(stage_buf + swz((uint32_t)(lane * 128 + ch * 16))) =
-                      make_float4(v[4 * ch], v[4 * ch + 1], v[4 * ch + 2], v[4 * ch + 3]);
-                __syncwarp();
-                const int row0 = grow - lane, col = gcol0 + lane;
-#pragma unroll 4
-                for (int rr = 0; rr < 32; ++rr)
-                  if (row0 + rr < p.M && col < p.N)
-                    static_cast<float*>(es.D)[(int64_t)(row0 + rr) * p.ldd + col] =
-                        *reinterpret_cast<const float*>(stage_buf + swz((uint32_t)(rr * 128 + lane * 4)));
-                __syncwarp();
-              } else if constexpr (kScaled == kI8ToF32) {
-                uint32_t packed[32];
-#pragma unroll
-                for (int j = 0; j < 32; ++j) packed[j] = __float_as_uint(v[j]);
-                epi_store_chunk<4>(p, packed, row_ok, grow, gcol0, grow - lane * p.maps.epi_row_step, stage_buf, 0, buf,
-                                   carry, c == c_hi - 1, lane, es);
-              } else {
-                uint32_t packed[16];
-#pragma unroll
-                for (int j = 0; j < 16; ++j) packed[j] = pack2<kScaled == kI8ToBF16>(v[2 * j], v[2 * j + 1]);
-                epi_store_chunk<2>(p, packed, row_ok, grow, gcol0, grow - lane * p.maps.epi_row_step, stage_buf, 0, buf,
-                                   carry, c == c_hi - 1, lane, es);
-              }
-            }
-          }
-          continue;
-        }
 #pragma unroll
         for (int cc = 0; cc < 4; ++cc) {
           const int c = c_lo + cc;

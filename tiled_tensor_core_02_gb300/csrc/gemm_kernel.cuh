@@ -164,10 +164,6 @@ struct GemmParams {
   // (b_half_map == 1; otherwise they load the whole box and read half of it)
   int b_half_map;
   CUtensorMap tmBh;
-  // CTA-pair int8 kernel with a scaled result: a scale for each row of A and
-  // for each column of B (fp32)
-  const float* scale_a;
-  const float* scale_b;
 };
 
 // Loads the k-block tile of an operand whose rows start at r0 and whose K

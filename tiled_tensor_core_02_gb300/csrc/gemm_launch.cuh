@@ -24,9 +24,6 @@ cudaError_t launch_pair_ew12(bool bf16, const GemmParams& p, int clusters, cudaS
 // Its int8 variant: fp16 copies of int8 operands, exact int32 result, 256-wide tiles.
 int pair_max_clusters_i8();
 cudaError_t launch_pair_i8(const GemmParams& p, int clusters, cudaStream_t stream);
-// ... and with the sums scaled (an I8Result other than kI8Sums), in inst_pair_i8_scaled.cu.
-enum I8Result : int;
-cudaError_t launch_pair_i8_scaled(I8Result out, const GemmParams& p, int clusters, cudaStream_t stream);
 
 template <int BN, int MODE>
 int gemm_smem_bytes() {

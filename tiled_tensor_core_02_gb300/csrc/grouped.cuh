@@ -27,7 +27,7 @@ struct GroupedParams {
   int64_t lda;
   const void* B;
   int64_t ldb, strideB;
-  const int32_t* offsets;
+  const int32_t* offsets;  // null: all rows are one group's
   int groups;
   int M;  // rows of all groups together: the bound of every offset
   int N, K;
@@ -50,6 +50,8 @@ struct GroupedParams {
   int c_vec, d_vec;  // rows of C, D start on 16-byte boundaries
   int b_stream;  // forward: a group's weights are read by one block of rows as a rule
   int tile_cols, stages;  // few-token kernel: output columns of a tile, its pipeline's stages
+  const float* scale_a;  // int8 products: a scale for each row of A and each column of B
+  const float* scale_b;
   uint32_t* err;
   uint64_t timeout_ns;
   int inject_stall;
@@ -59,6 +61,9 @@ struct GroupedParams {
 constexpr int kGroupedPairTile = 256;
 int grouped_pair_clusters();
 cudaError_t launch_grouped_pair(bool bf16, bool wgrad, const GroupedParams& p, int clusters, cudaStream_t stream);
+// The same kernel for int8 products: fp16 copies of the operands, all rows one
+// group (no offsets), exact int32 sums, a scaled result (p.out_f32, or fp16 / bf16).
+cudaError_t launch_pair_i8_scaled(bool bf16_out, const GroupedParams& p, int clusters, cudaStream_t stream);
 
 // The kernel for few tokens: token tiles of 16, 32, 64 and 128, tiles of 8 to 128
 // output columns.  Stages that fit for these tiles:

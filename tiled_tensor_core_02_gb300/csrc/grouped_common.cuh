@@ -37,7 +37,8 @@ __device__ __forceinline__ int group_tiles(const GroupedParams& p, const GroupTa
 template <int ROWS>
 __device__ __forceinline__ void build_group_table(const GroupedParams& p, const GroupTable& tb) {
   if (tb.offs != nullptr) {
-    for (int i = threadIdx.x; i <= p.groups; i += blockDim.x) tb.offs[i] = min(max(__ldg(p.offsets + i), 0), p.M);
+    for (int i = threadIdx.x; i <= p.groups; i += blockDim.x)
+      tb.offs[i] = p.offsets != nullptr ? min(max(__ldg(p.offsets + i), 0), p.M) : i * p.M;
     __syncthreads();
   }
   if (tb.start == nullptr) return;

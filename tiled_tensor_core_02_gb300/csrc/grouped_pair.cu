@@ -27,6 +27,10 @@
 //   accumulator is started and the epilogue warps add up the partial sums in
 //   registers, rounded to nearest.
 //
+// int8 products with scales run here too, on fp16 copies of the operands (every
+// int8 value is exact in fp16, every product and sum below 2^24 in fp32): one
+// group, an accumulator for every 1024 of K, the partial sums added up as int32.
+//
 // Results leave through a 4 KB block of shared memory per epilogue warp, 32 rows
 // of 128 bytes: written a row per lane, read back and stored four whole rows an
 // instruction, with no asynchronous copy to wait for and any row left out.
@@ -55,9 +59,12 @@ constexpr int kStagingBytes = kEpiWarpCount * 4096;
 constexpr int kBarBytes = 256;
 constexpr int kTableInts = 384;
 constexpr int kSmemBytes = 1024 + kStages * 2 * kShareBytes + kStagingBytes + kBarBytes + kTableInts * 4;
-constexpr int kChunkKBlocks = 12;  // fp32 results: 768 tokens to an accumulator
+// k-blocks of an accumulator where the partial sums are added up in registers:
+// fp32 results, 768 tokens; int8, 1024 products
+template <bool I8>
+constexpr int kChunkKBlocks = I8 ? 16 : 12;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
-static_assert(kChunkKBlocks % kKPS == 0, "accumulator chunks hold whole stages");
+static_assert(kChunkKBlocks<false> % kKPS == 0 && kChunkKBlocks<true> % kKPS == 0, "accumulator chunks hold whole stages");
 static_assert((kMaxGroups + 3) / 4 + 1 <= kTableInts, "a table of every fourth group's tiles has room");
 
 // Warps: producer, MMA issuer, in wgrad the one that clears the rows behind a
@@ -225,6 +232,7 @@ struct EpiTile {
   T* d;        // its first element of D, and of C (null without C)
   const T* c;
   int g, col0;
+  int64_t row;  // its first row of D
   int rows, cols;  // rows inside the group (wgrad: inside D); columns of D from col0 on
   int k_blocks;
 };
@@ -237,12 +245,51 @@ __device__ __forceinline__ EpiTile<T> epi_tile(const GroupedParams& p, const Gro
   const int64_t row0 = WGRAD ? r0 : (int64_t)x.lo + r0;
   e.g = x.g;
   e.col0 = x.cb * kTile + part * (kTile / 2);
+  e.row = row0;
   e.rows = max(0, min(32, WGRAD ? p.K - r0 : x.hi - x.lo - r0));
   e.cols = p.N - e.col0;
   e.d = static_cast<T*>(p.D) + (WGRAD ? (int64_t)x.g * p.strideD : 0) + row0 * p.ldd + e.col0;
   e.c = WGRAD && p.C != nullptr ? static_cast<const T*>(p.C) + (int64_t)x.g * p.strideC + row0 * p.ldc + e.col0 : nullptr;
   e.k_blocks = pair_loop<WGRAD>(p, x).k_blocks;
   return e;
+}
+
+// Sixteen int8 sums of a row, scaled: columns sc, bias on, `n` of them inside D.
+__device__ __forceinline__ void scaled_values(const GroupedParams& p, const uint32_t (&sums)[16], float scale,
+                                              const float* sc, const float* bias, int n, float (&v)[16]) {
+#pragma unroll
+  for (int j = 0; j < 16; ++j) v[j] = __int2float_rn((int32_t)sums[j]) * scale;
+  if (n >= 16 && ((reinterpret_cast<uintptr_t>(sc) | reinterpret_cast<uintptr_t>(bias)) & 15) == 0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 w = __ldg(reinterpret_cast<const float4*>(sc) + i);
+      v[4 * i] *= w.x;
+      v[4 * i + 1] *= w.y;
+      v[4 * i + 2] *= w.z;
+      v[4 * i + 3] *= w.w;
+    }
+    if (bias != nullptr) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 w = __ldg(reinterpret_cast<const float4*>(bias) + i);
+        v[4 * i] += w.x;
+        v[4 * i + 1] += w.y;
+        v[4 * i + 2] += w.z;
+        v[4 * i + 3] += w.w;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      if (j < n) {
+        v[j] *= __ldg(sc + j);
+        if (bias != nullptr) v[j] += __ldg(bias + j);
+      }
+  }
+  if (p.act != kActNone) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[j] = act_value(p.act, v[j]);
+  }
 }
 
 // Asks L2 for the tile's C, line by line and not as bulk copies: those go through
@@ -259,10 +306,13 @@ __device__ __forceinline__ void prefetch_c(const GroupedParams& p, const EpiTile
 
 // ADD: C is read (wgrad); a parameter of its own because the fp32 sums leave
 // few registers for it.
-template <bool BF16, bool WGRAD, bool F32, bool ADD>
+// I8: forward with int8 sums, scaled; BF16 then is the type of a 16-bit result.
+template <bool BF16, bool WGRAD, bool F32, bool ADD, bool I8 = false>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     grouped_pair_kernel(const __grid_constant__ GroupedParams p) {
-  static_assert(WGRAD || (!F32 && !ADD), "forward results are 16-bit and added to nothing");
+  static_assert(WGRAD || ((!F32 || I8) && !ADD), "forward results are 16-bit and added to nothing");
+  static_assert(!WGRAD || !I8, "int8 products are forward ones");
+  constexpr bool kSums = F32 || I8;  // partial sums in registers
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sA = smem;  // [stage][k-block of the stage, or 64 rows]
@@ -403,7 +453,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // ---------------------------------------------------------------- MMA issuer (even CTA)
     if (leader && lane == 0) {
       const bool b_mn = WGRAD || p.b_mn != 0;
-      const uint32_t idesc = idesc_f16(BF16, WGRAD, b_mn, kTile, kTile);
+      const uint32_t idesc = idesc_f16(BF16 && !I8, WGRAD, b_mn, kTile, kTile);
       const uint64_t a0 = smem_desc_sw128(smem_u32(sA), WGRAD ? (uint32_t)kHalfBytes : 16u, 1024);
       const uint64_t b0 = smem_desc_sw128(smem_u32(sB), b_mn ? (uint32_t)kHalfBytes : 16u, 1024);
       const uint64_t a_step = WGRAD ? 2048u >> 4 : 32u >> 4, b_step = b_mn ? 2048u >> 4 : 32u >> 4;
@@ -456,7 +506,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               phase ^= 1u;
             }
             if (!ready) ready = mbar_test_cluster(&tmem_empty[acc ^ 1], (((it + 1) >> 1) & 1) ^ 1u);
-          } while (!last && (!F32 || done < kChunkKBlocks));
+          } while (!last && (!kSums || done < kChunkKBlocks<I8>));
           if (!ok) break;
           mma_commit_pair(&tmem_full[acc], 0x3);
           ++it;
@@ -486,14 +536,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (t + num_pairs < tiles)
           prefetch_c(p, epi_tile<WGRAD, T>(p, grouped_tile<kTile, WGRAD>(p, tb, t + num_pairs), rank, q, part), lane);
       }
-      if constexpr (F32) {
-        uint32_t sums[kTile / 32][16];  // floats: this thread's row of the warp's 128 columns
+      if constexpr (kSums) {
+        uint32_t sums[kTile / 32][16];  // floats (int8: int32): this thread's row of the warp's 128 columns
 #pragma unroll
         for (int c = 0; c < kTile / 32; ++c)
 #pragma unroll
           for (int j = 0; j < 16; ++j) sums[c][j] = 0u;
         const int k_blocks = e0.k_blocks;
-        if constexpr (ADD) stage_rows_async(p, reinterpret_cast<const float*>(e0.c), e0.rows, e0.cols, lane, sb);
+        if constexpr (ADD && F32) stage_rows_async(p, reinterpret_cast<const float*>(e0.c), e0.rows, e0.cols, lane, sb);
         int kbeg = 0;
         do {
           const int acc = it & 1;
@@ -510,7 +560,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               tmem_ld_wait();
 #pragma unroll
               for (int j = 0; j < 16; ++j) {
-                sums[c][j] = __float_as_uint(__uint_as_float(sums[c][j]) + __uint_as_float(w[j]));
+                if constexpr (I8)
+                  sums[c][j] += (uint32_t)__float2int_rn(__uint_as_float(w[j]));  // an integer of at most 2^24
+                else
+                  sums[c][j] = __float_as_uint(__uint_as_float(sums[c][j]) + __uint_as_float(w[j]));
               }
             }
           }
@@ -518,13 +571,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&tmem_empty[acc]), 0));
           ++it;
-          kbeg += kChunkKBlocks;
+          kbeg += kChunkKBlocks<I8>;
         } while (kbeg < k_blocks);
         if (!ok) break;
         // found again rather than kept: the sums leave no registers for it
         int t_again = t;
         asm volatile("" : "+r"(t_again));
         const EpiTile<T> e = epi_tile<WGRAD, T>(p, grouped_tile<kTile, WGRAD>(p, tb, t_again), rank, q, part);
+        if constexpr (I8) {
+          const float scale = lane < e.rows ? __ldg(p.scale_a + e.row + lane) : 0.0f;
+          const float* sc = p.scale_b + e.col0;
+          const float* bias = p.bias != nullptr ? p.bias + e.col0 : nullptr;
+#pragma unroll
+          for (int u = 0; u < kUnits; ++u) {
+#pragma unroll
+            for (int h = 0; h < kUnit / 16; ++h) {
+              const int s16 = u * (kUnit / 16) + h;
+              float v[16];
+              scaled_values(p, sums[s16], scale, sc + s16 * 16, bias != nullptr ? bias + s16 * 16 : nullptr,
+                            e.cols - s16 * 16, v);
+              if constexpr (F32) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  *reinterpret_cast<float4*>(sb + staged<32>(lane, h * 4 + i)) =
+                      make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                  *reinterpret_cast<uint4*>(sb + staged<32>(lane, h * 2 + i)) =
+                      make_uint4(pack2<BF16>(v[8 * i], v[8 * i + 1]), pack2<BF16>(v[8 * i + 2], v[8 * i + 3]),
+                                 pack2<BF16>(v[8 * i + 4], v[8 * i + 5]), pack2<BF16>(v[8 * i + 6], v[8 * i + 7]));
+              }
+            }
+            __syncwarp();
+            copy_out(p, sb, e.d + u * kUnit, e.rows, e.cols - u * kUnit, lane);
+            __syncwarp();
+          }
+          continue;
+        }
         float* df = reinterpret_cast<float*>(e.d);
         const float* cf = reinterpret_cast<const float*>(e.c);
 #pragma unroll
@@ -661,7 +745,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
 }
 
-template <bool BF16, bool WGRAD, bool F32, bool ADD>
+template <bool BF16, bool WGRAD, bool F32, bool ADD, bool I8 = false>
 cudaError_t prepare() {
   static std::atomic<bool> done[64];
   int dev = 0;
@@ -669,7 +753,7 @@ cudaError_t prepare() {
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!done[dev].load()) {
-    e = cudaFuncSetAttribute(grouped_pair_kernel<BF16, WGRAD, F32, ADD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(grouped_pair_kernel<BF16, WGRAD, F32, ADD, I8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kSmemBytes);
     if (e != cudaSuccess) return e;
     done[dev].store(true);
@@ -694,9 +778,9 @@ int clusters_of() {
   return n;
 }
 
-template <bool BF16, bool WGRAD, bool F32, bool ADD>
+template <bool BF16, bool WGRAD, bool F32, bool ADD, bool I8 = false>
 cudaError_t launch(const GroupedParams& p, int clusters, cudaStream_t stream) {
-  cudaError_t e = prepare<BF16, WGRAD, F32, ADD>();
+  cudaError_t e = prepare<BF16, WGRAD, F32, ADD, I8>();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * clusters, 1, 1);
@@ -705,7 +789,7 @@ cudaError_t launch(const GroupedParams& p, int clusters, cudaStream_t stream) {
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   add_pdl_attribute(cfg, attr);
-  e = cudaLaunchKernelEx(&cfg, grouped_pair_kernel<BF16, WGRAD, F32, ADD>, p);
+  e = cudaLaunchKernelEx(&cfg, grouped_pair_kernel<BF16, WGRAD, F32, ADD, I8>, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -723,6 +807,12 @@ cudaError_t launch_grouped_pair(bool bf16, bool wgrad, const GroupedParams& p, i
   if (p.out_f32) return add ? TTC_PAIR(true, true, true) : TTC_PAIR(true, true, false);
   return add ? TTC_PAIR(true, false, true) : TTC_PAIR(true, false, false);
 #undef TTC_PAIR
+}
+
+cudaError_t launch_pair_i8_scaled(bool bf16_out, const GroupedParams& p, int clusters, cudaStream_t stream) {
+  if (p.out_f32) return launch<false, false, true, false, true>(p, clusters, stream);
+  return bf16_out ? launch<true, false, false, false, true>(p, clusters, stream)
+                  : launch<false, false, false, false, true>(p, clusters, stream);
 }
 
 }  // namespace ttc

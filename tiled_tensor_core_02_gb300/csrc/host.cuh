@@ -43,18 +43,4 @@ bool byte_ranges_overlap(const void* a, int64_t a_bytes, const void* b, int64_t 
 
 void count_launches(int n);
 
-// int8 products on the CTA-pair kernel with a scaled result: A (M x K) and B
-// (N x K), both with K contiguous and of any alignment, are widened into fp16
-// copies in the workspace (256-byte aligned, i8_pair_workspace bytes).  K > 0.
-struct I8Scale {
-  const float* a;
-  const float* b;
-  const float* bias;
-  int act;
-  ttc_dtype out;
-};
-size_t i8_pair_workspace(int64_t M, int64_t N, int64_t K);
-ttc_status i8_pair_scaled(int64_t M, int64_t N, int64_t K, const int8_t* A, int64_t lda, const int8_t* B, int64_t ldb,
-                          void* D, int64_t ldd, const I8Scale& scale, void* workspace, void* stream);
-
 }  // namespace ttc

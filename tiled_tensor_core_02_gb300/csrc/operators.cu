@@ -8,6 +8,7 @@
 #include "host.cuh"
 #include "i8_rows.cuh"
 #include "quantize.cuh"
+#include "repack.cuh"
 #include "ttc.h"
 
 using namespace ttc;
@@ -155,12 +156,24 @@ bool i8_tokens_plan(I8TokensParams& q, int block, const HostEnv& env) {
          encode_matrices(&q.tmB, u8, 1, p.B, p.K, p.N, p.ldb, 1, 0, 128, q.tile_cols, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// int8 products that take the CTA-pair kernel on fp16 copies.
+// int8 products of more tokens run on the CTA-pair kernel over fp16 copies of the
+// operands in the workspace, rows padded to 16 elements.  The copies' 16-byte
+// pieces and the tiles are counted in 32 bits.
 constexpr int64_t kI8FewTokens = 256;
+struct I8Copies {
+  int64_t ld;
+  size_t b_off, bytes;
+};
 bool takes_i8_pair(int64_t M, int64_t N, int64_t K) {
-  // the copies' 16-byte pieces and the tiles are counted in 32 bits
   return M > kI8FewTokens && N > 0 && K > 0 && blocks_of(K, 16) * (M > N ? M : N) < (1ll << 31) &&
-         blocks_of(M, 256) * blocks_of(N, 256) < (1ll << 30);
+         blocks_of(M, kGroupedPairTile) * blocks_of(N, kGroupedPairTile) < (1ll << 30);
+}
+I8Copies i8_copies(int64_t M, int64_t N, int64_t K) {
+  I8Copies c;
+  c.ld = blocks_of(K, 16) * 16;
+  c.b_off = (size_t)(blocks_of(M * c.ld * 2, 256) * 256);
+  c.bytes = c.b_off + (size_t)(blocks_of(N * c.ld * 2, 256) * 256);
+  return c;
 }
 
 }  // namespace
@@ -345,7 +358,7 @@ size_t ttc_gemm_i8_scaled_workspace_size(int64_t M, int64_t N, int64_t K, const 
   if (M <= 0 || N <= 0 || K <= 0 || K > TTC_I8_SCALED_MAX_K || lda < K || ldb < K || ldd < N || M > kSizeLimit ||
       N > kSizeLimit || !(is_16bit(out_dtype) || out_dtype == TTC_F32))
     return 0;
-  return takes_i8_pair(M, N, K) ? i8_pair_workspace(M, N, K) : 0;
+  return takes_i8_pair(M, N, K) ? i8_copies(M, N, K).bytes : 0;
 }
 
 ttc_status ttc_gemm_i8_scaled(int64_t M, int64_t N, int64_t K, const int8_t* A, int64_t lda, const float* scaleA,
@@ -368,16 +381,41 @@ ttc_status ttc_gemm_i8_scaled(int64_t M, int64_t N, int64_t K, const int8_t* A, 
                 byte_ranges_overlap(D, d_bytes, B, span_bytes(1, 0, N, ldb, K, 1))))
     return TTC_ERR_INVALID_ARG;
 
-  if (workspace != nullptr && aligned(workspace, 256) && takes_i8_pair(M, N, K) &&
-      workspace_bytes >= i8_pair_workspace(M, N, K)) {
-    const I8Scale scale{scaleA, scaleB, bias, (int)act, out_dtype};
-    return i8_pair_scaled(M, N, K, A, lda, B, ldb, D, ldd, scale, workspace, stream);
-  }
   HostEnv env;
   const ttc_status st = host_env(env);
   if (st != TTC_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const I8ResultType out = out_dtype == TTC_F32 ? kI8ResultF32 : out_dtype == TTC_BF16 ? kI8ResultBF16 : kI8ResultF16;
+  if (workspace != nullptr && aligned(workspace, 256) && takes_i8_pair(M, N, K) && !env.plain_loads) {
+    const I8Copies copies = i8_copies(M, N, K);
+    if (workspace_bytes >= copies.bytes) {
+      uint8_t* ws = static_cast<uint8_t*>(workspace);
+      const WidenSpec specs[2] = {{A, lda, M, K, ws, copies.ld}, {B, ldb, N, K, ws + copies.b_off, copies.ld}};
+      const int clusters = grouped_pair_clusters();
+      if (clusters <= 0) return TTC_ERR_CUDA;
+      GroupedParams f;
+      common_params(f, env, 1, M, N, K, ws, copies.ld, ws + copies.b_off, copies.ld, nullptr);
+      if (!pair_maps(f, false, TTC_F16, env)) return TTC_ERR_CUDA;
+      f.col_blocks = (int)blocks_of(N, kGroupedPairTile);
+      f.k_blocks = (int)blocks_of(K, kBK);
+      f.group_rows = 8;
+      f.alpha = 1.0f;
+      f.bias = bias;
+      f.act = (int)act;
+      f.scale_a = scaleA;
+      f.scale_b = scaleB;
+      f.out_f32 = out == kI8ResultF32;
+      f.D = D;
+      f.ldd = ldd;
+      f.d_vec = aligned(D, 16) && ldd * esize % 16 == 0;
+      const int64_t tiles = blocks_of(M, kGroupedPairTile) * f.col_blocks;
+      if (launch_widen_i8(specs, 2, env.sm_count, s) != cudaSuccess ||
+          launch_pair_i8_scaled(out == kI8ResultBF16, f, (int)(tiles < clusters ? tiles : clusters), s) != cudaSuccess)
+        return TTC_ERR_CUDA;
+      count_launches(2);
+      return TTC_OK;
+    }
+  }
   I8TokensParams q;
   std::memset(&q, 0, sizeof q);
   I8ScaledParams& p = q.p;
