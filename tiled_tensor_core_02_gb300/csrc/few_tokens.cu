@@ -2,9 +2,9 @@
 //   D[i, f] = act(alpha sum_k A[i, k] W_g[f, k] + bias_g[f]).
 //
 // With few tokens the cost is the stream of the weights, so these take the MMA's
-// 128-row side and the tokens its columns (16 to 128), the transpose of the
+// 128-row side and the tokens its columns (16 to 64), the transpose of the
 // other kernels' tiles: a stage of the pipeline is almost all weights, and the
-// MMA's time, 39 to 64 clocks for 16 to 128 columns, stays below the stream's.
+// MMA's time, 39 to 48 clocks for 16 to 64 columns, stays below the stream's.
 //
 // A tile is `tile_cols` output columns (8 to 128, chosen by the host so that the
 // tiles fill whole waves of SMs: 8192 columns are 147 tiles of 56, not 64 of 128)
@@ -15,7 +15,9 @@
 // One thread loads with TMA: a stage is 128 of K, as deep a ring of stages as
 // fits shared memory (what hides HBM's latency is the bytes on the way: 100 to
 // 200 KB an SM); one warp issues tcgen05.mma into two accumulators; four warps
-// drain them, a thread an output column, a register a token.
+// drain them, a thread an output column, a register a token.  Of a block's tokens
+// only those in the group are loaded, in boxes of at most 32: the others would
+// come from L2 as often as there are tiles.
 //
 // Bound by HBM: 16 rows of 8 groups, 14336 x 4096 bf16 (6 groups with rows, 705
 // MB): 107 us, 6.6 TB/s; the CTA-pair kernel takes 128.
@@ -39,10 +41,27 @@ __host__ __device__ constexpr int stage_bytes_of(int rows) { return rows * kStag
 // a narrower tile, barriers, group table.
 int fixed_bytes(int groups) { return 1024 + 16384 + kBarBytes + 2 * (groups + 2) * 4; }
 
+// All groups' blocks of tokens for one block of columns, then the next: blocks
+// that share a tile of weights follow one another (it comes from HBM once), and
+// large groups, whose other blocks find their weights in L2, are spread among the
+// small ones that keep HBM busy.
+template <int BT>
+__device__ __forceinline__ GroupedTile few_tile(const GroupedParams& p, const GroupTable& tb, int blocks, int t) {
+  GroupedTile x;
+  x.cb = t / blocks;
+  const int r = t - x.cb * blocks;
+  int first;
+  x.g = group_of_tile<BT>(p, tb, r, first);
+  x.rb = r - first;
+  group_rows(p, tb, x.g, x.lo, x.hi);
+  return x;
+}
+
 template <int BT, bool BF16>
 __global__ void __launch_bounds__(kThreads, 1) few_tokens_kernel(const __grid_constant__ GroupedParams p) {
   constexpr int kTokenBytes = stage_bytes_of(BT);
-  constexpr int kTmemCols = 2 * BT;  // two accumulators: 32 to 256 columns
+  constexpr int kBox = few_tokens_box(BT);
+  constexpr int kTmemCols = 2 * BT;  // two accumulators: 32 to 128 columns
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int w_bytes = stage_bytes_of(p.tile_cols);
@@ -62,6 +81,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_tokens_kernel(const __grid_co
   tb.offs = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + kBarBytes);
   tb.start = tb.offs + p.groups + 2;
   tb.step = 1;
+  tb.per = 1;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const WaitCtx wc{p.err, p.timeout_ns};
@@ -93,7 +113,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_tokens_kernel(const __grid_co
   grid_dependency_wait();
   grid_dependents_launch();
   build_group_table<BT>(p, tb);
-  const int tiles = table_tiles(p, tb);
+  const int blocks = table_tiles(p, tb);  // of tokens, of all groups
+  const int tiles = blocks * p.col_blocks;
   const int k_stages = (p.K + kStageK - 1) / kStageK;
   const int w_blk = p.tile_cols * kBK * 2;  // weights with K contiguous: from one k-block of a stage to the next
 
@@ -106,9 +127,10 @@ __global__ void __launch_bounds__(kThreads, 1) few_tokens_kernel(const __grid_co
       uint32_t phase = 0, armed = 0, armed_parity = 0;
       bool ok = true;
       for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-        const GroupedTile x = grouped_tile<BT, false>(p, tb, t);
+        const GroupedTile x = few_tile<BT>(p, tb, blocks, t);
         const int f0 = x.cb * p.tile_cols, t0 = x.lo + x.rb * BT;
         const int z = p.strideB != 0 ? x.g : 0;
+        const int boxes = (min(BT, x.hi - t0) + kBox - 1) / kBox;  // of tokens
         for (int ks = 0; ks < k_stages; ++ks) {
           const int k0 = ks * kStageK;
           const bool two = p.K - k0 > kBK;  // both k-blocks of the stage
@@ -120,7 +142,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_tokens_kernel(const __grid_co
           uint8_t* a = w + w_bytes;
           // weights with their rows contiguous come in boxes of 128 of K whatever K is
           mbar_arrive_expect_tx(&full[stage],
-                                (two || p.b_mn ? w_bytes : w_bytes / 2) + (two ? kTokenBytes : kTokenBytes / 2));
+                                (two || p.b_mn ? w_bytes : w_bytes / 2) + (two ? 2 : 1) * boxes * (kBox * kBK * 2));
           armed |= 1u << stage;
           armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
           if (p.b_mn) {
@@ -130,8 +152,11 @@ __global__ void __launch_bounds__(kThreads, 1) few_tokens_kernel(const __grid_co
             tma_load_3d(w, &p.tmB, k0, f0, z, &full[stage], pol_w);
             if (two) tma_load_3d(w + w_blk, &p.tmB, k0 + kBK, f0, z, &full[stage], pol_w);
           }
-          tma_load_3d(a, &p.tmA, k0, t0, 0, &full[stage], keep);
-          if (two) tma_load_3d(a + kTokenBytes / 2, &p.tmA, k0 + kBK, t0, 0, &full[stage], keep);
+          for (int b = 0; b < boxes; ++b) {
+            uint8_t* at = a + b * (kBox * kBK * 2);
+            tma_load_3d(at, &p.tmA, k0, t0 + b * kBox, 0, &full[stage], keep);
+            if (two) tma_load_3d(at + kTokenBytes / 2, &p.tmA, k0 + kBK, t0 + b * kBox, 0, &full[stage], keep);
+          }
           if (++stage == S) {
             stage = 0;
             phase ^= 1u;
@@ -198,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_tokens_kernel(const __grid_co
     const uint32_t tmem_mine = tmem_base + ((uint32_t)(q * 32) << 16);
     int it = 0;
     for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++it) {
-      const GroupedTile x = grouped_tile<BT, false>(p, tb, t);
+      const GroupedTile x = few_tile<BT>(p, tb, blocks, t);
       const int f = x.cb * p.tile_cols + col;
       const bool f_ok = col < p.tile_cols && f < p.N;
       const int row0 = x.lo + x.rb * BT, tokens = min(BT, x.hi - row0);
@@ -273,7 +298,6 @@ cudaError_t launch_few_tokens(bool bf16, int tokens, const GroupedParams& p, int
     case 16: return bf16 ? launch<16, true>(p, ctas, stream) : launch<16, false>(p, ctas, stream);
     case 32: return bf16 ? launch<32, true>(p, ctas, stream) : launch<32, false>(p, ctas, stream);
     case 64: return bf16 ? launch<64, true>(p, ctas, stream) : launch<64, false>(p, ctas, stream);
-    case 128: return bf16 ? launch<128, true>(p, ctas, stream) : launch<128, false>(p, ctas, stream);
   }
   return cudaErrorInvalidValue;
 }

@@ -65,8 +65,9 @@ cudaError_t launch_grouped_pair(bool bf16, bool wgrad, const GroupedParams& p, i
 // group (no offsets), exact int32 sums, a scaled result (p.out_f32, or fp16 / bf16).
 cudaError_t launch_pair_i8_scaled(bool bf16_out, const GroupedParams& p, int clusters, cudaStream_t stream);
 
-// The kernel for few tokens: token tiles of 16, 32, 64 and 128, tiles of 8 to 128
-// output columns.  Stages that fit for these tiles:
+// The kernel for few tokens: token tiles of 16, 32 and 64, tiles of 8 to 128
+// output columns.  tmA has boxes of few_tokens_box tokens.  Stages that fit:
+constexpr int few_tokens_box(int tokens) { return tokens < 32 ? tokens : 32; }
 int few_tokens_stages(int tokens, int tile_cols, int groups);
 cudaError_t launch_few_tokens(bool bf16, int tokens, const GroupedParams& p, int ctas, cudaStream_t stream);
 

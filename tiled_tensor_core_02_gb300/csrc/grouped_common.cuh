@@ -10,11 +10,13 @@ namespace ttc {
 // g, held to [0, M] (offs[groups] ends the last one); null where shared memory
 // has no room for it and the device's offsets are read instead.  start[i] is
 // the first tile of group i * step, its last entry the number of tiles; null in
-// the weights' gradient, where every group has as many tiles as another.
+// the weights' gradient, where every group has as many tiles as another.  A
+// block of a group's rows counts as `per` tiles.
 struct GroupTable {
   int* offs;
   int* start;
   int step;
+  int per;
 };
 
 __device__ __forceinline__ int offset_of(const GroupedParams& p, const GroupTable& tb, int g) {
@@ -30,7 +32,7 @@ template <int ROWS>
 __device__ __forceinline__ int group_tiles(const GroupedParams& p, const GroupTable& tb, int g) {
   int lo, hi;
   group_rows(p, tb, g, lo, hi);
-  return (hi - lo + ROWS - 1) / ROWS * p.col_blocks;
+  return (hi - lo + ROWS - 1) / ROWS * tb.per;
 }
 
 // Fills the table; all threads of the CTA.  ROWS: rows of a tile.

@@ -331,7 +331,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   int* stage_info = reinterpret_cast<int*>(bars + 3 * kStages + 7);
   int* table = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + kBarBytes);
   // the whole table where it has room, else only every fourth group's first tile
-  GroupTable tb{nullptr, nullptr, 1};
+  GroupTable tb{nullptr, nullptr, 1, p.col_blocks};
   if constexpr (WGRAD) {
     if (p.groups + 1 <= kTableInts) tb.offs = table;
   } else if (2 * (p.groups + 1) <= kTableInts) {

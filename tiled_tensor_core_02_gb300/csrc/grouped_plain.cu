@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_plain_kernel(const __grid
   const uint32_t tmem_base = *tmem_slot;
   grid_dependency_wait();
   grid_dependents_launch();
-  const GroupTable tb{offs, WGRAD ? nullptr : start, 1};
+  const GroupTable tb{offs, WGRAD ? nullptr : start, 1, p.col_blocks};
   build_group_table<kTile>(p, tb);
   const int tiles = WGRAD ? p.groups * p.row_blocks * p.col_blocks : table_tiles(p, tb);
 

@@ -181,57 +181,63 @@ __global__ void __launch_bounds__(kThreads, 1) i8_tokens_kernel(const __grid_con
     uint8_t* slot = slots + group * kSlotBytes;
     const uint32_t tmem_w =
         tmem_base + ((uint32_t)(quarter * 32) << 16) + kI8TokenCols + group * (kI8TokenStage / 2);
-    uint32_t wide_phase = 0;
+    // where this thread's bytes lie: of its row (the piece's place turned by the
+    // row), and of its pieces of the tokens, sixteen bytes each
+    constexpr int kPieces = BT * 8 / (kGroupWarps * 32);
+    constexpr int kBatch = kPieces < 4 ? kPieces : 4;
+    const bool in = row < q.tile_cols, any = quarter * 32 < q.tile_cols;
+    const int x_row = tid >> 3, x_c = tid & 7;  // its first piece; the others are kRows rows further each
+    constexpr int kRows = kGroupWarps * 4;
+    const uint32_t x_src = x_row * 128 + ((x_c ^ (x_row & 7)) << 4);
+    const uint32_t x_dst = (x_c >> 2) * (BT * 128) + x_row * 128;
+    const uint32_t x_lo = (((x_c & 3) * 2) ^ (x_row & 7)) << 4, x_hi = (((x_c & 3) * 2 + 1) ^ (x_row & 7)) << 4;
+    static_assert(kRows % 8 == 0, "the turn is the same for all of a thread's pieces");
+    uint32_t wide_phase = 0, phase = 0;
+    int stage = group;
     for (int n = group; n < n_stages; n += kGroups) {
-      const int stage = n % S;
       if (!mbar_wait(&wide_empty[group], wide_phase ^ 1u, wc)) break;  // first: see groups_of
-      if (!mbar_wait(&full[stage], (uint32_t)(n / S) & 1u, wc)) break;
+      if (!mbar_wait(&full[stage], phase, wc)) break;
       tc_fence_after();
       const uint8_t* w8 = ring + stage * stage_bytes;
-      const uint8_t* x8 = w8 + w_bytes;
-      if (quarter * 32 < q.tile_cols) {
-        const bool in = row < q.tile_cols;
+      const uint8_t* x8 = w8 + w_bytes + x_src;
+      // all loads before the first store: they do not move above one
+      uint4 xv[kBatch], wv[8 / kHalves];
 #pragma unroll
-        for (int h = half * (2 / kHalves); h < (half + 1) * (2 / kHalves); ++h) {
-          uint4 v[4];
+      for (int b = 0; b < kBatch; ++b) xv[b] = *reinterpret_cast<const uint4*>(x8 + b * (kRows * 128));
+      if (any) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            v[c] = in ? *reinterpret_cast<const uint4*>(w8 + row * 128 + (((h * 4 + c) ^ (row & 7)) << 4))
-                      : make_uint4(0u, 0u, 0u, 0u);
+        for (int c = 0; c < 8 / kHalves; ++c)
+          wv[c] = in ? *reinterpret_cast<const uint4*>(w8 + row * 128 + (((half * 4 + c) ^ (row & 7)) << 4))
+                     : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int h = 0; h < 2 / kHalves; ++h) {
           uint32_t w[32];
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            widen4(v[c].x, w[8 * c], w[8 * c + 1]);
-            widen4(v[c].y, w[8 * c + 2], w[8 * c + 3]);
-            widen4(v[c].z, w[8 * c + 4], w[8 * c + 5]);
-            widen4(v[c].w, w[8 * c + 6], w[8 * c + 7]);
+            widen4(wv[h * 4 + c].x, w[8 * c], w[8 * c + 1]);
+            widen4(wv[h * 4 + c].y, w[8 * c + 2], w[8 * c + 3]);
+            widen4(wv[h * 4 + c].z, w[8 * c + 4], w[8 * c + 5]);
+            widen4(wv[h * 4 + c].w, w[8 * c + 6], w[8 * c + 7]);
           }
-          tmem_st_32x32b_x32(tmem_w + h * 32, w);
+          tmem_st_32x32b_x32(tmem_w + (half + h) * 32, w);
         }
       }
-      // the tokens: sixteen bytes a piece
-      constexpr int kPieces = BT * 8 / (kGroupWarps * 32);
-      constexpr int kBatch = kPieces < 4 ? kPieces : 4;  // loads before the first store: they do not move above one
 #pragma unroll
-      for (int i0 = 0; i0 < kPieces; i0 += kBatch) {
-        uint4 v[kBatch];
+      for (int b0 = 0; b0 < kPieces; b0 += kBatch) {
+        if (b0 > 0) {
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-          const int r = (tid + kGroupWarps * 32 * (i0 + b)) >> 3, c = tid & 7;
-          v[b] = *reinterpret_cast<const uint4*>(x8 + r * 128 + ((c ^ (r & 7)) << 4));
+          for (int b = 0; b < kBatch; ++b) xv[b] = *reinterpret_cast<const uint4*>(x8 + (b0 + b) * (kRows * 128));
         }
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
-          const int r = (tid + kGroupWarps * 32 * (i0 + b)) >> 3, c = tid & 7;
           uint32_t h[8];
-          widen4(v[b].x, h[0], h[1]);
-          widen4(v[b].y, h[2], h[3]);
-          widen4(v[b].z, h[4], h[5]);
-          widen4(v[b].w, h[6], h[7]);
-          uint8_t* dst = slot + (c >> 2) * (BT * 128) + r * 128;
-          const int ch = (c & 3) * 2;
-          *reinterpret_cast<uint4*>(dst + ((ch ^ (r & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-          *reinterpret_cast<uint4*>(dst + (((ch + 1) ^ (r & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+          widen4(xv[b].x, h[0], h[1]);
+          widen4(xv[b].y, h[2], h[3]);
+          widen4(xv[b].z, h[4], h[5]);
+          widen4(xv[b].w, h[6], h[7]);
+          uint8_t* dst = slot + x_dst + (b0 + b) * (kRows * 128);
+          *reinterpret_cast<uint4*>(dst + x_lo) = make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4*>(dst + x_hi) = make_uint4(h[4], h[5], h[6], h[7]);
         }
       }
       tmem_st_wait();
@@ -239,10 +245,15 @@ __global__ void __launch_bounds__(kThreads, 1) i8_tokens_kernel(const __grid_con
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(&empty[stage]);
         mbar_arrive(&wide_full[group]);
+        mbar_arrive(&empty[stage]);
       }
       wide_phase ^= 1u;
+      stage += kGroups;
+      if (stage >= S) {
+        stage -= S;
+        phase ^= 1u;
+      }
     }
   }
   // every MMA is done (the issuer waited) and every byte is read

@@ -71,11 +71,13 @@ bool pair_maps(GroupedParams& p, bool wgrad, ttc_dtype dtype, const HostEnv& env
 }
 
 // Output columns of a few-token tile: as many as make the tiles of `rows` weights'
-// rows fill whole waves of SMs, in steps of 8 up to 128; with the columns
-// contiguous in memory (TMA boxes of 64) 64 or 128.
+// rows fill whole waves of SMs, in steps of 8 up to 128 (of more than three waves
+// the last one costs less than narrower tiles do: 64 groups, 4099 x 1536 x 2048 79.6
+// us with 128 columns, 84.8 with 112); with the columns contiguous in memory (TMA
+// boxes of 64) 64 or 128.
 int few_tile_cols(int64_t rows, int sm_count, bool cols_contiguous) {
   const int64_t waves = blocks_of(rows, 128ll * sm_count);
-  const int64_t c = blocks_of(blocks_of(rows, waves * sm_count), 8) * 8;
+  const int64_t c = waves > 3 ? 128 : blocks_of(blocks_of(rows, waves * sm_count), 8) * 8;
   if (cols_contiguous) return c > 64 ? 128 : 64;
   return (int)(c < 8 ? 8 : c > 128 ? 128 : c);
 }
@@ -88,24 +90,26 @@ bool few_maps(GroupedParams& p, ttc_dtype dtype, int tokens, int64_t matrices, c
   if (!tma_rows_ok(p.A, p.lda, 2) || !tma_rows_ok(p.B, p.ldb, 2) || !tma_stride_ok(p.groups, p.strideB, 2)) return false;
   p.tile_cols = few_tile_cols(matrices * p.N, env.sm_count, p.b_mn != 0);
   p.col_blocks = (int)blocks_of(p.N, p.tile_cols);
-  p.group_rows = 64;  // a tile's blocks of tokens next to one another: the weights come from L2 after the first
+  if ((blocks_of(p.M, tokens) + p.groups) * p.col_blocks > kSizeLimit) return false;
   p.b_stream = p.M <= matrices * tokens;
   p.stages = few_tokens_stages(tokens, p.tile_cols, p.groups);
   if (p.stages < 2) return false;
   const CUtensorMapDataType dt = dtype == TTC_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
   const int64_t mats = p.strideB != 0 ? p.groups : 1;
-  return encode_matrices(&p.tmA, dt, 2, p.A, p.K, p.M, p.lda, 1, 0, kBK, tokens, sw) &&
+  return encode_matrices(&p.tmA, dt, 2, p.A, p.K, p.M, p.lda, 1, 0, kBK, few_tokens_box(tokens), sw) &&
          (p.b_mn ? encode_matrices(&p.tmB, dt, 2, p.B, p.N, p.K, p.ldb, mats, p.strideB, 64, 128, sw)
                  : encode_matrices(&p.tmB, dt, 2, p.B, p.K, p.N, p.ldb, mats, p.strideB, kBK, p.tile_cols, sw));
 }
 
-// Block of tokens for groups of `mean` rows on average, `most` at most; 0: not few.
+// Block of tokens for groups of `mean` rows on average, `most` at most; 0: not
+// few.  Blocks of 64 and the CTA-pair kernel meet at about 80 rows a group (64
+// rows: 79.6 against 83 us in the case above; blocks of 128 leave shared memory
+// for three stages of the pipeline only, 87 to 94 us).
 int few_block(int64_t mean, int64_t most) {
   if (most <= 16 || mean <= 8) return 16;
   if (most <= 32 || mean <= 16) return 32;
-  if (mean <= 40) return 64;
-  return mean <= 80 ? 128 : 0;
+  return mean <= 80 ? 64 : 0;
 }
 
 // The tensor-core kernel for up to kI8FewTokens tokens: the tile's channels and
