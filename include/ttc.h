@@ -274,9 +274,9 @@ ttc_status ttc_gemm_i8_scaled(int64_t M, int64_t N, int64_t K,
                               void* workspace, size_t workspace_bytes, void* stream);
 
 /*
- * Workspace bytes of ttc_gemm_i8_scaled for these operands: 0 for few tokens,
- * whose weights are widened on their way through the SMs, and for invalid or
- * empty arguments.  Pure host computation; the pointers are only looked at for
+ * Workspace bytes that ttc_gemm_i8_scaled can use for these operands: 0 for few
+ * tokens, whose weights are widened on their way through the SMs, and for
+ * invalid or empty arguments.  Pure host computation; the pointers are only looked at for
  * their alignment.
  */
 size_t ttc_gemm_i8_scaled_workspace_size(int64_t M, int64_t N, int64_t K,

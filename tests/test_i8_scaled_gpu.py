@@ -269,3 +269,13 @@ def test_side_stream_and_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+
+
+# Sizes between the kernels: token blocks of 128 and few channels, many tokens with
+# and without the copies, rows that TMA cannot read on either side of their limit.
+@pytest.mark.parametrize("workspace", ["ask", "none"])
+@pytest.mark.parametrize("M,N,K", [(320, 520, 2048), (1024, 2056, 512), (700, 4096, 1040), (1100, 4099, 2048), (128, 1000, 333),
+                                   (129, 1000, 333), (2050, 136, 128)])
+def test_between_the_kernels(M, N, K, workspace):
+    for out in ("f32", "f16", "bf16"):
+        verify(M, N, K, out=out, act="relu", workspace=workspace, seed=M)

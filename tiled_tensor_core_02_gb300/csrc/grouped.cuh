@@ -31,7 +31,6 @@ struct GroupedParams {
   int groups;
   int M;  // rows of all groups together: the bound of every offset
   int N, K;
-  int a_vec, b_vec;  // plain loads: groups of 8 elements may be read as one vector
   int b_mn;          // forward: B_g is stored K x N (its columns contiguous)
   // tiles: blocks of D's columns, blocks of its rows (wgrad: per group; forward:
   // counted on the device), and how many row blocks share one column block

@@ -119,40 +119,6 @@ __device__ __forceinline__ void load_share(uint8_t* dst, const CUtensorMap* m, b
   }
 }
 
-// The warp's staging block: 32 rows of 4 W bytes in 16-byte pieces, turned so
-// that neither a row per lane nor whole rows meet a bank twice (eight lanes take
-// a row of 128 bytes, four lanes one of 64).
-template <int W>
-__device__ __forceinline__ int staged(int r, int piece) {
-  return W == 32 ? r * 128 + ((piece ^ (r & 7)) << 4) : r * 64 + ((piece ^ ((r >> 1) & 3)) << 4);
-}
-
-// Writes 32 staged rows to D: `rows` of them, from d0 on with pitch ldd, and `n`
-// columns are inside D.  Whole 128-byte lines where D allows it: stores of half
-// lines took 1.6 times as long (gradient to fp32 of 8 x 4096 x 4096, 128 tokens
-// a group: 172 us against 109).
-template <typename T>
-__device__ __forceinline__ void copy_out(const GroupedParams& p, const uint8_t* sb, T* d0, int rows, int n, int lane) {
-  constexpr int kElems = 16 / (int)sizeof(T), kCols = 128 / (int)sizeof(T);
-  const int whole = p.d_vec ? min(n, kCols) & ~(kElems - 1) : 0;  // columns stored as 16-byte pieces
-  const int piece = lane & 7, r0 = lane >> 3;
-  if (piece * kElems < whole) {
-    T* d = d0 + (int64_t)r0 * p.ldd + piece * kElems;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint4 v = *reinterpret_cast<const uint4*>(sb + staged<32>(i * 4 + r0, piece));
-      if (i * 4 + r0 < rows) *reinterpret_cast<uint4*>(d + (int64_t)(i * 4) * p.ldd) = v;
-    }
-  }
-  if (whole < min(n, kCols)) {
-#pragma unroll 1
-    for (int r = 0; r < rows; ++r)
-#pragma unroll 1
-      for (int c = whole + lane; c < min(n, kCols); c += 32)
-        d0[(int64_t)r * p.ldd + c] = *reinterpret_cast<const T*>(sb + staged<32>(r, c / kElems) + (c % kElems) * sizeof(T));
-  }
-}
-
 // The reverse for C, in two steps so that the loads are in flight meanwhile: 32
 // rows of 4 W bytes by whole rows into registers, zeros outside `rows` and `n`
 // columns, and through the staging block to a row per lane.
@@ -604,7 +570,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               }
             }
             __syncwarp();
-            copy_out(p, sb, e.d + u * kUnit, e.rows, e.cols - u * kUnit, lane);
+            copy_out<T, 4>(p, sb, e.d + u * kUnit, e.rows, e.cols - u * kUnit, lane);
             __syncwarp();
           }
           continue;
@@ -633,7 +599,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             *at = v;
           }
           __syncwarp();
-          copy_out(p, sb, df + c * 32, e.rows, e.cols - c * 32, lane);
+          copy_out<float, 4>(p, sb, df + c * 32, e.rows, e.cols - c * 32, lane);
           __syncwarp();
           if (ADD && c + 1 < kTile / 64)
             stage_rows_async(p, cf + c * 32 + 32, e.rows, e.cols - c * 32 - 32, lane, sb);
@@ -678,7 +644,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int h = 0; h < 2; ++h) {
             const int at = u * kUnit + h * 32, n = min(32, e0.cols - at);
             float v[32];
-            grouped_values<BF16>(p, w[h], nullptr, bias != nullptr && n > 0 ? bias + at : nullptr, n, v);
+            grouped_values<BF16>(p, w[h], bias != nullptr && n > 0 ? bias + at : nullptr, n, v);
             if (ADD) {
 #pragma unroll
               for (int j = 0; j < 16; ++j) {
@@ -695,7 +661,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (ADD && u + 1 < kUnits)
             copy_in(p, e0.c + (u + 1) * kUnit, e0.rows, e0.cols - (u + 1) * kUnit, lane, cw);
           __syncwarp();
-          copy_out(p, sb, e0.d + u * kUnit, e0.rows, e0.cols - u * kUnit, lane);
+          copy_out<T, 4>(p, sb, e0.d + u * kUnit, e0.rows, e0.cols - u * kUnit, lane);
           __syncwarp();
         }
       }

@@ -1,14 +1,17 @@
 // Grouped products for operands of any pitch and alignment: the kernel that is
-// right for every case.  One CTA per 128 x 128 tile, persistent; four warps
-// bring the operands into 128-byte-swizzled shared memory with plain loads
-// (generic_load_tile: vectors of 8 elements where rows are aligned, elements
-// otherwise, zeros outside the group's rows and the operand's extents), one
-// thread issues tcgen05.mma, four warps drain the accumulator.  In the
-// gradient of the weights the reduction runs over the group's rows, so both
-// operands lie with the reduction outermost, as the MMA takes them too.
+// right for every case.  One CTA per 128 x 128 tile, persistent; eight warps
+// bring the operands into 128-byte-swizzled shared memory, one thread issues
+// tcgen05.mma, four warps drain the accumulator.  In the gradient of the weights
+// the reduction runs over the group's rows, so both operands lie with the
+// reduction outermost, as the MMA takes them too.
 //
-// It is bound by the plain loads' latency; operands TMA can read take the
-// other kernels.
+// Eight elements that start at any 2-byte boundary lie in one or two aligned
+// 16-byte blocks; a thread loads those and shifts them into place, all of its
+// eight pieces of a k-block before it stores the first, so that up to 64 KB are on
+// the way.  Only blocks that hold a byte of the row are read; what is outside the
+// group's rows and the operand's extents is zero and not loaded.
+//
+// Bound by the loads' latency; operands TMA can read take the other kernels.
 #include "grouped_common.cuh"
 
 #include <atomic>
@@ -19,10 +22,151 @@ namespace {
 
 constexpr int kTile = kGroupedPlainTile;
 constexpr int kStages = 4;
-constexpr int kThreads = 32 * (4 + 1 + 4);  // producers, MMA issuer, epilogue
+constexpr int kProducers = 8;  // warps; then the MMA issuer, three spare ones, four of the epilogue
+constexpr int kEpiWarp0 = 12;
+constexpr int kThreads = 32 * (kEpiWarp0 + 4);
 constexpr int kOperandBytes = kTile * kBK * 2;
 constexpr int kTableBytes = 2 * (kMaxGroups + 4) * 4;
-constexpr int kSmemBytes = 1024 + kStages * 2 * kOperandBytes + 256 + kTableBytes;
+constexpr int kStagingBytes = 4 * 4096;
+constexpr int kSmemBytes = 1024 + kStages * 2 * kOperandBytes + kStagingBytes + 256 + kTableBytes;
+
+// A k-block's tile of an operand: ROWS rows of COLS contiguous elements from
+// (outer0, inner0) on, in 64-column slabs of ROWS 128-byte rows with the 128-byte
+// swizzle, the layout TMA writes.  One thread's pieces of eight elements.
+template <int ROWS, int COLS>
+struct TilePieces {
+  static constexpr int kPerRow = COLS / 8;
+  static constexpr int kCount = ROWS * kPerRow / (32 * kProducers);
+  uint4 lo[kCount], hi[kCount];
+  uint32_t phase[kCount];
+  int n[kCount];  // elements inside the operand
+
+  __device__ __forceinline__ void load(const void* src, int64_t ld, int outer0, int inner0, int outer_ext,
+                                       int inner_ext, int tid) {
+#pragma unroll
+    for (int i = 0; i < kCount; ++i) {
+      const int piece = tid + i * 32 * kProducers;
+      const int go = outer0 + piece / kPerRow, gi = inner0 + piece % kPerRow * 8;
+      n[i] = go < outer_ext ? max(0, min(8, inner_ext - gi)) : 0;
+      const uintptr_t at = reinterpret_cast<uintptr_t>(src) + ((int64_t)go * ld + gi) * 2;
+      phase[i] = (uint32_t)(at & 15);
+      const uint4* blk = reinterpret_cast<const uint4*>(at - phase[i]);
+      lo[i] = n[i] > 0 ? __ldg(blk) : make_uint4(0u, 0u, 0u, 0u);
+      hi[i] = (int)phase[i] + 2 * n[i] > 16 ? __ldg(blk + 1) : make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+
+  __device__ __forceinline__ void store(uint8_t* dst, int tid) const {
+    constexpr layout::SwizzleBytes128 swz{};
+#pragma unroll
+    for (int i = 0; i < kCount; ++i) {
+      uint32_t x[8] = {lo[i].x, lo[i].y, lo[i].z, lo[i].w, hi[i].x, hi[i].y, hi[i].z, hi[i].w};
+      // bytes down by the phase (even): stages of 8, 4 and 2
+      const bool s8 = phase[i] & 8, s4 = phase[i] & 4, s2 = phase[i] & 2;
+#pragma unroll
+      for (int k = 0; k < 6; ++k) x[k] = s8 ? x[k + 2] : x[k];
+#pragma unroll
+      for (int k = 0; k < 5; ++k) x[k] = s4 ? x[k + 1] : x[k];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[k] = s2 ? __byte_perm(x[k], x[k + 1], 0x5432) : x[k];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[k] = n[i] >= 2 * k + 2 ? x[k] : n[i] == 2 * k + 1 ? x[k] & 0xFFFFu : 0u;
+      const int piece = tid + i * 32 * kProducers, r = piece / kPerRow, c = piece % kPerRow;
+      *reinterpret_cast<uint4*>(dst + swz((uint32_t)((c / 8) * ROWS * 128 + r * 128 + (c % 8) * 16))) =
+          make_uint4(x[0], x[1], x[2], x[3]);
+    }
+  }
+};
+
+// The epilogue's walk: each warp 32 rows of every tile, in blocks of 128 bytes a
+// row through its staging block, so that C is read and D written a row an
+// instruction whatever their alignment.
+template <bool BF16, bool WGRAD, typename T>
+__device__ __forceinline__ void drain_tiles(const GroupedParams& p, const GroupTable& tb, int tiles, uint32_t tmem_base,
+                                            uint8_t* sb, uint64_t* tmem_full, uint64_t* tmem_empty, const WaitCtx& wc) {
+  constexpr int kUnit = 128 / (int)sizeof(T);  // columns
+  constexpr int kPer = 16 / (int)sizeof(T);    // of a 16-byte piece
+  const int q = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+  int it = 0;
+  for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++it) {
+    const GroupedTile x = grouped_tile<kTile, WGRAD>(p, tb, t);
+    const bool has_k = WGRAD ? x.hi > x.lo : p.k_blocks > 0;
+    const int acc = it & 1;
+    const int r0 = x.rb * kTile + q * 32;  // of the warp, in its group in forward
+    const int64_t row0 = WGRAD ? r0 : (int64_t)x.lo + r0;
+    const int rows = max(0, min(32, WGRAD ? p.K - r0 : x.hi - x.lo - r0));
+    const int col0 = x.cb * kTile;
+    T* d = static_cast<T*>(p.D) + (WGRAD ? (int64_t)x.g * p.strideD : 0) + row0 * p.ldd + col0;
+    const T* c = WGRAD && p.C != nullptr ? static_cast<const T*>(p.C) + (int64_t)x.g * p.strideC + row0 * p.ldc + col0
+                                         : nullptr;
+    const float* bias = !WGRAD && p.bias != nullptr ? p.bias + (int64_t)x.g * p.stride_bias + col0 : nullptr;
+    if (!mbar_wait(&tmem_full[acc], (it >> 1) & 1, wc)) break;
+    tc_fence_after();
+#pragma unroll 1
+    for (int at = 0; at < kTile; at += kUnit) {
+      const int n = min(kUnit, p.N - col0 - at);
+      if (c != nullptr) {
+        for (int j = lane; j < n; j += 32) {
+          const T* src = c + at + j;
+#pragma unroll 1
+          for (int r = 0; r < 32; r += 16) {  // sixteen loads on the way before the first store
+            T y[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) y[i] = r + i < rows ? src[(int64_t)(r + i) * p.ldc] : T{};
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              *reinterpret_cast<T*>(sb + staged<32>(r + i, j / kPer) + j % kPer * sizeof(T)) = y[i];
+          }
+        }
+        __syncwarp();
+      }
+#pragma unroll
+      for (int h = 0; h < kUnit; h += 32) {
+        uint32_t w[32];
+        if (has_k) {
+          tmem_ld_32x32b_x32(tmem_base + ((uint32_t)(q * 32) << 16) + acc * kTile + at + h, w);
+          tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) w[j] = 0u;
+        }
+        float v[32];
+        grouped_values<BF16>(p, w, bias != nullptr && n > h ? bias + at + h : nullptr, n - h, v);
+#pragma unroll
+        for (int i = 0; i < 32 / kPer; ++i) {
+          uint4* piece = reinterpret_cast<uint4*>(sb + staged<32>(lane, h / kPer + i));
+          uint32_t o[4];
+          uint4 old = make_uint4(0u, 0u, 0u, 0u);
+          if (c != nullptr) old = *piece;
+          const uint32_t cw[4] = {old.x, old.y, old.z, old.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if constexpr (sizeof(T) == 4) {
+              const float y = v[i * 4 + k];
+              o[k] = __float_as_uint(c != nullptr ? fmaf(p.beta, __uint_as_float(cw[k]), y) : y);
+            } else {
+              float y0 = v[i * 8 + 2 * k], y1 = v[i * 8 + 2 * k + 1];
+              if (c != nullptr) {
+                y0 = fmaf(p.beta, half_bits_to_float<BF16>((uint16_t)(cw[k] & 0xFFFFu)), y0);
+                y1 = fmaf(p.beta, half_bits_to_float<BF16>((uint16_t)(cw[k] >> 16)), y1);
+              }
+              o[k] = pack2<BF16>(y0, y1);
+            }
+          }
+          *piece = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+      }
+      if (at + kUnit >= kTile) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tmem_empty[acc]);
+      }
+      __syncwarp();
+      if (n > 0) copy_out<T, 8>(p, sb, d + at, rows, n, lane);
+      __syncwarp();
+    }
+  }
+}
 
 template <bool BF16, bool WGRAD>
 __global__ void __launch_bounds__(kThreads, 1) grouped_plain_kernel(const __grid_constant__ GroupedParams p) {
@@ -30,7 +174,8 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_plain_kernel(const __grid
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sA = smem;
   uint8_t* sB = sA + kStages * kOperandBytes;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sB + kStages * kOperandBytes);
+  uint8_t* staging = sB + kStages * kOperandBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(staging + kStagingBytes);
   uint64_t* full = bars;
   uint64_t* empty = bars + kStages;
   uint64_t* tmem_full = bars + 2 * kStages;
@@ -45,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_plain_kernel(const __grid
   const WaitCtx wc{p.err, p.timeout_ns};
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&full[s], 128);
+      mbar_init(&full[s], kProducers);
       mbar_init(&empty[s], 1);
     }
     for (int a = 0; a < 2; ++a) {
@@ -56,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_plain_kernel(const __grid
     mbar_init(drain_bar, 1);
     fence_barrier_init();
   }
-  if (warp == 4) {
+  if (warp == kProducers) {
     tmem_alloc(tmem_slot, 256);
     tmem_relinquish();
   }
@@ -70,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_plain_kernel(const __grid
   build_group_table<kTile>(p, tb);
   const int tiles = WGRAD ? p.groups * p.row_blocks * p.col_blocks : table_tiles(p, tb);
 
-  if (warp < 4) {
+  if (warp < kProducers) {
     // ---------------------------------------------------------------- producers
     int stage = 0;
     uint32_t phase = 0;
@@ -86,28 +231,40 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_plain_kernel(const __grid
         }
         uint8_t* a = sA + stage * kOperandBytes;
         uint8_t* b = sB + stage * kOperandBytes;
+        const int tid = threadIdx.x;
         if constexpr (WGRAD) {
           const int r0 = x.lo + kb * kBK;
-          generic_load_tile<kBK, kTile, false>(a, p.A, p.lda, r0, x.rb * kTile, x.hi, p.K, p.a_vec != 0, threadIdx.x);
-          generic_load_tile<kBK, kTile, false>(b, p.B, p.ldb, r0, n0, x.hi, p.N, p.b_vec != 0, threadIdx.x);
+          TilePieces<kBK, kTile> pa, pb;
+          pa.load(p.A, p.lda, r0, x.rb * kTile, x.hi, p.K, tid);
+          pb.load(p.B, p.ldb, r0, n0, x.hi, p.N, tid);
+          pa.store(a, tid);
+          pb.store(b, tid);
         } else {
           const uint16_t* bg = static_cast<const uint16_t*>(p.B) + (int64_t)x.g * p.strideB;
-          generic_load_tile<kTile, kBK, false>(a, p.A, p.lda, x.lo + x.rb * kTile, kb * kBK, x.hi, p.K, p.a_vec != 0,
-                                               threadIdx.x);
-          if (p.b_mn)
-            generic_load_tile<kBK, kTile, false>(b, bg, p.ldb, kb * kBK, n0, p.K, p.N, p.b_vec != 0, threadIdx.x);
-          else
-            generic_load_tile<kTile, kBK, false>(b, bg, p.ldb, n0, kb * kBK, p.N, p.K, p.b_vec != 0, threadIdx.x);
+          TilePieces<kTile, kBK> pa;
+          pa.load(p.A, p.lda, x.lo + x.rb * kTile, kb * kBK, x.hi, p.K, tid);
+          if (p.b_mn) {
+            TilePieces<kBK, kTile> pb;
+            pb.load(bg, p.ldb, kb * kBK, n0, p.K, p.N, tid);
+            pa.store(a, tid);
+            pb.store(b, tid);
+          } else {
+            TilePieces<kTile, kBK> pb;
+            pb.load(bg, p.ldb, n0, kb * kBK, p.N, p.K, tid);
+            pa.store(a, tid);
+            pb.store(b, tid);
+          }
         }
         fence_proxy_async_smem();
-        mbar_arrive(&full[stage]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[stage]);
         if (++stage == kStages) {
           stage = 0;
           phase ^= 1u;
         }
       }
     }
-  } else if (warp == 4) {
+  } else if (warp == kProducers) {
     // ---------------------------------------------------------------- MMA issuer
     if (lane == 0) {
       const bool b_mn = WGRAD || p.b_mn != 0;
@@ -154,54 +311,18 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_plain_kernel(const __grid
         drain_wait(drain_bar, 0, 100000000ull);
       }
     }
-  } else {
+  } else if (warp >= kEpiWarp0) {
     // ---------------------------------------------------------------- epilogue
-    const int q = warp & 3;
-    const int esize = p.out_f32 ? 4 : 2;
-    int it = 0;
-    for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++it) {
-      const GroupedTile x = grouped_tile<kTile, WGRAD>(p, tb, t);
-      const bool has_k = WGRAD ? x.hi > x.lo : p.k_blocks > 0;
-      const int acc = it & 1;
-      // D's row of this thread, and the group's first element of C and D
-      const int r = x.rb * kTile + q * 32 + lane;
-      const int64_t row = WGRAD ? r : (int64_t)x.lo + r;
-      const bool row_ok = WGRAD ? r < p.K : row < x.hi;
-      char* d_row = static_cast<char*>(p.D) + ((WGRAD ? (int64_t)x.g * p.strideD : 0) + row * p.ldd) * esize;
-      const char* c_row =
-          p.C != nullptr ? static_cast<const char*>(p.C) + ((int64_t)x.g * p.strideC + row * p.ldc) * esize : nullptr;
-      const float* bias = p.bias != nullptr ? p.bias + (int64_t)x.g * p.stride_bias : nullptr;
-      if (!mbar_wait(&tmem_full[acc], (it >> 1) & 1, wc)) break;
-      tc_fence_after();
-#pragma unroll 1
-      for (int c = 0; c < kTile / 32; ++c) {
-        const int col0 = x.cb * kTile + c * 32;
-        uint32_t w[32];
-        if (has_k) {
-          tmem_ld_32x32b_x32(tmem_base + ((uint32_t)(q * 32) << 16) + acc * kTile + c * 32, w);
-          tmem_ld_wait();
-        } else {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) w[j] = 0u;
-        }
-        if (c == kTile / 32 - 1) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&tmem_empty[acc]);
-        }
-        const int n = min(32, p.N - col0);
-        if (row_ok && n > 0) {
-          float v[32];
-          grouped_values<BF16>(p, w, c_row != nullptr ? c_row + (int64_t)col0 * esize : nullptr,
-                               bias != nullptr ? bias + col0 : nullptr, n, v);
-          store_row<BF16>(p, v, d_row + (int64_t)col0 * esize, n);
-        }
-      }
-    }
+    if (p.out_f32)
+      drain_tiles<BF16, WGRAD, float>(p, tb, tiles, tmem_base, staging + (warp - kEpiWarp0) * 4096, tmem_full, tmem_empty,
+                                      wc);
+    else
+      drain_tiles<BF16, WGRAD, uint16_t>(p, tb, tiles, tmem_base, staging + (warp - kEpiWarp0) * 4096, tmem_full,
+                                         tmem_empty, wc);
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 4) {
+  if (warp == kProducers) {
     tc_fence_after();
     tmem_dealloc(tmem_base, 256);
   }

@@ -35,7 +35,7 @@ constexpr int kI8RowsChunk = 256;     // of K
 
 cudaError_t launch_i8_rows(const I8ScaledParams& p, I8ResultType out, cudaStream_t stream);
 
-// The tensor-core kernel for up to a few hundred tokens (i8_tokens.cu): token
+// The tensor-core kernel for some hundred tokens (i8_tokens.cu): token
 // blocks of 16, 32, 64 and 128, tiles of 8 to 128 output channels, K shared by the
 // `split` CTAs of a cluster.  A CTA holds an accumulator for every 1024 of its K,
 // 256 columns of them: at most kI8TokenCols / block * 1024 of K a CTA.
@@ -51,6 +51,7 @@ struct I8TokensParams {
 constexpr int kI8TokenCols = 256;
 constexpr int kI8TokenStage = 128;
 int i8_tokens_stages(int block, int tile_cols);
+int i8_tokens_clusters(int split);  // clusters of `split` CTAs that the device holds (0 on error)
 cudaError_t launch_i8_tokens(const I8TokensParams& p, int block, I8ResultType out, cudaStream_t stream);
 
 }  // namespace ttc

@@ -376,6 +376,32 @@ int i8_tokens_stages(int block, int tile_cols) {
   return n > kMaxStages ? kMaxStages : n < groups_of(block) ? 0 : n;
 }
 
+// One CTA an SM, whatever its block: all of tensor memory.
+int i8_tokens_clusters(int split) {
+  static std::atomic<int> known[64][9];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64 || split < 1 || split > 8) return 0;
+  int n = known[dev][split].load();
+  if (n > 0) return n;
+  if (cudaFuncSetAttribute(i8_tokens_kernel<128, kI8ResultBF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) !=
+      cudaSuccess)
+    return 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)split, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = kSmemLimit;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)split;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, i8_tokens_kernel<128, kI8ResultBF16>, &cfg) != cudaSuccess) return 0;
+  known[dev][split].store(n);
+  return n;
+}
+
 cudaError_t launch_i8_tokens(const I8TokensParams& q, int block, I8ResultType out, cudaStream_t stream) {
   switch (block) {
     case 16: return launch_block<16>(q, out, stream);

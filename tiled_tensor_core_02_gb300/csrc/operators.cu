@@ -45,8 +45,6 @@ void common_params(GroupedParams& p, const HostEnv& env, int64_t groups, int64_t
   p.M = (int)M;
   p.N = (int)N;
   p.K = (int)K;
-  p.a_vec = aligned(A, 16) && lda % 8 == 0;
-  p.b_vec = aligned(B, 16) && ldb % 8 == 0;
   p.group_rows = 16;
   p.err = env.err;
   p.timeout_ns = env.timeout_ns;
@@ -112,33 +110,39 @@ int few_block(int64_t mean, int64_t most) {
   return mean <= 80 ? 64 : 0;
 }
 
-// The tensor-core kernel for up to kI8FewTokens tokens: the tile's channels and
-// the split of K whose CTAs are done soonest.  A stage takes the widening groups
-// 0.33 us or HBM's share of an SM its bytes, whichever is more; an exchange of
-// sums about two microseconds.  False where TMA cannot read the operands or K is
-// too long for its accumulators.
-bool i8_tokens_plan(I8TokensParams& q, int block, const HostEnv& env) {
+// The tensor-core kernel that widens the weights on its way: the tile's channels
+// and the split of K whose CTAs are done soonest, and an estimate of its time in
+// microseconds.  A stage takes the widening groups 0.33 us (0.9 with its products
+// for blocks of 128 tokens) or HBM's share of an SM its bytes, whichever is more; a
+// tile 1.5 us (5) besides, an exchange of sums two.  Clusters that do not fit next
+// to the others wait for a whole wave, so the rounds are counted in clusters that
+// the device holds (of eight CTAs 15, not 19: 256 x 512 x 2048 took 18 us instead
+// of 10 where that was overlooked).  False where TMA cannot read the operands or K
+// is too long for its accumulators.
+bool i8_tokens_plan(I8TokensParams& q, int block, const HostEnv& env, double& cost_us) {
   I8ScaledParams& p = q.p;
   if (env.plain_loads || p.K == 0 || !tma_rows_ok(p.A, p.lda, 1) || !tma_rows_ok(p.B, p.ldb, 1)) return false;
   const int64_t stages = blocks_of(p.K, kI8TokenStage), most = kI8TokenCols / block * (1024 / kI8TokenStage);
   const int64_t blocks = blocks_of(p.M, block);
+  if (blocks > 65535) return false;
+  const double widen = block >= 128 ? 0.9 : 0.33, tile = block >= 128 ? 5.0 : 1.5;
   double best = 0.0;
   const int splits[6] = {1, 2, 3, 4, 6, 8};
   for (int split : splits) {
     const int64_t per = blocks_of(stages, split);
     if (per > most || split > stages) continue;
-    // larger clusters leave SMs of a processor group over (36 clusters of 4 fit 152 SMs)
-    const int64_t sms = env.sm_count * (split <= 2 ? 152 : split < 8 ? 144 : 128) / 152;
+    const int64_t clusters = i8_tokens_clusters(split);
+    if (clusters < 1) continue;
     for (int64_t waves = 1; waves <= 64; ++waves) {
-      const int64_t room = waves * sms / (split * blocks);  // tiles
-      if (room < 1) continue;
-      const int64_t cols = blocks_of(blocks_of(p.N, room), 8) * 8;
+      const int64_t room = waves * clusters / blocks;  // tiles
+      if (room < 1 && waves < 64) continue;
+      const int64_t cols = blocks_of(blocks_of(p.N, room < 1 ? 1 : room), 8) * 8;
       if (cols > 128 && waves < 64) continue;
       const int64_t c = cols > 128 ? 128 : cols;
-      const int64_t ctas = blocks_of(p.N, c) * split * blocks;
-      const double hbm = (double)c * kI8TokenStage / 44500.0, widen = block >= 128 ? 0.5 : 0.33;
-      const double cost = (double)blocks_of(ctas, sms > 0 ? sms : 1) * ((double)per * (hbm > widen ? hbm : widen) + 1.5) +
-                          (split > 1 ? 2.0 : 0.0);
+      const double hbm = (double)c * kI8TokenStage / 44500.0;
+      const double cost =
+          (double)blocks_of(blocks_of(p.N, c) * blocks, clusters) * ((double)per * (hbm > widen ? hbm : widen) + tile) +
+          (split > 1 ? 2.0 : 0.0);
       if (best == 0.0 || cost < best) {
         best = cost;
         q.tile_cols = (int)c;
@@ -149,6 +153,7 @@ bool i8_tokens_plan(I8TokensParams& q, int block, const HostEnv& env) {
       break;
     }
   }
+  cost_us = best + 2.0;
   if (best == 0.0) return false;
   q.stages = i8_tokens_stages(block, q.tile_cols);
   if (q.stages < 1) return false;
@@ -160,17 +165,26 @@ bool i8_tokens_plan(I8TokensParams& q, int block, const HostEnv& env) {
          encode_matrices(&q.tmB, u8, 1, p.B, p.K, p.N, p.ldb, 1, 0, 128, q.tile_cols, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// int8 products of more tokens run on the CTA-pair kernel over fp16 copies of the
+// int8 products of many tokens run on the CTA-pair kernel over fp16 copies of the
 // operands in the workspace, rows padded to 16 elements.  The copies' 16-byte
-// pieces and the tiles are counted in 32 bits.
-constexpr int64_t kI8FewTokens = 256;
+// pieces and the tiles are counted in 32 bits.  Up to 256 tokens the kernel above
+// is the faster (256 x 8192 x 8192 82 us, 260 here 96), where TMA can read the
+// operands; else this one from 129 on (x 4416 x 1455: 128 tokens on plain loads
+// 21 us, 192 31; 257 here 22).  Beyond 256 the estimates decide: about ten
+// microseconds, the copies, and a round of tiles its share of K (measured within
+// a tenth from 512 x 512 x 2048, 20 us, to 1024 x 8192 x 8192, 140).
 struct I8Copies {
   int64_t ld;
   size_t b_off, bytes;
 };
-bool takes_i8_pair(int64_t M, int64_t N, int64_t K) {
-  return M > kI8FewTokens && N > 0 && K > 0 && blocks_of(K, 16) * (M > N ? M : N) < (1ll << 31) &&
+bool takes_i8_pair(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* B, int64_t ldb) {
+  const bool tma = tma_rows_ok(A, lda, 1) && tma_rows_ok(B, ldb, 1);
+  return M > (tma ? 256 : 128) && N > 0 && K > 0 && blocks_of(K, 16) * (M > N ? M : N) < (1ll << 31) &&
          blocks_of(M, kGroupedPairTile) * blocks_of(N, kGroupedPairTile) < (1ll << 30);
+}
+double i8_pair_cost_us(int64_t M, int64_t N, int64_t K, int clusters) {
+  const int64_t tiles = blocks_of(M, kGroupedPairTile) * blocks_of(N, kGroupedPairTile);
+  return 10.0 + (double)(M + N) * (double)K / 1.5e6 + (double)blocks_of(tiles, clusters) * (double)K / 200.0;
 }
 I8Copies i8_copies(int64_t M, int64_t N, int64_t K) {
   I8Copies c;
@@ -216,7 +230,6 @@ ttc_status ttc_gemm_grouped(int64_t groups, int64_t M, int64_t N, int64_t K, con
   GroupedParams p;
   common_params(p, env, groups, M, N, K, A, lda, B, ldb, offsets);
   p.strideB = strideB;
-  p.b_vec = p.b_vec && (groups == 1 || strideB % 8 == 0);
   p.b_mn = layoutB == TTC_ROW_MAJOR;
   p.col_blocks = (int)col_blocks;
   p.k_blocks = (int)blocks_of(K, kBK);
@@ -358,11 +371,11 @@ ttc_status ttc_quantize_rows(int64_t rows, int64_t cols, const void* X, int64_t 
 
 size_t ttc_gemm_i8_scaled_workspace_size(int64_t M, int64_t N, int64_t K, const int8_t* A, int64_t lda, const int8_t* B,
                                          int64_t ldb, const void* D, int64_t ldd, ttc_dtype out_dtype) {
-  (void)A, (void)B, (void)D;
+  (void)D;
   if (M <= 0 || N <= 0 || K <= 0 || K > TTC_I8_SCALED_MAX_K || lda < K || ldb < K || ldd < N || M > kSizeLimit ||
       N > kSizeLimit || !(is_16bit(out_dtype) || out_dtype == TTC_F32))
     return 0;
-  return takes_i8_pair(M, N, K) ? i8_copies(M, N, K).bytes : 0;
+  return takes_i8_pair(M, N, K, A, lda, B, ldb) ? i8_copies(M, N, K).bytes : 0;
 }
 
 ttc_status ttc_gemm_i8_scaled(int64_t M, int64_t N, int64_t K, const int8_t* A, int64_t lda, const float* scaleA,
@@ -390,13 +403,34 @@ ttc_status ttc_gemm_i8_scaled(int64_t M, int64_t N, int64_t K, const int8_t* A, 
   if (st != TTC_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const I8ResultType out = out_dtype == TTC_F32 ? kI8ResultF32 : out_dtype == TTC_BF16 ? kI8ResultBF16 : kI8ResultF16;
-  if (workspace != nullptr && aligned(workspace, 256) && takes_i8_pair(M, N, K) && !env.plain_loads) {
+  I8TokensParams q;
+  std::memset(&q, 0, sizeof q);
+  I8ScaledParams& p = q.p;
+  p.A = A;
+  p.lda = lda;
+  p.B = B;
+  p.ldb = ldb;
+  p.scaleA = scaleA;
+  p.scaleB = scaleB;
+  p.bias = bias;
+  p.D = D;
+  p.ldd = ldd;
+  p.M = (int)M;
+  p.N = (int)N;
+  p.K = (int)K;
+  p.act = (int)act;
+  p.a_vec = aligned(A, 16) && lda % 16 == 0;
+  p.b_vec = aligned(B, 16) && ldb % 16 == 0;
+  const int block = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+  double few_us = 0.0;
+  const bool few = M > 16 && i8_tokens_plan(q, block, env, few_us);
+  if (workspace != nullptr && aligned(workspace, 256) && takes_i8_pair(M, N, K, A, lda, B, ldb) && !env.plain_loads) {
     const I8Copies copies = i8_copies(M, N, K);
-    if (workspace_bytes >= copies.bytes) {
+    const int clusters = grouped_pair_clusters();
+    if (clusters <= 0) return TTC_ERR_CUDA;
+    if (workspace_bytes >= copies.bytes && !(few && few_us < i8_pair_cost_us(M, N, K, clusters))) {
       uint8_t* ws = static_cast<uint8_t*>(workspace);
       const WidenSpec specs[2] = {{A, lda, M, K, ws, copies.ld}, {B, ldb, N, K, ws + copies.b_off, copies.ld}};
-      const int clusters = grouped_pair_clusters();
-      if (clusters <= 0) return TTC_ERR_CUDA;
       GroupedParams f;
       common_params(f, env, 1, M, N, K, ws, copies.ld, ws + copies.b_off, copies.ld, nullptr);
       if (!pair_maps(f, false, TTC_F16, env)) return TTC_ERR_CUDA;
@@ -420,26 +454,7 @@ ttc_status ttc_gemm_i8_scaled(int64_t M, int64_t N, int64_t K, const int8_t* A, 
       return TTC_OK;
     }
   }
-  I8TokensParams q;
-  std::memset(&q, 0, sizeof q);
-  I8ScaledParams& p = q.p;
-  p.A = A;
-  p.lda = lda;
-  p.B = B;
-  p.ldb = ldb;
-  p.scaleA = scaleA;
-  p.scaleB = scaleB;
-  p.bias = bias;
-  p.D = D;
-  p.ldd = ldd;
-  p.M = (int)M;
-  p.N = (int)N;
-  p.K = (int)K;
-  p.act = (int)act;
-  p.a_vec = aligned(A, 16) && lda % 16 == 0;
-  p.b_vec = aligned(B, 16) && ldb % 16 == 0;
-  const int block = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
-  if (M > 16 && M <= kI8FewTokens && i8_tokens_plan(q, block, env)) {
+  if (few) {
     if (launch_i8_tokens(q, block, out, s) != cudaSuccess) return TTC_ERR_CUDA;
     count_launches(1);
     return TTC_OK;
