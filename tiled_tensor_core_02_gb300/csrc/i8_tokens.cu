@@ -1,4 +1,4 @@
-// int8 products for up to a few hundred tokens on the tensor cores:
+// int8 products for some hundred tokens on the tensor cores:
 //   D[i, f] = act(scaleA[i] scaleB[f] sum_k A[i, k] B[f, k] + bias[f]).
 //
 // There is no int8 tcgen05.mma on this device (and the warp-level one does 262
@@ -40,14 +40,14 @@ constexpr int kThreads = 32 * (kWarp0 + kWidenWarps);
 // kGroups stages before are done, and with them, in order, of all earlier ones.
 // In a ring of at least kGroups stages the place's previous use is then over, and
 // cannot be taken for the one the group waits for.
-constexpr int groups_of(int block) { return block >= 128 ? 2 : 4; }
+constexpr int kGroups = 4, kGroupWarps = kWidenWarps / kGroups;
 constexpr int kMaxStages = 16;
 constexpr int kSmemLimit = 227 * 1024;
 constexpr int kAccStages = 1024 / kI8TokenStage;  // stages of an accumulator
 
 constexpr int kAlign = 1024;
 int ring_stage_bytes(int block, int tile_cols) { return (block + tile_cols) * kI8TokenStage; }
-int fixed_bytes(int block) { return kAlign + 1024 + groups_of(block) * block * kI8TokenStage * 2; }
+int fixed_bytes(int block) { return kAlign + 1024 + kGroups * block * kI8TokenStage * 2; }
 int total_bytes(int block, int tile_cols, int stages) {
   const int n = fixed_bytes(block) + stages * ring_stage_bytes(block, tile_cols);
   const int sums = kAlign + 1024 + block * 128 * 4;  // the exchange reuses the slots and the ring
@@ -57,15 +57,13 @@ int total_bytes(int block, int tile_cols, int stages) {
 template <int BT, int OUT>
 __global__ void __launch_bounds__(kThreads, 1) i8_tokens_kernel(const __grid_constant__ I8TokensParams q) {
   constexpr int kSlotBytes = BT * kI8TokenStage * 2;
-  constexpr int kGroups = groups_of(BT), kGroupWarps = kWidenWarps / kGroups;
-  constexpr int kHalves = kGroupWarps / 4;  // warps that share a row of the weights
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem);  // in front: the exchange at the end leaves them alone
   uint8_t* slots = smem + 1024;                        // [group][k-block][token][64 fp16]
   uint8_t* ring = slots + kGroups * kSlotBytes;        // [stage][weights, tokens]
   const I8ScaledParams& p = q.p;
-  const int w_bytes = q.tile_cols * kI8TokenStage, stage_bytes = w_bytes + BT * kI8TokenStage, S = q.stages;  // at least the groups
+  const int w_bytes = q.tile_cols * kI8TokenStage, stage_bytes = w_bytes + BT * kI8TokenStage, S = q.stages;
   uint64_t* full = bars;
   uint64_t* empty = bars + kMaxStages;
   uint64_t* wide_full = bars + 2 * kMaxStages;
@@ -176,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1) i8_tokens_kernel(const __grid_con
   } else if (warp >= kWarp0) {
     // ---------------------------------------------------------------- widening
     const int group = (warp - kWarp0) / kGroupWarps, quarter = warp & 3;
-    const int half = ((warp - kWarp0) >> 2) % kHalves, tid = (int)threadIdx.x % (kGroupWarps * 32);
+    const int tid = (int)threadIdx.x % (kGroupWarps * 32);
     const int row = quarter * 32 + lane;  // of the weights' tile, and of tensor memory
     uint8_t* slot = slots + group * kSlotBytes;
     const uint32_t tmem_w =
@@ -184,7 +182,6 @@ __global__ void __launch_bounds__(kThreads, 1) i8_tokens_kernel(const __grid_con
     // where this thread's bytes lie: of its row (the piece's place turned by the
     // row), and of its pieces of the tokens, sixteen bytes each
     constexpr int kPieces = BT * 8 / (kGroupWarps * 32);
-    constexpr int kBatch = kPieces < 4 ? kPieces : 4;
     const bool in = row < q.tile_cols, any = quarter * 32 < q.tile_cols;
     const int x_row = tid >> 3, x_c = tid & 7;  // its first piece; the others are kRows rows further each
     constexpr int kRows = kGroupWarps * 4;
@@ -195,22 +192,21 @@ __global__ void __launch_bounds__(kThreads, 1) i8_tokens_kernel(const __grid_con
     uint32_t wide_phase = 0, phase = 0;
     int stage = group;
     for (int n = group; n < n_stages; n += kGroups) {
-      if (!mbar_wait(&wide_empty[group], wide_phase ^ 1u, wc)) break;  // first: see groups_of
+      if (!mbar_wait(&wide_empty[group], wide_phase ^ 1u, wc)) break;  // first: see kGroups
       if (!mbar_wait(&full[stage], phase, wc)) break;
       tc_fence_after();
       const uint8_t* w8 = ring + stage * stage_bytes;
       const uint8_t* x8 = w8 + w_bytes + x_src;
       // all loads before the first store: they do not move above one
-      uint4 xv[kBatch], wv[8 / kHalves];
+      uint4 xv[kPieces], wv[8];
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b) xv[b] = *reinterpret_cast<const uint4*>(x8 + b * (kRows * 128));
+      for (int i = 0; i < kPieces; ++i) xv[i] = *reinterpret_cast<const uint4*>(x8 + i * (kRows * 128));
       if (any) {
 #pragma unroll
-        for (int c = 0; c < 8 / kHalves; ++c)
-          wv[c] = in ? *reinterpret_cast<const uint4*>(w8 + row * 128 + (((half * 4 + c) ^ (row & 7)) << 4))
-                     : make_uint4(0u, 0u, 0u, 0u);
+        for (int c = 0; c < 8; ++c)
+          wv[c] = in ? *reinterpret_cast<const uint4*>(w8 + row * 128 + ((c ^ (row & 7)) << 4)) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-        for (int h = 0; h < 2 / kHalves; ++h) {
+        for (int h = 0; h < 2; ++h) {
           uint32_t w[32];
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
@@ -219,26 +215,19 @@ __global__ void __launch_bounds__(kThreads, 1) i8_tokens_kernel(const __grid_con
             widen4(wv[h * 4 + c].z, w[8 * c + 4], w[8 * c + 5]);
             widen4(wv[h * 4 + c].w, w[8 * c + 6], w[8 * c + 7]);
           }
-          tmem_st_32x32b_x32(tmem_w + (half + h) * 32, w);
+          tmem_st_32x32b_x32(tmem_w + h * 32, w);
         }
       }
 #pragma unroll
-      for (int b0 = 0; b0 < kPieces; b0 += kBatch) {
-        if (b0 > 0) {
-#pragma unroll
-          for (int b = 0; b < kBatch; ++b) xv[b] = *reinterpret_cast<const uint4*>(x8 + (b0 + b) * (kRows * 128));
-        }
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-          uint32_t h[8];
-          widen4(xv[b].x, h[0], h[1]);
-          widen4(xv[b].y, h[2], h[3]);
-          widen4(xv[b].z, h[4], h[5]);
-          widen4(xv[b].w, h[6], h[7]);
-          uint8_t* dst = slot + x_dst + (b0 + b) * (kRows * 128);
-          *reinterpret_cast<uint4*>(dst + x_lo) = make_uint4(h[0], h[1], h[2], h[3]);
-          *reinterpret_cast<uint4*>(dst + x_hi) = make_uint4(h[4], h[5], h[6], h[7]);
-        }
+      for (int i = 0; i < kPieces; ++i) {
+        uint32_t h[8];
+        widen4(xv[i].x, h[0], h[1]);
+        widen4(xv[i].y, h[2], h[3]);
+        widen4(xv[i].z, h[4], h[5]);
+        widen4(xv[i].w, h[6], h[7]);
+        uint8_t* dst = slot + x_dst + i * (kRows * 128);
+        *reinterpret_cast<uint4*>(dst + x_lo) = make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint4*>(dst + x_hi) = make_uint4(h[4], h[5], h[6], h[7]);
       }
       tmem_st_wait();
       fence_proxy_async_smem();
@@ -263,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1) i8_tokens_kernel(const __grid_con
 
   // ------------------------------------------------------------------ sums and result
   // four sets of four warps; set g takes the tokens from g * kCols on, a thread a channel
-  constexpr int kCols = BT >= 64 ? BT / 4 : 16;
+  constexpr int kCols = 16;
   int32_t* red = reinterpret_cast<int32_t*>(slots);  // [token][128 channels]
   const int tokens = min(BT, p.M - token0);
   auto result = [&](int32_t s, int token, int f) {
@@ -373,7 +362,7 @@ cudaError_t launch_block(const I8TokensParams& q, I8ResultType out, cudaStream_t
 
 int i8_tokens_stages(int block, int tile_cols) {
   const int n = (kSmemLimit - fixed_bytes(block)) / ring_stage_bytes(block, tile_cols);
-  return n > kMaxStages ? kMaxStages : n < groups_of(block) ? 0 : n;
+  return n > kMaxStages ? kMaxStages : n < kGroups ? 0 : n;
 }
 
 // One CTA an SM, whatever its block: all of tensor memory.
@@ -383,7 +372,7 @@ int i8_tokens_clusters(int split) {
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64 || split < 1 || split > 8) return 0;
   int n = known[dev][split].load();
   if (n > 0) return n;
-  if (cudaFuncSetAttribute(i8_tokens_kernel<128, kI8ResultBF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) !=
+  if (cudaFuncSetAttribute(i8_tokens_kernel<64, kI8ResultBF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) !=
       cudaSuccess)
     return 0;
   cudaLaunchConfig_t cfg = {};
@@ -397,7 +386,7 @@ int i8_tokens_clusters(int split) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaOccupancyMaxActiveClusters(&n, i8_tokens_kernel<128, kI8ResultBF16>, &cfg) != cudaSuccess) return 0;
+  if (cudaOccupancyMaxActiveClusters(&n, i8_tokens_kernel<64, kI8ResultBF16>, &cfg) != cudaSuccess) return 0;
   known[dev][split].store(n);
   return n;
 }
@@ -407,7 +396,6 @@ cudaError_t launch_i8_tokens(const I8TokensParams& q, int block, I8ResultType ou
     case 16: return launch_block<16>(q, out, stream);
     case 32: return launch_block<32>(q, out, stream);
     case 64: return launch_block<64>(q, out, stream);
-    case 128: return launch_block<128>(q, out, stream);
   }
   return cudaErrorInvalidValue;
 }

@@ -112,9 +112,10 @@ int few_block(int64_t mean, int64_t most) {
 
 // The tensor-core kernel that widens the weights on its way: the tile's channels
 // and the split of K whose CTAs are done soonest, and an estimate of its time in
-// microseconds.  A stage takes the widening groups 0.33 us (0.9 with its products
-// for blocks of 128 tokens) or HBM's share of an SM its bytes, whichever is more; a
-// tile 1.5 us (5) besides, an exchange of sums two.  Clusters that do not fit next
+// microseconds.  A stage takes 0.4 or HBM's share of an SM its bytes, whichever is
+// more, a tile six besides and an exchange of sums 1.5 (measured within a tenth
+// from 128 x 4096 x 4096, 13.8 us, to 1024 x 14336 x 4096, 219; blocks of 128 tokens
+// took longer: 46 us against 38 for 128 x 14336 x 4096).  Clusters that do not fit next
 // to the others wait for a whole wave, so the rounds are counted in clusters that
 // the device holds (of eight CTAs 15, not 19: 256 x 512 x 2048 took 18 us instead
 // of 10 where that was overlooked).  False where TMA cannot read the operands or K
@@ -125,7 +126,6 @@ bool i8_tokens_plan(I8TokensParams& q, int block, const HostEnv& env, double& co
   const int64_t stages = blocks_of(p.K, kI8TokenStage), most = kI8TokenCols / block * (1024 / kI8TokenStage);
   const int64_t blocks = blocks_of(p.M, block);
   if (blocks > 65535) return false;
-  const double widen = block >= 128 ? 0.9 : 0.33, tile = block >= 128 ? 5.0 : 1.5;
   double best = 0.0;
   const int splits[6] = {1, 2, 3, 4, 6, 8};
   for (int split : splits) {
@@ -139,10 +139,9 @@ bool i8_tokens_plan(I8TokensParams& q, int block, const HostEnv& env, double& co
       const int64_t cols = blocks_of(blocks_of(p.N, room < 1 ? 1 : room), 8) * 8;
       if (cols > 128 && waves < 64) continue;
       const int64_t c = cols > 128 ? 128 : cols;
-      const double hbm = (double)c * kI8TokenStage / 44500.0;
-      const double cost =
-          (double)blocks_of(blocks_of(p.N, c) * blocks, clusters) * ((double)per * (hbm > widen ? hbm : widen) + tile) +
-          (split > 1 ? 2.0 : 0.0);
+      const double hbm = (double)c * kI8TokenStage / 44500.0, stage = hbm > 0.4 ? hbm : 0.4;
+      const double cost = (double)blocks_of(blocks_of(p.N, c) * blocks, clusters) *
+                          ((double)per * stage + 6.0 + (split > 1 ? 1.5 : 0.0));
       if (best == 0.0 || cost < best) {
         best = cost;
         q.tile_cols = (int)c;
@@ -153,7 +152,7 @@ bool i8_tokens_plan(I8TokensParams& q, int block, const HostEnv& env, double& co
       break;
     }
   }
-  cost_us = best + 2.0;
+  cost_us = best;
   if (best == 0.0) return false;
   q.stages = i8_tokens_stages(block, q.tile_cols);
   if (q.stages < 1) return false;
@@ -421,7 +420,7 @@ ttc_status ttc_gemm_i8_scaled(int64_t M, int64_t N, int64_t K, const int8_t* A, 
   p.act = (int)act;
   p.a_vec = aligned(A, 16) && lda % 16 == 0;
   p.b_vec = aligned(B, 16) && ldb % 16 == 0;
-  const int block = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+  const int block = M <= 16 ? 16 : M <= 32 ? 32 : 64;
   double few_us = 0.0;
   const bool few = M > 16 && i8_tokens_plan(q, block, env, few_us);
   if (workspace != nullptr && aligned(workspace, 256) && takes_i8_pair(M, N, K, A, lda, B, ldb) && !env.plain_loads) {
