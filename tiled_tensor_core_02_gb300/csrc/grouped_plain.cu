@@ -11,7 +11,11 @@
 // the way.  Only blocks that hold a byte of the row are read; what is outside the
 // group's rows and the operand's extents is zero and not loaded.
 //
-// Bound by the loads' latency; operands TMA can read take the other kernels.
+// Bound by the producers, which a k-block of 2 x 16 KB takes 1.1 us (asking L2 for
+// its lines four k-blocks ahead changed nothing): 8192 rows over 8 groups, 4099 x
+// 4099, 1164 us or 236 TFLOP/s; 856 rows over 32 groups, 2712 x 3337, 349 us, where
+// loads of single elements took 1633.  Operands TMA can read take the other
+// kernels.
 #include "grouped_common.cuh"
 
 #include <atomic>
@@ -22,9 +26,9 @@ namespace {
 
 constexpr int kTile = kGroupedPlainTile;
 constexpr int kStages = 4;
-constexpr int kProducers = 8;  // warps; then the MMA issuer, three spare ones, four of the epilogue
-constexpr int kEpiWarp0 = 12;
-constexpr int kThreads = 32 * (kEpiWarp0 + 4);
+constexpr int kProducers = 8;  // warps; then four of the epilogue and the MMA issuer
+constexpr int kIssuer = kProducers + 4;
+constexpr int kThreads = 32 * (kIssuer + 1);
 constexpr int kOperandBytes = kTile * kBK * 2;
 constexpr int kTableBytes = 2 * (kMaxGroups + 4) * 4;
 constexpr int kStagingBytes = 4 * 4096;
@@ -32,7 +36,9 @@ constexpr int kSmemBytes = 1024 + kStages * 2 * kOperandBytes + kStagingBytes + 
 
 // A k-block's tile of an operand: ROWS rows of COLS contiguous elements from
 // (outer0, inner0) on, in 64-column slabs of ROWS 128-byte rows with the 128-byte
-// swizzle, the layout TMA writes.  One thread's pieces of eight elements.
+// swizzle, the layout TMA writes.  One thread's pieces of eight elements.  (Leaving
+// pieces outside D's rows and columns out put branches between the loads: 1683 us
+// against 1164 for 8192 rows, 8 groups, 4099 x 4099.)
 template <int ROWS, int COLS>
 struct TilePieces {
   static constexpr int kPerRow = COLS / 8;
@@ -62,13 +68,13 @@ struct TilePieces {
     for (int i = 0; i < kCount; ++i) {
       uint32_t x[8] = {lo[i].x, lo[i].y, lo[i].z, lo[i].w, hi[i].x, hi[i].y, hi[i].z, hi[i].w};
       // bytes down by the phase (even): stages of 8, 4 and 2
-      const bool s8 = phase[i] & 8, s4 = phase[i] & 4, s2 = phase[i] & 2;
+      const bool s8 = phase[i] & 8, s4 = phase[i] & 4;
 #pragma unroll
       for (int k = 0; k < 6; ++k) x[k] = s8 ? x[k + 2] : x[k];
 #pragma unroll
       for (int k = 0; k < 5; ++k) x[k] = s4 ? x[k + 1] : x[k];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) x[k] = s2 ? __byte_perm(x[k], x[k + 1], 0x5432) : x[k];
+      for (int k = 0; k < 4; ++k) x[k] = __funnelshift_r(x[k], x[k + 1], (phase[i] & 2) * 8);
 #pragma unroll
       for (int k = 0; k < 4; ++k) x[k] = n[i] >= 2 * k + 2 ? x[k] : n[i] == 2 * k + 1 ? x[k] & 0xFFFFu : 0u;
       const int piece = tid + i * 32 * kProducers, r = piece / kPerRow, c = piece % kPerRow;
@@ -77,6 +83,9 @@ struct TilePieces {
     }
   }
 };
+
+using Inner = TilePieces<kTile, kBK>;  // the reduction lies innermost
+using Outer = TilePieces<kBK, kTile>;  // outermost
 
 // The epilogue's walk: each warp 32 rows of every tile, in blocks of 128 bytes a
 // row through its staging block, so that C is read and D written a row an
@@ -201,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_plain_kernel(const __grid
     mbar_init(drain_bar, 1);
     fence_barrier_init();
   }
-  if (warp == kProducers) {
+  if (warp == kIssuer) {
     tmem_alloc(tmem_slot, 256);
     tmem_relinquish();
   }
@@ -234,23 +243,24 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_plain_kernel(const __grid
         const int tid = threadIdx.x;
         if constexpr (WGRAD) {
           const int r0 = x.lo + kb * kBK;
-          TilePieces<kBK, kTile> pa, pb;
+          Outer pa, pb;
           pa.load(p.A, p.lda, r0, x.rb * kTile, x.hi, p.K, tid);
           pb.load(p.B, p.ldb, r0, n0, x.hi, p.N, tid);
           pa.store(a, tid);
           pb.store(b, tid);
         } else {
           const uint16_t* bg = static_cast<const uint16_t*>(p.B) + (int64_t)x.g * p.strideB;
-          TilePieces<kTile, kBK> pa;
-          pa.load(p.A, p.lda, x.lo + x.rb * kTile, kb * kBK, x.hi, p.K, tid);
+          const int k0 = kb * kBK;
+          Inner pa;
+          pa.load(p.A, p.lda, x.lo + x.rb * kTile, k0, x.hi, p.K, tid);
           if (p.b_mn) {
-            TilePieces<kBK, kTile> pb;
-            pb.load(bg, p.ldb, kb * kBK, n0, p.K, p.N, tid);
+            Outer pb;
+            pb.load(bg, p.ldb, k0, n0, p.K, p.N, tid);
             pa.store(a, tid);
             pb.store(b, tid);
           } else {
-            TilePieces<kTile, kBK> pb;
-            pb.load(bg, p.ldb, n0, kb * kBK, p.N, p.K, tid);
+            Inner pb;
+            pb.load(bg, p.ldb, n0, k0, p.N, p.K, tid);
             pa.store(a, tid);
             pb.store(b, tid);
           }
@@ -264,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_plain_kernel(const __grid
         }
       }
     }
-  } else if (warp == kProducers) {
+  } else if (warp == kIssuer) {
     // ---------------------------------------------------------------- MMA issuer
     if (lane == 0) {
       const bool b_mn = WGRAD || p.b_mn != 0;
@@ -311,18 +321,18 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_plain_kernel(const __grid
         drain_wait(drain_bar, 0, 100000000ull);
       }
     }
-  } else if (warp >= kEpiWarp0) {
+  } else {
     // ---------------------------------------------------------------- epilogue
     if (p.out_f32)
-      drain_tiles<BF16, WGRAD, float>(p, tb, tiles, tmem_base, staging + (warp - kEpiWarp0) * 4096, tmem_full, tmem_empty,
+      drain_tiles<BF16, WGRAD, float>(p, tb, tiles, tmem_base, staging + (warp - kProducers) * 4096, tmem_full, tmem_empty,
                                       wc);
     else
-      drain_tiles<BF16, WGRAD, uint16_t>(p, tb, tiles, tmem_base, staging + (warp - kEpiWarp0) * 4096, tmem_full,
+      drain_tiles<BF16, WGRAD, uint16_t>(p, tb, tiles, tmem_base, staging + (warp - kProducers) * 4096, tmem_full,
                                          tmem_empty, wc);
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kProducers) {
+  if (warp == kIssuer) {
     tc_fence_after();
     tmem_dealloc(tmem_base, 256);
   }
