@@ -11,8 +11,11 @@ Names follow the C header include/ttc.h:
   ttc_status_string(status) -> str
   ttc_set_knob(knob, value) -> status
   ttc_launch_count() -> int
-plus `gemm(...)`, a convenience wrapper on torch tensors that reads the
-layouts and leading dimensions off the tensors' strides.
+  ttc_gemm_grouped, ttc_gemm_grouped_wgrad, ttc_quantize_rows,
+  ttc_gemm_i8_scaled[_workspace_size] -> status (size)
+plus `gemm(...)`, `gemm_grouped(...)`, `gemm_grouped_wgrad(...)`,
+`quantize_rows(...)` and `gemm_i8_scaled(...)`, convenience wrappers on torch
+tensors that read the layouts and leading dimensions off the tensors' strides.
 """
 from __future__ import annotations
 
@@ -259,4 +262,192 @@ def gemm(a, b, c=None, out=None, *, alpha=1.0, beta=0.0, bias=None, act="none", 
                   ldd, float(alpha), float(beta), bptr, ACT[act], DTYPE[dt], stream)
     if check and st != 0:
         raise TTCError(st)
+    return out
+
+
+def _row_pitch(t, what):
+    """Pitch of a 2-D tensor that must be row-major."""
+    if t.dim() != 2:
+        raise ValueError(f"{what} must have two dimensions")
+    rows, cols = t.shape
+    if (cols > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) < cols):
+        raise ValueError(f"{what} must be row-major")
+    return max(t.stride(0), cols, 1)
+
+
+def _group_pitch(t, what):
+    """(stride, pitch) of a 3-D tensor of row-major matrices."""
+    if t.dim() != 3:
+        raise ValueError(f"{what} must have three dimensions")
+    return (t.stride(0), _row_pitch(t[0], what)) if t.shape[0] else (0, max(t.shape[2], 1))
+
+
+def _same(device, dtypes, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} must be on {device}")
+        if t is not None and t.dtype not in dtypes:
+            raise ValueError(f"{name} must be of {' or '.join(str(d) for d in dtypes)}")
+
+
+def _check_offsets(offsets, groups, device):
+    import torch
+
+    _same(device, (torch.int32,), offsets=offsets)
+    if offsets.dim() != 1 or offsets.numel() != groups + 1 or not offsets.is_contiguous():
+        raise ValueError("offsets must be groups + 1 contiguous int32")
+
+
+def _finish(status, what, check):
+    if check and status != 0:
+        raise TTCError(status, what)
+
+
+def _half(t, what):
+    import torch
+
+    if t.dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError(f"{what} must be of torch.float16 or torch.bfloat16")
+    return "f16" if t.dtype == torch.float16 else "bf16"
+
+
+def gemm_grouped(a, b, offsets, out=None, *, alpha=1.0, bias=None, act="none", stream=None, check=True):
+    """out[i] = act(alpha * a[i] @ b[g] + bias[g]) for the rows i of every group g
+    (offsets[g] <= i < offsets[g + 1]); other rows of out are left as they are.
+
+    a: M x K row-major, b: groups x K x N, each matrix row- or column-major
+    (fp16/bf16 CUDA tensors; b.transpose(1, 2) of the weights gives the gradient
+    of the rows), offsets: groups + 1 int32 on the device, bias: groups x N fp32.
+    Returns out (M x N; a new one is not initialised where no group has rows)."""
+    import torch
+
+    dt = _half(a, "a")
+    lda = _row_pitch(a, "a")
+    if b.dim() != 3 or b.shape[1] != a.shape[1]:
+        raise ValueError("b must be groups x K x N with a's K")
+    (M, K), (groups, _, N) = a.shape, b.shape
+    _same(a.device, (a.dtype,), b=b, out=out)
+    _same(a.device, (torch.float32,), bias=bias)
+    _check_offsets(offsets, groups, a.device)
+    if out is None:
+        out = torch.empty((M, N), dtype=a.dtype, device=a.device)
+    if out.shape != (M, N):
+        raise ValueError("out must be M x N")
+    ldd = _row_pitch(out, "out")
+    lb, ldb = _matrix_layout(b[0], K, N) if groups else (ROW_MAJOR, max(N, 1))
+    stride_bias = 0
+    if bias is not None:
+        if bias.shape != (groups, N) or (N > 1 and bias.stride(1) != 1):
+            raise ValueError("bias must be groups x N, its rows contiguous")
+        stride_bias = bias.stride(0)
+    if stream is None:
+        stream = torch.cuda.current_stream(a.device).cuda_stream
+    _finish(ttc_gemm_grouped(groups, M, N, K, a.data_ptr(), lda, offsets.data_ptr(), b.data_ptr(), ldb, b.stride(0), lb,
+                             out.data_ptr(), ldd, float(alpha), None if bias is None else bias.data_ptr(), stride_bias,
+                             ACT[act], DTYPE[dt], stream), "ttc_gemm_grouped", check)
+    return out
+
+
+def gemm_grouped_wgrad(a, b, offsets, c=None, out=None, *, alpha=1.0, beta=0.0, out_dtype=None, stream=None, check=True):
+    """out[g] = alpha * a_g.T @ b_g + beta * c[g], a_g and b_g the rows of group g:
+    the gradient of gemm_grouped's weights.
+
+    a: M x K, b: M x N row-major (fp16/bf16 CUDA tensors), offsets: groups + 1
+    int32 on the device; c, out: groups x K x N, row-major, of a's type or fp32
+    (out_dtype, for a new out: fp32).  c may be out itself.  Returns out."""
+    import torch
+
+    dt = _half(a, "a")
+    lda, ldb = _row_pitch(a, "a"), _row_pitch(b, "b")
+    (M, K), N, groups = a.shape, b.shape[1], offsets.numel() - 1
+    if b.shape[0] != M:
+        raise ValueError("a and b must have the same rows")
+    _same(a.device, (a.dtype,), b=b)
+    _check_offsets(offsets, groups, a.device)
+    if out is None:
+        out = torch.empty((groups, K, N), dtype=out_dtype or torch.float32, device=a.device)
+    _same(a.device, (a.dtype, torch.float32), out=out)
+    _same(a.device, (out.dtype,), c=c)
+    if out.shape != (groups, K, N) or (c is not None and c.shape != out.shape):
+        raise ValueError("c and out must be groups x K x N")
+    stride_d, ldd = _group_pitch(out, "out")
+    stride_c, ldc = (0, max(N, 1)) if c is None else _group_pitch(c, "c")
+    odt = "f32" if out.dtype == torch.float32 else dt
+    if stream is None:
+        stream = torch.cuda.current_stream(a.device).cuda_stream
+    _finish(ttc_gemm_grouped_wgrad(groups, M, N, K, a.data_ptr(), lda, b.data_ptr(), ldb, offsets.data_ptr(),
+                                   None if c is None else c.data_ptr(), ldc, stride_c, out.data_ptr(), ldd, stride_d,
+                                   float(alpha), float(beta), DTYPE[dt], DTYPE[odt], stream),
+            "ttc_gemm_grouped_wgrad", check)
+    return out
+
+
+def quantize_rows(x, out=None, scale=None, *, stream=None, check=True):
+    """(q, scale): int8 rows and their fp32 scales, x[i] near scale[i] * q[i].
+
+    x: rows x cols row-major CUDA tensor (fp16/bf16/fp32).  A new q has rows on
+    16-byte boundaries, which gemm_i8_scaled reads fastest."""
+    import torch
+
+    _same(x.device, (torch.float16, torch.bfloat16, torch.float32), x=x)
+    ldx = _row_pitch(x, "x")
+    rows, cols = x.shape
+    if out is None:
+        out = torch.empty((rows, -(-cols // 16) * 16), dtype=torch.int8, device=x.device)[:, :cols]
+    if scale is None:
+        scale = torch.empty(rows, dtype=torch.float32, device=x.device)
+    _same(x.device, (torch.int8,), out=out)
+    _same(x.device, (torch.float32,), scale=scale)
+    if out.shape != x.shape or scale.shape != (rows,) or not scale.is_contiguous():
+        raise ValueError("out must have x's shape and scale its rows")
+    ldq = _row_pitch(out, "out")
+    dt = {torch.float16: "f16", torch.bfloat16: "bf16", torch.float32: "f32"}[x.dtype]
+    if stream is None:
+        stream = torch.cuda.current_stream(x.device).cuda_stream
+    _finish(ttc_quantize_rows(rows, cols, x.data_ptr(), ldx, DTYPE[dt], out.data_ptr(), ldq, scale.data_ptr(), stream),
+            "ttc_quantize_rows", check)
+    return out, scale
+
+
+def gemm_i8_scaled(a, scale_a, b, scale_b, out=None, *, out_dtype=None, bias=None, act="none", workspace=None,
+                   stream=None, check=True):
+    """out = act((a @ b.T) * scale_a[:, None] * scale_b + bias), the int8 product exact.
+
+    a: M x K, b: N x K int8 row-major CUDA tensors as quantize_rows makes them,
+    scale_a: M, scale_b and bias: N fp32.  out: M x N row-major, of out_dtype
+    (fp16, bf16 or fp32; a new out: bf16).  workspace: uint8 tensor of
+    ttc_gemm_i8_scaled_workspace_size() bytes; None takes one from torch's
+    allocator where the sizes want one.  Returns out."""
+    import torch
+
+    _same(a.device, (torch.int8,), a=a, b=b)
+    _same(a.device, (torch.float32,), scale_a=scale_a, scale_b=scale_b, bias=bias)
+    lda, ldb = _row_pitch(a, "a"), _row_pitch(b, "b")
+    (M, K), N = a.shape, b.shape[0]
+    if b.shape[1] != K:
+        raise ValueError("inner dimensions differ")
+    for name, t, n in (("scale_a", scale_a, M), ("scale_b", scale_b, N), ("bias", bias, N)):
+        if t is not None and (t.shape != (n,) or not t.is_contiguous()):
+            raise ValueError(f"{name} must be {n} contiguous fp32")
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype or torch.bfloat16, device=a.device)
+    _same(a.device, (torch.float16, torch.bfloat16, torch.float32), out=out)
+    if out.shape != (M, N):
+        raise ValueError("out must be M x N")
+    ldd = _row_pitch(out, "out")
+    odt = DTYPE[{torch.float16: "f16", torch.bfloat16: "bf16", torch.float32: "f32"}[out.dtype]]
+    own_stream = stream
+    if stream is None:
+        stream = torch.cuda.current_stream(a.device).cuda_stream
+    if workspace is None:
+        need = ttc_gemm_i8_scaled_workspace_size(M, N, K, a.data_ptr(), lda, b.data_ptr(), ldb, out.data_ptr(), ldd, odt)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=a.device)
+            if own_stream is not None:  # its memory stays taken until that stream is done with it
+                workspace.record_stream(torch.cuda.ExternalStream(own_stream, device=a.device))
+    _finish(ttc_gemm_i8_scaled(M, N, K, a.data_ptr(), lda, scale_a.data_ptr(), b.data_ptr(), ldb, scale_b.data_ptr(),
+                               out.data_ptr(), ldd, None if bias is None else bias.data_ptr(), ACT[act], odt,
+                               None if workspace is None else workspace.data_ptr(),
+                               0 if workspace is None else workspace.numel() * workspace.element_size(), stream),
+            "ttc_gemm_i8_scaled", check)
     return out
