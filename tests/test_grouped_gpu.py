@@ -341,3 +341,19 @@ def test_gradients_against_differences():
             tol_b += float((np.abs(vb[g]) * (2 * (hi - lo) + 1) * 2.0 ** -24 * s).sum())
         assert abs((got_a * va).sum() - da) <= tol_a
         assert abs(sum((got_b[g] * vb[g]).sum() for g in range(p.G)) - db) <= tol_b
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("n,pad", [(261, 3), (258, 6), (390, 10), (7, 1), (1021, 3)])
+def test_wgrad_columns_behind_the_last_whole_vector(n, pad, out):
+    """Widths that end inside a 16-byte vector, rows that start on one; half a tile
+    or more lies behind the last column."""
+    for in_place in (False, True):
+        Wgrad([0, 130, 130, 700], 700, n, 300, out=out, beta=1.0, pad=(4, pad, pad, pad), seed=n).verify(in_place=in_place)
+    Wgrad([0, 130, 130, 700], 700, n, 300, out=out, pad=(4, pad, pad, pad), seed=n).verify(alpha=0.5)
+
+
+@pytest.mark.parametrize("n,pad", [(261, 3), (390, 10), (1021, 3)])
+def test_columns_behind_the_last_whole_vector(n, pad):
+    for layout in ("row", "col"):
+        Grouped([0, 130, 130, 700], 700, n, 320, layout=layout, pad=(0, pad if layout == "row" else 0, pad), seed=n).verify()

@@ -279,3 +279,9 @@ def test_side_stream_and_graph():
 def test_between_the_kernels(M, N, K, workspace):
     for out in ("f32", "f16", "bf16"):
         verify(M, N, K, out=out, act="relu", workspace=workspace, seed=M)
+
+
+@pytest.mark.parametrize("M,N,K", [(1100, 4099, 2048), (2050, 4097, 1024)])
+@pytest.mark.parametrize("out", ["f32", "f16", "bf16"])
+def test_columns_behind_the_last_whole_vector(M, N, K, out):
+    verify(M, N, K, out=out, pad=(0, 0, -N % 8), seed=N)

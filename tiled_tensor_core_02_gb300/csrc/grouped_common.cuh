@@ -171,7 +171,8 @@ __device__ __forceinline__ int staged(int r, int piece) {
 template <typename T, int kAtOnce>
 __device__ __forceinline__ void copy_out(const GroupedParams& p, const uint8_t* sb, T* d0, int rows, int n, int lane) {
   constexpr int kElems = 16 / (int)sizeof(T), kCols = 128 / (int)sizeof(T);
-  const int whole = p.d_vec ? min(n, kCols) & ~(kElems - 1) : 0;  // columns stored as 16-byte pieces
+  n = max(0, min(n, kCols));  // a warp's columns may all lie behind D's last
+  const int whole = p.d_vec ? n & ~(kElems - 1) : 0;  // columns stored as 16-byte pieces
   const int piece = lane & 7, r0 = lane >> 3;
   if (piece * kElems < whole) {
     T* d = d0 + (int64_t)r0 * p.ldd + piece * kElems;
@@ -181,8 +182,8 @@ __device__ __forceinline__ void copy_out(const GroupedParams& p, const uint8_t* 
       if (i * 4 + r0 < rows) *reinterpret_cast<uint4*>(d + (int64_t)(i * 4) * p.ldd) = v;
     }
   }
-  if (whole < min(n, kCols)) {
-    for (int c = whole + lane; c < min(n, kCols); c += 32) {
+  if (whole < n) {
+    for (int c = whole + lane; c < n; c += 32) {
       T* d = d0 + c;
 #pragma unroll 1
       for (int r = 0; r < rows; r += kAtOnce) {
