@@ -357,3 +357,25 @@ def test_wgrad_columns_behind_the_last_whole_vector(n, pad, out):
 def test_columns_behind_the_last_whole_vector(n, pad):
     for layout in ("row", "col"):
         Grouped([0, 130, 130, 700], 700, n, 320, layout=layout, pad=(0, pad if layout == "row" else 0, pad), seed=n).verify()
+
+
+@pytest.mark.parametrize("beta", [1.0, 0.5])
+@pytest.mark.parametrize("n,ldd", [(264, 264), (261, 264), (520, 523)])
+def test_wgrad_in_place_and_apart_agree(n, ldd, beta):
+    """fp32 gradients added to in place and out of it differ by roundings only; the
+    padding stays as it is."""
+    M, K, groups = 700, 300, 3
+    g = torch.Generator(device="cuda").manual_seed(5)
+    a = torch.randn((M, K + 4), generator=g, device="cuda").bfloat16()[:, :K]
+    b = torch.randn((M, -(-n // 8) * 8), generator=g, device="cuda").bfloat16()[:, :n]
+    offsets = torch.tensor([0, 130, 130, 700], dtype=torch.int32, device="cuda")
+    first = torch.randn((groups, K, ldd), generator=g, device="cuda")
+    buf = first.clone()
+    ttc.gemm_grouped_wgrad(a, b, offsets, c=buf[:, :, :n], out=buf[:, :, :n], beta=beta)
+    apart = ttc.gemm_grouped_wgrad(a, b, offsets, c=first[:, :, :n], beta=beta)
+    assert torch.equal(buf[:, :, n:], first[:, :, n:])
+    assert torch.equal(buf[1, :, :n], beta * first[1, :, :n])  # an empty group
+    # the partial sums are the same; C joins them first or last, a rounding of each partial result either
+    # way, and of 570 products of normal values none is near 200
+    size = apart.abs().double() + first[:, :, :n].abs().double() + 200.0
+    assert ((buf[:, :, :n].double() - apart.double()).abs() <= 8 * 2.0 ** -24 * size).all()

@@ -26,6 +26,12 @@
 //   of the result after 2000 to 5600 tokens).  Every kChunkKBlocks k-blocks a fresh
 //   accumulator is started and the epilogue warps add up the partial sums in
 //   registers, rounded to nearest.
+// * C (wgrad) comes while the tile's products do.  16-bit C is read before the
+//   accumulator is waited for; fp32 C joins the partial sums 32 columns at a time
+//   between the accumulators.  Read at the end, a block at a time, or all of it at
+//   the tile's start, it met the next tile's operands on their way from L2, which
+//   they fill, and held the tensor cores up: 8 x 4096 x 4096, 16384 tokens, 414 and
+//   424 us against 381 (without C 335).
 //
 // int8 products with scales run here too, on fp16 copies of the operands (every
 // int8 value is exact in fp16, every product and sum below 2^24 in fp32): one
@@ -119,64 +125,72 @@ __device__ __forceinline__ void load_share(uint8_t* dst, const CUtensorMap* m, b
   }
 }
 
-// The reverse for C, in two steps so that the loads are in flight meanwhile: 32
-// rows of 4 W bytes by whole rows into registers, zeros outside `rows` and `n`
-// columns, and through the staging block to a row per lane.
-template <int W, typename T>
-__device__ __forceinline__ void copy_in(const GroupedParams& p, const T* c0, int rows, int n, int lane,
-                                        uint32_t (&w)[W]) {
-  constexpr int kElems = 16 / (int)sizeof(T);
-  constexpr int kLanes = W / 4;  // of a row
-  const int r0 = lane / kLanes, c = (lane % kLanes) * kElems;
+// A lane's row of the staging block; the block may be written again afterwards.
+__device__ __forceinline__ void row_of_block(const uint8_t* sb, int lane, uint32_t (&w)[32]) {
 #pragma unroll
-  for (int i = 0; i < kLanes; ++i) {
-    const int r = i * (32 / kLanes) + r0;
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (r < rows) {
-      const T* src = c0 + (int64_t)r * p.ldc + c;
-      if (p.c_vec && c + kElems <= n) {
-        v = *reinterpret_cast<const uint4*>(src);
-      } else if (c < n) {
-        uint32_t ws[4] = {0u, 0u, 0u, 0u};
-#pragma unroll 1
-        for (int e = 0; e < min(kElems, n - c); ++e) {
-          uint32_t x;
-          if constexpr (sizeof(T) == 4)
-            x = __float_as_uint(src[e]);
-          else
-            x = (uint32_t)src[e] << ((e & 1) * 16);
-          const int at = sizeof(T) == 4 ? e : e >> 1;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) ws[k] |= k == at ? x : 0u;
-        }
-        v = make_uint4(ws[0], ws[1], ws[2], ws[3]);
-      }
-    }
+  for (int i = 0; i < 8; ++i) {
+    const uint4 v = *reinterpret_cast<const uint4*>(sb + staged<32>(lane, i));
     w[4 * i] = v.x;
     w[4 * i + 1] = v.y;
     w[4 * i + 2] = v.z;
     w[4 * i + 3] = v.w;
   }
-}
-
-template <int W>
-__device__ __forceinline__ void stage_rows(uint8_t* sb, int lane, const uint32_t (&w)[W]) {
-  constexpr int kLanes = W / 4;
-#pragma unroll
-  for (int i = 0; i < kLanes; ++i)
-    *reinterpret_cast<uint4*>(sb + staged<W>(i * (32 / kLanes) + lane / kLanes, lane % kLanes)) =
-        make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
   __syncwarp();
 }
 
-// Both steps for 32 fp32 columns without a register, asynchronously where C
-// allows it: the sums' 128 registers leave none (any that is spilled goes to L2,
-// nearly all of L1 being shared memory here; with C held in registers ahead of
-// its use the 1024-token case above took 320 to 370 us).  copy_async_wait and a
-// __syncwarp come before the rows' use.
+// The reverse for C: N units of 32 rows by 128 bytes, all of them on their way
+// before the first is used, then one after the other through the staging block to
+// a row per lane.  Zeros outside `rows` and `n` columns.
+template <int N, typename T>
+__device__ __forceinline__ void load_c(const GroupedParams& p, const T* c0, int rows, int n, int lane, uint8_t* sb,
+                                       uint32_t (&w)[N][32]) {
+  constexpr int kElems = 16 / (int)sizeof(T), kCols = 128 / (int)sizeof(T);
+  const int piece = lane & 7, r0 = lane >> 3;
+  if (p.c_vec && n >= N * kCols) {
+    const T* src = c0 + (int64_t)r0 * p.ldc + piece * kElems;
+#pragma unroll
+    for (int i = 0; i < 8; ++i, src += 4 * p.ldc)
+#pragma unroll
+      for (int u = 0; u < N; ++u) {
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (i * 4 + r0 < rows) v = *reinterpret_cast<const uint4*>(src + u * kCols);
+        w[u][4 * i] = v.x;
+        w[u][4 * i + 1] = v.y;
+        w[u][4 * i + 2] = v.z;
+        w[u][4 * i + 3] = v.w;
+      }
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        *reinterpret_cast<uint4*>(sb + staged<32>(i * 4 + r0, piece)) =
+            make_uint4(w[u][4 * i], w[u][4 * i + 1], w[u][4 * i + 2], w[u][4 * i + 3]);
+      __syncwarp();
+      row_of_block(sb, lane, w[u]);
+    }
+  } else {
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+#pragma unroll 1
+      for (int c = lane; c < kCols; c += 32)
+#pragma unroll 1
+        for (int r = 0; r < 32; ++r)
+          *reinterpret_cast<T*>(sb + staged<32>(r, c / kElems) + (c % kElems) * sizeof(T)) =
+              r < rows && u * kCols + c < n ? c0[(int64_t)r * p.ldc + u * kCols + c] : T{};
+      __syncwarp();
+      row_of_block(sb, lane, w[u]);
+    }
+  }
+}
+
+// 32 rows by 32 fp32 columns into the staging block without a register (the sums'
+// 128 leave none: any that is spilled goes to L2, nearly all of L1 being shared
+// memory here), asynchronously where C allows it; copy_async_wait and a __syncwarp
+// come before their use.
 __device__ __forceinline__ void stage_rows_async(const GroupedParams& p, const float* c0, int rows, int n, int lane,
                                                  uint8_t* sb) {
-  const int whole = p.c_vec ? min(n, 32) & ~3 : 0;
+  n = max(0, min(n, 32));
+  const int whole = p.c_vec ? n & ~3 : 0;
   const int piece = lane & 7, r0 = lane >> 3;
   if (piece * 4 < whole) {
     const float* src = c0 + (int64_t)r0 * p.ldc + piece * 4;
@@ -184,7 +198,7 @@ __device__ __forceinline__ void stage_rows_async(const GroupedParams& p, const f
     for (int i = 0; i < 8; ++i)
       if (i * 4 + r0 < rows) copy_async_16(sb + staged<32>(i * 4 + r0, piece), src + (int64_t)(i * 4) * p.ldc);
   }
-  if (whole < min(n, 32)) {
+  if (whole < n) {
 #pragma unroll 1
     for (int r = 0; r < rows; ++r)
       if (lane >= whole && lane < n)
@@ -221,7 +235,7 @@ __device__ __forceinline__ EpiTile<T> epi_tile(const GroupedParams& p, const Gro
 }
 
 // Sixteen int8 sums of a row, scaled: columns sc, bias on, `n` of them inside D.
-__device__ __forceinline__ void scaled_values(const GroupedParams& p, const uint32_t (&sums)[16], float scale,
+__device__ __forceinline__ void scaled_values(const GroupedParams& p, const uint32_t* sums, float scale,
                                               const float* sc, const float* bias, int n, float (&v)[16]) {
 #pragma unroll
   for (int j = 0; j < 16; ++j) v[j] = __int2float_rn((int32_t)sums[j]) * scale;
@@ -256,18 +270,6 @@ __device__ __forceinline__ void scaled_values(const GroupedParams& p, const uint
 #pragma unroll
     for (int j = 0; j < 16; ++j) v[j] = act_value(p.act, v[j]);
   }
-}
-
-// Asks L2 for the tile's C, line by line and not as bulk copies: those go through
-// the unit that brings the operands.
-template <typename T>
-__device__ __forceinline__ void prefetch_c(const GroupedParams& p, const EpiTile<T>& e, int lane) {
-  if (lane >= e.rows) return;
-  const T* row = e.c + (int64_t)lane * p.ldc;
-  constexpr int kLine = 128 / (int)sizeof(T);
-#pragma unroll
-  for (int c = 0; c < kTile / 2; c += kLine)
-    if (c < e.cols) prefetch_l2_line(row + c);
 }
 
 // ADD: C is read (wgrad); a parameter of its own because the fp32 sums leave
@@ -496,24 +498,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int t = pair; ok && t < tiles; t += num_pairs) {
       const EpiTile<T> e0 = epi_tile<WGRAD, T>(p, grouped_tile<kTile, WGRAD>(p, tb, t), rank, q, part);
-      if constexpr (ADD && !F32) {
-        // C of the pair's next tile toward L2
-        if (t == pair) prefetch_c(p, e0, lane);
-        if (t + num_pairs < tiles)
-          prefetch_c(p, epi_tile<WGRAD, T>(p, grouped_tile<kTile, WGRAD>(p, tb, t + num_pairs), rank, q, part), lane);
-      }
       if constexpr (kSums) {
-        uint32_t sums[kTile / 32][16];  // floats (int8: int32): this thread's row of the warp's 128 columns
+        // floats (int8: int32): this thread's row of the warp's 128 columns
+        uint32_t sums[kTile / 64][32];
 #pragma unroll
-        for (int c = 0; c < kTile / 32; ++c)
+        for (int c = 0; c < kTile / 64; ++c)
 #pragma unroll
-          for (int j = 0; j < 16; ++j) sums[c][j] = 0u;
+          for (int j = 0; j < 32; ++j) sums[c][j] = 0u;
         const int k_blocks = e0.k_blocks;
-        if constexpr (ADD && F32) stage_rows_async(p, reinterpret_cast<const float*>(e0.c), e0.rows, e0.cols, lane, sb);
         int kbeg = 0;
+        // C joins the sums 32 columns at a time while the products are on their way,
+        // as many before each partial sum that all have before the last
+        const float* cf = reinterpret_cast<const float*>(e0.c);
+        const int chunks = max(1, (k_blocks + kChunkKBlocks<I8> - 1) / kChunkKBlocks<I8>);
+        int joined = 0, chunk = 0;
+        if constexpr (ADD) stage_rows_async(p, cf, e0.rows, e0.cols, lane, sb);
         do {
+          if constexpr (ADD) {
+            const int due = min(kTile / 64, kTile / 64 * ++chunk / chunks);
+#pragma unroll
+            for (int u = 0; u < kTile / 64; ++u) {
+              if (u < joined || u >= due) continue;
+              copy_async_wait();
+              __syncwarp();
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float4 c = *reinterpret_cast<const float4*>(sb + staged<32>(lane, i));
+                sums[u][4 * i] = __float_as_uint(fmaf(p.beta, c.x, __uint_as_float(sums[u][4 * i])));
+                sums[u][4 * i + 1] = __float_as_uint(fmaf(p.beta, c.y, __uint_as_float(sums[u][4 * i + 1])));
+                sums[u][4 * i + 2] = __float_as_uint(fmaf(p.beta, c.z, __uint_as_float(sums[u][4 * i + 2])));
+                sums[u][4 * i + 3] = __float_as_uint(fmaf(p.beta, c.w, __uint_as_float(sums[u][4 * i + 3])));
+              }
+              __syncwarp();
+              if (u + 1 < kTile / 64) stage_rows_async(p, cf + u * 32 + 32, e0.rows, e0.cols - u * 32 - 32, lane, sb);
+            }
+            joined = due;
+          }
           const int acc = it & 1;
           if (!mbar_wait(&tmem_full[acc], (it >> 1) & 1, wc)) {
+            if constexpr (ADD) copy_async_wait();
             ok = false;
             break;
           }
@@ -526,10 +549,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               tmem_ld_wait();
 #pragma unroll
               for (int j = 0; j < 16; ++j) {
+                uint32_t& sum = sums[c / 2][c % 2 * 16 + j];
                 if constexpr (I8)
-                  sums[c][j] += (uint32_t)__float2int_rn(__uint_as_float(w[j]));  // an integer of at most 2^24
+                  sum += (uint32_t)__float2int_rn(__uint_as_float(w[j]));  // an integer of at most 2^24
+                else if constexpr (ADD)
+                  sum = __float_as_uint(fmaf(p.alpha, __uint_as_float(w[j]), __uint_as_float(sum)));
                 else
-                  sums[c][j] = __float_as_uint(__uint_as_float(sums[c][j]) + __uint_as_float(w[j]));
+                  sum = __float_as_uint(__uint_as_float(sum) + __uint_as_float(w[j]));
               }
             }
           }
@@ -554,7 +580,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int h = 0; h < kUnit / 16; ++h) {
               const int s16 = u * (kUnit / 16) + h;
               float v[16];
-              scaled_values(p, sums[s16], scale, sc + s16 * 16, bias != nullptr ? bias + s16 * 16 : nullptr,
+              scaled_values(p, sums[s16 / 2] + s16 % 2 * 16, scale, sc + s16 * 16, bias != nullptr ? bias + s16 * 16 : nullptr,
                             e.cols - s16 * 16, v);
               if constexpr (F32) {
 #pragma unroll
@@ -576,43 +602,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           continue;
         }
         float* df = reinterpret_cast<float*>(e.d);
-        const float* cf = reinterpret_cast<const float*>(e.c);
 #pragma unroll
         for (int c = 0; c < kTile / 64; ++c) {
-          if constexpr (ADD) {
-            copy_async_wait();
-            __syncwarp();
-          }
-          // a lane's own row: C there, if any, gives way to D
+          const float scale = ADD ? 1.0f : p.alpha;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint32_t(&sum)[16] = sums[2 * c + (i >> 2)];
-            const int j = 4 * (i & 3);
-            float4* at = reinterpret_cast<float4*>(sb + staged<32>(lane, i));
-            float4 v = make_float4(p.alpha * __uint_as_float(sum[j]), p.alpha * __uint_as_float(sum[j + 1]),
-                                   p.alpha * __uint_as_float(sum[j + 2]), p.alpha * __uint_as_float(sum[j + 3]));
-            if constexpr (ADD) {
-              const float4 w = *at;
-              v = make_float4(fmaf(p.beta, w.x, v.x), fmaf(p.beta, w.y, v.y), fmaf(p.beta, w.z, v.z),
-                              fmaf(p.beta, w.w, v.w));
-            }
-            *at = v;
-          }
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<float4*>(sb + staged<32>(lane, i)) =
+                make_float4(scale * __uint_as_float(sums[c][4 * i]), scale * __uint_as_float(sums[c][4 * i + 1]),
+                            scale * __uint_as_float(sums[c][4 * i + 2]), scale * __uint_as_float(sums[c][4 * i + 3]));
           __syncwarp();
           copy_out<float, 4>(p, sb, df + c * 32, e.rows, e.cols - c * 32, lane);
           __syncwarp();
-          if (ADD && c + 1 < kTile / 64)
-            stage_rows_async(p, cf + c * 32 + 32, e.rows, e.cols - c * 32 - 32, lane, sb);
         }
       } else {
         const int acc = it & 1;
-        uint32_t cw[32];  // C of the next unit
-        if (ADD) copy_in(p, e0.c, e0.rows, e0.cols, lane, cw);
+        uint32_t cw[ADD ? kUnits : 1][32];
+        if constexpr (ADD) load_c(p, e0.c, e0.rows, e0.cols, lane, sb, cw);
         if (!mbar_wait(&tmem_full[acc], (it >> 1) & 1, wc)) break;
         ++it;
         tc_fence_after();
         const float* bias = !WGRAD && p.bias != nullptr ? p.bias + (int64_t)e0.g * p.stride_bias + e0.col0 : nullptr;
-#pragma unroll 1
+#pragma unroll (ADD ? kUnits : 1)
         for (int u = 0; u < kUnits; ++u) {
           uint32_t w[2][32];
           if (e0.k_blocks > 0) {
@@ -629,17 +639,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&tmem_empty[acc]), 0));
           }
           if (e0.cols <= u * kUnit) continue;
-          if constexpr (ADD) {
-            stage_rows(sb, lane, cw);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const uint4 v = *reinterpret_cast<const uint4*>(sb + staged<32>(lane, i));
-              cw[4 * i] = v.x;
-              cw[4 * i + 1] = v.y;
-              cw[4 * i + 2] = v.z;
-              cw[4 * i + 3] = v.w;
-            }
-          }
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int at = u * kUnit + h * 32, n = min(32, e0.cols - at);
@@ -648,8 +647,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (ADD) {
 #pragma unroll
               for (int j = 0; j < 16; ++j) {
-                v[2 * j] = fmaf(p.beta, half_bits_to_float<BF16>((uint16_t)(cw[h * 16 + j] & 0xFFFFu)), v[2 * j]);
-                v[2 * j + 1] = fmaf(p.beta, half_bits_to_float<BF16>((uint16_t)(cw[h * 16 + j] >> 16)), v[2 * j + 1]);
+                v[2 * j] = fmaf(p.beta, half_bits_to_float<BF16>((uint16_t)(cw[ADD ? u : 0][h * 16 + j] & 0xFFFFu)), v[2 * j]);
+                v[2 * j + 1] = fmaf(p.beta, half_bits_to_float<BF16>((uint16_t)(cw[ADD ? u : 0][h * 16 + j] >> 16)), v[2 * j + 1]);
               }
             }
 #pragma unroll
@@ -658,8 +657,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                   make_uint4(pack2<BF16>(v[8 * ch], v[8 * ch + 1]), pack2<BF16>(v[8 * ch + 2], v[8 * ch + 3]),
                              pack2<BF16>(v[8 * ch + 4], v[8 * ch + 5]), pack2<BF16>(v[8 * ch + 6], v[8 * ch + 7]));
           }
-          if (ADD && u + 1 < kUnits)
-            copy_in(p, e0.c + (u + 1) * kUnit, e0.rows, e0.cols - (u + 1) * kUnit, lane, cw);
           __syncwarp();
           copy_out<T, 4>(p, sb, e0.d + u * kUnit, e0.rows, e0.cols - u * kUnit, lane);
           __syncwarp();
