@@ -234,37 +234,38 @@ __device__ __forceinline__ EpiTile<T> epi_tile(const GroupedParams& p, const Gro
   return e;
 }
 
-// Sixteen int8 sums of a row, scaled: columns sc, bias on, `n` of them inside D.
-__device__ __forceinline__ void scaled_values(const GroupedParams& p, const uint32_t* sums, float scale,
-                                              const float* sc, const float* bias, int n, float (&v)[16]) {
+// A lane's four of the warp's 128 columns, zeros outside `n` columns.
+__device__ __forceinline__ float4 four_columns(const float* c0, int lane, int n) {
+  const float* c = c0 + lane * 4;
+  n -= lane * 4;
+  if (n >= 4 && (reinterpret_cast<uintptr_t>(c) & 15) == 0) return __ldg(reinterpret_cast<const float4*>(c));
+  return make_float4(n > 0 ? __ldg(c) : 0.0f, n > 1 ? __ldg(c + 1) : 0.0f, n > 2 ? __ldg(c + 2) : 0.0f,
+                     n > 3 ? __ldg(c + 3) : 0.0f);
+}
+
+// Sixteen sums of a row (columns s16 * 16 on), scaled: each lane has four columns'
+// scales and biases and hands them round.  Loaded where they are used, they cost
+// the epilogue a wait for L2 every sixteen columns (10.5 us a tile of 256 x 256
+// x 560 in place of 7).
+__device__ __forceinline__ void scaled_values(const GroupedParams& p, const uint32_t* sums, float scale, float4 sc,
+                                              float4 bias, int s16, float (&v)[16]) {
 #pragma unroll
-  for (int j = 0; j < 16; ++j) v[j] = __int2float_rn((int32_t)sums[j]) * scale;
-  if (n >= 16 && ((reinterpret_cast<uintptr_t>(sc) | reinterpret_cast<uintptr_t>(bias)) & 15) == 0) {
+  for (int i = 0; i < 4; ++i) {
+    const int src = s16 * 4 + i;
+    const float w[4] = {__shfl_sync(0xFFFFFFFFu, sc.x, src), __shfl_sync(0xFFFFFFFFu, sc.y, src),
+                        __shfl_sync(0xFFFFFFFFu, sc.z, src), __shfl_sync(0xFFFFFFFFu, sc.w, src)};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[4 * i + k] = __uint_as_float(sums[4 * i + k]) * scale * w[k];
+  }
+  if (p.bias != nullptr) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float4 w = __ldg(reinterpret_cast<const float4*>(sc) + i);
-      v[4 * i] *= w.x;
-      v[4 * i + 1] *= w.y;
-      v[4 * i + 2] *= w.z;
-      v[4 * i + 3] *= w.w;
+      const int src = s16 * 4 + i;
+      v[4 * i] += __shfl_sync(0xFFFFFFFFu, bias.x, src);
+      v[4 * i + 1] += __shfl_sync(0xFFFFFFFFu, bias.y, src);
+      v[4 * i + 2] += __shfl_sync(0xFFFFFFFFu, bias.z, src);
+      v[4 * i + 3] += __shfl_sync(0xFFFFFFFFu, bias.w, src);
     }
-    if (bias != nullptr) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float4 w = __ldg(reinterpret_cast<const float4*>(bias) + i);
-        v[4 * i] += w.x;
-        v[4 * i + 1] += w.y;
-        v[4 * i + 2] += w.z;
-        v[4 * i + 3] += w.w;
-      }
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 16; ++j)
-      if (j < n) {
-        v[j] *= __ldg(sc + j);
-        if (bias != nullptr) v[j] += __ldg(bias + j);
-      }
   }
   if (p.act != kActNone) {
 #pragma unroll
@@ -499,7 +500,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int t = pair; ok && t < tiles; t += num_pairs) {
       const EpiTile<T> e0 = epi_tile<WGRAD, T>(p, grouped_tile<kTile, WGRAD>(p, tb, t), rank, q, part);
       if constexpr (kSums) {
-        // floats (int8: int32): this thread's row of the warp's 128 columns
+        // floats (int8 with more than one accumulator: int32): this thread's row of the
+        // warp's 128 columns
         uint32_t sums[kTile / 64][32];
 #pragma unroll
         for (int c = 0; c < kTile / 64; ++c)
@@ -541,7 +543,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             break;
           }
           tc_fence_after();
-          if (k_blocks > 0) {
+          if (I8 && k_blocks <= kChunkKBlocks<I8>) {
+            // one accumulator: its values are the sums, whole numbers in fp32
+#pragma unroll
+            for (int c = 0; c < kTile / 64; ++c) tmem_ld_32x32b_x32(tmem_mine + acc * kTile + c * 32, sums[c]);
+            tmem_ld_wait();
+          } else if (k_blocks > 0) {
 #pragma unroll
             for (int c = 0; c < kTile / 32; ++c) {
               uint32_t w[16];
@@ -572,16 +579,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const EpiTile<T> e = epi_tile<WGRAD, T>(p, grouped_tile<kTile, WGRAD>(p, tb, t_again), rank, q, part);
         if constexpr (I8) {
           const float scale = lane < e.rows ? __ldg(p.scale_a + e.row + lane) : 0.0f;
-          const float* sc = p.scale_b + e.col0;
-          const float* bias = p.bias != nullptr ? p.bias + e.col0 : nullptr;
+          const float4 sc = four_columns(p.scale_b + e.col0, lane, e.cols);
+          const float4 bias =
+              p.bias != nullptr ? four_columns(p.bias + e.col0, lane, e.cols) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (k_blocks > kChunkKBlocks<I8>) {
+#pragma unroll
+            for (int c = 0; c < kTile / 64; ++c)
+#pragma unroll
+              for (int j = 0; j < 32; ++j) sums[c][j] = __float_as_uint(__int2float_rn((int32_t)sums[c][j]));
+          }
 #pragma unroll
           for (int u = 0; u < kUnits; ++u) {
 #pragma unroll
             for (int h = 0; h < kUnit / 16; ++h) {
               const int s16 = u * (kUnit / 16) + h;
               float v[16];
-              scaled_values(p, sums[s16 / 2] + s16 % 2 * 16, scale, sc + s16 * 16, bias != nullptr ? bias + s16 * 16 : nullptr,
-                            e.cols - s16 * 16, v);
+              scaled_values(p, sums[s16 / 2] + s16 % 2 * 16, scale, sc, bias, s16, v);
               if constexpr (F32) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
