@@ -126,27 +126,30 @@ __device__ __forceinline__ GroupedTile grouped_tile(const GroupedParams& p, cons
   return x;
 }
 
-// 32 values of a row (`n` of them inside D) from their accumulator: alpha, bias,
-// activation.
-template <bool BF16>
-__device__ __forceinline__ void grouped_values(const GroupedParams& p, const uint32_t (&r)[32], const float* bias, int n,
+// A lane's four of the warp's 128 columns, zeros outside `n` columns.
+__device__ __forceinline__ float4 four_columns(const float* c0, int lane, int n) {
+  const float* c = c0 + lane * 4;
+  n -= lane * 4;
+  if (n >= 4 && (reinterpret_cast<uintptr_t>(c) & 15) == 0) return __ldg(reinterpret_cast<const float4*>(c));
+  return make_float4(n > 0 ? __ldg(c) : 0.0f, n > 1 ? __ldg(c + 1) : 0.0f, n > 2 ? __ldg(c + 2) : 0.0f,
+                     n > 3 ? __ldg(c + 3) : 0.0f);
+}
+
+// 32 values of a row (columns s32 * 32 on of the warp's 128) from their
+// accumulator: alpha, bias, activation.  Each lane has four columns' biases and
+// hands them round: loaded here they would cost a wait for L2 each time.
+__device__ __forceinline__ void grouped_values(const GroupedParams& p, const uint32_t (&r)[32], float4 bias, int s32,
                                                float (&v)[32]) {
 #pragma unroll
   for (int j = 0; j < 32; ++j) v[j] = p.alpha * __uint_as_float(r[j]);
-  if (bias != nullptr) {
-    if (n >= 32 && (reinterpret_cast<uintptr_t>(bias) & 15) == 0) {
+  if (p.bias != nullptr) {
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const float4 w = __ldg(reinterpret_cast<const float4*>(bias) + u);
-        v[4 * u] += w.x;
-        v[4 * u + 1] += w.y;
-        v[4 * u + 2] += w.z;
-        v[4 * u + 3] += w.w;
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if (j < n) v[j] += __ldg(bias + j);
+    for (int i = 0; i < 8; ++i) {
+      const int src = s32 * 8 + i;
+      v[4 * i] += __shfl_sync(0xFFFFFFFFu, bias.x, src);
+      v[4 * i + 1] += __shfl_sync(0xFFFFFFFFu, bias.y, src);
+      v[4 * i + 2] += __shfl_sync(0xFFFFFFFFu, bias.z, src);
+      v[4 * i + 3] += __shfl_sync(0xFFFFFFFFu, bias.w, src);
     }
   }
   if (p.act != kActNone) {

@@ -234,15 +234,6 @@ __device__ __forceinline__ EpiTile<T> epi_tile(const GroupedParams& p, const Gro
   return e;
 }
 
-// A lane's four of the warp's 128 columns, zeros outside `n` columns.
-__device__ __forceinline__ float4 four_columns(const float* c0, int lane, int n) {
-  const float* c = c0 + lane * 4;
-  n -= lane * 4;
-  if (n >= 4 && (reinterpret_cast<uintptr_t>(c) & 15) == 0) return __ldg(reinterpret_cast<const float4*>(c));
-  return make_float4(n > 0 ? __ldg(c) : 0.0f, n > 1 ? __ldg(c + 1) : 0.0f, n > 2 ? __ldg(c + 2) : 0.0f,
-                     n > 3 ? __ldg(c + 3) : 0.0f);
-}
-
 // Sixteen sums of a row (columns s16 * 16 on), scaled: each lane has four columns'
 // scales and biases and hands them round.  Loaded where they are used, they cost
 // the epilogue a wait for L2 every sixteen columns (10.5 us a tile of 256 x 256
@@ -629,12 +620,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       } else {
         const int acc = it & 1;
+        float4 bias = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (!WGRAD && p.bias != nullptr)
+          bias = four_columns(p.bias + (int64_t)e0.g * p.stride_bias + e0.col0, lane, e0.cols);
         uint32_t cw[ADD ? kUnits : 1][32];
         if constexpr (ADD) load_c(p, e0.c, e0.rows, e0.cols, lane, sb, cw);
         if (!mbar_wait(&tmem_full[acc], (it >> 1) & 1, wc)) break;
         ++it;
         tc_fence_after();
-        const float* bias = !WGRAD && p.bias != nullptr ? p.bias + (int64_t)e0.g * p.stride_bias + e0.col0 : nullptr;
 #pragma unroll (ADD ? kUnits : 1)
         for (int u = 0; u < kUnits; ++u) {
           uint32_t w[2][32];
@@ -654,9 +647,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (e0.cols <= u * kUnit) continue;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const int at = u * kUnit + h * 32, n = min(32, e0.cols - at);
             float v[32];
-            grouped_values<BF16>(p, w[h], bias != nullptr && n > 0 ? bias + at : nullptr, n, v);
+            grouped_values(p, w[h], bias, u * 2 + h, v);
             if (ADD) {
 #pragma unroll
               for (int j = 0; j < 16; ++j) {

@@ -108,7 +108,8 @@ __device__ __forceinline__ void drain_tiles(const GroupedParams& p, const GroupT
     T* d = static_cast<T*>(p.D) + (WGRAD ? (int64_t)x.g * p.strideD : 0) + row0 * p.ldd + col0;
     const T* c = WGRAD && p.C != nullptr ? static_cast<const T*>(p.C) + (int64_t)x.g * p.strideC + row0 * p.ldc + col0
                                          : nullptr;
-    const float* bias = !WGRAD && p.bias != nullptr ? p.bias + (int64_t)x.g * p.stride_bias + col0 : nullptr;
+    float4 bias = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (!WGRAD && p.bias != nullptr) bias = four_columns(p.bias + (int64_t)x.g * p.stride_bias + col0, lane, p.N - col0);
     if (!mbar_wait(&tmem_full[acc], (it >> 1) & 1, wc)) break;
     tc_fence_after();
 #pragma unroll 1
@@ -140,7 +141,7 @@ __device__ __forceinline__ void drain_tiles(const GroupedParams& p, const GroupT
           for (int j = 0; j < 32; ++j) w[j] = 0u;
         }
         float v[32];
-        grouped_values<BF16>(p, w, bias != nullptr && n > h ? bias + at + h : nullptr, n - h, v);
+        grouped_values(p, w, bias, (at + h) / 32, v);
 #pragma unroll
         for (int i = 0; i < 32 / kPer; ++i) {
           uint4* piece = reinterpret_cast<uint4*>(sb + staged<32>(lane, h / kPer + i));
