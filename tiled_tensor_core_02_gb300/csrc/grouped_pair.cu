@@ -45,6 +45,10 @@
 // rows by the stage's 128 k, so that a stage takes as few TMA instructions as
 // one with K contiguous: with a box per k-block the issuing thread, at about 70 ns
 // an instruction, set the pace.
+//
+// Bound by the tensor cores, at clocks that the power cap holds to 1.5 to 1.6 GHz:
+// 16384 x 4096 x 4096 bf16 over 8 equal groups 305 us forward, 300 for the weights'
+// gradient in bf16 and 335 in fp32; int8 8192 x 14336 x 4096 566 us with its copies.
 #include <atomic>
 #include <type_traits>
 
