@@ -68,25 +68,33 @@ bool pair_maps(GroupedParams& p, bool wgrad, ttc_dtype dtype, const HostEnv& env
                  : encode_matrices(&p.tmB, dt, 2, p.B, p.K, p.N, p.ldb, mats, p.strideB, kBK, 128, sw));
 }
 
-// Output columns of a few-token tile: as many as make the tiles of `rows` weights'
-// rows fill whole waves of SMs, in steps of 8 up to 128 (of more than three waves
-// the last one costs less than narrower tiles do: 64 groups, 4099 x 1536 x 2048 79.6
-// us with 128 columns, 84.8 with 112); with the columns contiguous in memory (TMA
-// boxes of 64) 64 or 128.
-int few_tile_cols(int64_t rows, int sm_count, bool cols_contiguous) {
-  const int64_t waves = blocks_of(rows, 128ll * sm_count);
-  const int64_t c = waves > 3 ? 128 : blocks_of(blocks_of(rows, waves * sm_count), 8) * 8;
+// Output columns of a few-token tile: as few, in steps of 8 up to 128, as let the
+// tiles of `blocks` blocks of tokens fill whole waves of SMs (of more than three
+// waves the last one costs less than narrower tiles do: 64 groups, 4099 x 1536 x 2048
+// 79.6 us with 128 columns, 84.8 with 112); with the columns contiguous in memory
+// (TMA boxes of 64) 64 or 128.
+int few_tile_cols(int64_t blocks, int64_t n, int sm_count, bool cols_contiguous) {
+  int64_t c = 128;
+  for (int64_t waves = 1; waves <= 3; ++waves) {
+    const int64_t room = waves * sm_count / blocks;  // tiles of a block of tokens
+    if (room < 1 || blocks_of(n, room) > 128) continue;
+    c = blocks_of(blocks_of(n, room), 8) * 8;
+    break;
+  }
   if (cols_contiguous) return c > 64 ? 128 : 64;
-  return (int)(c < 8 ? 8 : c > 128 ? 128 : c);
+  return (int)c;
 }
 
 // Sets up the few-token kernel's tiles and tensor maps; false where TMA cannot
 // read the operands or no pipeline fits.  `matrices`: how many weight matrices
-// are likely to be read.
+// are likely to be read.  Groups near the mean take one block more as often as not
+// (256 rows of 4 groups, 1088 x 1040: tiles for four blocks 16.0 us, for six 11.1).
 bool few_maps(GroupedParams& p, ttc_dtype dtype, int tokens, int64_t matrices, const HostEnv& env) {
   if (env.plain_loads || p.M == 0 || p.K == 0) return false;
   if (!tma_rows_ok(p.A, p.lda, 2) || !tma_rows_ok(p.B, p.ldb, 2) || !tma_stride_ok(p.groups, p.strideB, 2)) return false;
-  p.tile_cols = few_tile_cols(matrices * p.N, env.sm_count, p.b_mn != 0);
+  const int64_t whole = blocks_of(blocks_of(p.M, matrices), tokens) * matrices;
+  const int64_t half_more = blocks_of(2 * p.M + tokens * matrices, 2 * tokens);
+  p.tile_cols = few_tile_cols(whole > half_more ? whole : half_more, p.N, env.sm_count, p.b_mn != 0);
   p.col_blocks = (int)blocks_of(p.N, p.tile_cols);
   if ((blocks_of(p.M, tokens) + p.groups) * p.col_blocks > kSizeLimit) return false;
   p.b_stream = p.M <= matrices * tokens;
