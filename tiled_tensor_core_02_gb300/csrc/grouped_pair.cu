@@ -37,6 +37,10 @@
 // int8 value is exact in fp16, every product and sum below 2^24 in fp32): one
 // group, an accumulator for every 1024 of K, the partial sums added up as int32.
 //
+// Where two halves of each of the last wave's tiles find a pair, the wave takes them
+// as halves of 128 columns: half the MMA's time and half the epilogue (1120 rows of 7
+// groups, 896 x 2944 20.7 -> 17.6 us; long walks at capped clocks gain nothing).
+//
 // Results leave through a 4 KB block of shared memory per epilogue warp, 32 rows
 // of 128 bytes: written a row per lane, read back and stored four whole rows an
 // instruction, with no asynchronous copy to wait for and any row left out.
@@ -83,9 +87,36 @@ constexpr int kEpiWarp0 = 4;
 constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarpCount);
 
 // A stage's k-blocks (0 to 2), the steps of 16 in its last one where that is
-// the tile's last, and whether it is.
-__device__ __forceinline__ int stage_word(int nkb, int last_steps, bool last) {
-  return nkb | (last ? last_steps << 4 | 256 : (kBK / kUmmaK) << 4);
+// the tile's last, whether it is, and whether the tile is half a tile.
+__device__ __forceinline__ int stage_word(int nkb, int last_steps, bool last, bool narrow) {
+  return nkb | (last ? last_steps << 4 | 256 : (kBK / kUmmaK) << 4) | (narrow ? 512 : 0);
+}
+
+// What the pairs take in turn: `whole` tiles, then halves of tiles.
+struct PairWalk {
+  int whole, items;
+};
+__device__ __forceinline__ PairWalk pair_walk(int tiles, int pairs) {
+  const int rest = tiles % pairs;
+  PairWalk w{tiles, tiles};
+  if (2 * rest <= pairs) {
+    w.whole = tiles - rest;
+    w.items = tiles + rest;
+  }
+  return w;
+}
+
+struct PairItem {
+  GroupedTile x;
+  int half;  // of the tile's columns; -1: all of them
+};
+template <bool WGRAD>
+__device__ __forceinline__ PairItem pair_item(const GroupedParams& p, const GroupTable& tb, const PairWalk& w, int t) {
+  const int over = t - w.whole;
+  PairItem it;
+  it.half = over < 0 ? -1 : over & 1;
+  it.x = grouped_tile<kTile, WGRAD>(p, tb, over < 0 ? t : w.whole + (over >> 1));
+  return it;
 }
 
 struct PairLoop {
@@ -150,40 +181,36 @@ __device__ __forceinline__ void load_c(const GroupedParams& p, const T* c0, int 
                                        uint32_t (&w)[N][32]) {
   constexpr int kElems = 16 / (int)sizeof(T), kCols = 128 / (int)sizeof(T);
   const int piece = lane & 7, r0 = lane >> 3;
-  if (p.c_vec && n >= N * kCols) {
-    const T* src = c0 + (int64_t)r0 * p.ldc + piece * kElems;
+  const T* src = c0 + (int64_t)r0 * p.ldc + piece * kElems;
 #pragma unroll
-    for (int i = 0; i < 8; ++i, src += 4 * p.ldc)
-#pragma unroll
-      for (int u = 0; u < N; ++u) {
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (i * 4 + r0 < rows) v = *reinterpret_cast<const uint4*>(src + u * kCols);
-        w[u][4 * i] = v.x;
-        w[u][4 * i + 1] = v.y;
-        w[u][4 * i + 2] = v.z;
-        w[u][4 * i + 3] = v.w;
-      }
+  for (int i = 0; i < 8; ++i, src += 4 * p.ldc)
 #pragma unroll
     for (int u = 0; u < N; ++u) {
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (p.c_vec && n >= (u + 1) * kCols && i * 4 + r0 < rows) v = *reinterpret_cast<const uint4*>(src + u * kCols);
+      w[u][4 * i] = v.x;
+      w[u][4 * i + 1] = v.y;
+      w[u][4 * i + 2] = v.z;
+      w[u][4 * i + 3] = v.w;
+    }
+#pragma unroll
+  for (int u = 0; u < N; ++u) {
+    if (n <= u * kCols) continue;  // zeros, if they were used
+    if (p.c_vec && n >= (u + 1) * kCols) {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         *reinterpret_cast<uint4*>(sb + staged<32>(i * 4 + r0, piece)) =
             make_uint4(w[u][4 * i], w[u][4 * i + 1], w[u][4 * i + 2], w[u][4 * i + 3]);
-      __syncwarp();
-      row_of_block(sb, lane, w[u]);
-    }
-  } else {
-#pragma unroll
-    for (int u = 0; u < N; ++u) {
+    } else {
 #pragma unroll 1
       for (int c = lane; c < kCols; c += 32)
 #pragma unroll 1
         for (int r = 0; r < 32; ++r)
           *reinterpret_cast<T*>(sb + staged<32>(r, c / kElems) + (c % kElems) * sizeof(T)) =
               r < rows && u * kCols + c < n ? c0[(int64_t)r * p.ldc + u * kCols + c] : T{};
-      __syncwarp();
-      row_of_block(sb, lane, w[u]);
     }
+    __syncwarp();
+    row_of_block(sb, lane, w[u]);
   }
 }
 
@@ -210,28 +237,31 @@ __device__ __forceinline__ void stage_rows_async(const GroupedParams& p, const f
   }
 }
 
-// What an epilogue warp has of a tile: 32 rows by 128 columns.
+// What an epilogue warp has of a tile: 32 rows by 128 columns (of half a tile 64).
 template <typename T>
 struct EpiTile {
   T* d;        // its first element of D, and of C (null without C)
   const T* c;
   int g, col0;
+  int at;       // the accumulator's column of col0
   int64_t row;  // its first row of D
-  int rows, cols;  // rows inside the group (wgrad: inside D); columns of D from col0 on
+  int rows, cols;  // rows inside the group (wgrad: inside D); columns of the tile inside D, from col0 on
   int k_blocks;
 };
 
 template <bool WGRAD, typename T>
-__device__ __forceinline__ EpiTile<T> epi_tile(const GroupedParams& p, const GroupedTile& x, uint32_t rank, int q,
+__device__ __forceinline__ EpiTile<T> epi_tile(const GroupedParams& p, const PairItem& item, uint32_t rank, int q,
                                                int part) {
+  const GroupedTile& x = item.x;
   EpiTile<T> e;
   const int r0 = x.rb * kTile + (int)rank * 128 + q * 32;
   const int64_t row0 = WGRAD ? r0 : (int64_t)x.lo + r0;
   e.g = x.g;
-  e.col0 = x.cb * kTile + part * (kTile / 2);
+  e.at = part * (item.half < 0 ? kTile / 2 : kTile / 4);
+  e.col0 = x.cb * kTile + max(item.half, 0) * (kTile / 2) + e.at;
   e.row = row0;
   e.rows = max(0, min(32, WGRAD ? p.K - r0 : x.hi - x.lo - r0));
-  e.cols = p.N - e.col0;
+  e.cols = min(p.N - e.col0, item.half < 0 ? kTile / 2 : kTile / 4);
   e.d = static_cast<T*>(p.D) + (WGRAD ? (int64_t)x.g * p.strideD : 0) + row0 * p.ldd + e.col0;
   e.c = WGRAD && p.C != nullptr ? static_cast<const T*>(p.C) + (int64_t)x.g * p.strideC + row0 * p.ldc + e.col0 : nullptr;
   e.k_blocks = pair_loop<WGRAD>(p, x).k_blocks;
@@ -341,7 +371,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   grid_dependency_wait();
   grid_dependents_launch();
   build_group_table<kTile>(p, tb);
-  const int tiles = WGRAD ? p.groups * p.row_blocks * p.col_blocks : table_tiles(p, tb);
+  const PairWalk walk = pair_walk(WGRAD ? p.groups * p.row_blocks * p.col_blocks : table_tiles(p, tb), num_pairs);
 
   if (warp == 0) {
     // ---------------------------------------------------------------- producer (both CTAs)
@@ -353,10 +383,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       uint32_t armed = 0, armed_parity = 0;          // stages armed on `full` (even CTA)
       uint32_t fixed = 0, fix_parity = 0, fix_phase = 0;  // stages armed on `fix`
       bool ok = true;
-      for (int t = pair; ok && t < tiles; t += num_pairs) {
-        const GroupedTile x = grouped_tile<kTile, WGRAD>(p, tb, t);
+      for (int t = pair; ok && t < walk.items; t += num_pairs) {
+        const PairItem item = pair_item<WGRAD>(p, tb, walk, t);
+        const GroupedTile& x = item.x;
         const PairLoop l = pair_loop<WGRAD>(p, x);
-        const int n0 = x.cb * kTile + (int)rank * 128;
+        // of half a tile the MMA reads 64 columns, the first of the 128 that are loaded
+        const int n0 = x.cb * kTile + (item.half < 0 ? (int)rank * 128 : item.half * 128 + (int)rank * 64);
         const int m0 = (WGRAD ? 0 : x.lo) + x.rb * kTile + (int)rank * 128;
         // forward: whether this CTA's, and the other's, rows of A hold any of the group
         const bool a_on = WGRAD || m0 < x.hi;
@@ -369,7 +401,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             ok = false;
             break;
           }
-          if (leader) stage_info[stage] = stage_word(nkb, l.last_steps, kb0 + nkb >= l.k_blocks);
+          if (leader) stage_info[stage] = stage_word(nkb, l.last_steps, kb0 + nkb >= l.k_blocks, item.half >= 0);
           const bool b_mn = WGRAD || p.b_mn;
           const int bytes_a = nkb > 0 ? share_bytes(WGRAD, nkb) : 0, bytes_b = nkb > 0 ? share_bytes(b_mn, nkb) : 0;
           const bool clear = WGRAD && l.fix_rows != 0 && kb0 + nkb == l.k_blocks;
@@ -417,7 +449,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // ---------------------------------------------------------------- MMA issuer (even CTA)
     if (leader && lane == 0) {
       const bool b_mn = WGRAD || p.b_mn != 0;
-      const uint32_t idesc = idesc_f16(BF16 && !I8, WGRAD, b_mn, kTile, kTile);
+      const uint32_t idesc_whole = idesc_f16(BF16 && !I8, WGRAD, b_mn, kTile, kTile);
+      const uint32_t idesc_half = idesc_f16(BF16 && !I8, WGRAD, b_mn, kTile, kTile / 2);
       const uint64_t a0 = smem_desc_sw128(smem_u32(sA), WGRAD ? (uint32_t)kHalfBytes : 16u, 1024);
       const uint64_t b0 = smem_desc_sw128(smem_u32(sB), b_mn ? (uint32_t)kHalfBytes : 16u, 1024);
       const uint64_t a_step = WGRAD ? 2048u >> 4 : 32u >> 4, b_step = b_mn ? 2048u >> 4 : 32u >> 4;
@@ -429,7 +462,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       uint32_t phase = 0;
       bool ready = true;  // whether the next accumulator is known to be free
       // the first use of each accumulator passes at once
-      for (int t = pair; ok && t < tiles; t += num_pairs) {
+      for (int t = pair; ok && t < walk.items; t += num_pairs) {
         bool last = false;
         do {  // an accumulator: the tile's, or a chunk of it
           const int acc = it & 1;
@@ -450,6 +483,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int info = stage_info[stage];
             const int nkb = info & 15, steps = (info >> 4) & 15;
             last = (info & 256) != 0;
+            const uint32_t idesc = (info & 512) != 0 ? idesc_half : idesc_whole;
             tc_fence_after();
 #pragma unroll
             for (int j = 0; j < kKPS; ++j) {
@@ -489,11 +523,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     constexpr int kUnit = 128 / (int)sizeof(T);    // columns that 128 bytes hold
     constexpr int kUnits = kTile / 2 / kUnit;      // of this warp
     uint8_t* sb = staging + ew * 4096;
-    const uint32_t tmem_mine = tmem_base + ((uint32_t)(q * 32) << 16) + part * (kTile / 2);
+    const uint32_t tmem_mine = tmem_base + ((uint32_t)(q * 32) << 16);
     int it = 0;
     bool ok = true;
-    for (int t = pair; ok && t < tiles; t += num_pairs) {
-      const EpiTile<T> e0 = epi_tile<WGRAD, T>(p, grouped_tile<kTile, WGRAD>(p, tb, t), rank, q, part);
+    for (int t = pair; ok && t < walk.items; t += num_pairs) {
+      const EpiTile<T> e0 = epi_tile<WGRAD, T>(p, pair_item<WGRAD>(p, tb, walk, t), rank, q, part);
       if constexpr (kSums) {
         // floats (int8 with more than one accumulator: int32): this thread's row of the
         // warp's 128 columns
@@ -541,13 +575,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (I8 && k_blocks <= kChunkKBlocks<I8>) {
             // one accumulator: its values are the sums, whole numbers in fp32
 #pragma unroll
-            for (int c = 0; c < kTile / 64; ++c) tmem_ld_32x32b_x32(tmem_mine + acc * kTile + c * 32, sums[c]);
+            for (int c = 0; c < kTile / 64; ++c) tmem_ld_32x32b_x32(tmem_mine + e0.at + acc * kTile + c * 32, sums[c]);
             tmem_ld_wait();
           } else if (k_blocks > 0) {
 #pragma unroll
             for (int c = 0; c < kTile / 32; ++c) {
               uint32_t w[16];
-              tmem_ld_32x32b_x16<0>(tmem_mine + acc * kTile + c * 16, w);
+              tmem_ld_32x32b_x16<0>(tmem_mine + e0.at + acc * kTile + c * 16, w);
               tmem_ld_wait();
 #pragma unroll
               for (int j = 0; j < 16; ++j) {
@@ -571,7 +605,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // found again rather than kept: the sums leave no registers for it
         int t_again = t;
         asm volatile("" : "+r"(t_again));
-        const EpiTile<T> e = epi_tile<WGRAD, T>(p, grouped_tile<kTile, WGRAD>(p, tb, t_again), rank, q, part);
+        const EpiTile<T> e = epi_tile<WGRAD, T>(p, pair_item<WGRAD>(p, tb, walk, t_again), rank, q, part);
         if constexpr (I8) {
           const float scale = lane < e.rows ? __ldg(p.scale_a + e.row + lane) : 0.0f;
           const float4 sc = four_columns(p.scale_b + e.col0, lane, e.cols);
@@ -636,8 +670,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int u = 0; u < kUnits; ++u) {
           uint32_t w[2][32];
           if (e0.k_blocks > 0) {
-            tmem_ld_32x32b_x32(tmem_mine + acc * kTile + u * kUnit, w[0]);
-            tmem_ld_32x32b_x32(tmem_mine + acc * kTile + u * kUnit + 32, w[1]);
+            tmem_ld_32x32b_x32(tmem_mine + e0.at + acc * kTile + u * kUnit, w[0]);
+            tmem_ld_32x32b_x32(tmem_mine + e0.at + acc * kTile + u * kUnit + 32, w[1]);
             tmem_ld_wait();
           } else {
 #pragma unroll
@@ -677,9 +711,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int stage = 0;
     uint32_t fix_phase = 0;
     bool ok = true;
-    for (int t = pair; ok && t < tiles; t += num_pairs) {
-      const GroupedTile x = grouped_tile<kTile, WGRAD>(p, tb, t);
-      const PairLoop l = pair_loop<WGRAD>(p, x);
+    for (int t = pair; ok && t < walk.items; t += num_pairs) {
+      const PairLoop l = pair_loop<WGRAD>(p, pair_item<WGRAD>(p, tb, walk, t).x);
       const int stages = max(1, (l.k_blocks + kKPS - 1) / kKPS);
       if (l.fix_rows != 0) {
         const int s = (stage + stages - 1) % kStages;

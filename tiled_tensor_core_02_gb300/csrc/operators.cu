@@ -264,7 +264,7 @@ ttc_status ttc_gemm_grouped(int64_t groups, int64_t M, int64_t N, int64_t K, con
     p.group_rows = 8;
     p.b_stream = M <= groups * kGroupedPairTile;
     const int64_t tiles = (blocks_of(M, kGroupedPairTile) + (groups < M ? groups : M)) * p.col_blocks;
-    if (launch_grouped_pair(dtype == TTC_BF16, false, p, (int)(tiles < clusters ? tiles : clusters),
+    if (launch_grouped_pair(dtype == TTC_BF16, false, p, (int)(2 * tiles < clusters ? 2 * tiles : clusters),
                             static_cast<cudaStream_t>(stream)) != cudaSuccess)
       return TTC_ERR_CUDA;
     count_launches(1);
@@ -336,7 +336,7 @@ ttc_status ttc_gemm_grouped_wgrad(int64_t groups, int64_t M, int64_t N, int64_t 
     p.col_blocks = (int)blocks_of(N, kGroupedPairTile);
     p.group_rows = 8;
     const int64_t tiles = groups * p.row_blocks * p.col_blocks;
-    if (launch_grouped_pair(dtype == TTC_BF16, true, p, (int)(tiles < clusters ? tiles : clusters),
+    if (launch_grouped_pair(dtype == TTC_BF16, true, p, (int)(2 * tiles < clusters ? 2 * tiles : clusters),
                             static_cast<cudaStream_t>(stream)) != cudaSuccess)
       return TTC_ERR_CUDA;
     count_launches(1);
@@ -455,7 +455,7 @@ ttc_status ttc_gemm_i8_scaled(int64_t M, int64_t N, int64_t K, const int8_t* A, 
       f.d_vec = aligned(D, 16) && ldd * esize % 16 == 0;
       const int64_t tiles = blocks_of(M, kGroupedPairTile) * f.col_blocks;
       if (launch_widen_i8(specs, 2, env.sm_count, s) != cudaSuccess ||
-          launch_pair_i8_scaled(out == kI8ResultBF16, f, (int)(tiles < clusters ? tiles : clusters), s) != cudaSuccess)
+          launch_pair_i8_scaled(out == kI8ResultBF16, f, (int)(2 * tiles < clusters ? 2 * tiles : clusters), s) != cudaSuccess)
         return TTC_ERR_CUDA;
       count_launches(2);
       return TTC_OK;
