@@ -197,11 +197,18 @@ __global__ void __launch_bounds__(kThreads, 1) few_tokens_kernel(const __grid_co
         tc_fence_after();
         const uint64_t wd = w0 + (uint32_t)(stage * stage_bytes >> 4);
         const uint64_t ad = a0 + (uint32_t)(stage * stage_bytes >> 4);
+        const uint32_t add = ks != 0;
+        if (steps == kStageK / kUmmaK) {  // no condition between the MMAs: each would cost as much as one
+          mma_f16_lead(lead, d, wd, ad, idesc, add);
 #pragma unroll
-        for (int k = 0; k < kStageK / kUmmaK; ++k)
-          if (k < steps)
+          for (int k = 1; k < kStageK / kUmmaK; ++k)
+            mma_f16_lead(lead, d, wd + (k >> 2) * w_kb + (k & 3) * w_step, ad + (k >> 2) * kTokenKb + (k & 3) * 2u, idesc, 1u);
+        } else {
+#pragma unroll 1
+          for (int k = 0; k < steps; ++k)
             mma_f16_lead(lead, d, wd + (k >> 2) * w_kb + (k & 3) * w_step, ad + (k >> 2) * kTokenKb + (k & 3) * 2u, idesc,
-                         (ks | k) != 0);
+                         add | (k != 0 ? 1u : 0u));
+        }
         any = true;
         mma_commit_lead(lead, &empty[stage]);
         if (++stage == S) {

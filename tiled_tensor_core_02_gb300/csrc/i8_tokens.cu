@@ -161,11 +161,18 @@ __global__ void __launch_bounds__(kThreads, 1) i8_tokens_kernel(const __grid_con
       const uint32_t d = tmem_base + (n / kAccStages) * BT;
       const uint32_t w = tmem_base + kI8TokenCols + g * (kI8TokenStage / 2);
       const uint64_t x = x0 + (uint32_t)(g * kSlotBytes >> 4);
+      const uint32_t add = n % kAccStages != 0;
+      if (steps == kI8TokenStage / kUmmaK) {
+        // without a condition between them an MMA takes 16 clocks to issue, with one 57
+        mma_f16_ta_lead(lead, d, w, x, idesc, add);
 #pragma unroll
-      for (int k = 0; k < kI8TokenStage / kUmmaK; ++k)
-        if (k < steps)
-          mma_f16_ta_lead(lead, d, w + 8 * k, x + (k >> 2) * kTokenKb + (k & 3) * 2u, idesc,
-                          (n % kAccStages != 0) || k != 0);
+        for (int k = 1; k < kI8TokenStage / kUmmaK; ++k)
+          mma_f16_ta_lead(lead, d, w + 8 * k, x + (k >> 2) * kTokenKb + (k & 3) * 2u, idesc, 1u);
+      } else {
+#pragma unroll 1
+        for (int k = 0; k < steps; ++k)
+          mma_f16_ta_lead(lead, d, w + 8 * k, x + (k >> 2) * kTokenKb + (k & 3) * 2u, idesc, add | (k != 0 ? 1u : 0u));
+      }
       mma_commit_lead(lead, &wide_empty[g]);
       if (++g == kGroups) {
         g = 0;
