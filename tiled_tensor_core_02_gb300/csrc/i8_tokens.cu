@@ -256,6 +256,10 @@ __global__ void __launch_bounds__(kThreads, 1) i8_tokens_kernel(const __grid_con
       }
     }
   }
+  // a thread's channel from here on, and what its results take: asked for before the wait
+  const int col = threadIdx.x & 127, f = f0 + col;
+  const bool f_ok = col < q.tile_cols && f < p.N;
+  const float scale_b = f_ok ? __ldg(p.scaleB + f) : 0.0f, bias = f_ok && p.bias != nullptr ? __ldg(p.bias + f) : 0.0f;
   // every MMA is done (the issuer waited) and every byte is read
   tc_fence_before();
   __syncthreads();
@@ -263,12 +267,12 @@ __global__ void __launch_bounds__(kThreads, 1) i8_tokens_kernel(const __grid_con
 
   // ------------------------------------------------------------------ sums and result
   // four sets of four warps; set g takes the tokens from g * kCols on, a thread a channel
-  constexpr int kCols = 16;
+  constexpr int kCols = BT >= 64 ? 16 : 8;
   int32_t* red = reinterpret_cast<int32_t*>(slots);  // [token][128 channels]
   const int tokens = min(BT, p.M - token0);
-  auto result = [&](int32_t s, int token, int f) {
-    float v = __int2float_rn(s) * __ldg(p.scaleA + token) * __ldg(p.scaleB + f);
-    if (p.bias != nullptr) v += __ldg(p.bias + f);
+  auto result = [&](int32_t s, int token, float scale_a) {
+    float v = __int2float_rn(s) * scale_a * scale_b;
+    if (p.bias != nullptr) v += bias;
     v = act_value(p.act, v);
     const int64_t o = (int64_t)token * p.ldd + f;
     if constexpr (OUT == kI8ResultF32)
@@ -278,47 +282,52 @@ __global__ void __launch_bounds__(kThreads, 1) i8_tokens_kernel(const __grid_con
   };
   if (warp >= kWarp0) {
     const int group = (warp - kWarp0) >> 2, quarter = warp & 3;
-    const int c0 = group * kCols, col = quarter * 32 + lane;
+    const int c0 = group * kCols;
     if (c0 < BT && quarter * 32 < q.tile_cols) {
       const int parts = (n_stages + kAccStages - 1) / kAccStages;
+      int32_t sum[kCols];
 #pragma unroll
-      for (int c = 0; c < kCols; c += 16) {
-        int32_t sum[16];
+      for (int j = 0; j < kCols; ++j) sum[j] = 0;
+      for (int a = 0; a < parts; ++a) {
+        uint32_t w[kCols];
+        const uint32_t from = tmem_base + ((uint32_t)(quarter * 32) << 16) + a * BT + c0;
+        if constexpr (kCols == 16)
+          tmem_ld_32x32b_x16<0>(from, w);
+        else
+          tmem_ld_32x32b_x8(from, w);
+        tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < 16; ++j) sum[j] = 0;
-        for (int a = 0; a < parts; ++a) {
-          uint32_t w[16];
-          tmem_ld_32x32b_x16<0>(tmem_base + ((uint32_t)(quarter * 32) << 16) + a * BT + c0 + c, w);
-          tmem_ld_wait();
+        for (int j = 0; j < kCols; ++j) sum[j] += __float2int_rn(__uint_as_float(w[j]));
+      }
 #pragma unroll
-          for (int j = 0; j < 16; ++j) sum[j] += __float2int_rn(__uint_as_float(w[j]));
-        }
-        const int f = f0 + col;
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const int i = c0 + c + j;
-          if (p.split > 1)
-            red[i * 128 + col] = sum[j];
-          else if (i < tokens && col < q.tile_cols && f < p.N)
-            result(sum[j], token0 + i, f);
-        }
+      for (int j = 0; j < kCols; ++j) {
+        const int i = c0 + j;
+        if (p.split > 1)
+          red[i * 128 + col] = sum[j];
+        else if (i < tokens && f_ok)
+          result(sum[j], token0 + i, __ldg(p.scaleA + token0 + i));
       }
     }
   }
   if (p.split > 1) {
     cluster_sync();
     // each CTA of the cluster adds up and stores its share
-    for (int e = rank * kThreads + threadIdx.x; e < tokens * 128; e += p.split * kThreads) {
-      const int col = e & 127, f = f0 + col;
-      if (col >= q.tile_cols || f >= p.N) continue;
+    static_assert(kThreads % 128 == 0, "a thread keeps its channel");
+    for (int e = rank * kThreads + threadIdx.x; f_ok && e < tokens * 128; e += p.split * kThreads) {
+      const float scale_a = __ldg(p.scaleA + token0 + (e >> 7));
       const uint32_t at = smem_u32(red + e);
       int32_t s = 0;
-      for (int r = 0; r < p.split; ++r) {
-        uint32_t v;
-        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(mapa_shared(at, (uint32_t)r)) : "memory");
-        s += (int32_t)v;
+      for (int r0 = 0; r0 < p.split; r0 += 4) {  // four loads on the way
+        uint32_t v[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          v[r] = 0;
+          if (r0 + r < p.split)
+            asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v[r]) : "r"(mapa_shared(at, (uint32_t)(r0 + r))) : "memory");
+        }
+        s += (int32_t)(v[0] + v[1] + v[2] + v[3]);
       }
-      result(s, token0 + (e >> 7), f);
+      result(s, token0 + (e >> 7), scale_a);
     }
     cluster_sync();  // no CTA leaves while another may read its sums
   }
