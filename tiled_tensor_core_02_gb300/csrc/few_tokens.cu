@@ -20,7 +20,7 @@
 // come from L2 as often as there are tiles.
 //
 // Bound by HBM: 16 rows of 8 groups, 14336 x 4096 bf16 (6 groups with rows, 705
-// MB): 107 us, 6.6 TB/s; the CTA-pair kernel takes 128.
+// MB): 105 us, 6.7 TB/s; the CTA-pair kernel takes 128.
 #include <atomic>
 
 #include "grouped_common.cuh"
