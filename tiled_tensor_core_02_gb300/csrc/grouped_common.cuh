@@ -98,16 +98,17 @@ struct GroupedTile {
   int rb, cb;    // block of D's rows (forward: counted from the group's first row) and of its columns
 };
 
-// Tiles of a group walk `group_rows` row blocks of one column block before the
+__device__ __forceinline__ int divide(int n, FastDiv f) { return (int)((__umulhi((uint32_t)n, f.mul) + (uint32_t)n) >> f.shift); }
+
+// Tiles of a group walk 2^group_shift row blocks of one column block before the
 // next column block, so that CTAs at work together share panels of A and B.
 template <int ROWS, bool WGRAD>
 __device__ __forceinline__ GroupedTile grouped_tile(const GroupedParams& p, const GroupTable& tb, int t) {
   GroupedTile x;
   int first, rows;
   if constexpr (WGRAD) {
-    const int per = p.row_blocks * p.col_blocks;
-    x.g = t / per;
-    first = x.g * per;
+    x.g = divide(t, p.by_group);
+    first = x.g * p.row_blocks * p.col_blocks;
     group_rows(p, tb, x.g, x.lo, x.hi);
     rows = p.row_blocks;
   } else {
@@ -116,13 +117,16 @@ __device__ __forceinline__ GroupedTile grouped_tile(const GroupedParams& p, cons
     rows = (x.hi - x.lo + ROWS - 1) / ROWS;
   }
   int r = t - first;
-  const int band = p.group_rows * p.col_blocks;
-  const int b = r / band;
-  const int above = b * p.group_rows;
-  const int size = min(rows - above, p.group_rows);
-  r -= b * band;
-  x.rb = above + r % size;
-  x.cb = r / size;
+  const int b = divide(r, p.by_band), above = b << p.group_shift;
+  const int size = rows - above;  // row blocks of the band, where it is the last one
+  r -= (b * p.col_blocks) << p.group_shift;
+  if (size >= 1 << p.group_shift) {
+    x.cb = r >> p.group_shift;
+    x.rb = above + (r & ((1 << p.group_shift) - 1));
+  } else {
+    x.cb = WGRAD ? divide(r, p.by_rest) : r / size;
+    x.rb = above + r - x.cb * size;
+  }
   return x;
 }
 

@@ -32,6 +32,19 @@ int64_t span_bytes(int64_t count, int64_t stride, int64_t rows, int64_t ld, int6
   return n > ((__int128)1 << 60) ? 1ll << 60 : (int64_t)n;
 }
 
+// The walk over the tiles: bands of 2^shift row blocks.
+void set_walk(GroupedParams& p, int64_t row_blocks, int64_t col_blocks, int shift) {
+  p.row_blocks = (int)row_blocks;
+  p.col_blocks = (int)col_blocks;
+  p.group_shift = shift;
+  p.by_band = fast_div((uint32_t)(col_blocks << shift));
+  if (row_blocks > 0) {
+    p.by_group = fast_div((uint32_t)(row_blocks * col_blocks));
+    const int64_t rest = row_blocks & ((1ll << shift) - 1);
+    p.by_rest = fast_div(rest > 0 ? (uint32_t)rest : 1u);
+  }
+}
+
 // Parameters both grouped products share.
 void common_params(GroupedParams& p, const HostEnv& env, int64_t groups, int64_t M, int64_t N, int64_t K, const void* A,
                    int64_t lda, const void* B, int64_t ldb, const int32_t* offsets) {
@@ -45,7 +58,6 @@ void common_params(GroupedParams& p, const HostEnv& env, int64_t groups, int64_t
   p.M = (int)M;
   p.N = (int)N;
   p.K = (int)K;
-  p.group_rows = 16;
   p.err = env.err;
   p.timeout_ns = env.timeout_ns;
   p.inject_stall = env.inject_stall;
@@ -238,7 +250,6 @@ ttc_status ttc_gemm_grouped(int64_t groups, int64_t M, int64_t N, int64_t K, con
   common_params(p, env, groups, M, N, K, A, lda, B, ldb, offsets);
   p.strideB = strideB;
   p.b_mn = layoutB == TTC_ROW_MAJOR;
-  p.col_blocks = (int)col_blocks;
   p.k_blocks = (int)blocks_of(K, kBK);
   p.alpha = alpha;
   p.bias = bias;
@@ -260,8 +271,7 @@ ttc_status ttc_gemm_grouped(int64_t groups, int64_t M, int64_t N, int64_t K, con
   if (pair_maps(p, false, dtype, env)) {
     const int clusters = grouped_pair_clusters();
     if (clusters <= 0) return TTC_ERR_CUDA;
-    p.col_blocks = (int)blocks_of(N, kGroupedPairTile);
-    p.group_rows = 8;
+    set_walk(p, 0, blocks_of(N, kGroupedPairTile), 3);
     p.b_stream = M <= groups * kGroupedPairTile;
     const int64_t tiles = (blocks_of(M, kGroupedPairTile) + (groups < M ? groups : M)) * p.col_blocks;
     if (launch_grouped_pair(dtype == TTC_BF16, false, p, (int)(2 * tiles < clusters ? 2 * tiles : clusters),
@@ -270,6 +280,7 @@ ttc_status ttc_gemm_grouped(int64_t groups, int64_t M, int64_t N, int64_t K, con
     count_launches(1);
     return TTC_OK;
   }
+  set_walk(p, 0, col_blocks, 4);
   const int64_t tiles = (blocks_of(M, kGroupedPlainTile) + (groups < M ? groups : M)) * col_blocks;
   const int ctas = (int)(tiles < env.sm_count ? tiles : env.sm_count);
   if (launch_grouped_plain(dtype == TTC_BF16, false, p, ctas, static_cast<cudaStream_t>(stream)) != cudaSuccess)
@@ -314,8 +325,7 @@ ttc_status ttc_gemm_grouped_wgrad(int64_t groups, int64_t M, int64_t N, int64_t 
   GroupedParams p;
   common_params(p, env, groups, M, N, K, A, lda, B, ldb, offsets);
   p.b_mn = 1;
-  p.row_blocks = (int)row_blocks;
-  p.col_blocks = (int)col_blocks;
+  set_walk(p, row_blocks, col_blocks, 4);
   p.alpha = alpha;
   p.beta = beta;
   p.out_f32 = out_dtype == TTC_F32;
@@ -332,9 +342,7 @@ ttc_status ttc_gemm_grouped_wgrad(int64_t groups, int64_t M, int64_t N, int64_t 
   if (pair_maps(p, true, dtype, env)) {
     const int clusters = grouped_pair_clusters();
     if (clusters <= 0) return TTC_ERR_CUDA;
-    p.row_blocks = (int)blocks_of(K, kGroupedPairTile);
-    p.col_blocks = (int)blocks_of(N, kGroupedPairTile);
-    p.group_rows = 8;
+    set_walk(p, blocks_of(K, kGroupedPairTile), blocks_of(N, kGroupedPairTile), 3);
     const int64_t tiles = groups * p.row_blocks * p.col_blocks;
     if (launch_grouped_pair(dtype == TTC_BF16, true, p, (int)(2 * tiles < clusters ? 2 * tiles : clusters),
                             static_cast<cudaStream_t>(stream)) != cudaSuccess)
@@ -441,9 +449,8 @@ ttc_status ttc_gemm_i8_scaled(int64_t M, int64_t N, int64_t K, const int8_t* A, 
       GroupedParams f;
       common_params(f, env, 1, M, N, K, ws, copies.ld, ws + copies.b_off, copies.ld, nullptr);
       if (!pair_maps(f, false, TTC_F16, env)) return TTC_ERR_CUDA;
-      f.col_blocks = (int)blocks_of(N, kGroupedPairTile);
+      set_walk(f, 0, blocks_of(N, kGroupedPairTile), 3);
       f.k_blocks = (int)blocks_of(K, kBK);
-      f.group_rows = 8;
       f.alpha = 1.0f;
       f.bias = bias;
       f.act = (int)act;
