@@ -179,6 +179,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_tokens_kernel(const __grid_co
     const uint32_t w_step = (w_mn ? 2048u : 32u) >> 4;
     const uint32_t w_kb = (uint32_t)(w_mn ? kBK * 128 : w_blk) >> 4;
     constexpr uint32_t kTokenKb = BT * 128 >> 4;
+    const int whole = p.K / kStageK;  // stages without a tail of K
     bool ok = true, any = false;
     if (p.inject_stall) ok = mbar_wait_warp(stall_bar, 0, wc);  // nothing arrives here
     int stage = 0, it = 0;
@@ -189,7 +190,6 @@ __global__ void __launch_bounds__(kThreads, 1) few_tokens_kernel(const __grid_co
       tc_fence_after();
       const uint32_t d = tmem_base + acc * BT;
       for (int ks = 0; ks < k_stages; ++ks) {
-        const int steps = min(kStageK / kUmmaK, (p.K - ks * kStageK + kUmmaK - 1) / kUmmaK);
         if (!mbar_wait_warp(&full[stage], phase, wc)) {
           ok = false;
           break;
@@ -198,12 +198,15 @@ __global__ void __launch_bounds__(kThreads, 1) few_tokens_kernel(const __grid_co
         const uint64_t wd = w0 + (uint32_t)(stage * stage_bytes >> 4);
         const uint64_t ad = a0 + (uint32_t)(stage * stage_bytes >> 4);
         const uint32_t add = ks != 0;
-        if (steps == kStageK / kUmmaK) {  // no condition between the MMAs: each would cost as much as one
-          mma_f16_lead(lead, d, wd, ad, idesc, add);
+        if (ks < whole) {  // no condition between the MMAs: each would cost as much as one
+          const uint32_t w_lo = (uint32_t)wd, w_hi = (uint32_t)(wd >> 32), a_lo = (uint32_t)ad, a_hi = (uint32_t)(ad >> 32);
+          mma_f16_lead_lo(lead, d, w_lo, w_hi, a_lo, a_hi, idesc, add);
 #pragma unroll
           for (int k = 1; k < kStageK / kUmmaK; ++k)
-            mma_f16_lead(lead, d, wd + (k >> 2) * w_kb + (k & 3) * w_step, ad + (k >> 2) * kTokenKb + (k & 3) * 2u, idesc, 1u);
+            mma_f16_lead_lo(lead, d, w_lo + (k >> 2) * w_kb + (k & 3) * w_step, w_hi, a_lo + (k >> 2) * kTokenKb + (k & 3) * 2u,
+                            a_hi, idesc, 1u);
         } else {
+          const int steps = (p.K - ks * kStageK + kUmmaK - 1) / kUmmaK;
 #pragma unroll 1
           for (int k = 0; k < steps; ++k)
             mma_f16_lead(lead, d, wd + (k >> 2) * w_kb + (k & 3) * w_step, ad + (k >> 2) * kTokenKb + (k & 3) * 2u, idesc,

@@ -148,12 +148,12 @@ __global__ void __launch_bounds__(kThreads, 1) i8_tokens_kernel(const __grid_con
     const uint32_t idesc = idesc_f16(false, false, false, 128, BT);
     const uint64_t x0 = smem_desc_sw128(smem_u32(slots), 16u, 1024);
     constexpr uint32_t kTokenKb = BT * 128 >> 4;
+    const int whole = p.K / kI8TokenStage - s_lo;  // stages without a tail of K
     bool ok = true;
     if (q.inject_stall) ok = mbar_wait_warp(stall_bar, 0, wc);  // nothing arrives here
     int g = 0;
     uint32_t phase = 0;
     for (int n = 0; ok && n < n_stages; ++n) {
-      const int steps = min(kI8TokenStage / kUmmaK, (p.K - (s_lo + n) * kI8TokenStage + kUmmaK - 1) / kUmmaK);
       if (!mbar_wait_warp(&wide_full[g], phase, wc)) {
         ok = false;
         break;
@@ -163,13 +163,15 @@ __global__ void __launch_bounds__(kThreads, 1) i8_tokens_kernel(const __grid_con
       const uint32_t w = tmem_base + kI8TokenCols + g * (kI8TokenStage / 2);
       const uint64_t x = x0 + (uint32_t)(g * kSlotBytes >> 4);
       const uint32_t add = n % kAccStages != 0;
-      if (steps == kI8TokenStage / kUmmaK) {
-        // without a condition between them an MMA takes 16 clocks to issue, with one 57
-        mma_f16_ta_lead(lead, d, w, x, idesc, add);
+      if (n < whole) {
+        // without a condition between them an MMA takes about 25 clocks to issue, with one 57
+        const uint32_t x_lo = (uint32_t)x, x_hi = (uint32_t)(x >> 32);
+        mma_f16_ta_lead_lo(lead, d, w, x_lo, x_hi, idesc, add);
 #pragma unroll
         for (int k = 1; k < kI8TokenStage / kUmmaK; ++k)
-          mma_f16_ta_lead(lead, d, w + 8 * k, x + (k >> 2) * kTokenKb + (k & 3) * 2u, idesc, 1u);
+          mma_f16_ta_lead_lo(lead, d, w + 8 * k, x_lo + (k >> 2) * kTokenKb + (k & 3) * 2u, x_hi, idesc, 1u);
       } else {
+        const int steps = (p.K - (s_lo + n) * kI8TokenStage + kUmmaK - 1) / kUmmaK;
 #pragma unroll 1
         for (int k = 0; k < steps; ++k)
           mma_f16_ta_lead(lead, d, w + 8 * k, x + (k >> 2) * kTokenKb + (k & 3) * 2u, idesc, add | (k != 0 ? 1u : 0u));
