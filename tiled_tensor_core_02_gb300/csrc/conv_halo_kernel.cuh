@@ -215,12 +215,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kHaloThreads, 1)
           }
         }
       }
-      if (!ok && leader) {
-        // every box this CTA armed for completes once both CTAs' loads have landed
-        for (int s = 0; s < S; ++s)
-          if (armed_mask & (1u << s)) drain_wait(&full[s], (armed_parity >> s) & 1u, 100000000ull);
-        for (int h = 0; h < 2; ++h)
-          if (harmed_mask & (1u << h)) drain_wait(&hfull[h], (harmed_parity >> h) & 1u, 100000000ull);
+      // a box this CTA armed for completes once both CTAs' loads have landed
+      if (leader) {
+        drain_ring(full, S, armed_mask, armed_parity);
+        drain_ring(hfull, 2, harmed_mask, harmed_parity);
+      } else {
+        drain_odd_cta(wc);
       }
     }
   } else if (warp == 1) {

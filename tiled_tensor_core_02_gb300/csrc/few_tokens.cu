@@ -163,11 +163,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_tokens_kernel(const __grid_co
           }
         }
       }
-      if (!ok) {
-        // loads in flight land before the CTA may exit
-        for (int s = 0; s < S; ++s)
-          if (armed & (1u << s)) drain_wait(&full[s], (armed_parity >> s) & 1u, 100000000ull);
-      }
+      drain_ring(full, S, armed, armed_parity);
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer

@@ -235,12 +235,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * kEW, 1)
           }
         }
       }
-      if (!ok && leader) {
-        // every stage this CTA armed completes once both CTAs' loads for it
-        // have landed; wait for them before the pair may exit
-        for (int s = 0; s < S; ++s)
-          if (armed_mask & (1u << s)) drain_wait(&full[s], (armed_parity >> s) & 1u, 100000000ull);
-      }
+      // a stage completes once both CTAs' loads for it have landed
+      if (leader)
+        drain_ring(full, S, armed_mask, armed_parity);
+      else
+        drain_odd_cta(wc);
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer (even CTA)

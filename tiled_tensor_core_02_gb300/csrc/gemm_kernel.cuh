@@ -309,9 +309,30 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
 // Waits for a barrier phase during shutdown, ignoring errors raised by other
 // threads: used only to let copies this thread started land before exit.
 __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, uint64_t budget_ns) {
+  if (mbar_try_wait(bar, parity)) return;
   const uint64_t t0 = globaltimer_ns();
   while (!mbar_try_wait(bar, parity)) {
     if (globaltimer_ns() - t0 > budget_ns) return;
+  }
+}
+
+// Lets every load that a producer started land before its CTA goes on to exit,
+// also where it issued its last one without an error: consumers that gave up
+// after an error elsewhere in the grid do not wait for it.  `armed` has a bit for
+// each of the ring's barriers in use, `parity` their last phase.
+__device__ __forceinline__ void drain_ring(uint64_t* bars, int stages, uint32_t armed, uint32_t parity) {
+  for (int s = 0; s < stages; ++s)
+    if (armed & (1u << s)) drain_wait(&bars[s], (parity >> s) & 1u, 100000000ull);
+}
+
+// The same for the odd CTA of a pair, whose loads complete on the even CTA's
+// barriers, which only that CTA can wait on, and waits on for the stages that it
+// armed itself.  After an error it may have given up a stage earlier; loads take
+// some microseconds to land.
+__device__ __forceinline__ void drain_odd_cta(const WaitCtx& w) {
+  if (!error_raised(w)) return;
+  const uint64_t t0 = globaltimer_ns();
+  while (globaltimer_ns() - t0 < 1000000ull) {
   }
 }
 
@@ -1081,11 +1102,7 @@ __global__ void __launch_bounds__(ModeTraits<MODE>::kThreads, 1) gemm_kernel(con
             }
           }
         }
-        if (!ok) {
-          // Let every load this thread started land before the CTA exits.
-          for (int s = 0; s < S; ++s)
-            if (issued_mask & (1u << s)) drain_wait(&full[s], (issued_parity >> s) & 1u, 100000000ull);
-        }
+        drain_ring(full, S, issued_mask, issued_parity);
       }
     } else if constexpr (Tr::kStaged) {
       if (warp == 0) {
@@ -1123,10 +1140,7 @@ __global__ void __launch_bounds__(ModeTraits<MODE>::kThreads, 1) gemm_kernel(con
               }
             }
           }
-          if (!ok) {
-            for (int s2 = 0; s2 < S8; ++s2)
-              if (issued_mask & (1u << s2)) drain_wait(&full8[s2], (issued_parity >> s2) & 1u, 100000000ull);
-          }
+          drain_ring(full8, S8, issued_mask, issued_parity);
         }
       } else {
         // converter warps: int8 staging slot -> fp16 MMA slot.  Group g widens

@@ -408,6 +408,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint32_t full_leader = mapa_shared(smem_u32(&full[stage]), 0);
           if (clear) {
             mbar_arrive_expect_tx(&fix[stage], bytes_a + bytes_b);
+            armed &= ~(1u << stage);  // what it held has landed; `full` goes on without the producer
             fixed |= 1u << stage;
             fix_parity = (fix_parity & ~(1u << stage)) | (fix_phase & (1u << stage));
             fix_phase ^= 1u << stage;
@@ -437,13 +438,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           kb0 += kKPS;
         } while (kb0 < l.k_blocks);
       }
-      if (!ok) {
-        // loads in flight land before the pair may exit
-        for (int s = 0; s < kStages; ++s) {
-          if (leader && (armed & (1u << s))) drain_wait(&full[s], (armed_parity >> s) & 1u, 100000000ull);
-          if (fixed & (1u << s)) drain_wait(&fix[s], (fix_parity >> s) & 1u, 100000000ull);
-        }
-      }
+      // a stage completes once both CTAs' loads for it have landed, one to be cleared with this CTA's
+      drain_ring(fix, kStages, fixed, fix_parity);
+      if (leader)
+        drain_ring(full, kStages, armed, armed_parity);
+      else
+        drain_odd_cta(wc);
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer (even CTA)

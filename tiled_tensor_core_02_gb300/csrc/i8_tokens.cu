@@ -119,12 +119,8 @@ __global__ void __launch_bounds__(kThreads, 1) i8_tokens_kernel(const __grid_con
       const uint64_t pol_w = gridDim.y == 1 ? policy_evict_first() : keep;
       int stage = 0;
       uint32_t phase = 0, armed = 0, armed_parity = 0;
-      bool ok = true;
       for (int n = 0; n < n_stages; ++n) {
-        if (!mbar_wait(&empty[stage], phase ^ 1u, wc)) {
-          ok = false;
-          break;
-        }
+        if (!mbar_wait(&empty[stage], phase ^ 1u, wc)) break;
         uint8_t* w = ring + stage * stage_bytes;
         mbar_arrive_expect_tx(&full[stage], stage_bytes);
         armed |= 1u << stage;
@@ -136,11 +132,7 @@ __global__ void __launch_bounds__(kThreads, 1) i8_tokens_kernel(const __grid_con
           phase ^= 1u;
         }
       }
-      if (!ok) {
-        // loads in flight land before the CTA may exit
-        for (int s = 0; s < S; ++s)
-          if (armed & (1u << s)) drain_wait(&full[s], (armed_parity >> s) & 1u, 100000000ull);
-      }
+      drain_ring(full, S, armed, armed_parity);
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer
