@@ -218,13 +218,26 @@ def ttc_launch_count() -> int:
 def _matrix_layout(t, rows, cols):
     """(layout, ld) of a 2-D tensor viewed as a rows x cols matrix."""
     s0, s1 = t.stride()
+    empty = rows == 0 or cols == 0
+    # rows (columns) of which there are several start at least a row's (column's) length apart
+    by_rows = empty or rows == 1 or s0 >= cols
+    by_cols = empty or cols == 1 or s1 >= rows
     if cols == 1 and rows >= 1 and s0 == 1:
         return COL_MAJOR, max(s1, rows)
-    if s1 == 1 or cols == 1:
+    if (s1 == 1 or cols == 1) and by_rows:
         return ROW_MAJOR, max(s0, cols, 1)
-    if s0 == 1 or rows == 1:
+    if (s0 == 1 or rows == 1) and by_cols:
         return COL_MAJOR, max(s1, rows, 1)
-    raise ValueError("operand must be row- or column-major (one unit stride)")
+    raise ValueError("operand must be row- or column-major (one unit stride, rows that do not overlap)")
+
+
+def _result_pitch(t, rows, cols, what):
+    """Pitch of a row-major tensor that holds a rows x cols matrix."""
+    if t.dim() != 2 or t.shape[0] < rows or t.shape[1] < cols:
+        raise ValueError(f"{what} must be M x N")
+    if (t.stride(1) != 1 and cols > 1) or (rows > 1 and t.stride(0) < cols):
+        raise ValueError(f"{what} must be row-major")
+    return max(t.stride(0), cols)
 
 
 def gemm(a, b, c=None, out=None, *, alpha=1.0, beta=0.0, bias=None, act="none", stream=None,
@@ -245,13 +258,9 @@ def gemm(a, b, c=None, out=None, *, alpha=1.0, beta=0.0, bias=None, act="none", 
         out = torch.empty((M, N), dtype=odt, device=a.device)
     la, lda = _matrix_layout(a, M, K)
     lb, ldb = _matrix_layout(b, K, N)
-    if out.stride(1) != 1 and N > 1:
-        raise ValueError("out must be row-major")
-    ldd = max(out.stride(0), N)
+    ldd = _result_pitch(out, M, N, "out")
     if c is not None:
-        if c.stride(1) != 1 and N > 1:
-            raise ValueError("c must be row-major")
-        ldc = max(c.stride(0), N)
+        ldc = _result_pitch(c, M, N, "c")
         cptr = c.data_ptr()
     else:
         ldc, cptr = N, None
