@@ -1,6 +1,6 @@
 """Strides that the C calls cannot describe are refused by the torch wrappers: rows
 (or columns) that start less than a row's length apart, as in expanded tensors, which
-the kernels would read as others and behind the tensor's end (no GPU)."""
+the kernels would read as others and behind the tensor's end."""
 import pytest
 import torch
 
@@ -65,6 +65,13 @@ def test_gemm_sum_and_result(bad):
         ttc.gemm(z(4, 8), z(8, 5), out=bad())
     with pytest.raises(ValueError):
         ttc.gemm(z(4, 8), z(8, 5), c=bad(), out=z(4, 5), beta=1.0)
+
+
+@pytest.mark.gpu
+def test_a_sum_that_is_not_read_may_have_any_strides():
+    a, b = torch.randn(4, 8, device="cuda").to(BF), torch.randn(8, 5, device="cuda").to(BF)
+    c = torch.full((1, 5), float("nan"), dtype=BF, device="cuda").expand(4, 5)
+    assert torch.equal(ttc.gemm(a, b, c=c), ttc.gemm(a, b))
 
 
 R, C = ttc.ROW_MAJOR, ttc.COL_MAJOR

@@ -259,7 +259,7 @@ def gemm(a, b, c=None, out=None, *, alpha=1.0, beta=0.0, bias=None, act="none", 
     la, lda = _matrix_layout(a, M, K)
     lb, ldb = _matrix_layout(b, K, N)
     ldd = _result_pitch(out, M, N, "out")
-    if c is not None:
+    if c is not None and beta != 0.0:  # read
         ldc = _result_pitch(c, M, N, "c")
         cptr = c.data_ptr()
     else:
