@@ -231,6 +231,15 @@ def _matrix_layout(t, rows, cols):
     raise ValueError("operand must be row- or column-major (one unit stride, rows that do not overlap)")
 
 
+def _stream_of(stream, device):
+    """The address of the stream that a call's work goes to: the caller's, else the current one."""
+    import torch
+
+    if device.type != "cuda":
+        raise ValueError("operands must be CUDA tensors")
+    return torch.cuda.current_stream(device).cuda_stream if stream is None else stream
+
+
 def _result_pitch(t, rows, cols, what):
     """Pitch of a row-major tensor that holds a rows x cols matrix."""
     if t.dim() != 2 or t.shape[0] < rows or t.shape[1] < cols:
@@ -264,9 +273,11 @@ def gemm(a, b, c=None, out=None, *, alpha=1.0, beta=0.0, bias=None, act="none", 
         cptr = c.data_ptr()
     else:
         ldc, cptr = N, None
+    for name, t in (("b", b), ("c", c), ("out", out), ("bias", bias)):
+        if t is not None and t.device != a.device:
+            raise ValueError(f"{name} must be on {a.device}")
     bptr = bias.data_ptr() if bias is not None else None
-    if stream is None:
-        stream = torch.cuda.current_stream(a.device).cuda_stream
+    stream = _stream_of(stream, a.device)
     st = ttc_gemm(M, N, K, a.data_ptr(), lda, la, b.data_ptr(), ldb, lb, cptr, ldc, out.data_ptr(),
                   ldd, float(alpha), float(beta), bptr, ACT[act], DTYPE[dt], stream)
     if check and st != 0:
@@ -349,8 +360,7 @@ def gemm_grouped(a, b, offsets, out=None, *, alpha=1.0, bias=None, act="none", s
         if bias.shape != (groups, N) or (N > 1 and bias.stride(1) != 1):
             raise ValueError("bias must be groups x N, its rows contiguous")
         stride_bias = bias.stride(0)
-    if stream is None:
-        stream = torch.cuda.current_stream(a.device).cuda_stream
+    stream = _stream_of(stream, a.device)
     _finish(ttc_gemm_grouped(groups, M, N, K, a.data_ptr(), lda, offsets.data_ptr(), b.data_ptr(), ldb, b.stride(0), lb,
                              out.data_ptr(), ldd, float(alpha), None if bias is None else bias.data_ptr(), stride_bias,
                              ACT[act], DTYPE[dt], stream), "ttc_gemm_grouped", check)
@@ -382,8 +392,7 @@ def gemm_grouped_wgrad(a, b, offsets, c=None, out=None, *, alpha=1.0, beta=0.0, 
     stride_d, ldd = _group_pitch(out, "out")
     stride_c, ldc = (0, max(N, 1)) if c is None else _group_pitch(c, "c")
     odt = "f32" if out.dtype == torch.float32 else dt
-    if stream is None:
-        stream = torch.cuda.current_stream(a.device).cuda_stream
+    stream = _stream_of(stream, a.device)
     _finish(ttc_gemm_grouped_wgrad(groups, M, N, K, a.data_ptr(), lda, b.data_ptr(), ldb, offsets.data_ptr(),
                                    None if c is None else c.data_ptr(), ldc, stride_c, out.data_ptr(), ldd, stride_d,
                                    float(alpha), float(beta), DTYPE[dt], DTYPE[odt], stream),
@@ -411,8 +420,7 @@ def quantize_rows(x, out=None, scale=None, *, stream=None, check=True):
         raise ValueError("out must have x's shape and scale its rows")
     ldq = _row_pitch(out, "out")
     dt = {torch.float16: "f16", torch.bfloat16: "bf16", torch.float32: "f32"}[x.dtype]
-    if stream is None:
-        stream = torch.cuda.current_stream(x.device).cuda_stream
+    stream = _stream_of(stream, x.device)
     _finish(ttc_quantize_rows(rows, cols, x.data_ptr(), ldx, DTYPE[dt], out.data_ptr(), ldq, scale.data_ptr(), stream),
             "ttc_quantize_rows", check)
     return out, scale
@@ -445,9 +453,10 @@ def gemm_i8_scaled(a, scale_a, b, scale_b, out=None, *, out_dtype=None, bias=Non
         raise ValueError("out must be M x N")
     ldd = _row_pitch(out, "out")
     odt = DTYPE[{torch.float16: "f16", torch.bfloat16: "bf16", torch.float32: "f32"}[out.dtype]]
+    if workspace is not None and (workspace.device != a.device or not workspace.is_contiguous()):
+        raise ValueError(f"workspace must be on {a.device} and contiguous")
     own_stream = stream
-    if stream is None:
-        stream = torch.cuda.current_stream(a.device).cuda_stream
+    stream = _stream_of(stream, a.device)
     if workspace is None:
         need = ttc_gemm_i8_scaled_workspace_size(M, N, K, a.data_ptr(), lda, b.data_ptr(), ldb, out.data_ptr(), ldd, odt)
         if need:
