@@ -16,6 +16,8 @@ Names follow the C header include/ttc.h:
 plus `gemm(...)`, `gemm_grouped(...)`, `gemm_grouped_wgrad(...)`,
 `quantize_rows(...)` and `gemm_i8_scaled(...)`, convenience wrappers on torch
 tensors that read the layouts and leading dimensions off the tensors' strides.
+Their work goes to `stream`, an address, or to the current stream; the caller
+orders it behind its inputs, and what reads a result on another stream behind it.
 """
 from __future__ import annotations
 
@@ -240,6 +242,31 @@ def _stream_of(stream, device):
     return torch.cuda.current_stream(device).cuda_stream if stream is None else stream
 
 
+def _scratch(shape, dtype, device, stream):
+    """A new tensor for work on `stream` (an address, or None: the current one).
+
+    torch hands a freed block out again as soon as the stream it was allocated on
+    has the work in order, so memory for another stream comes from that stream's blocks:
+    one of the current stream's may still be read or written there."""
+    import torch
+
+    if stream is None or stream == torch.cuda.current_stream(device).cuda_stream:
+        return torch.empty(shape, dtype=dtype, device=device)
+    own = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
+    with torch.cuda.stream(own):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _result(shape, dtype, device, stream):
+    """_scratch for a result, which the current stream is going to read."""
+    import torch
+
+    t = _scratch(shape, dtype, device, stream)
+    if stream is not None:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def _result_pitch(t, rows, cols, what):
     """Pitch of a row-major tensor that holds a rows x cols matrix."""
     if t.dim() != 2 or t.shape[0] < rows or t.shape[1] < cols:
@@ -264,7 +291,7 @@ def gemm(a, b, c=None, out=None, *, alpha=1.0, beta=0.0, bias=None, act="none", 
     dt = {torch.float16: "f16", torch.bfloat16: "bf16", torch.int8: "i8"}[a.dtype]
     odt = torch.int32 if dt == "i8" else a.dtype
     if out is None:
-        out = torch.empty((M, N), dtype=odt, device=a.device)
+        out = _result((M, N), odt, a.device, stream)
     la, lda = _matrix_layout(a, M, K)
     lb, ldb = _matrix_layout(b, K, N)
     ldd = _result_pitch(out, M, N, "out")
@@ -350,7 +377,7 @@ def gemm_grouped(a, b, offsets, out=None, *, alpha=1.0, bias=None, act="none", s
     _same(a.device, (torch.float32,), bias=bias)
     _check_offsets(offsets, groups, a.device)
     if out is None:
-        out = torch.empty((M, N), dtype=a.dtype, device=a.device)
+        out = _result((M, N), a.dtype, a.device, stream)
     if out.shape != (M, N):
         raise ValueError("out must be M x N")
     ldd = _row_pitch(out, "out")
@@ -384,7 +411,7 @@ def gemm_grouped_wgrad(a, b, offsets, c=None, out=None, *, alpha=1.0, beta=0.0, 
     _same(a.device, (a.dtype,), b=b)
     _check_offsets(offsets, groups, a.device)
     if out is None:
-        out = torch.empty((groups, K, N), dtype=out_dtype or torch.float32, device=a.device)
+        out = _result((groups, K, N), out_dtype or torch.float32, a.device, stream)
     _same(a.device, (a.dtype, torch.float32), out=out)
     _same(a.device, (out.dtype,), c=c)
     if out.shape != (groups, K, N) or (c is not None and c.shape != out.shape):
@@ -411,9 +438,9 @@ def quantize_rows(x, out=None, scale=None, *, stream=None, check=True):
     ldx = _row_pitch(x, "x")
     rows, cols = x.shape
     if out is None:
-        out = torch.empty((rows, -(-cols // 16) * 16), dtype=torch.int8, device=x.device)[:, :cols]
+        out = _result((rows, -(-cols // 16) * 16), torch.int8, x.device, stream)[:, :cols]
     if scale is None:
-        scale = torch.empty(rows, dtype=torch.float32, device=x.device)
+        scale = _result((rows,), torch.float32, x.device, stream)
     _same(x.device, (torch.int8,), out=out)
     _same(x.device, (torch.float32,), scale=scale)
     if out.shape != x.shape or scale.shape != (rows,) or not scale.is_contiguous():
@@ -447,7 +474,7 @@ def gemm_i8_scaled(a, scale_a, b, scale_b, out=None, *, out_dtype=None, bias=Non
         if t is not None and (t.shape != (n,) or not t.is_contiguous()):
             raise ValueError(f"{name} must be {n} contiguous fp32")
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype or torch.bfloat16, device=a.device)
+        out = _result((M, N), out_dtype or torch.bfloat16, a.device, stream)
     _same(a.device, (torch.float16, torch.bfloat16, torch.float32), out=out)
     if out.shape != (M, N):
         raise ValueError("out must be M x N")
@@ -455,14 +482,11 @@ def gemm_i8_scaled(a, scale_a, b, scale_b, out=None, *, out_dtype=None, bias=Non
     odt = DTYPE[{torch.float16: "f16", torch.bfloat16: "bf16", torch.float32: "f32"}[out.dtype]]
     if workspace is not None and (workspace.device != a.device or not workspace.is_contiguous()):
         raise ValueError(f"workspace must be on {a.device} and contiguous")
-    own_stream = stream
     stream = _stream_of(stream, a.device)
     if workspace is None:
         need = ttc_gemm_i8_scaled_workspace_size(M, N, K, a.data_ptr(), lda, b.data_ptr(), ldb, out.data_ptr(), ldd, odt)
         if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=a.device)
-            if own_stream is not None:  # its memory stays taken until that stream is done with it
-                workspace.record_stream(torch.cuda.ExternalStream(own_stream, device=a.device))
+            workspace = _scratch((need,), torch.uint8, a.device, stream)
     _finish(ttc_gemm_i8_scaled(M, N, K, a.data_ptr(), lda, scale_a.data_ptr(), b.data_ptr(), ldb, scale_b.data_ptr(),
                                out.data_ptr(), ldd, None if bias is None else bias.data_ptr(), ACT[act], odt,
                                None if workspace is None else workspace.data_ptr(),
