@@ -6,6 +6,11 @@
 
 namespace ttc {
 
+// The tensor cores cut, not round, each addition to an accumulator, an error that
+// grows with the number of them: fp32 results start a fresh accumulator every so
+// many k-blocks, 768 tokens, and the partial sums are added up rounded to nearest.
+constexpr int kSumKBlocks = 12;
+
 // The group table of a CTA in shared memory.  offs[g] is the first row of group
 // g, held to [0, M] (offs[groups] ends the last one); null where shared memory
 // has no room for it and the device's offsets are read instead.  start[i] is

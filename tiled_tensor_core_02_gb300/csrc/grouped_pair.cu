@@ -74,9 +74,9 @@ constexpr int kBarBytes = 256;
 constexpr int kTableInts = 384;
 constexpr int kSmemBytes = 1024 + kStages * 2 * kShareBytes + kStagingBytes + kBarBytes + kTableInts * 4;
 // k-blocks of an accumulator where the partial sums are added up in registers:
-// fp32 results, 768 tokens; int8, 1024 products
+// fp32 results, or int8, 1024 products
 template <bool I8>
-constexpr int kChunkKBlocks = I8 ? 16 : 12;
+constexpr int kChunkKBlocks = I8 ? 16 : kSumKBlocks;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 static_assert(kChunkKBlocks<false> % kKPS == 0 && kChunkKBlocks<true> % kKPS == 0, "accumulator chunks hold whole stages");
 static_assert((kMaxGroups + 3) / 4 + 1 <= kTableInts, "a table of every fourth group's tiles has room");

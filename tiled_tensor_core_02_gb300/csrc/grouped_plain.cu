@@ -11,6 +11,10 @@
 // the way.  Only blocks that hold a byte of the row are read; what is outside the
 // group's rows and the operand's extents is zero and not loaded.
 //
+// fp32 gradients start a fresh accumulator every kSumKBlocks k-blocks, whose values
+// the epilogue warps add up in tensor memory: 7e-7 of the result however many
+// tokens there are, where one accumulator over 8192 is at 6.4e-6.
+//
 // Bound by the producers, which a k-block of 2 x 16 KB takes 1.1 us (asking L2 for
 // its lines four k-blocks ahead changed nothing): 8192 rows over 8 groups, 4099 x
 // 4099, 1164 us or 236 TFLOP/s; 856 rows over 32 groups, 2712 x 3337, 349 us, where
@@ -19,6 +23,7 @@
 #include "grouped_common.cuh"
 
 #include <atomic>
+#include <type_traits>
 
 namespace ttc {
 
@@ -87,6 +92,40 @@ struct TilePieces {
 using Inner = TilePieces<kTile, kBK>;  // the reduction lies innermost
 using Outer = TilePieces<kBK, kTile>;  // outermost
 
+// Tensor memory behind the two accumulators, for fp32 gradients: the sum of a tile's
+// accumulators (there are no registers for 128 columns a thread).
+constexpr int kSumsAt = 2 * kTile;
+
+// Adds `more` accumulators of a tile, the it-th on, to the one behind them, in the
+// warp's rows; false after an error.
+__device__ __forceinline__ bool add_accumulators(uint32_t tmem_mine, int it, int more, uint64_t* tmem_full,
+                                                 uint64_t* tmem_empty, const WaitCtx& wc) {
+  for (int i = 0; i <= more; ++i, ++it) {
+    if (!mbar_wait(&tmem_full[it & 1], (it >> 1) & 1, wc)) return false;
+    tc_fence_after();
+    const uint32_t acc = tmem_mine + (it & 1) * kTile, sums = tmem_mine + kSumsAt;
+#pragma unroll 1
+    for (int at = 0; at < kTile; at += 32) {
+      uint32_t w[32], s[32];
+      tmem_ld_32x32b_x32(acc + at, w);
+      if (i > 0) tmem_ld_32x32b_x32(sums + at, s);
+      tmem_ld_wait();
+      if (i > 0) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(__uint_as_float(s[j]) + __uint_as_float(w[j]));
+      }
+      tmem_st_32x32b_x32((i < more ? sums : acc) + at, w);
+    }
+    tmem_st_wait();
+    if (i < more) {
+      tc_fence_before();
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) mbar_arrive(&tmem_empty[it & 1]);
+    }
+  }
+  return true;
+}
+
 // The epilogue's walk: each warp 32 rows of every tile, in blocks of 128 bytes a
 // row through its staging block, so that C is read and D written a row an
 // instruction whatever their alignment.
@@ -95,11 +134,22 @@ __device__ __forceinline__ void drain_tiles(const GroupedParams& p, const GroupT
                                             uint8_t* sb, uint64_t* tmem_full, uint64_t* tmem_empty, const WaitCtx& wc) {
   constexpr int kUnit = 128 / (int)sizeof(T);  // columns
   constexpr int kPer = 16 / (int)sizeof(T);    // of a 16-byte piece
+  // rows of single columns read before the first is stored: short tiles of gradients are all
+  // stores (1023 rows, 32 groups, 1001 x 1023 bf16: 56 us, by eight 80), forward by eight 1067 us
+  // against 1088 (8192 rows, 8 groups, 4099 x 4099)
+  constexpr int kAtOnce = WGRAD ? 32 : 8;
   const int q = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
   int it = 0;
   for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++it) {
     const GroupedTile x = grouped_tile<kTile, WGRAD>(p, tb, t);
     const bool has_k = WGRAD ? x.hi > x.lo : p.k_blocks > 0;
+    if constexpr (WGRAD && sizeof(T) == 4) {
+      const int more = ((x.hi - x.lo + kBK - 1) / kBK - 1) / kSumKBlocks;
+      if (more > 0) {
+        if (!add_accumulators(tmem_base + ((uint32_t)(q * 32) << 16), it, more, tmem_full, tmem_empty, wc)) break;
+        it += more;
+      }
+    }
     const int acc = it & 1;
     const int r0 = x.rb * kTile + q * 32;  // of the warp, in its group in forward
     const int64_t row0 = WGRAD ? r0 : (int64_t)x.lo + r0;
@@ -118,15 +168,12 @@ __device__ __forceinline__ void drain_tiles(const GroupedParams& p, const GroupT
       if (c != nullptr) {
         for (int j = lane; j < n; j += 32) {
           const T* src = c + at + j;
-#pragma unroll 1
-          for (int r = 0; r < 32; r += 16) {  // sixteen loads on the way before the first store
-            T y[16];
+          T y[32];  // all of them on their way before the first store
 #pragma unroll
-            for (int i = 0; i < 16; ++i) y[i] = r + i < rows ? src[(int64_t)(r + i) * p.ldc] : T{};
+          for (int r = 0; r < 32; ++r) y[r] = r < rows ? src[(int64_t)r * p.ldc] : T{};
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              *reinterpret_cast<T*>(sb + staged<32>(r + i, j / kPer) + j % kPer * sizeof(T)) = y[i];
-          }
+          for (int r = 0; r < 32; ++r)
+            *reinterpret_cast<T*>(sb + staged<32>(r, j / kPer) + j % kPer * sizeof(T)) = y[r];
         }
         __syncwarp();
       }
@@ -172,13 +219,14 @@ __device__ __forceinline__ void drain_tiles(const GroupedParams& p, const GroupT
         if (lane == 0) mbar_arrive(&tmem_empty[acc]);
       }
       __syncwarp();
-      if (n > 0) copy_out<T, 8>(p, sb, d + at, rows, n, lane);
+      if (n > 0) copy_out<T, kAtOnce>(p, sb, d + at, rows, n, lane);
       __syncwarp();
     }
   }
 }
 
-template <bool BF16, bool WGRAD>
+// F32: gradients in fp32.
+template <bool BF16, bool WGRAD, bool F32>
 __global__ void __launch_bounds__(kThreads, 1) grouped_plain_kernel(const __grid_constant__ GroupedParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -212,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_plain_kernel(const __grid
     fence_barrier_init();
   }
   if (warp == kIssuer) {
-    tmem_alloc(tmem_slot, 256);
+    tmem_alloc(tmem_slot, F32 ? 512 : 256);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -287,35 +335,44 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_plain_kernel(const __grid
       if (p.inject_stall) ok = mbar_wait(stall_bar, 0, wc);  // nothing arrives here
       int stage = 0, it = 0;
       uint32_t phase = 0;
-      for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x, ++it) {
+      for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
         const GroupedTile x = grouped_tile<kTile, WGRAD>(p, tb, t);
         const int nkb = WGRAD ? (x.hi - x.lo + kBK - 1) / kBK : p.k_blocks;
-        const int acc = it & 1;
-        if (!mbar_wait(&tmem_empty[acc], ((it >> 1) & 1) ^ 1u, wc)) break;
-        tc_fence_after();
-        for (int kb = 0; kb < nkb; ++kb) {
-          if (!mbar_wait(&full[stage], phase, wc)) {
+        const int per_acc = F32 ? kSumKBlocks : nkb;
+        int kb0 = 0;
+        do {  // an accumulator: the tile's, or a part of its reduction
+          const int acc = it & 1, n = min(per_acc, nkb - kb0);
+          if (!mbar_wait(&tmem_empty[acc], ((it >> 1) & 1) ^ 1u, wc)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint64_t ad = a0 + (uint32_t)(stage * (kOperandBytes >> 4));
-          const uint64_t bd = b0 + (uint32_t)(stage * (kOperandBytes >> 4));
+          for (int kb = 0; kb < n; ++kb) {
+            if (!mbar_wait(&full[stage], phase, wc)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint64_t ad = a0 + (uint32_t)(stage * (kOperandBytes >> 4));
+            const uint64_t bd = b0 + (uint32_t)(stage * (kOperandBytes >> 4));
 #pragma unroll
-          for (int k = 0; k < kBK / kUmmaK; ++k)
-            mma_f16(tmem_base + acc * kTile, ad + k * a_step, bd + k * b_step, idesc, (kb | k) != 0);
-          any = true;
-          mma_commit(&empty[stage]);
-          if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1u;
+            for (int k = 0; k < kBK / kUmmaK; ++k)
+              mma_f16(tmem_base + acc * kTile, ad + k * a_step, bd + k * b_step, idesc, (kb | k) != 0);
+            any = true;
+            mma_commit(&empty[stage]);
+            if (++stage == kStages) {
+              stage = 0;
+              phase ^= 1u;
+            }
           }
-        }
-        if (!ok) break;
-        if (nkb == 0)
-          mbar_arrive(&tmem_full[acc]);
-        else
-          mma_commit(&tmem_full[acc]);
+          if (!ok) break;
+          if (nkb == 0)
+            mbar_arrive(&tmem_full[acc]);
+          else
+            mma_commit(&tmem_full[acc]);
+          ++it;
+          kb0 += n;
+        } while (kb0 < nkb);
       }
       if (any) {
         mma_commit(drain_bar);
@@ -324,22 +381,18 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_plain_kernel(const __grid
     }
   } else {
     // ---------------------------------------------------------------- epilogue
-    if (p.out_f32)
-      drain_tiles<BF16, WGRAD, float>(p, tb, tiles, tmem_base, staging + (warp - kProducers) * 4096, tmem_full, tmem_empty,
-                                      wc);
-    else
-      drain_tiles<BF16, WGRAD, uint16_t>(p, tb, tiles, tmem_base, staging + (warp - kProducers) * 4096, tmem_full,
-                                         tmem_empty, wc);
+    using T = typename std::conditional<F32, float, uint16_t>::type;
+    drain_tiles<BF16, WGRAD, T>(p, tb, tiles, tmem_base, staging + (warp - kProducers) * 4096, tmem_full, tmem_empty, wc);
   }
   tc_fence_before();
   __syncthreads();
   if (warp == kIssuer) {
     tc_fence_after();
-    tmem_dealloc(tmem_base, 256);
+    tmem_dealloc(tmem_base, F32 ? 512 : 256);
   }
 }
 
-template <bool BF16, bool WGRAD>
+template <bool BF16, bool WGRAD, bool F32>
 cudaError_t launch(const GroupedParams& p, int ctas, cudaStream_t stream) {
   static std::atomic<bool> done[64];
   int dev = 0;
@@ -347,7 +400,7 @@ cudaError_t launch(const GroupedParams& p, int ctas, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!done[dev].load()) {
-    e = cudaFuncSetAttribute(grouped_plain_kernel<BF16, WGRAD>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    e = cudaFuncSetAttribute(grouped_plain_kernel<BF16, WGRAD, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (e != cudaSuccess) return e;
     done[dev].store(true);
   }
@@ -358,15 +411,16 @@ cudaError_t launch(const GroupedParams& p, int ctas, cudaStream_t stream) {
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   add_pdl_attribute(cfg, attr);
-  e = cudaLaunchKernelEx(&cfg, grouped_plain_kernel<BF16, WGRAD>, p);
+  e = cudaLaunchKernelEx(&cfg, grouped_plain_kernel<BF16, WGRAD, F32>, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_grouped_plain(bool bf16, bool wgrad, const GroupedParams& p, int ctas, cudaStream_t stream) {
-  if (wgrad) return bf16 ? launch<true, true>(p, ctas, stream) : launch<false, true>(p, ctas, stream);
-  return bf16 ? launch<true, false>(p, ctas, stream) : launch<false, false>(p, ctas, stream);
+  if (!wgrad) return bf16 ? launch<true, false, false>(p, ctas, stream) : launch<false, false, false>(p, ctas, stream);
+  if (p.out_f32) return bf16 ? launch<true, true, true>(p, ctas, stream) : launch<false, true, true>(p, ctas, stream);
+  return bf16 ? launch<true, true, false>(p, ctas, stream) : launch<false, true, false>(p, ctas, stream);
 }
 
 }  // namespace ttc
