@@ -54,7 +54,7 @@ def test_producers_wait_for_their_loads(name):
     text = source(name)
     armed = {m.group(1) for m in re.finditer(r"mbar_arrive_expect_tx\(&(\w+)\[", text)}
     assert armed == set(RINGS[name])
-    calls = list(re.finditer(r"\bdrain_ring\(\s*(\w+)\s*,", text))
+    calls = list(re.finditer(r"\bdrain_ring(?:_lanes)?\(\s*(\w+)\s*,", text))
     calls = [c for c in calls if c.group(1) in armed]
     assert [c.group(1) for c in calls] == RINGS[name]
     for c in calls:
@@ -62,7 +62,7 @@ def test_producers_wait_for_their_loads(name):
         heads = enclosing(text, c.start())
         if "leader" in heads[0]:
             heads = heads[1:]
-        assert re.search(r"\(lane == 0\)", heads[0]), heads[0]
+        assert re.search(r"\(lane == 0\)|^if \(warp == 0\)$", heads[0]), heads[0]
         before = text[:c.start()].rstrip()
         assert not before.endswith(")") or before.endswith("if (leader)"), before[-40:]
     assert not re.search(r"if \(!ok[^{;]*\{?\s*(for[^{;]*;[^{;]*;[^{)]*\)\s*)?(if[^;{]*)?drain_", text)

@@ -112,13 +112,14 @@ __global__ void __launch_bounds__(kThreads, 1) i8_tokens_kernel(const __grid_con
   grid_dependency_wait();
   grid_dependents_launch();
 
+  uint32_t armed = 0, armed_parity = 0;  // stages that the producer has armed
   if (warp == 0) {
     // ---------------------------------------------------------------- producer
     if (lane == 0) {
       const uint64_t keep = policy_evict_last();
       const uint64_t pol_w = gridDim.y == 1 ? policy_evict_first() : keep;
       int stage = 0;
-      uint32_t phase = 0, armed = 0, armed_parity = 0;
+      uint32_t phase = 0;
       for (int n = 0; n < n_stages; ++n) {
         if (!mbar_wait(&empty[stage], phase ^ 1u, wc)) break;
         uint8_t* w = ring + stage * stage_bytes;
@@ -132,7 +133,6 @@ __global__ void __launch_bounds__(kThreads, 1) i8_tokens_kernel(const __grid_con
           phase ^= 1u;
         }
       }
-      drain_ring(full, S, armed, armed_parity);
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer
@@ -255,7 +255,10 @@ __global__ void __launch_bounds__(kThreads, 1) i8_tokens_kernel(const __grid_con
   const int col = threadIdx.x & 127, f = f0 + col;
   const bool f_ok = col < q.tile_cols && f < p.N;
   const float scale_b = f_ok ? __ldg(p.scaleB + f) : 0.0f, bias = f_ok && p.bias != nullptr ? __ldg(p.bias + f) : 0.0f;
-  // every MMA is done (the issuer waited) and every byte is read
+  if (warp == 0) {  // after the loads above, which would come late behind it
+    drain_ring_lanes(full, armed, armed_parity);
+  }
+  // every MMA is done (the issuer waited) and every byte is there and read
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
