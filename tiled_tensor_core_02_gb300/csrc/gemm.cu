@@ -654,7 +654,6 @@ ttc_status host_env(HostEnv& env) {
   env.timeout_ns = (uint64_t)g_timeout_ns.load();
   env.inject_stall = g_inject_stall.load();
   env.plain_loads = g_force_generic_load.load() != 0;
-  env.plain_stores = g_force_generic_store.load() != 0;
   return TTC_OK;
 }
 

@@ -22,7 +22,6 @@ struct HostEnv {
   uint64_t timeout_ns;  // budget of a kernel's barrier waits
   int inject_stall;
   bool plain_loads;  // TTC_KNOB_FORCE_GENERIC_LOAD
-  bool plain_stores;  // TTC_KNOB_FORCE_GENERIC_STORE
 };
 
 // The current device, set up on first use.

@@ -36,7 +36,7 @@ constexpr int kI8RowsChunk = 256;     // of K
 cudaError_t launch_i8_rows(const I8ScaledParams& p, I8ResultType out, cudaStream_t stream);
 
 // The tensor-core kernel for some hundred tokens (i8_tokens.cu): token
-// blocks of 16, 32 and 64, tiles of 8 to 128 output channels, K shared by the
+// blocks of 32 and 64, tiles of 8 to 128 output channels, K shared by the
 // `split` CTAs of a cluster.  A CTA holds an accumulator for every 1024 of its K,
 // 256 columns of them: at most kI8TokenCols / block * 1024 of K a CTA.
 struct I8TokensParams {

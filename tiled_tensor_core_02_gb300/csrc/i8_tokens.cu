@@ -265,7 +265,8 @@ __global__ void __launch_bounds__(kThreads, 1) i8_tokens_kernel(const __grid_con
 
   // ------------------------------------------------------------------ sums and result
   // four sets of four warps; set g takes the tokens from g * kCols on, a thread a channel
-  constexpr int kCols = BT >= 64 ? 16 : 8;
+  constexpr int kCols = BT / 4;
+  static_assert(kCols == 8 || kCols == 16, "blocks of 32 or 64 tokens");
   int32_t* red = reinterpret_cast<int32_t*>(slots);  // [token][128 channels]
   const int tokens = min(BT, p.M - token0);
   auto result = [&](int32_t s, int token, float scale_a) {
@@ -281,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1) i8_tokens_kernel(const __grid_con
   if (warp >= kWarp0) {
     const int group = (warp - kWarp0) >> 2, quarter = warp & 3;
     const int c0 = group * kCols;
-    if (c0 < BT && quarter * 32 < q.tile_cols) {
+    if (quarter * 32 < q.tile_cols) {
       const int parts = (n_stages + kAccStages - 1) / kAccStages;
       int32_t sum[kCols];
 #pragma unroll
@@ -411,7 +412,6 @@ int i8_tokens_clusters(int split) {
 
 cudaError_t launch_i8_tokens(const I8TokensParams& q, int block, I8ResultType out, cudaStream_t stream) {
   switch (block) {
-    case 16: return launch_block<16>(q, out, stream);
     case 32: return launch_block<32>(q, out, stream);
     case 64: return launch_block<64>(q, out, stream);
   }

@@ -436,7 +436,7 @@ ttc_status ttc_gemm_i8_scaled(int64_t M, int64_t N, int64_t K, const int8_t* A, 
   p.act = (int)act;
   p.a_vec = aligned(A, 16) && lda % 16 == 0;
   p.b_vec = aligned(B, 16) && ldb % 16 == 0;
-  const int block = M <= 16 ? 16 : M <= 32 ? 32 : 64;
+  const int block = M <= 32 ? 32 : 64;
   double few_us = 0.0;
   const bool few = M > 16 && i8_tokens_plan(q, block, env, few_us);
   if (workspace != nullptr && aligned(workspace, 256) && takes_i8_pair(M, N, K, A, lda, B, ldb) && !env.plain_loads) {
