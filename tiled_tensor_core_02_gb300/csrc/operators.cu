@@ -84,7 +84,10 @@ bool pair_maps(GroupedParams& p, bool wgrad, ttc_dtype dtype, const HostEnv& env
 // tiles of `blocks` blocks of tokens fill whole waves of SMs (of more than three
 // waves the last one costs less than narrower tiles do: 64 groups, 4099 x 1536 x 2048
 // 79.6 us with 128 columns, 84.8 with 112); with the columns contiguous in memory
-// (TMA boxes of 64) 64 or 128.
+// (TMA boxes of 64) 64 or 128.  `blocks` is an estimate, so the second and third wave
+// may miss: over 48 random cases of up to 64 rows a group they took 0.88 (8 groups,
+// 34 rows, 2944 x 1728: 15.7 us against 18.0) to 1.36 times (7 groups, 33 rows,
+// 2752 x 2432: 17.0 against 12.5) what one wave, else 128 columns, takes.
 int few_tile_cols(int64_t blocks, int64_t n, int sm_count, bool cols_contiguous) {
   int64_t c = 128;
   for (int64_t waves = 1; waves <= 3; ++waves) {
@@ -120,14 +123,19 @@ bool few_maps(GroupedParams& p, ttc_dtype dtype, int tokens, int64_t matrices, c
                  : encode_matrices(&p.tmB, dt, 2, p.B, p.K, p.N, p.ldb, mats, p.strideB, kBK, p.tile_cols, sw));
 }
 
-// Block of tokens for groups of `mean` rows on average, `most` at most; 0: not
-// few.  Blocks of 64 and the CTA-pair kernel meet at about 80 rows a group (64
-// rows: 79.6 against 83 us in the case above; blocks of 128 leave shared memory
-// for three stages of the pipeline only, 87 to 94 us).
-int few_block(int64_t mean, int64_t most) {
-  if (most <= 16 || mean <= 8) return 16;
-  if (most <= 32 || mean <= 16) return 32;
-  return mean <= 80 ? 64 : 0;
+// Block of tokens for `rows` rows of `groups` groups; 0: not few.  Up to 64 rows a
+// group on the average blocks of 64 are the faster where groups are alike: 64 rows of
+// 8, 16, 32 and 64 groups, 4096 x 4096, 8192 x 1024, 1024 x 4096 and 1536 x 2048, 46, 50, 47
+// and 74 us against the CTA-pair kernel's 52, 51, 51 and 76.  Uneven groups, of which the
+// larger read their weights again, come out on either side (53, 58, 53 and 73 against 52,
+// 51, 51 and 77).  Above, even ones need a second block: 72 rows 65, 85, 70 and 95 against
+// 52, 51, 52 and 76.  (Blocks of 128 leave shared memory for three stages of the
+// pipeline only: 87 to 94 us in the case above.)
+int few_block(int64_t rows, int64_t groups) {
+  const int64_t mean = blocks_of(rows, groups);
+  if (rows <= 16 || mean <= 8) return 16;
+  if (rows <= 32 || mean <= 16) return 32;
+  return rows / groups <= 64 ? 64 : 0;
 }
 
 // The tensor-core kernel that widens the weights on its way: the tile's channels
@@ -259,7 +267,7 @@ ttc_status ttc_gemm_grouped(int64_t groups, int64_t M, int64_t N, int64_t K, con
   p.ldd = ldd;
   p.d_vec = aligned(D, 16) && ldd % 8 == 0;
   const int64_t likely = groups < M ? groups : M;  // groups with rows, as far as the host knows
-  const int block = few_block(blocks_of(M, likely), M);
+  const int block = few_block(M, likely);
   if (block != 0 && few_maps(p, dtype, block, likely, env)) {
     const int64_t tiles = (blocks_of(M, block) + likely) * p.col_blocks;
     if (launch_few_tokens(dtype == TTC_BF16, block, p, (int)(tiles < env.sm_count ? tiles : env.sm_count),
