@@ -207,7 +207,8 @@ ttc_status ttc_gemm_grouped(int64_t groups, int64_t M, int64_t N, int64_t K,
  * the gradient of its result, D_g is the gradient of a row-major B_g; with A
  * and B exchanged, of a column-major one.  C_g and D_g are row-major at
  * C + g * strideC and D + g * strideD (pitches ldc, ldd >= N).  out_dtype, the
- * type of C and D, is dtype (fp16 or bf16) or TTC_F32; sums are fp32.  C is
+ * type of C and D, is dtype (fp16 or bf16) or TTC_F32; sums are fp32 (for fp32
+ * results partial sums of 768 rows, added up rounded to nearest).  C is
  * read only when beta != 0 and may be D itself (same pitch and stride), which
  * adds up micro-batches in place.  offsets as in ttc_gemm_grouped.  An empty
  * group gives D_g = beta * C_g (zeros with beta == 0).

@@ -22,16 +22,16 @@
 //   CTA's `full` barrier, as the producers do for every other stage.  The
 //   producer goes on with the next tile meanwhile.
 // * fp32 results (wgrad): the tensor cores cut, not round, each addition to the
-//   accumulator, an error that grows with the number of tokens (measured 4.5e-6
-//   of the result after 2000 to 5600 tokens).  Every kChunkKBlocks k-blocks a fresh
+//   accumulator, an error that grows with the number of tokens (6.4e-6
+//   of the result after 8192).  Every kChunkKBlocks k-blocks a fresh
 //   accumulator is started and the epilogue warps add up the partial sums in
 //   registers, rounded to nearest.
 // * C (wgrad) comes while the tile's products do.  16-bit C is read before the
 //   accumulator is waited for; fp32 C joins the partial sums 32 columns at a time
 //   between the accumulators.  Read at the end, a block at a time, or all of it at
 //   the tile's start, it met the next tile's operands on their way from L2, which
-//   they fill, and held the tensor cores up: 8 x 4096 x 4096, 16384 tokens, 414 and
-//   424 us against 381 (without C 335).
+//   they fill, and held the tensor cores up: 8 x 4096 x 4096, 16384 tokens in equal
+//   groups, 414 and 424 us against 381 in one burst of all (without C 335).
 //
 // int8 products with scales run here too, on fp16 copies of the operands (every
 // int8 value is exact in fp16, every product and sum below 2^24 in fp32): one
@@ -50,9 +50,10 @@
 // one with K contiguous: with a box per k-block the issuing thread, at about 70 ns
 // an instruction, set the pace.
 //
-// Bound by the tensor cores, at clocks that the power cap holds to 1.5 to 1.6 GHz:
-// 16384 x 4096 x 4096 bf16 over 8 equal groups 305 us forward, 300 for the weights'
-// gradient in bf16 and 335 in fp32; int8 8192 x 14336 x 4096 566 us with its copies.
+// Bound by the tensor cores.  In bursts (replayed; the power cap, which holds longer
+// runs to 1.5 to 1.6 GHz, adds a tenth): 16384 x 4096 x 4096 bf16 over 8 equal groups
+// 305 us forward, 302 for the weights' gradient in bf16 (331 added to C) and 346 to 372
+// in fp32 (399 to 415 added to C); int8 8192 x 14336 x 4096 568 us with its copies.
 #include <atomic>
 #include <type_traits>
 

@@ -15,11 +15,12 @@
 // the epilogue warps add up in tensor memory: 7e-7 of the result however many
 // tokens there are, where one accumulator over 8192 is at 6.4e-6.
 //
-// Bound by the producers, which a k-block of 2 x 16 KB takes 1.1 us (asking L2 for
+// Bound by the producers, which a k-block of 2 x 16 KB takes 1.0 us (asking L2 for
 // its lines four k-blocks ahead changed nothing): 8192 rows over 8 groups, 4099 x
-// 4099, 1164 us or 236 TFLOP/s; 856 rows over 32 groups, 2712 x 3337, 349 us, where
-// loads of single elements took 1633.  Operands TMA can read take the other
-// kernels.
+// 4099, 1064 us or 259 TFLOP/s, the gradient 1110; 856 rows over 32 groups, 2712 x
+// 3337, 320 us, where loads of single elements took 1633; 32 rows over 4 groups,
+// 1001 x 4095, 69 us, 64 k-blocks one after the other.  Operands TMA can read take
+// the other kernels.
 #include "grouped_common.cuh"
 
 #include <atomic>

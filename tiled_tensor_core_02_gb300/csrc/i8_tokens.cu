@@ -25,7 +25,7 @@
 // activation follow.
 //
 // Bound by HBM's share of an SM or the widening of a stage (0.3 to 0.4 us), whichever
-// is more, and at these sizes by what surrounds the stream: 24 x 8192 x 8192 17.2 us,
+// is more, and at these sizes by what surrounds the stream: 24 x 8192 x 8192 17.0 us,
 // 10 of them at 6.7 TB/s, 1.7 before the first stage is there, 4 for the sums and
 // their exchange; 256 x 4096 x 4096 17.6 us.
 #include <atomic>
