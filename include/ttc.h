@@ -76,10 +76,15 @@ typedef enum {
 
 typedef enum { TTC_ROW_MAJOR = 0, TTC_COL_MAJOR = 1 } ttc_layout;
 
-typedef enum { TTC_ACT_NONE = 0, TTC_ACT_RELU = 1, TTC_ACT_GELU_TANH = 2 } ttc_act;
+/* TTC_ACT_SILU = v / (1 + exp(-v)) is one of the gated calls only; others refuse it (TTC_ERR_INVALID_ARG). */
+typedef enum { TTC_ACT_NONE = 0, TTC_ACT_RELU = 1, TTC_ACT_GELU_TANH = 2, TTC_ACT_SILU = 3 } ttc_act;
 
-/* TTC_F32 is the type of inputs and outputs of the calls that say so. */
-typedef enum { TTC_F16 = 0, TTC_BF16 = 1, TTC_I8 = 2, TTC_F32 = 3 } ttc_dtype;
+/*
+ * TTC_F32, and the 8-bit floats (e4m3: 4 bits of exponent, 3 of fraction, no
+ * infinities, up to 448; e5m2: up to 57344), are types of the calls that say
+ * so; others refuse the 8-bit ones as unknown.
+ */
+typedef enum { TTC_F16 = 0, TTC_BF16 = 1, TTC_I8 = 2, TTC_F32 = 3, TTC_F8_E4M3 = 4, TTC_F8_E5M2 = 5 } ttc_dtype;
 
 /*
  * D = act(alpha * A * B + beta * C + bias).  See the file comment for the
@@ -283,6 +288,130 @@ ttc_status ttc_gemm_i8_scaled(int64_t M, int64_t N, int64_t K,
 size_t ttc_gemm_i8_scaled_workspace_size(int64_t M, int64_t N, int64_t K,
                                          const int8_t* A, int64_t lda, const int8_t* B, int64_t ldb,
                                          const void* D, int64_t ldd, ttc_dtype out_dtype);
+
+/*
+ * A gated feed-forward block's first half in one launch: both projections, the
+ * activation and the product.  For every group g and every row i of it
+ *   G[i, :] = A[i, :] * Bgate_g,  U[i, :] = A[i, :] * Bup_g,
+ *   D[i, :] = act(G[i, :]) * U[i, :]   (element by element).
+ * act: any ttc_act, TTC_ACT_SILU included; without an activation the two are
+ * multiplied as they are.  A is M x K and D is M x N, both row-major.  Bgate_g
+ * and Bup_g are K x N, at g * strideB elements from Bgate and Bup, alike in
+ * layout and pitch (layoutB, ldb as in ttc_gemm); a matrix that holds both next
+ * to one another is given as two addresses.  fp16 or bf16 in and out; sums,
+ * activation and product are fp32, D is rounded once.
+ *
+ * Groups are those of ttc_gemm_grouped: offsets[g] .. offsets[g + 1] - 1 are
+ * group g's rows, read on the device and held to [0, M]; rows of no group are
+ * not written.  offsets may be NULL with groups == 1: all M rows are its.
+ *
+ * gate and up: NULL, or both M x N with pitch ldp, where G and U are kept,
+ * rounded, for ttc_gemm_gated_grad; they may be halves of one M x 2N buffer.
+ * D is computed from what they were before that rounding.
+ *
+ * Asynchronous on `stream`; allocates nothing; may be captured (ttc_gemm's
+ * notes apply).  Operands TMA can read (see ttc_gemm_grouped) run faster.
+ * TTC_ERR_INVALID_ARG: negative sizes or strides, pitches below the extent, NULL
+ * or misaligned pointers (one of gate and up NULL among them), an output
+ * overlapping an input or another output (side by side in rows of one pitch is
+ * no overlap), offsets NULL with groups > 1, an unknown enum value.
+ * TTC_ERR_UNSUPPORTED: TTC_I8 or TTC_F32, more than 1024 groups, sizes beyond
+ * 2^31 - 2^24.  groups, M or N == 0 is a no-op; K == 0 gives products of zeros.
+ */
+ttc_status ttc_gemm_gated(int64_t groups, int64_t M, int64_t N, int64_t K,
+                          const void* A, int64_t lda, const int32_t* offsets,
+                          const void* Bgate, const void* Bup, int64_t ldb, int64_t strideB, ttc_layout layoutB,
+                          void* D, int64_t ldd,
+                          void* gate, void* up, int64_t ldp,
+                          ttc_act act, ttc_dtype dtype, void* stream);
+
+/*
+ * Its backward pass up to the projections, in one launch: with A the gradient of
+ * the block's result (M x K, K the result's width) and B_g = K x N the transpose
+ * of the weights that follow the product, the gradient of D is dH = A * B_g, and
+ *   dgate = dH * U * act'(G),  dup = dH * act(G),  D = act(G) * U,
+ * G and U what ttc_gemm_gated kept (gate and up, pitch ldp).  dH is not rounded in
+ * between; dgate and dup (pitch lddp) are, once.  D may be NULL; where it is
+ * given it holds the block's product again, which the gradient of the following
+ * weights reads, so that the forward pass need not keep it.  ReLU's derivative at
+ * 0 is 0.  dgate and dup may be gate and up themselves (same pitch), or halves of
+ * one M x 2N buffer.  With both weights one 2N x K matrix W, rows of gate first,
+ * and P = [dgate dup], the input's gradient is ttc_gemm(P * W) and the weights'
+ * P^T * X, or their grouped forms.
+ *
+ * Groups, layouts, asynchrony and errors as ttc_gemm_gated; gate, up, dgate and
+ * dup are needed.  K == 0 gives zero gradients.
+ */
+ttc_status ttc_gemm_gated_grad(int64_t groups, int64_t M, int64_t N, int64_t K,
+                               const void* A, int64_t lda, const int32_t* offsets,
+                               const void* B, int64_t ldb, int64_t strideB, ttc_layout layoutB,
+                               const void* gate, const void* up, int64_t ldp,
+                               void* dgate, void* dup, int64_t lddp,
+                               void* D, int64_t ldd,
+                               ttc_act act, ttc_dtype dtype, void* stream);
+
+/*
+ * 8-bit floats with a scale for each block, the operands of ttc_gemm_f8_blocks:
+ *   scale = max |x| / top,  q = round(x * (1 / scale)) over each block,
+ * top the largest finite value of q_dtype (TTC_F8_E4M3: 448, TTC_F8_E5M2:
+ * 57344), every operation fp32 and rounded to nearest, the last one to the
+ * nearest 8-bit float with ties to even.  X is rows x cols, row-major with pitch
+ * ldx, of `dtype` (TTC_F16, TTC_BF16 or TTC_F32).  Q (pitch ldq) is X, or with
+ * transpose == 1 its transpose, cols x rows; a block is block_rows (1 or 128) rows
+ * by 128 columns of Q, fewer at its edges, and scale[(r / block_rows) * lds +
+ * c / 128] that of Q[r, c].  For a product along X's columns quantize X, along its
+ * rows (gradients of weights) its transpose; square blocks of X and of its
+ * transpose hold the same values.
+ *
+ * A block whose scale would be below 2^-126 counts as zeros: scale 0 and Q 0.  A
+ * block with a NaN or an infinity gets that as its scale and zeros in Q, so that
+ * its products are NaN.  Only Q's and scale's elements are written.
+ * Asynchronous on `stream`; allocates nothing.
+ * TTC_ERR_INVALID_ARG: negative sizes, pitches below the extent, NULL or misaligned
+ * pointers, overlapping arrays, another block_rows or transpose, an unknown enum
+ * value.  TTC_ERR_UNSUPPORTED: other types, sizes beyond 2^31 - 2^24.  rows or
+ * cols == 0 is a no-op.
+ */
+ttc_status ttc_quantize_blocks(int64_t rows, int64_t cols, const void* X, int64_t ldx, ttc_dtype dtype,
+                               int block_rows, int transpose,
+                               void* Q, int64_t ldq, ttc_dtype q_dtype,
+                               float* scale, int64_t lds, void* stream);
+
+/*
+ * Product of 8-bit floats with a scale for each block of 128 along K: for every
+ * group g and every row i of it
+ *   D[i, j] = act(sum over b of scaleA[i, b] * scaleB_g[j / block_rows_b, b] *
+ *                 sum over k of block b of A[i, k] * B_g[j, k], + C[i, j] + bias_g[j]).
+ * A is M x K and B_g is N x K, both row-major (typeA, typeB: TTC_F8_E4M3 or
+ * TTC_F8_E5M2, also one of each) as ttc_quantize_blocks writes them; scaleA is
+ * M x ceil(K / 128) with pitch ldsa, scaleB_g ceil(N / block_rows_b) x ceil(K / 128)
+ * with pitch ldsb, block_rows_b 1 or 128, all fp32 of any value (zero, negative
+ * and NaN among them).  B_g, scaleB_g and bias_g are strideB, strideSB and
+ * strideBias elements apart.  The sum over a block is the tensor cores' fp32 sum;
+ * the two scales' product, its product with that sum, the sum over the blocks, C,
+ * bias and activation are fp32, rounded to nearest.  C (pitch ldc, or NULL) and D
+ * have the type out_dtype: TTC_F16, TTC_BF16 or TTC_F32; C may be D itself with
+ * the same pitch, which adds up micro-batches in place.  bias_g is fp32[N]; bias
+ * may be NULL.
+ *
+ * Groups are those of ttc_gemm_grouped (offsets may be NULL with groups == 1: all M
+ * rows are its); rows of no group are not written.
+ * Asynchronous on `stream`; allocates nothing; may be captured (ttc_gemm's notes
+ * apply).  Rows of A and B on 16-byte boundaries run faster.
+ * TTC_ERR_INVALID_ARG: negative sizes or strides, pitches below the extent, NULL or
+ * misaligned pointers, D overlapping an input other than C in place, offsets NULL
+ * with groups > 1, another block_rows_b, an unknown enum value or act (TTC_ACT_SILU
+ * among them).  TTC_ERR_UNSUPPORTED: other types, more than 1024 groups, sizes
+ * beyond 2^31 - 2^24.  groups, M or N == 0 is a no-op; K == 0 gives act(C + bias_g).
+ */
+ttc_status ttc_gemm_f8_blocks(int64_t groups, int64_t M, int64_t N, int64_t K,
+                              const void* A, int64_t lda, ttc_dtype typeA, const float* scaleA, int64_t ldsa,
+                              const int32_t* offsets,
+                              const void* B, int64_t ldb, int64_t strideB, ttc_dtype typeB,
+                              const float* scaleB, int64_t ldsb, int64_t strideSB, int block_rows_b,
+                              const void* C, int64_t ldc, void* D, int64_t ldd,
+                              const float* bias, int64_t strideBias,
+                              ttc_act act, ttc_dtype out_dtype, void* stream);
 
 /*
  * As ttc_gemm, with caller-provided device workspace.  An operand that TMA

@@ -13,9 +13,13 @@ Names follow the C header include/ttc.h:
   ttc_launch_count() -> int
   ttc_gemm_grouped, ttc_gemm_grouped_wgrad, ttc_quantize_rows,
   ttc_gemm_i8_scaled[_workspace_size] -> status (size)
+  ttc_gemm_gated, ttc_gemm_gated_grad, ttc_quantize_blocks, ttc_gemm_f8_blocks
+  -> status
 plus `gemm(...)`, `gemm_grouped(...)`, `gemm_grouped_wgrad(...)`,
-`quantize_rows(...)` and `gemm_i8_scaled(...)`, convenience wrappers on torch
-tensors that read the layouts and leading dimensions off the tensors' strides.
+`quantize_rows(...)`, `gemm_i8_scaled(...)`, `gemm_gated(...)`,
+`gemm_gated_grad(...)`, `quantize_blocks(...)` and `gemm_f8_blocks(...)`,
+convenience wrappers on torch tensors that read the layouts and leading
+dimensions off the tensors' strides.
 Their work goes to `stream`, an address, or to the current stream; the caller
 orders it behind its inputs, and what reads a result on another stream behind it.
 """
@@ -27,8 +31,8 @@ import os
 from . import _build
 
 ROW_MAJOR, COL_MAJOR = 0, 1
-ACT = {"none": 0, "relu": 1, "gelu_tanh": 2}
-DTYPE = {"f16": 0, "bf16": 1, "i8": 2, "f32": 3}
+ACT = {"none": 0, "relu": 1, "gelu_tanh": 2, "silu": 3}
+DTYPE = {"f16": 0, "bf16": 1, "i8": 2, "f32": 3, "f8_e4m3": 4, "f8_e5m2": 5}
 STATUS = {0: "TTC_OK", 1: "TTC_ERR_INVALID_ARG", 2: "TTC_ERR_UNSUPPORTED", 3: "TTC_ERR_CUDA",
           4: "TTC_ERR_TIMEOUT", 5: "TTC_ERR_SCRATCH_TOO_SMALL"}
 STATIC_SCRATCH_BYTES = 16 * 1024 * 1024
@@ -42,6 +46,7 @@ EXPORTS = ("ttc_gemm", "ttc_gemm_strided_batched", "ttc_gemm_ws", "ttc_gemm_work
            "ttc_gemm_static_scratch", "ttc_transpose", "ttc_conv2d_fprop",
            "ttc_gemm_grouped", "ttc_gemm_grouped_wgrad", "ttc_quantize_rows", "ttc_gemm_i8_scaled",
            "ttc_gemm_i8_scaled_workspace_size",
+           "ttc_gemm_gated", "ttc_gemm_gated_grad", "ttc_quantize_blocks", "ttc_gemm_f8_blocks",
            "ttc_get_device_error", "ttc_status_string", "ttc_set_knob", "ttc_launch_count", "ttc_gemm_plan")
 
 _lib = None
@@ -97,6 +102,16 @@ def load():
     L.ttc_gemm_i8_scaled.restype = i
     L.ttc_gemm_i8_scaled_workspace_size.argtypes = [i64, i64, i64, vp, i64, vp, i64, vp, i64, i]
     L.ttc_gemm_i8_scaled_workspace_size.restype = ctypes.c_size_t
+    L.ttc_gemm_gated.argtypes = [i64, i64, i64, i64, vp, i64, vp, vp, vp, i64, i64, i, vp, i64, vp, vp, i64, i, i, vp]
+    L.ttc_gemm_gated.restype = i
+    L.ttc_gemm_gated_grad.argtypes = [i64, i64, i64, i64, vp, i64, vp, vp, i64, i64, i, vp, vp, i64, vp, vp, i64, vp, i64, i,
+                                      i, vp]
+    L.ttc_gemm_gated_grad.restype = i
+    L.ttc_quantize_blocks.argtypes = [i64, i64, vp, i64, i, i, i, vp, i64, i, vp, i64, vp]
+    L.ttc_quantize_blocks.restype = i
+    L.ttc_gemm_f8_blocks.argtypes = [i64, i64, i64, i64, vp, i64, i, vp, i64, vp, vp, i64, i64, i, vp, i64, i64, i, vp, i64,
+                                     vp, i64, vp, i64, i, i, vp]
+    L.ttc_gemm_f8_blocks.restype = i
     L.ttc_get_device_error.argtypes = [vp]
     L.ttc_get_device_error.restype = i
     L.ttc_status_string.argtypes = [i]
@@ -163,6 +178,29 @@ def ttc_gemm_i8_scaled(M, N, K, A, lda, scaleA, B, ldb, scaleB, D, ldd, bias, ac
 
 def ttc_gemm_i8_scaled_workspace_size(M, N, K, A, lda, B, ldb, D, ldd, out_dtype) -> int:
     return load().ttc_gemm_i8_scaled_workspace_size(M, N, K, A, lda, B, ldb, D, ldd, out_dtype)
+
+
+def ttc_gemm_gated(groups, M, N, K, A, lda, offsets, Bgate, Bup, ldb, strideB, layoutB, D, ldd, gate, up, ldp, act, dtype,
+                   stream) -> int:
+    """offsets: device address of groups + 1 int32, or None with one group; gate, up: None, or where to keep them."""
+    return load().ttc_gemm_gated(groups, M, N, K, A, lda, offsets, Bgate, Bup, ldb, strideB, layoutB, D, ldd, gate, up, ldp,
+                                 act, dtype, stream)
+
+
+def ttc_gemm_gated_grad(groups, M, N, K, A, lda, offsets, B, ldb, strideB, layoutB, gate, up, ldp, dgate, dup, lddp, D, ldd,
+                        act, dtype, stream) -> int:
+    return load().ttc_gemm_gated_grad(groups, M, N, K, A, lda, offsets, B, ldb, strideB, layoutB, gate, up, ldp, dgate, dup,
+                                      lddp, D, ldd, act, dtype, stream)
+
+
+def ttc_quantize_blocks(rows, cols, X, ldx, dtype, block_rows, transpose, Q, ldq, q_dtype, scale, lds, stream) -> int:
+    return load().ttc_quantize_blocks(rows, cols, X, ldx, dtype, block_rows, transpose, Q, ldq, q_dtype, scale, lds, stream)
+
+
+def ttc_gemm_f8_blocks(groups, M, N, K, A, lda, typeA, scaleA, ldsa, offsets, B, ldb, strideB, typeB, scaleB, ldsb, strideSB,
+                       block_rows_b, C, ldc, D, ldd, bias, strideBias, act, out_dtype, stream) -> int:
+    return load().ttc_gemm_f8_blocks(groups, M, N, K, A, lda, typeA, scaleA, ldsa, offsets, B, ldb, strideB, typeB, scaleB,
+                                     ldsb, strideSB, block_rows_b, C, ldc, D, ldd, bias, strideBias, act, out_dtype, stream)
 
 
 def ttc_gemm_ws(M, N, K, A, lda, layoutA, B, ldb, layoutB, C, ldc, D, ldd, alpha, beta, bias, act,
@@ -492,4 +530,198 @@ def gemm_i8_scaled(a, scale_a, b, scale_b, out=None, *, out_dtype=None, bias=Non
                                None if workspace is None else workspace.data_ptr(),
                                0 if workspace is None else workspace.numel() * workspace.element_size(), stream),
             "ttc_gemm_i8_scaled", check)
+    return out
+
+
+def _weights(b, groups, K, what):
+    """(N, layout, pitch, stride) of K x N weights: a matrix, or with groups one each."""
+    if b.dim() != (2 if groups is None else 3) or b.shape[-2] != K or (groups is not None and b.shape[0] != groups):
+        raise ValueError(f"{what} must be {'K x N' if groups is None else 'groups x K x N'} with a's K")
+    N = b.shape[-1]
+    if groups == 0:
+        return N, ROW_MAJOR, max(N, 1), 0
+    layout, ld = _matrix_layout(b if groups is None else b[0], K, N)
+    return N, layout, ld, 0 if groups is None else b.stride(0)
+
+
+def _half_of(t, N, what):
+    """The two M x N halves of an M x 2N tensor, their pitch."""
+    if t.dim() != 2 or t.shape[1] != 2 * N:
+        raise ValueError(f"{what} must be M x 2N")
+    return t.data_ptr(), t.data_ptr() + N * t.element_size(), _row_pitch(t, what)
+
+
+def _groups_of(offsets, device):
+    """Number of groups, None without offsets."""
+    if offsets is None:
+        return None
+    _check_offsets(offsets, offsets.numel() - 1, device)
+    if offsets.numel() < 1:
+        raise ValueError("offsets must be groups + 1 contiguous int32")
+    return offsets.numel() - 1
+
+
+def gemm_gated(a, b_gate, b_up, out=None, *, offsets=None, pre=None, act="silu", stream=None, check=True):
+    """out = act(a @ b_gate) * (a @ b_up): a gated feed-forward block up to its last projection.
+
+    a: M x K row-major, b_gate and b_up: K x N, row- or column-major alike (fp16/bf16
+    CUDA tensors; halves of one weight matrix are views of it).  With offsets (groups + 1
+    int32 on the device) the weights are groups x K x N and group g's rows use the g-th;
+    rows of no group are left as they are.  pre: M x 2N row-major, or True for a new one:
+    a @ b_gate and a @ b_up are kept side by side in it for gemm_gated_grad.
+    Returns out (M x N), with pre True (out, pre)."""
+    import torch
+
+    dt = _half(a, "a")
+    lda = _row_pitch(a, "a")
+    M, K = a.shape
+    groups = _groups_of(offsets, a.device)
+    N, layout, ldb, stride_b = _weights(b_gate, groups, K, "b_gate")
+    if b_up.shape != b_gate.shape or _weights(b_up, groups, K, "b_up") != (N, layout, ldb, stride_b):
+        raise ValueError("b_up must have b_gate's shape and strides")
+    new = pre is True
+    if new:
+        pre = _result((M, 2 * N), a.dtype, a.device, stream)
+    if out is None:
+        out = _result((M, N), a.dtype, a.device, stream)
+    _same(a.device, (a.dtype,), b_gate=b_gate, b_up=b_up, out=out, pre=pre)
+    if out.shape != (M, N):
+        raise ValueError("out must be M x N")
+    if pre is not None and pre.shape[0] != M:
+        raise ValueError("pre must be M x 2N")
+    ldd = _row_pitch(out, "out")
+    gate, up, ldp = (None, None, 0) if pre is None else _half_of(pre, N, "pre")
+    stream = _stream_of(stream, a.device)
+    _finish(ttc_gemm_gated(1 if groups is None else groups, M, N, K, a.data_ptr(), lda,
+                           None if offsets is None else offsets.data_ptr(), b_gate.data_ptr(), b_up.data_ptr(), ldb, stride_b,
+                           layout, out.data_ptr(), ldd, gate, up, ldp, ACT[act], DTYPE[dt], stream), "ttc_gemm_gated", check)
+    return (out, pre) if new else out
+
+
+def gemm_gated_grad(a, b, pre, dpre=None, out=None, *, offsets=None, act="silu", stream=None, check=True):
+    """Gradients of gemm_gated's two products, from the gradient of what follows them.
+
+    a: M x K row-major, the gradient of the block's result; b: K x N, row- or column-major:
+    the last projection read backwards, so that a @ b is the gradient of gemm_gated's out
+    (with offsets groups x K x N).  pre: M x 2N as gemm_gated kept it.  dpre: M x 2N, may be
+    pre itself.  out: M x N, or None: gets act(gate) * up again, for the gradient of b.
+    Returns dpre: dpre @ W, W the weights one above the other (2N x K'), is the gradient of
+    gemm_gated's a, and dpre.T @ a' that of W."""
+    import torch
+
+    dt = _half(a, "a")
+    lda = _row_pitch(a, "a")
+    M, K = a.shape
+    groups = _groups_of(offsets, a.device)
+    N, layout, ldb, stride_b = _weights(b, groups, K, "b")
+    if dpre is None:
+        dpre = _result((M, 2 * N), a.dtype, a.device, stream)
+    _same(a.device, (a.dtype,), b=b, pre=pre, dpre=dpre, out=out)
+    if pre.shape[0] != M or dpre.shape != pre.shape or (out is not None and out.shape != (M, N)):
+        raise ValueError("pre and dpre must be M x 2N, out M x N")
+    gate, up, ldp = _half_of(pre, N, "pre")
+    dgate, dup, lddp = _half_of(dpre, N, "dpre")
+    ldd = N if out is None else _row_pitch(out, "out")
+    stream = _stream_of(stream, a.device)
+    _finish(ttc_gemm_gated_grad(1 if groups is None else groups, M, N, K, a.data_ptr(), lda,
+                                None if offsets is None else offsets.data_ptr(), b.data_ptr(), ldb, stride_b, layout, gate, up,
+                                ldp, dgate, dup, lddp, None if out is None else out.data_ptr(), ldd, ACT[act], DTYPE[dt],
+                                stream), "ttc_gemm_gated_grad", check)
+    return dpre
+
+
+def _float8(dtype, what):
+    import torch
+
+    names = {torch.float8_e4m3fn: "f8_e4m3", torch.float8_e5m2: "f8_e5m2"}
+    if dtype not in names:
+        raise ValueError(f"{what} must be of torch.float8_e4m3fn or torch.float8_e5m2")
+    return names[dtype]
+
+
+def quantize_blocks(x, out=None, scale=None, *, block_rows=1, transpose=False, dtype=None, stream=None, check=True):
+    """(q, scale): 8-bit floats and a fp32 scale for each block of block_rows (1 or 128) x 128.
+
+    x: rows x cols row-major CUDA tensor (fp16/bf16/fp32).  q is x, or with transpose its
+    transpose, over the scales: q[i, j] * scale[i // block_rows, j // 128] is near it.
+    dtype, for a new q: torch.float8_e4m3fn (default) or torch.float8_e5m2.  A new q has rows
+    on 16-byte boundaries, which gemm_f8_blocks reads fastest."""
+    import torch
+
+    _same(x.device, (torch.float16, torch.bfloat16, torch.float32), x=x)
+    ldx = _row_pitch(x, "x")
+    if block_rows not in (1, 128):
+        raise ValueError("block_rows must be 1 or 128")
+    rows, cols = x.shape
+    r, c = (cols, rows) if transpose else (rows, cols)
+    if out is None:
+        out = _result((r, -(-c // 16) * 16), dtype or torch.float8_e4m3fn, x.device, stream)[:, :c]
+    q_dtype = _float8(out.dtype, "out")
+    shape = (-(-r // block_rows), -(-c // 128))
+    if scale is None:
+        scale = _result(shape, torch.float32, x.device, stream)
+    _same(x.device, (out.dtype,), out=out)
+    _same(x.device, (torch.float32,), scale=scale)
+    if out.shape != (r, c) or scale.shape != shape:
+        raise ValueError("out must have x's (the transpose's) shape and scale one element a block")
+    ldq, lds = _row_pitch(out, "out"), _row_pitch(scale, "scale")
+    dt = {torch.float16: "f16", torch.bfloat16: "bf16", torch.float32: "f32"}[x.dtype]
+    stream = _stream_of(stream, x.device)
+    _finish(ttc_quantize_blocks(rows, cols, x.data_ptr(), ldx, DTYPE[dt], block_rows, int(transpose), out.data_ptr(), ldq,
+                                DTYPE[q_dtype], scale.data_ptr(), lds, stream), "ttc_quantize_blocks", check)
+    return out, scale
+
+
+def gemm_f8_blocks(a, scale_a, b, scale_b, out=None, *, offsets=None, c=None, out_dtype=None, bias=None, act="none",
+                   stream=None, check=True):
+    """out = act((a over its scales) @ (b over its scales).T + c + bias), as quantize_blocks makes a and b.
+
+    a: M x K, b: N x K (torch.float8_e4m3fn or float8_e5m2 row-major CUDA tensors); scale_a: M x
+    blocks of 128 of K, scale_b: N x blocks, or blocks of 128 of N x blocks, fp32.  With offsets
+    (groups + 1 int32 on the device) b, scale_b and bias have a group dimension in front and group
+    g's rows of a use the g-th; rows of no group are left as they are.  out: M x N row-major, of
+    out_dtype (fp16, bf16 or fp32; a new out: bf16); c, of out's type, may be out itself; bias: N
+    fp32.  Returns out."""
+    import torch
+
+    ta, tb = _float8(a.dtype, "a"), _float8(b.dtype, "b")
+    lda = _row_pitch(a, "a")
+    M, K = a.shape
+    groups = _groups_of(offsets, a.device)
+    dims = 2 if groups is None else 3
+    if b.dim() != dims or b.shape[-1] != K or scale_b.dim() != dims or (groups is not None and (b.shape[0] != groups or scale_b.shape[0] != groups)):
+        raise ValueError("b and scale_b must be N x K and its blocks, with offsets one of each a group")
+    N, blocks = b.shape[-2], -(-K // 128)
+    if scale_a.shape != (M, blocks):
+        raise ValueError("scale_a must be M x blocks of 128 of K")
+    if scale_b.shape[-2:] == (N, blocks):
+        block_rows = 1
+    elif scale_b.shape[-2:] == (-(-N // 128), blocks):
+        block_rows = 128
+    else:
+        raise ValueError("scale_b must have N rows, or one for 128 of them, and a column for 128 of K")
+    if bias is not None and (bias.shape != ((N,) if groups is None else (groups, N)) or (N > 1 and bias.stride(-1) != 1)):
+        raise ValueError("bias must be N, with offsets groups x N, its rows contiguous")
+    if out is None:
+        out = _result((M, N), out_dtype or torch.bfloat16, a.device, stream)
+    _same(a.device, (torch.float16, torch.bfloat16, torch.float32), out=out)
+    _same(a.device, (b.dtype,), b=b)
+    _same(a.device, (torch.float32,), scale_a=scale_a, scale_b=scale_b, bias=bias)
+    _same(a.device, (out.dtype,), c=c)
+    if out.shape != (M, N) or (c is not None and c.shape != (M, N)):
+        raise ValueError("out and c must be M x N")
+    ldd, ldc = _row_pitch(out, "out"), N if c is None else _row_pitch(c, "c")
+    lds_a = _row_pitch(scale_a, "scale_a")
+    if groups is None:
+        (stride_b, ldb), (stride_sb, lds_b) = (0, _row_pitch(b, "b")), (0, _row_pitch(scale_b, "scale_b"))
+    else:
+        (stride_b, ldb), (stride_sb, lds_b) = _group_pitch(b, "b"), _group_pitch(scale_b, "scale_b")
+    odt = DTYPE[{torch.float16: "f16", torch.bfloat16: "bf16", torch.float32: "f32"}[out.dtype]]
+    stream = _stream_of(stream, a.device)
+    _finish(ttc_gemm_f8_blocks(1 if groups is None else groups, M, N, K, a.data_ptr(), lda, DTYPE[ta], scale_a.data_ptr(), lds_a,
+                               None if offsets is None else offsets.data_ptr(), b.data_ptr(), ldb, stride_b, DTYPE[tb],
+                               scale_b.data_ptr(), lds_b, stride_sb, block_rows, None if c is None else c.data_ptr(), ldc,
+                               out.data_ptr(), ldd, None if bias is None else bias.data_ptr(),
+                               0 if groups is None or bias is None else bias.stride(0), ACT[act], odt, stream),
+            "ttc_gemm_f8_blocks", check)
     return out

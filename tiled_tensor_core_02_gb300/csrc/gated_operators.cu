@@ -1,0 +1,174 @@
+// Host side of the gated feed-forward blocks: argument checks, the choice of a
+// kernel, tensor maps, launch.  See include/ttc.h for the contract.
+#include "operators_host.cuh"
+
+using namespace ttc;
+
+namespace {
+
+bool is_gated_act(ttc_act a) { return is_act(a) || a == TTC_ACT_SILU; }
+
+// A matrix of M rows and N columns.
+struct Rows {
+  const void* p;
+  int64_t ld;
+};
+int64_t rows_bytes(int64_t M, int64_t ld, int64_t N) { return span_bytes(1, 0, M, ld, N, 2); }
+bool overlap(Rows a, Rows b, int64_t M, int64_t N) {
+  return a.p != nullptr && b.p != nullptr && byte_ranges_overlap(a.p, rows_bytes(M, a.ld, N), b.p, rows_bytes(M, b.ld, N));
+}
+// Two matrices of the same pitch may lie side by side in one buffer: then their
+// spans overlap, their elements do not.
+bool side_by_side(Rows a, Rows b, int64_t N) {
+  if (a.ld != b.ld) return false;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  const uint64_t apart = (x < y ? y - x : x - y) % (uint64_t)(2 * a.ld);
+  return apart >= (uint64_t)(2 * N) && (uint64_t)(2 * a.ld) - apart >= (uint64_t)(2 * N);
+}
+bool clash(Rows a, Rows b, int64_t M, int64_t N) { return overlap(a, b, M, N) && !side_by_side(a, b, N); }
+
+// What both calls refuse of their products' operands; TTC_OK with `nothing` set for
+// an empty result.  The reads of A and B end inside a_bytes and b_bytes.
+struct Products {
+  bool nothing;
+  int64_t a_bytes, b_bytes;
+};
+ttc_status check_products(int64_t groups, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const int32_t* offsets,
+                          const void* B, int64_t ldb, int64_t strideB, ttc_layout layoutB, ttc_act act, ttc_dtype dtype,
+                          Products& out) {
+  out = Products{false, 0, 0};
+  if (groups < 0 || M < 0 || N < 0 || K < 0 || strideB < 0) return TTC_ERR_INVALID_ARG;
+  if (layoutB != TTC_ROW_MAJOR && layoutB != TTC_COL_MAJOR) return TTC_ERR_INVALID_ARG;
+  if (!is_gated_act(act) || !is_dtype(dtype)) return TTC_ERR_INVALID_ARG;
+  if (!is_16bit(dtype)) return TTC_ERR_UNSUPPORTED;
+  if (groups == 0 || M == 0 || N == 0) {
+    out.nothing = true;
+    return TTC_OK;
+  }
+  if (offsets == nullptr && groups != 1) return TTC_ERR_INVALID_ARG;
+  if (lda < at_least_1(K) || ldb < at_least_1(layoutB == TTC_ROW_MAJOR ? N : K)) return TTC_ERR_INVALID_ARG;
+  if (K > 0 && (A == nullptr || B == nullptr || !aligned(A, 2) || !aligned(B, 2))) return TTC_ERR_INVALID_ARG;
+  if (!aligned(offsets, 4)) return TTC_ERR_INVALID_ARG;
+  if (groups > kMaxGroups || M > kSizeLimit || N > kSizeLimit || K > kSizeLimit || lda > kSizeLimit || ldb > kSizeLimit ||
+      strideB > kStrideLimit)
+    return TTC_ERR_UNSUPPORTED;
+  if ((blocks_of(M, kGroupedPlainTile) + groups) * blocks_of(N, kGatedPlainCols) > kSizeLimit) return TTC_ERR_UNSUPPORTED;
+  if (K > 0) {
+    const int64_t b_rows = layoutB == TTC_ROW_MAJOR ? K : N, b_cols = layoutB == TTC_ROW_MAJOR ? N : K;
+    out.a_bytes = rows_bytes(M, lda, K);
+    out.b_bytes = span_bytes(groups, strideB, b_rows, ldb, b_cols, 2);
+  }
+  return TTC_OK;
+}
+
+// Whether an output may be written while A and B (of `b_bytes`) are read.
+bool hits_operands(Rows d, int64_t M, int64_t N, const Products& o, const void* A, const void* B, const void* U) {
+  if (d.p == nullptr || o.a_bytes == 0) return false;
+  const int64_t bytes = rows_bytes(M, d.ld, N);
+  return byte_ranges_overlap(d.p, bytes, A, o.a_bytes) || byte_ranges_overlap(d.p, bytes, B, o.b_bytes) ||
+         (U != nullptr && byte_ranges_overlap(d.p, bytes, U, o.b_bytes));
+}
+
+bool rows_on_16(const void* p, int64_t ld) { return aligned(p, 16) && ld % 8 == 0; }
+
+template <typename P>
+void gated_params(P& p, const HostEnv& env, int64_t groups, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,
+                  const int32_t* offsets, const void* B, int64_t ldb, int64_t strideB, ttc_layout layoutB, ttc_act act) {
+  std::memset(&p, 0, sizeof p);
+  common_params(p, env, groups, M, N, K, A, lda, B, ldb, offsets);
+  p.strideB = strideB;
+  p.b_mn = layoutB == TTC_ROW_MAJOR;
+  p.k_blocks = (int)blocks_of(K, kBK);
+  p.alpha = 1.0f;
+  p.act = (int)act;
+}
+
+// Launches the kernel for these operands.  `cols`: columns of D that a tile of plain
+// loads, or of a CTA pair's 256-wide tile over kGroupedPlainTile, has.
+template <typename P>
+ttc_status launch_gated(P& p, bool bf16, int plain_cols, const HostEnv& env, cudaStream_t stream) {
+  const int64_t groups = p.groups < p.M ? p.groups : p.M;  // that have rows
+  const int64_t col_blocks = blocks_of(p.N, plain_cols);
+  set_walk(p, 0, col_blocks, 4);
+  const int64_t tiles = (blocks_of(p.M, kGroupedPlainTile) + groups) * col_blocks;
+  if (launch_gated_plain(bf16, p, (int)(tiles < env.sm_count ? tiles : env.sm_count), stream) != cudaSuccess)
+    return TTC_ERR_CUDA;
+  count_launches(1);
+  return TTC_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+ttc_status ttc_gemm_gated(int64_t groups, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const int32_t* offsets,
+                          const void* Bgate, const void* Bup, int64_t ldb, int64_t strideB, ttc_layout layoutB, void* D,
+                          int64_t ldd, void* gate, void* up, int64_t ldp, ttc_act act, ttc_dtype dtype, void* stream) {
+  Products o;
+  ttc_status st = check_products(groups, M, N, K, A, lda, offsets, Bgate, ldb, strideB, layoutB, act, dtype, o);
+  if (st != TTC_OK || o.nothing) return st;
+  const bool save = gate != nullptr || up != nullptr;
+  if (D == nullptr || ldd < N || !aligned(D, 2) || (K > 0 && (Bup == nullptr || !aligned(Bup, 2)))) return TTC_ERR_INVALID_ARG;
+  if (save && (gate == nullptr || up == nullptr || ldp < N || !aligned(gate, 2) || !aligned(up, 2))) return TTC_ERR_INVALID_ARG;
+  if (ldd > kSizeLimit || (save && ldp > kSizeLimit)) return TTC_ERR_UNSUPPORTED;
+  const Rows d{D, ldd}, g{gate, ldp}, u{up, ldp};
+  if (hits_operands(d, M, N, o, A, Bgate, Bup) || hits_operands(g, M, N, o, A, Bgate, Bup) ||
+      hits_operands(u, M, N, o, A, Bgate, Bup) || clash(d, g, M, N) || clash(d, u, M, N) || clash(g, u, M, N))
+    return TTC_ERR_INVALID_ARG;
+
+  HostEnv env;
+  st = host_env(env);
+  if (st != TTC_OK) return st;
+  GatedForward p;
+  gated_params(p, env, groups, M, N, K, A, lda, offsets, Bgate, ldb, strideB, layoutB, act);
+  p.U = Bup;
+  p.D = D;
+  p.ldd = ldd;
+  p.d_vec = rows_on_16(D, ldd);
+  p.gate = gate;
+  p.up = up;
+  p.ldp = ldp;
+  p.p_vec = rows_on_16(gate, ldp) && rows_on_16(up, ldp);
+  return launch_gated(p, dtype == TTC_BF16, kGatedPlainCols, env, static_cast<cudaStream_t>(stream));
+}
+
+ttc_status ttc_gemm_gated_grad(int64_t groups, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,
+                               const int32_t* offsets, const void* B, int64_t ldb, int64_t strideB, ttc_layout layoutB,
+                               const void* gate, const void* up, int64_t ldp, void* dgate, void* dup, int64_t lddp, void* D,
+                               int64_t ldd, ttc_act act, ttc_dtype dtype, void* stream) {
+  Products o;
+  ttc_status st = check_products(groups, M, N, K, A, lda, offsets, B, ldb, strideB, layoutB, act, dtype, o);
+  if (st != TTC_OK || o.nothing) return st;
+  if (gate == nullptr || up == nullptr || dgate == nullptr || dup == nullptr || ldp < N || lddp < N || (D != nullptr && ldd < N))
+    return TTC_ERR_INVALID_ARG;
+  if (!aligned(gate, 2) || !aligned(up, 2) || !aligned(dgate, 2) || !aligned(dup, 2) || !aligned(D, 2)) return TTC_ERR_INVALID_ARG;
+  if (ldp > kSizeLimit || lddp > kSizeLimit || (D != nullptr && ldd > kSizeLimit)) return TTC_ERR_UNSUPPORTED;
+  const Rows g{gate, ldp}, u{up, ldp}, dg{dgate, lddp}, du{dup, lddp}, d{D, ldd};
+  const bool in_place = gate == dgate && up == dup && ldp == lddp;
+  if (hits_operands(dg, M, N, o, A, B, nullptr) || hits_operands(du, M, N, o, A, B, nullptr) ||
+      hits_operands(d, M, N, o, A, B, nullptr) || clash(dg, du, M, N) || clash(d, g, M, N) || clash(d, u, M, N) ||
+      clash(d, dg, M, N) || clash(d, du, M, N))
+    return TTC_ERR_INVALID_ARG;
+  if (!in_place && (clash(dg, g, M, N) || clash(dg, u, M, N) || clash(du, g, M, N) || clash(du, u, M, N)))
+    return TTC_ERR_INVALID_ARG;
+
+  HostEnv env;
+  st = host_env(env);
+  if (st != TTC_OK) return st;
+  GatedGrad p;
+  gated_params(p, env, groups, M, N, K, A, lda, offsets, B, ldb, strideB, layoutB, act);
+  p.D = D;
+  p.ldd = ldd;
+  p.d_vec = rows_on_16(D, ldd);
+  p.gate = const_cast<void*>(gate);
+  p.up = const_cast<void*>(up);
+  p.ldp = ldp;
+  p.p_vec = rows_on_16(gate, ldp) && rows_on_16(up, ldp);
+  p.dgate = dgate;
+  p.dup = dup;
+  p.lddp = lddp;
+  p.dp_vec = rows_on_16(dgate, lddp) && rows_on_16(dup, lddp);
+  return launch_gated(p, dtype == TTC_BF16, kGroupedPlainTile, env, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

@@ -13,6 +13,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 namespace ttc {
 
@@ -73,6 +74,35 @@ struct GroupedParams {
   FastDiv by_band, by_group, by_rest;
 };
 
+// Gated feed-forward blocks run on the grouped kernels too (offsets null: dense).
+//
+//   forward  D = act(A B) * (A U): B and U the gate's and the other projection's
+//            weights, alike in layout, pitch and stride; both products are kept
+//            where gate and up are given.
+//   grad     with dH = A B: dgate = dH * up * act'(gate), dup = dH * act(gate), and
+//            D = act(gate) * up where D is given.
+struct GatedParams : GroupedParams {
+  CUtensorMap tmU;  // forward: the kernels that load with TMA
+  const void* U;
+  void* gate;  // M x N; forward: written (or null), grad: read
+  void* up;
+  int64_t ldp;
+  int p_vec;
+  void* dgate;  // grad: written; may be gate and up themselves
+  void* dup;
+  int64_t lddp;
+  int dp_vec;
+};
+// The two as types of their own: kernels take one or the other.
+struct GatedForward : GatedParams {};
+struct GatedGrad : GatedParams {};
+template <typename P>
+constexpr bool kIsGatedForward = std::is_same<P, GatedForward>::value;
+template <typename P>
+constexpr bool kIsGatedGrad = std::is_same<P, GatedGrad>::value;
+template <typename P>
+constexpr bool kIsGated = kIsGatedForward<P> || kIsGatedGrad<P>;
+
 // Tile of the kernel of CTA pairs: 256 x 256.
 constexpr int kGroupedPairTile = 256;
 int grouped_pair_clusters();
@@ -90,5 +120,9 @@ cudaError_t launch_few_tokens(bool bf16, int tokens, const GroupedParams& p, int
 // Tile of the kernels that load with plain loads: 128 x 128.
 constexpr int kGroupedPlainTile = 128;
 cudaError_t launch_grouped_plain(bool bf16, bool wgrad, const GroupedParams& p, int ctas, cudaStream_t stream);
+// Gated blocks: tiles of 128 rows by 64 columns of D forward, of 128 by 128 of its gradient.
+constexpr int kGatedPlainCols = 64;
+cudaError_t launch_gated_plain(bool bf16, const GatedForward& p, int ctas, cudaStream_t stream);
+cudaError_t launch_gated_plain(bool bf16, const GatedGrad& p, int ctas, cudaStream_t stream);
 
 }  // namespace ttc

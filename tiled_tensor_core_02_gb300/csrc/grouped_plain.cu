@@ -21,7 +21,7 @@
 // 3337, 320 us, where loads of single elements took 1633; 32 rows over 4 groups,
 // 1001 x 4095, 69 us, 64 k-blocks one after the other.  Operands TMA can read take
 // the other kernels.
-#include "grouped_common.cuh"
+#include "gated_common.cuh"
 
 #include <atomic>
 #include <type_traits>
@@ -92,6 +92,8 @@ struct TilePieces {
 
 using Inner = TilePieces<kTile, kBK>;  // the reduction lies innermost
 using Outer = TilePieces<kBK, kTile>;  // outermost
+using HalfTile = TilePieces<kGatedPlainCols, kBK>;  // half of a gated block's columns, either way
+static_assert(kGatedPlainCols == kBK && 2 * kGatedPlainCols == kTile, "a gated tile's halves are square");
 
 // Tensor memory behind the two accumulators, for fp32 gradients: the sum of a tile's
 // accumulators (there are no registers for 128 columns a thread).
@@ -226,9 +228,48 @@ __device__ __forceinline__ void drain_tiles(const GroupedParams& p, const GroupT
   }
 }
 
-// F32: gradients in fp32.
-template <bool BF16, bool WGRAD, bool F32>
-__global__ void __launch_bounds__(kThreads, 1) grouped_plain_kernel(const __grid_constant__ GroupedParams p) {
+// The walk of a gated block's epilogue: forward both products of 64 columns lie side
+// by side in an accumulator, its gradient has two units of 64 columns.
+template <bool BF16, typename P>
+__device__ __forceinline__ void drain_gated(const P& p, const GroupTable& tb, int tiles, uint32_t tmem_base, uint8_t* sb,
+                                            uint64_t* tmem_full, uint64_t* tmem_empty, const WaitCtx& wc) {
+  const int q = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+  const bool has_k = p.k_blocks > 0;
+  int it = 0;
+  for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++it) {
+    const GroupedTile x = grouped_tile<kTile, false>(p, tb, t);
+    const int acc = it & 1;
+    const int r0 = x.rb * kTile + q * 32;
+    const int64_t row = (int64_t)x.lo + r0;
+    const int rows = max(0, min(32, x.hi - x.lo - r0));
+    const uint32_t at = tmem_base + ((uint32_t)(q * 32) << 16) + acc * kTile;
+    const auto wait = [&] {
+      const bool ok = mbar_wait_warp(&tmem_full[acc], (it >> 1) & 1, wc);
+      tc_fence_after();
+      return ok;
+    };
+    const auto release = [&] {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tmem_empty[acc]);
+    };
+    if constexpr (kIsGatedForward<P>) {
+      const int col = x.cb * kGatedPlainCols;
+      if (!wait()) break;
+      gated_forward_unit<BF16>(p, at, at + kGatedPlainCols, has_k, row, rows, col, p.N - col, sb, lane, release);
+    } else {
+      const int col = x.cb * kTile;
+      if (!gated_grad_unit<BF16>(p, at, has_k, row, rows, col, p.N - col, sb, lane, wait, [] {})) break;
+      if (!gated_grad_unit<BF16>(p, at + 64, has_k, row, rows, col + 64, p.N - col - 64, sb, lane, [] { return true; }, release))
+        break;
+    }
+  }
+}
+
+// F32: gradients in fp32.  P: GroupedParams, or those of a gated block.
+template <bool BF16, bool WGRAD, bool F32, typename P = GroupedParams>
+__global__ void __launch_bounds__(kThreads, 1) grouped_plain_kernel(const __grid_constant__ P p) {
+  static_assert(!kIsGated<P> || !(WGRAD || F32), "gated blocks are forward products");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sA = smem;
@@ -303,7 +344,18 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_plain_kernel(const __grid
           const int k0 = kb * kBK;
           Inner pa;
           pa.load(p.A, p.lda, x.lo + x.rb * kTile, k0, x.hi, p.K, tid);
-          if (p.b_mn) {
+          if constexpr (kIsGatedForward<P>) {
+            // 64 columns of the one's weights, then the same of the other's
+            const uint16_t* ug = static_cast<const uint16_t*>(p.U) + (int64_t)x.g * p.strideB;
+            HalfTile pg, pu;
+            const int outer = p.b_mn ? k0 : x.cb * kGatedPlainCols, inner = p.b_mn ? x.cb * kGatedPlainCols : k0;
+            const int outer_ext = p.b_mn ? p.K : p.N, inner_ext = p.b_mn ? p.N : p.K;
+            pg.load(bg, p.ldb, outer, inner, outer_ext, inner_ext, tid);
+            pu.load(ug, p.ldb, outer, inner, outer_ext, inner_ext, tid);
+            pa.store(a, tid);
+            pg.store(b, tid);
+            pu.store(b + kOperandBytes / 2, tid);
+          } else if (p.b_mn) {
             Outer pb;
             pb.load(bg, p.ldb, k0, n0, p.K, p.N, tid);
             pa.store(a, tid);
@@ -383,7 +435,11 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_plain_kernel(const __grid
   } else {
     // ---------------------------------------------------------------- epilogue
     using T = typename std::conditional<F32, float, uint16_t>::type;
-    drain_tiles<BF16, WGRAD, T>(p, tb, tiles, tmem_base, staging + (warp - kProducers) * 4096, tmem_full, tmem_empty, wc);
+    uint8_t* sb = staging + (warp - kProducers) * 4096;
+    if constexpr (kIsGated<P>)
+      drain_gated<BF16>(p, tb, tiles, tmem_base, sb, tmem_full, tmem_empty, wc);
+    else
+      drain_tiles<BF16, WGRAD, T>(p, tb, tiles, tmem_base, sb, tmem_full, tmem_empty, wc);
   }
   tc_fence_before();
   __syncthreads();
@@ -393,15 +449,15 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_plain_kernel(const __grid
   }
 }
 
-template <bool BF16, bool WGRAD, bool F32>
-cudaError_t launch(const GroupedParams& p, int ctas, cudaStream_t stream) {
+template <bool BF16, bool WGRAD, bool F32, typename P>
+cudaError_t launch(const P& p, int ctas, cudaStream_t stream) {
   static std::atomic<bool> done[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!done[dev].load()) {
-    e = cudaFuncSetAttribute(grouped_plain_kernel<BF16, WGRAD, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    e = cudaFuncSetAttribute(grouped_plain_kernel<BF16, WGRAD, F32, P>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (e != cudaSuccess) return e;
     done[dev].store(true);
   }
@@ -412,7 +468,7 @@ cudaError_t launch(const GroupedParams& p, int ctas, cudaStream_t stream) {
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   add_pdl_attribute(cfg, attr);
-  e = cudaLaunchKernelEx(&cfg, grouped_plain_kernel<BF16, WGRAD, F32>, p);
+  e = cudaLaunchKernelEx(&cfg, grouped_plain_kernel<BF16, WGRAD, F32, P>, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -422,6 +478,14 @@ cudaError_t launch_grouped_plain(bool bf16, bool wgrad, const GroupedParams& p, 
   if (!wgrad) return bf16 ? launch<true, false, false>(p, ctas, stream) : launch<false, false, false>(p, ctas, stream);
   if (p.out_f32) return bf16 ? launch<true, true, true>(p, ctas, stream) : launch<false, true, true>(p, ctas, stream);
   return bf16 ? launch<true, true, false>(p, ctas, stream) : launch<false, true, false>(p, ctas, stream);
+}
+
+cudaError_t launch_gated_plain(bool bf16, const GatedForward& p, int ctas, cudaStream_t stream) {
+  return bf16 ? launch<true, false, false>(p, ctas, stream) : launch<false, false, false>(p, ctas, stream);
+}
+
+cudaError_t launch_gated_plain(bool bf16, const GatedGrad& p, int ctas, cudaStream_t stream) {
+  return bf16 ? launch<true, false, false>(p, ctas, stream) : launch<false, false, false>(p, ctas, stream);
 }
 
 }  // namespace ttc
