@@ -23,7 +23,7 @@
 // MB): 105 us, 6.7 TB/s; the CTA-pair kernel takes 128.
 #include <atomic>
 
-#include "grouped_common.cuh"
+#include "gated_common.cuh"
 
 namespace ttc {
 
@@ -57,17 +57,42 @@ __device__ __forceinline__ GroupedTile few_tile(const GroupedParams& p, const Gr
   return x;
 }
 
-template <int BT, bool BF16>
-__global__ void __launch_bounds__(kThreads, 1) few_tokens_kernel(const __grid_constant__ GroupedParams p) {
+// 16 tokens of an output column of a gated block's gradient: what the products are
+// multiplied with comes while they are on their way.
+struct KeptTokens {
+  uint16_t gate[16], up[16];
+};
+__device__ __forceinline__ void load_kept(const GatedParams& p, int64_t row, int f, int tokens, bool f_ok, KeptTokens& k) {
+  const uint16_t* g = static_cast<const uint16_t*>(p.gate) + row * p.ldp + f;
+  const uint16_t* u = static_cast<const uint16_t*>(p.up) + row * p.ldp + f;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    const bool in = f_ok && j < tokens;
+    k.gate[j] = in ? g[j * p.ldp] : (uint16_t)0;
+    k.up[j] = in ? u[j * p.ldp] : (uint16_t)0;
+  }
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint16_t round_half(float v) {
+  return (uint16_t)(pack2<BF16>(v, 0.0f) & 0xFFFFu);
+}
+
+// P: GroupedParams, or those of a gated block; forward, a tile has the same columns of both
+// projections' weights in each stage and an accumulator for each.
+template <int BT, bool BF16, typename P>
+__global__ void __launch_bounds__(kThreads, 1) few_tokens_kernel(const __grid_constant__ P p) {
   constexpr int kTokenBytes = stage_bytes_of(BT);
   constexpr int kBox = few_tokens_box(BT);
-  constexpr int kTmemCols = 2 * BT;  // two accumulators: 32 to 128 columns
+  constexpr int kMats = kIsGatedForward<P> ? 2 : 1;  // weight matrices
+  constexpr int kAcc = kMats * BT;                   // columns of an accumulator
+  constexpr int kTmemCols = 2 * kAcc;  // two accumulators: 32 to 256 columns
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int w_bytes = stage_bytes_of(p.tile_cols);
-  const int stage_bytes = w_bytes + kTokenBytes;
+  const int stage_bytes = kMats * w_bytes + kTokenBytes;
   const int S = p.stages;
-  uint8_t* ring = smem;  // [stage][weights, tokens]
+  uint8_t* ring = smem;  // [stage][weights (of both projections), tokens]
   uint64_t* bars = reinterpret_cast<uint64_t*>(ring + S * stage_bytes + 16384);
   uint64_t* full = bars;
   uint64_t* empty = bars + kMaxStages;
@@ -99,6 +124,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_tokens_kernel(const __grid_co
       mbar_init(drain_bar, 1);
       prefetch_tmap(&p.tmA);
       prefetch_tmap(&p.tmB);
+      if constexpr (kMats == 2) prefetch_tmap(&p.tmU);
     }
     fence_barrier_init();
   }
@@ -139,10 +165,10 @@ __global__ void __launch_bounds__(kThreads, 1) few_tokens_kernel(const __grid_co
             break;
           }
           uint8_t* w = ring + stage * stage_bytes;
-          uint8_t* a = w + w_bytes;
+          uint8_t* a = w + kMats * w_bytes;
           // weights with their rows contiguous come in boxes of 128 of K whatever K is
           mbar_arrive_expect_tx(&full[stage],
-                                (two || p.b_mn ? w_bytes : w_bytes / 2) + (two ? 2 : 1) * boxes * (kBox * kBK * 2));
+                                kMats * (two || p.b_mn ? w_bytes : w_bytes / 2) + (two ? 2 : 1) * boxes * (kBox * kBK * 2));
           armed |= 1u << stage;
           armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
           if (p.b_mn) {
@@ -151,6 +177,11 @@ __global__ void __launch_bounds__(kThreads, 1) few_tokens_kernel(const __grid_co
           } else {
             tma_load_3d(w, &p.tmB, k0, f0, z, &full[stage], pol_w);
             if (two) tma_load_3d(w + w_blk, &p.tmB, k0 + kBK, f0, z, &full[stage], pol_w);
+          }
+          if constexpr (kMats == 2) {  // 64 columns at most: one box where they are contiguous
+            const int c0 = p.b_mn ? f0 : k0, c1 = p.b_mn ? k0 : f0;
+            tma_load_3d(w + w_bytes, &p.tmU, c0, c1, z, &full[stage], pol_w);
+            if (two && !p.b_mn) tma_load_3d(w + w_bytes + w_blk, &p.tmU, k0 + kBK, f0, z, &full[stage], pol_w);
           }
           for (int b = 0; b < boxes; ++b) {
             uint8_t* at = a + b * (kBox * kBK * 2);
@@ -171,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_tokens_kernel(const __grid_co
     const bool w_mn = p.b_mn;
     const uint32_t idesc = idesc_f16(BF16, w_mn, false, 128, BT);
     const uint64_t w0 = smem_desc_sw128(smem_u32(ring), w_mn ? 64 * kStageK * 2 : 16u, 1024);
-    const uint64_t a0 = smem_desc_sw128(smem_u32(ring + w_bytes), 16u, 1024);
+    const uint64_t a0 = smem_desc_sw128(smem_u32(ring + kMats * w_bytes), 16u, 1024);
     const uint32_t w_step = (w_mn ? 2048u : 32u) >> 4;
     const uint32_t w_kb = (uint32_t)(w_mn ? kBK * 128 : w_blk) >> 4;
     constexpr uint32_t kTokenKb = BT * 128 >> 4;
@@ -184,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_tokens_kernel(const __grid_co
       const int acc = it & 1;
       if (!mbar_wait_warp(&tmem_empty[acc], ((it >> 1) & 1) ^ 1u, wc)) break;
       tc_fence_after();
-      const uint32_t d = tmem_base + acc * BT;
+      const uint32_t d = tmem_base + acc * kAcc;
       for (int ks = 0; ks < k_stages; ++ks) {
         if (!mbar_wait_warp(&full[stage], phase, wc)) {
           ok = false;
@@ -194,19 +225,24 @@ __global__ void __launch_bounds__(kThreads, 1) few_tokens_kernel(const __grid_co
         const uint64_t wd = w0 + (uint32_t)(stage * stage_bytes >> 4);
         const uint64_t ad = a0 + (uint32_t)(stage * stage_bytes >> 4);
         const uint32_t add = ks != 0;
-        if (ks < whole) {  // no condition between the MMAs: each would cost as much as one
-          const uint32_t w_lo = (uint32_t)wd, w_hi = (uint32_t)(wd >> 32), a_lo = (uint32_t)ad, a_hi = (uint32_t)(ad >> 32);
-          mma_f16_lead_lo(lead, d, w_lo, w_hi, a_lo, a_hi, idesc, add);
 #pragma unroll
-          for (int k = 1; k < kStageK / kUmmaK; ++k)
-            mma_f16_lead_lo(lead, d, w_lo + (k >> 2) * w_kb + (k & 3) * w_step, w_hi, a_lo + (k >> 2) * kTokenKb + (k & 3) * 2u,
-                            a_hi, idesc, 1u);
-        } else {
-          const int steps = (p.K - ks * kStageK + kUmmaK - 1) / kUmmaK;
+        for (int m = 0; m < kMats; ++m) {
+          const uint64_t wm = wd + (uint32_t)(m * w_bytes >> 4);
+          const uint32_t dm = d + m * BT;
+          if (ks < whole) {  // no condition between the MMAs: each would cost as much as one
+            const uint32_t w_lo = (uint32_t)wm, w_hi = (uint32_t)(wm >> 32), a_lo = (uint32_t)ad, a_hi = (uint32_t)(ad >> 32);
+            mma_f16_lead_lo(lead, dm, w_lo, w_hi, a_lo, a_hi, idesc, add);
+#pragma unroll
+            for (int k = 1; k < kStageK / kUmmaK; ++k)
+              mma_f16_lead_lo(lead, dm, w_lo + (k >> 2) * w_kb + (k & 3) * w_step, w_hi, a_lo + (k >> 2) * kTokenKb + (k & 3) * 2u,
+                              a_hi, idesc, 1u);
+          } else {
+            const int steps = (p.K - ks * kStageK + kUmmaK - 1) / kUmmaK;
 #pragma unroll 1
-          for (int k = 0; k < steps; ++k)
-            mma_f16_lead(lead, d, wd + (k >> 2) * w_kb + (k & 3) * w_step, ad + (k >> 2) * kTokenKb + (k & 3) * 2u, idesc,
-                         add | (k != 0 ? 1u : 0u));
+            for (int k = 0; k < steps; ++k)
+              mma_f16_lead(lead, dm, wm + (k >> 2) * w_kb + (k & 3) * w_step, ad + (k >> 2) * kTokenKb + (k & 3) * 2u, idesc,
+                           add | (k != 0 ? 1u : 0u));
+          }
         }
         any = true;
         mma_commit_lead(lead, &empty[stage]);
@@ -235,26 +271,49 @@ __global__ void __launch_bounds__(kThreads, 1) few_tokens_kernel(const __grid_co
       const int row0 = x.lo + x.rb * BT, tokens = min(BT, x.hi - row0);
       const float bias = p.bias != nullptr && f_ok ? __ldg(p.bias + (int64_t)x.g * p.stride_bias + f) : 0.0f;
       uint16_t* d = static_cast<uint16_t*>(p.D) + (int64_t)row0 * p.ldd + f;
+      KeptTokens kept;
+      if constexpr (kIsGatedGrad<P>) load_kept(p, row0, f, tokens, f_ok, kept);
       const int acc = it & 1;
       if (!mbar_wait(&tmem_full[acc], (it >> 1) & 1, wc)) break;
       tc_fence_after();
 #pragma unroll 1
       for (int c = 0; c < BT; c += 16) {
-        uint32_t w[16];
-        tmem_ld_32x32b_x16<0>(tmem_mine + acc * BT + c, w);
+        uint32_t w[16], w2[16];
+        tmem_ld_32x32b_x16<0>(tmem_mine + acc * kAcc + c, w);
+        if constexpr (kMats == 2) tmem_ld_32x32b_x16<0>(tmem_mine + acc * kAcc + BT + c, w2);
         tmem_ld_wait();
         if (c + 16 == BT) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&tmem_empty[acc]);
         }
+        if constexpr (kIsGatedGrad<P>) {
+          if (c > 0) load_kept(p, row0 + c, f, tokens - c, f_ok, kept);
+        }
         if (f_ok) {
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             if (c + j < tokens) {
-              float v = p.alpha * __uint_as_float(w[j]);
-              if (p.bias != nullptr) v += bias;
-              d[(int64_t)(c + j) * p.ldd] = (uint16_t)(pack2<BF16>(act_value(p.act, v), 0.0f) & 0xFFFFu);
+              const int64_t r = c + j;
+              if constexpr (kIsGatedForward<P>) {
+                const float g = __uint_as_float(w[j]), u = __uint_as_float(w2[j]);
+                d[r * p.ldd] = round_half<BF16>(gated_act(p.act, g) * u);
+                if (p.gate != nullptr) {
+                  static_cast<uint16_t*>(p.gate)[(row0 + r) * p.ldp + f] = round_half<BF16>(g);
+                  static_cast<uint16_t*>(p.up)[(row0 + r) * p.ldp + f] = round_half<BF16>(u);
+                }
+              } else if constexpr (kIsGatedGrad<P>) {
+                const float dh = __uint_as_float(w[j]);
+                const float u = half_bits_to_float<BF16>(kept.up[j]), g = half_bits_to_float<BF16>(kept.gate[j]);
+                const ActSlope a = act_slope(p.act, g);
+                static_cast<uint16_t*>(p.dgate)[(row0 + r) * p.lddp + f] = round_half<BF16>(dh * u * a.slope);
+                static_cast<uint16_t*>(p.dup)[(row0 + r) * p.lddp + f] = round_half<BF16>(dh * a.value);
+                if (p.D != nullptr) d[r * p.ldd] = round_half<BF16>(gated_act(p.act, g) * u);
+              } else {
+                float v = p.alpha * __uint_as_float(w[j]);
+                if (p.bias != nullptr) v += bias;
+                d[r * p.ldd] = round_half<BF16>(act_value(p.act, v));
+              }
             }
           }
         }
@@ -269,43 +328,56 @@ __global__ void __launch_bounds__(kThreads, 1) few_tokens_kernel(const __grid_co
   }
 }
 
-template <int BT, bool BF16>
-cudaError_t launch(const GroupedParams& p, int ctas, cudaStream_t stream) {
+template <int BT, bool BF16, typename P>
+cudaError_t launch(const P& p, int ctas, cudaStream_t stream) {
   static std::atomic<bool> done[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!done[dev].load()) {
-    e = cudaFuncSetAttribute(few_tokens_kernel<BT, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+    e = cudaFuncSetAttribute(few_tokens_kernel<BT, BF16, P>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
     if (e != cudaSuccess) return e;
     done[dev].store(true);
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas, 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = fixed_bytes(p.groups) + p.stages * stage_bytes_of(p.tile_cols + BT);
+  cfg.dynamicSmemBytes = fixed_bytes(p.groups) + p.stages * stage_bytes_of((kIsGatedForward<P> ? 2 : 1) * p.tile_cols + BT);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   add_pdl_attribute(cfg, attr);
-  e = cudaLaunchKernelEx(&cfg, few_tokens_kernel<BT, BF16>, p);
+  e = cudaLaunchKernelEx(&cfg, few_tokens_kernel<BT, BF16, P>, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
 
-int few_tokens_stages(int tokens, int tile_cols, int groups) {
-  const int n = (kSmemLimit - fixed_bytes(groups)) / stage_bytes_of(tile_cols + tokens);
+int few_tokens_stages(int tokens, int weight_rows, int groups) {
+  const int n = (kSmemLimit - fixed_bytes(groups)) / stage_bytes_of(weight_rows + tokens);
   return n > kMaxStages ? kMaxStages : n;
 }
 
-cudaError_t launch_few_tokens(bool bf16, int tokens, const GroupedParams& p, int ctas, cudaStream_t stream) {
+template <typename P>
+static cudaError_t launch_blocks(bool bf16, int tokens, const P& p, int ctas, cudaStream_t stream) {
   switch (tokens) {
     case 16: return bf16 ? launch<16, true>(p, ctas, stream) : launch<16, false>(p, ctas, stream);
     case 32: return bf16 ? launch<32, true>(p, ctas, stream) : launch<32, false>(p, ctas, stream);
     case 64: return bf16 ? launch<64, true>(p, ctas, stream) : launch<64, false>(p, ctas, stream);
   }
   return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_few_tokens(bool bf16, int tokens, const GroupedParams& p, int ctas, cudaStream_t stream) {
+  return launch_blocks(bf16, tokens, p, ctas, stream);
+}
+
+cudaError_t launch_few_tokens(bool bf16, int tokens, const GatedForward& p, int ctas, cudaStream_t stream) {
+  return launch_blocks(bf16, tokens, p, ctas, stream);
+}
+
+cudaError_t launch_few_tokens(bool bf16, int tokens, const GatedGrad& p, int ctas, cudaStream_t stream) {
+  return launch_blocks(bf16, tokens, p, ctas, stream);
 }
 
 }  // namespace ttc

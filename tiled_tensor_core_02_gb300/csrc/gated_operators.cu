@@ -83,12 +83,43 @@ void gated_params(P& p, const HostEnv& env, int64_t groups, int64_t M, int64_t N
   p.act = (int)act;
 }
 
-// Launches the kernel for these operands.  `cols`: columns of D that a tile of plain
-// loads, or of a CTA pair's 256-wide tile over kGroupedPlainTile, has.
+// The other projection's map, where TMA reads its weights as it reads the gate's.
+bool map_up(GatedForward& p, ttc_dtype dtype, int box_rows) {
+  if (!tma_rows_ok(p.U, p.ldb, 2)) return false;
+  const CUtensorMapDataType dt = dtype == TTC_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
+  const int64_t mats = p.strideB != 0 ? p.groups : 1;
+  return p.b_mn ? encode_matrices(&p.tmU, dt, 2, p.U, p.N, p.K, p.ldb, mats, p.strideB, 64, 128, sw)
+                : encode_matrices(&p.tmU, dt, 2, p.U, p.K, p.N, p.ldb, mats, p.strideB, kBK, box_rows, sw);
+}
+bool map_up(GatedGrad&, ttc_dtype, int) { return true; }
+
+// Launches the kernel for these operands, as ttc_gemm_grouped chooses it.
 template <typename P>
-ttc_status launch_gated(P& p, bool bf16, int plain_cols, const HostEnv& env, cudaStream_t stream) {
-  const int64_t groups = p.groups < p.M ? p.groups : p.M;  // that have rows
-  const int64_t col_blocks = blocks_of(p.N, plain_cols);
+ttc_status launch_gated(P& p, ttc_dtype dtype, const HostEnv& env, cudaStream_t stream) {
+  constexpr bool kForward = kIsGatedForward<P>;
+  const bool bf16 = dtype == TTC_BF16;
+  const int64_t groups = p.groups < p.M ? p.groups : p.M;  // that have rows, as far as the host knows
+  const int block = few_block(p.M, groups);
+  if (block != 0 && few_maps(p, dtype, block, groups, env, kForward) && map_up(p, dtype, p.tile_cols)) {
+    const int64_t tiles = (blocks_of(p.M, block) + groups) * p.col_blocks;
+    if (launch_few_tokens(bf16, block, p, (int)(tiles < env.sm_count ? tiles : env.sm_count), stream) != cudaSuccess)
+      return TTC_ERR_CUDA;
+    count_launches(1);
+    return TTC_OK;
+  }
+  if (pair_maps(p, false, dtype, env) && map_up(p, dtype, 128)) {
+    const int clusters = grouped_pair_clusters();
+    if (clusters <= 0) return TTC_ERR_CUDA;
+    set_walk(p, 0, blocks_of(p.N, kForward ? kGatedPairCols : kGroupedPairTile), 3);
+    p.b_stream = p.M <= p.groups * kGroupedPairTile;
+    const int64_t tiles = (blocks_of(p.M, kGroupedPairTile) + groups) * p.col_blocks;
+    if (launch_gated_pair(bf16, p, (int)(2 * tiles < clusters ? 2 * tiles : clusters), stream) != cudaSuccess)
+      return TTC_ERR_CUDA;
+    count_launches(1);
+    return TTC_OK;
+  }
+  const int64_t col_blocks = blocks_of(p.N, kForward ? kGatedPlainCols : kGroupedPlainTile);
   set_walk(p, 0, col_blocks, 4);
   const int64_t tiles = (blocks_of(p.M, kGroupedPlainTile) + groups) * col_blocks;
   if (launch_gated_plain(bf16, p, (int)(tiles < env.sm_count ? tiles : env.sm_count), stream) != cudaSuccess)
@@ -129,7 +160,7 @@ ttc_status ttc_gemm_gated(int64_t groups, int64_t M, int64_t N, int64_t K, const
   p.up = up;
   p.ldp = ldp;
   p.p_vec = rows_on_16(gate, ldp) && rows_on_16(up, ldp);
-  return launch_gated(p, dtype == TTC_BF16, kGatedPlainCols, env, static_cast<cudaStream_t>(stream));
+  return launch_gated(p, dtype, env, static_cast<cudaStream_t>(stream));
 }
 
 ttc_status ttc_gemm_gated_grad(int64_t groups, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,
@@ -168,7 +199,7 @@ ttc_status ttc_gemm_gated_grad(int64_t groups, int64_t M, int64_t N, int64_t K, 
   p.dup = dup;
   p.lddp = lddp;
   p.dp_vec = rows_on_16(dgate, lddp) && rows_on_16(dup, lddp);
-  return launch_gated(p, dtype == TTC_BF16, kGroupedPlainTile, env, static_cast<cudaStream_t>(stream));
+  return launch_gated(p, dtype, env, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -107,15 +107,22 @@ constexpr bool kIsGated = kIsGatedForward<P> || kIsGatedGrad<P>;
 constexpr int kGroupedPairTile = 256;
 int grouped_pair_clusters();
 cudaError_t launch_grouped_pair(bool bf16, bool wgrad, const GroupedParams& p, int clusters, cudaStream_t stream);
+// The same kernel for gated blocks: 256 x 128 tiles of D forward, 256 x 256 of its gradient.
+constexpr int kGatedPairCols = 128;
+cudaError_t launch_gated_pair(bool bf16, const GatedForward& p, int clusters, cudaStream_t stream);
+cudaError_t launch_gated_pair(bool bf16, const GatedGrad& p, int clusters, cudaStream_t stream);
 // The same kernel for int8 products: fp16 copies of the operands, all rows one
 // group (no offsets), exact int32 sums, a scaled result (p.out_f32, or fp16 / bf16).
 cudaError_t launch_pair_i8_scaled(bool bf16_out, const GroupedParams& p, int clusters, cudaStream_t stream);
 
 // The kernel for few tokens: token tiles of 16, 32 and 64, tiles of 8 to 128
-// output columns.  tmA has boxes of few_tokens_box tokens.  Stages that fit:
+// output columns (gated forward: 64, as many rows of either weights a stage).  tmA
+// has boxes of few_tokens_box tokens.  Stages that fit:
 constexpr int few_tokens_box(int tokens) { return tokens < 32 ? tokens : 32; }
-int few_tokens_stages(int tokens, int tile_cols, int groups);
+int few_tokens_stages(int tokens, int weight_rows, int groups);
 cudaError_t launch_few_tokens(bool bf16, int tokens, const GroupedParams& p, int ctas, cudaStream_t stream);
+cudaError_t launch_few_tokens(bool bf16, int tokens, const GatedForward& p, int ctas, cudaStream_t stream);
+cudaError_t launch_few_tokens(bool bf16, int tokens, const GatedGrad& p, int ctas, cudaStream_t stream);
 
 // Tile of the kernels that load with plain loads: 128 x 128.
 constexpr int kGroupedPlainTile = 128;

@@ -57,8 +57,8 @@
 #include <atomic>
 #include <type_traits>
 
+#include "gated_common.cuh"
 #include "gemm2sm_kernel.cuh"
-#include "grouped_common.cuh"
 
 namespace ttc {
 
@@ -299,13 +299,64 @@ __device__ __forceinline__ void scaled_values(const GroupedParams& p, const uint
   }
 }
 
+// A gated block's tiles: this warp's 32 rows by 64 columns of D forward (of half a
+// tile 32), by 128 (of half a tile 64) of its gradient.
+template <bool BF16, typename P>
+__device__ __forceinline__ void gated_tiles(const P& p, const GroupTable& tb, const PairWalk& walk, int pair, int num_pairs,
+                                            uint32_t rank, int q, int part, uint32_t tmem_mine, uint8_t* sb, int lane,
+                                            uint64_t* tmem_full, uint64_t* tmem_empty, const WaitCtx& wc) {
+  const bool has_k = p.k_blocks > 0;
+  int it = 0;
+  for (int t = pair; t < walk.items; t += num_pairs, ++it) {
+    const PairItem item = pair_item<false>(p, tb, walk, t);
+    const GroupedTile& x = item.x;
+    const int r0 = x.rb * kTile + (int)rank * 128 + q * 32;
+    const int64_t row = (int64_t)x.lo + r0;
+    const int rows = max(0, min(32, x.hi - x.lo - r0));
+    const int acc = it & 1;
+    const uint32_t at = tmem_mine + acc * kTile;
+    const auto wait = [&] {
+      const bool ok = mbar_wait_warp(&tmem_full[acc], (it >> 1) & 1, wc);
+      tc_fence_after();
+      return ok;
+    };
+    const auto release = [&] {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&tmem_empty[acc]), 0));
+    };
+    if constexpr (kIsGatedForward<P>) {
+      const int width = item.half < 0 ? kTile / 4 : kTile / 8;  // of this warp; the tile has twice as many
+      const int col = x.cb * (kTile / 2) + max(item.half, 0) * (kTile / 4) + part * width;
+      if (!wait()) return;
+      gated_forward_unit<BF16>(p, at + part * width, at + (2 + part) * width, has_k, row, rows, col, min(width, p.N - col), sb,
+                               lane, release);
+    } else {
+      const int units = item.half < 0 ? 2 : 1;
+      const int col = x.cb * kTile + max(item.half, 0) * (kTile / 2) + part * units * 64;
+#pragma unroll 1
+      for (int u = 0; u < units; ++u)
+        if (!gated_grad_unit<BF16>(p, at + (part * units + u) * 64, has_k, row, rows, col + u * 64, p.N - col - u * 64, sb, lane,
+                                   [&] { return u > 0 || wait(); },
+                                   [&] {
+                                     if (u == units - 1) release();
+                                   }))
+          return;
+    }
+  }
+}
+
 // ADD: C is read (wgrad); a parameter of its own because the fp32 sums leave
 // few registers for it.
 // I8: forward with int8 sums, scaled; BF16 then is the type of a 16-bit result.
-template <bool BF16, bool WGRAD, bool F32, bool ADD, bool I8 = false>
+// P: GroupedParams, or those of a gated block, whose forward tiles are 256 rows by 128
+// columns of D: the even CTA stages the gate's 128 columns of weights, the odd one the
+// other projection's, so that an accumulator holds both side by side.
+template <bool BF16, bool WGRAD, bool F32, bool ADD, bool I8 = false, typename P = GroupedParams>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    grouped_pair_kernel(const __grid_constant__ GroupedParams p) {
+    grouped_pair_kernel(const __grid_constant__ P p) {
   static_assert(WGRAD || ((!F32 || I8) && !ADD), "forward results are 16-bit and added to nothing");
+  static_assert(!kIsGated<P> || !(WGRAD || F32 || ADD || I8), "gated blocks are forward products");
   static_assert(!WGRAD || !I8, "int8 products are forward ones");
   constexpr bool kSums = F32 || I8;  // partial sums in registers
   extern __shared__ uint8_t smem_raw[];
@@ -358,6 +409,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(drain_bar, 1);
       prefetch_tmap(&p.tmA);
       prefetch_tmap(&p.tmB);
+      if constexpr (kIsGatedForward<P>) prefetch_tmap(&p.tmU);
     }
     fence_barrier_init();
   }
@@ -389,7 +441,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const GroupedTile& x = item.x;
         const PairLoop l = pair_loop<WGRAD>(p, x);
         // of half a tile the MMA reads 64 columns, the first of the 128 that are loaded
-        const int n0 = x.cb * kTile + (item.half < 0 ? (int)rank * 128 : item.half * 128 + (int)rank * 64);
+        int n0 = x.cb * kTile + (item.half < 0 ? (int)rank * 128 : item.half * 128 + (int)rank * 64);
+        const CUtensorMap* map_b = &p.tmB;
+        if constexpr (kIsGatedForward<P>) {
+          n0 = x.cb * (kTile / 2) + max(item.half, 0) * (kTile / 4);
+          if (!leader) map_b = &p.tmU;
+        }
         const int m0 = (WGRAD ? 0 : x.lo) + x.rb * kTile + (int)rank * 128;
         // forward: whether this CTA's, and the other's, rows of A hold any of the group
         const bool a_on = WGRAD || m0 < x.hi;
@@ -427,10 +484,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // nothing to load
           } else if (clear) {
             load_share<false>(a, &p.tmA, WGRAD, nkb, m0, k0, 0, &fix[stage], 0, keep);
-            load_share<false>(b, &p.tmB, b_mn, nkb, n0, k0, zb, &fix[stage], 0, pol_b);
+            load_share<false>(b, map_b, b_mn, nkb, n0, k0, zb, &fix[stage], 0, pol_b);
           } else {
             if (a_on) load_share<true>(a, &p.tmA, WGRAD, nkb, m0, k0, 0, nullptr, full_leader, keep);
-            load_share<true>(b, &p.tmB, b_mn, nkb, n0, k0, zb, nullptr, full_leader, pol_b);
+            load_share<true>(b, map_b, b_mn, nkb, n0, k0, zb, nullptr, full_leader, pol_b);
           }
           if (++stage == kStages) {
             stage = 0;
@@ -527,6 +584,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t tmem_mine = tmem_base + ((uint32_t)(q * 32) << 16);
     int it = 0;
     bool ok = true;
+    if constexpr (kIsGated<P>) {
+      gated_tiles<BF16>(p, tb, walk, pair, num_pairs, rank, q, part, tmem_mine, sb, lane, tmem_full, tmem_empty, wc);
+      ok = false;
+    }
     for (int t = pair; ok && t < walk.items; t += num_pairs) {
       const EpiTile<T> e0 = epi_tile<WGRAD, T>(p, pair_item<WGRAD>(p, tb, walk, t), rank, q, part);
       if constexpr (kSums) {
@@ -751,7 +812,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
 }
 
-template <bool BF16, bool WGRAD, bool F32, bool ADD, bool I8 = false>
+template <bool BF16, bool WGRAD, bool F32, bool ADD, bool I8 = false, typename P = GroupedParams>
 cudaError_t prepare() {
   static std::atomic<bool> done[64];
   int dev = 0;
@@ -759,8 +820,8 @@ cudaError_t prepare() {
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!done[dev].load()) {
-    e = cudaFuncSetAttribute(grouped_pair_kernel<BF16, WGRAD, F32, ADD, I8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kSmemBytes);
+    e = cudaFuncSetAttribute(grouped_pair_kernel<BF16, WGRAD, F32, ADD, I8, P>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (e != cudaSuccess) return e;
     done[dev].store(true);
   }
@@ -784,9 +845,9 @@ int clusters_of() {
   return n;
 }
 
-template <bool BF16, bool WGRAD, bool F32, bool ADD, bool I8 = false>
-cudaError_t launch(const GroupedParams& p, int clusters, cudaStream_t stream) {
-  cudaError_t e = prepare<BF16, WGRAD, F32, ADD, I8>();
+template <bool BF16, bool WGRAD, bool F32, bool ADD, bool I8 = false, typename P = GroupedParams>
+cudaError_t launch(const P& p, int clusters, cudaStream_t stream) {
+  cudaError_t e = prepare<BF16, WGRAD, F32, ADD, I8, P>();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * clusters, 1, 1);
@@ -795,7 +856,7 @@ cudaError_t launch(const GroupedParams& p, int clusters, cudaStream_t stream) {
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   add_pdl_attribute(cfg, attr);
-  e = cudaLaunchKernelEx(&cfg, grouped_pair_kernel<BF16, WGRAD, F32, ADD, I8>, p);
+  e = cudaLaunchKernelEx(&cfg, grouped_pair_kernel<BF16, WGRAD, F32, ADD, I8, P>, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -813,6 +874,16 @@ cudaError_t launch_grouped_pair(bool bf16, bool wgrad, const GroupedParams& p, i
   if (p.out_f32) return add ? TTC_PAIR(true, true, true) : TTC_PAIR(true, true, false);
   return add ? TTC_PAIR(true, false, true) : TTC_PAIR(true, false, false);
 #undef TTC_PAIR
+}
+
+cudaError_t launch_gated_pair(bool bf16, const GatedForward& p, int clusters, cudaStream_t stream) {
+  return bf16 ? launch<true, false, false, false, false>(p, clusters, stream)
+              : launch<false, false, false, false, false>(p, clusters, stream);
+}
+
+cudaError_t launch_gated_pair(bool bf16, const GatedGrad& p, int clusters, cudaStream_t stream) {
+  return bf16 ? launch<true, false, false, false, false>(p, clusters, stream)
+              : launch<false, false, false, false, false>(p, clusters, stream);
 }
 
 cudaError_t launch_pair_i8_scaled(bool bf16_out, const GroupedParams& p, int clusters, cudaStream_t stream) {

@@ -75,4 +75,64 @@ inline bool pair_maps(GroupedParams& p, bool wgrad, ttc_dtype dtype, const HostE
                  : encode_matrices(&p.tmB, dt, 2, p.B, p.K, p.N, p.ldb, mats, p.strideB, kBK, 128, sw));
 }
 
+// Output columns of a few-token tile: as few, in steps of 8 up to 128, as let the
+// tiles of `blocks` blocks of tokens fill whole waves of SMs (of more than three
+// waves the last one costs less than narrower tiles do: 64 groups, 4099 x 1536 x 2048
+// 79.6 us with 128 columns, 84.8 with 112); with the columns contiguous in memory
+// (TMA boxes of 64) 64 or 128.  `blocks` is an estimate, so the second and third wave
+// may miss: over 48 random cases of up to 64 rows a group they took 0.88 (8 groups,
+// 34 rows, 2944 x 1728: 15.7 us against 18.0) to 1.36 times (7 groups, 33 rows,
+// 2752 x 2432: 17.0 against 12.5) what one wave, else 128 columns, takes.
+inline int few_tile_cols(int64_t blocks, int64_t n, int sm_count, bool cols_contiguous, int most) {
+  int64_t c = most;
+  for (int64_t waves = 1; waves <= 3; ++waves) {
+    const int64_t room = waves * sm_count / blocks;  // tiles of a block of tokens
+    if (room < 1 || blocks_of(n, room) > most) continue;
+    c = blocks_of(blocks_of(n, room), 8) * 8;
+    break;
+  }
+  if (cols_contiguous) return c > 64 ? most : 64;
+  return (int)c;
+}
+
+// Sets up the few-token kernel's tiles and tensor maps; false where TMA cannot
+// read the operands or no pipeline fits.  `matrices`: how many weight matrices
+// are likely to be read.  Groups near the mean take one block more as often as not
+// (256 rows of 4 groups, 1088 x 1040: tiles for four blocks 16.0 us, for six 11.1).
+// `pair`: columns of two weight matrices lie in a stage (p.tmB is the first's map; the
+// other's, alike, is the caller's).
+inline bool few_maps(GroupedParams& p, ttc_dtype dtype, int tokens, int64_t matrices, const HostEnv& env, bool pair = false) {
+  if (env.plain_loads || p.M == 0 || p.K == 0) return false;
+  if (!tma_rows_ok(p.A, p.lda, 2) || !tma_rows_ok(p.B, p.ldb, 2) || !tma_stride_ok(p.groups, p.strideB, 2)) return false;
+  const int64_t whole = blocks_of(blocks_of(p.M, matrices), tokens) * matrices;
+  const int64_t half_more = blocks_of(2 * p.M + tokens * matrices, 2 * tokens);
+  p.tile_cols = few_tile_cols(whole > half_more ? whole : half_more, p.N, env.sm_count, p.b_mn != 0, pair ? 64 : 128);
+  p.col_blocks = (int)blocks_of(p.N, p.tile_cols);
+  if ((blocks_of(p.M, tokens) + p.groups) * p.col_blocks > kSizeLimit) return false;
+  p.b_stream = p.M <= matrices * tokens;
+  p.stages = few_tokens_stages(tokens, (pair ? 2 : 1) * p.tile_cols, p.groups);
+  if (p.stages < 2) return false;
+  const CUtensorMapDataType dt = dtype == TTC_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
+  const int64_t mats = p.strideB != 0 ? p.groups : 1;
+  return encode_matrices(&p.tmA, dt, 2, p.A, p.K, p.M, p.lda, 1, 0, kBK, few_tokens_box(tokens), sw) &&
+         (p.b_mn ? encode_matrices(&p.tmB, dt, 2, p.B, p.N, p.K, p.ldb, mats, p.strideB, 64, 128, sw)
+                 : encode_matrices(&p.tmB, dt, 2, p.B, p.K, p.N, p.ldb, mats, p.strideB, kBK, p.tile_cols, sw));
+}
+
+// Block of tokens for `rows` rows of `groups` groups; 0: not few.  Up to 64 rows a
+// group on the average blocks of 64 are the faster where groups are alike: 64 rows of
+// 8, 16, 32 and 64 groups, 4096 x 4096, 8192 x 1024, 1024 x 4096 and 1536 x 2048, 46, 50, 47
+// and 74 us against the CTA-pair kernel's 52, 51, 51 and 76.  Uneven groups, of which the
+// larger read their weights again, come out on either side (53, 58, 53 and 73 against 52,
+// 51, 51 and 77).  Above, even ones need a second block: 72 rows 65, 85, 70 and 95 against
+// 52, 51, 52 and 76.  (Blocks of 128 leave shared memory for three stages of the
+// pipeline only: 87 to 94 us in the case above.)
+inline int few_block(int64_t rows, int64_t groups) {
+  const int64_t mean = blocks_of(rows, groups);
+  if (rows <= 16 || mean <= 8) return 16;
+  if (rows <= 32 || mean <= 16) return 32;
+  return rows / groups <= 64 ? 64 : 0;
+}
+
 }  // namespace ttc
