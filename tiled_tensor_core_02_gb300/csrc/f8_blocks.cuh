@@ -27,6 +27,10 @@ struct F8Params : GroupedParams {
 constexpr int kF8PlainTile = 64;
 cudaError_t launch_f8_plain(const F8Params& p, F8Result out, int ctas, cudaStream_t stream);
 
+// CTA pairs: tiles of 256 x 256 (kGroupedPairTile) of operands TMA can read.
+int f8_pair_clusters();
+cudaError_t launch_f8_pair(const F8Params& p, F8Result out, int clusters, cudaStream_t stream);
+
 // Rows (or blocks of 128 rows) of 8-bit floats from 16- or 32-bit ones.
 struct F8QuantParams {
   const void* x;

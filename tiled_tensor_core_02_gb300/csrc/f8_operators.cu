@@ -10,6 +10,17 @@ namespace {
 bool is_f8(ttc_dtype t) { return t == TTC_F8_E4M3 || t == TTC_F8_E5M2; }
 bool is_any_dtype(ttc_dtype t) { return is_dtype(t) || is_f8(t); }
 
+// Tensor maps of the operands, a block of 128 k by so many rows a box; false where TMA
+// cannot read them.
+bool f8_maps(F8Params& p, int rows_a, int rows_b, const HostEnv& env) {
+  if (env.plain_loads || p.K == 0) return false;
+  if (!tma_rows_ok(p.A, p.lda, 1) || !tma_rows_ok(p.B, p.ldb, 1) || !tma_stride_ok(p.groups, p.strideB, 1)) return false;
+  const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
+  return encode_matrices(&p.tmA, u8, 1, p.A, p.K, p.M, p.lda, 1, 0, kF8Block, rows_a, sw) &&
+         encode_matrices(&p.tmB, u8, 1, p.B, p.K, p.N, p.ldb, p.strideB != 0 ? p.groups : 1, p.strideB, kF8Block, rows_b, sw);
+}
+
 }  // namespace
 
 extern "C" {
@@ -110,6 +121,16 @@ ttc_status ttc_gemm_f8_blocks(int64_t groups, int64_t M, int64_t N, int64_t K, c
   const F8Result out = out_dtype == TTC_F32 ? kF8ResultF32 : out_dtype == TTC_BF16 ? kF8ResultBF16 : kF8ResultF16;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int64_t likely = groups < M ? groups : M;  // groups with rows, as far as the host knows
+  if (f8_maps(p, 128, 128, env)) {
+    const int clusters = f8_pair_clusters();
+    if (clusters <= 0) return TTC_ERR_CUDA;
+    set_walk(p, 0, blocks_of(N, kGroupedPairTile), 3);
+    p.b_stream = M <= groups * kGroupedPairTile;
+    const int64_t tiles = (blocks_of(M, kGroupedPairTile) + likely) * p.col_blocks;
+    if (launch_f8_pair(p, out, (int)(2 * tiles < clusters ? 2 * tiles : clusters), s) != cudaSuccess) return TTC_ERR_CUDA;
+    count_launches(1);
+    return TTC_OK;
+  }
   set_walk(p, 0, col_blocks, 4);
   const int64_t tiles = (blocks_of(M, kF8PlainTile) + likely) * col_blocks, room = 4ll * env.sm_count;
   if (launch_f8_plain(p, out, (int)(tiles < room ? tiles : room), s) != cudaSuccess) return TTC_ERR_CUDA;

@@ -135,6 +135,33 @@ __device__ __forceinline__ GroupedTile grouped_tile(const GroupedParams& p, cons
   return x;
 }
 
+// CTA pairs: what they take in turn, `whole` tiles, then halves of tiles.
+struct PairWalk {
+  int whole, items;
+};
+__device__ __forceinline__ PairWalk pair_walk(int tiles, int pairs) {
+  const int rest = tiles % pairs;
+  PairWalk w{tiles, tiles};
+  if (2 * rest <= pairs) {
+    w.whole = tiles - rest;
+    w.items = tiles + rest;
+  }
+  return w;
+}
+
+struct PairItem {
+  GroupedTile x;
+  int half;  // of the tile's columns; -1: all of them
+};
+template <bool WGRAD>
+__device__ __forceinline__ PairItem pair_item(const GroupedParams& p, const GroupTable& tb, const PairWalk& w, int t) {
+  const int over = t - w.whole;
+  PairItem it;
+  it.half = over < 0 ? -1 : over & 1;
+  it.x = grouped_tile<kGroupedPairTile, WGRAD>(p, tb, over < 0 ? t : w.whole + (over >> 1));
+  return it;
+}
+
 // A lane's four of the warp's 128 columns, zeros outside `n` columns.
 __device__ __forceinline__ float4 four_columns(const float* c0, int lane, int n) {
   const float* c = c0 + lane * 4;

@@ -93,33 +93,6 @@ __device__ __forceinline__ int stage_word(int nkb, int last_steps, bool last, bo
   return nkb | (last ? last_steps << 4 | 256 : (kBK / kUmmaK) << 4) | (narrow ? 512 : 0);
 }
 
-// What the pairs take in turn: `whole` tiles, then halves of tiles.
-struct PairWalk {
-  int whole, items;
-};
-__device__ __forceinline__ PairWalk pair_walk(int tiles, int pairs) {
-  const int rest = tiles % pairs;
-  PairWalk w{tiles, tiles};
-  if (2 * rest <= pairs) {
-    w.whole = tiles - rest;
-    w.items = tiles + rest;
-  }
-  return w;
-}
-
-struct PairItem {
-  GroupedTile x;
-  int half;  // of the tile's columns; -1: all of them
-};
-template <bool WGRAD>
-__device__ __forceinline__ PairItem pair_item(const GroupedParams& p, const GroupTable& tb, const PairWalk& w, int t) {
-  const int over = t - w.whole;
-  PairItem it;
-  it.half = over < 0 ? -1 : over & 1;
-  it.x = grouped_tile<kTile, WGRAD>(p, tb, over < 0 ? t : w.whole + (over >> 1));
-  return it;
-}
-
 struct PairLoop {
   int k_blocks;  // of the tile
   int fix_rows;  // wgrad: rows of the last k-block inside the group where that is no multiple of 16, else 0
