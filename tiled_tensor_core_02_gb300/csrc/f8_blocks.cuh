@@ -21,6 +21,7 @@ struct F8Params : GroupedParams {
   int a_e5m2, b_e5m2;  // else e4m3
   int64_t lds_a, lds_b, stride_sb;  // scale_a, scale_b: pitches, and from one group's to the next
   int b_shift;  // rows of B a scale: 2^0 or 2^7
+  int sa_vec, sb_vec;  // rows of scales start on 16-byte boundaries
 };
 
 // Any pitch and alignment: tiles of 64 x 64, warp-level products of fp16 copies.

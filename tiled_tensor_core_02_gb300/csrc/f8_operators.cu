@@ -108,6 +108,8 @@ ttc_status ttc_gemm_f8_blocks(int64_t groups, int64_t M, int64_t N, int64_t K, c
   p.lds_b = ldsb;
   p.stride_sb = strideSB;
   p.b_shift = block_rows_b == 1 ? 0 : 7;
+  p.sa_vec = aligned(scaleA, 16) && ldsa % 4 == 0;
+  p.sb_vec = aligned(scaleB, 16) && ldsb % 4 == 0 && (groups == 1 || strideSB % 4 == 0);
   p.bias = bias;
   p.stride_bias = strideBias;
   p.act = (int)act;

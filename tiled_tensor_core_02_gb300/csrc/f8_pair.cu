@@ -2,16 +2,24 @@
 // (kind::f8f6f4), operands by TMA.
 //
 // The scales change with every 128 of K, so the tensor cores add up one such block at
-// a time: each goes into one of two accumulators in tensor memory, and the epilogue warps
-// add it, scaled, to the tile's sums in their registers (a thread has one row and 128
-// columns) while the tensor cores fill the other.  For that they have 512 clocks, the
-// MMAs' time at fp8's rate; a warp takes its four loads of 32 columns one ahead of the
-// additions, two columns an instruction.  The sums take most of a thread's registers, so the
-// four warps that load and issue hand theirs over.
+// a time, for 128 columns each: four accumulators of tensor memory take turns, and the
+// epilogue warps add them, scaled, to the tile's sums in their registers.  Half of the
+// sixteen warps take one of a block's two accumulators, half the other; a thread has one
+// row and 64 columns, read 16 at a time.  That is what hides the way from an accumulator's
+// last MMA to its being free again (about 0.5 us, and the additions): 8192 x 14336 x 4096 with
+// GELU took 690 us by eight warps of 128 columns and these accumulators, 602 with two of 256
+// columns, 510 as it is; loads of 32 columns 594, of 8 533.  The MMAs alone take 255 us
+// with 256 columns an instruction, 313 with 128.
 //
-// Scales of A come a block of four of K ahead, one row a lane.  B's are one for all of
-// a warp's columns (blocks of 128 rows), or one a column: then a lane fetches four
-// columns' and hands them round through the warp's staging block.
+// Two warps bring the scales of four blocks of K at a time into shared memory: A's by row, B's
+// one for 128 columns or one a column.  In the epilogue's own hands they took registers that
+// the sums need, and what is spilled goes to L2, nearly all of L1 being shared memory here.
+// For the same reason the four warps that load and issue hand registers over.  The MMAs are
+// issued by a converged warp: by one thread of it, which moves descriptors to uniform registers
+// each time, an accumulator took 0.38 us instead of 0.22.
+//
+// Bound by the epilogue: 0.54 us a block of K and tile, and at a tile's end 2.4 us with GELU
+// (1.3 of them its exponentials and quotients), during which the tensor cores get two blocks ahead.
 #include <atomic>
 #include <type_traits>
 
@@ -25,79 +33,61 @@ namespace {
 constexpr int kTile = kGroupedPairTile;
 constexpr int kShareBytes = 128 * kF8Block;  // a CTA's share of one operand's block
 constexpr int kEpiWarp0 = 4;
-constexpr int kEpiWarpCount = 8;
+constexpr int kEpiWarpCount = 16;
 constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarpCount);
+constexpr int kLoaders = 64;  // threads that load scales: warps 2 and 3
 constexpr int kStagingBytes = kEpiWarpCount * 4096;
 constexpr int kBarBytes = 256;
 constexpr int kTableInts = 384;
-// Scales by column take 4 KB an epilogue warp: a stage less.
-template <bool BY_COLUMN>
-constexpr int kStagesOf = BY_COLUMN ? 5 : 6;
-constexpr int kSmemBytes = 1024 + 6 * 2 * kShareBytes + kStagingBytes + kBarBytes + kTableInts * 4;
-static_assert(kEpiWarpCount * 4096 <= 2 * kShareBytes, "a stage has room for the scales");
+constexpr int kStages = 4;
+// Scales of a chunk of K: A's of 128 rows, four each, then B's.
+constexpr int kAhead = 4;       // blocks of K of a chunk
+constexpr int kScaleSlots = 2;  // chunks on their way
+constexpr int kScaleBytes = 128 * kAhead * 4 + kTile * kAhead * 4 + 16;
+constexpr int kSmemBytes =
+    1024 + kStages * 2 * kShareBytes + kStagingBytes + kScaleSlots * kScaleBytes + kBarBytes + kTableInts * 4;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 static_assert((kMaxGroups + 3) / 4 + 1 <= kTableInts, "a table of every fourth group's tiles has room");
 // Registers a thread: at launch, of the first four warps, of the epilogue's.
-constexpr int kRegsLaunch = 168, kRegsFew = 72, kRegsMany = 216;
+constexpr int kRegsLaunch = 96, kRegsFew = 64, kRegsMany = 104;
 static_assert(128 * kRegsFew + (kThreads - 128) * kRegsMany <= kThreads * kRegsLaunch, "the shares fit the launch's registers");
-constexpr int kLoad = 32;  // columns of an accumulator a load
-constexpr int kAhead = 4;  // blocks of K whose scales are fetched together
+constexpr int kLoad = 16;  // columns a load
+constexpr int kAccs = 4, kAccCols = 128;  // accumulators; columns of each, from either CTA's weights half of them
 
-// Where an epilogue warp's part of a tile lies.
+// Where an epilogue warp's part of a tile lies: 32 rows, 64 columns (none of half a tile for
+// the warps of the second accumulator).
 struct Part {
-  int g, col0, at, width;  // group; first column of D and of the accumulator; columns (128, of half a tile 64)
+  int g, col0, cols;  // group; first column of D; columns inside D
   int64_t row;
   int rows;
 };
 __device__ __forceinline__ Part part_of(const F8Params& p, const GroupTable& tb, const PairWalk& walk, int t, uint32_t rank, int q,
-                                        int half) {
+                                        int half, int second) {
   const PairItem item = pair_item<false>(p, tb, walk, t);
   const GroupedTile& x = item.x;
   const int r0 = x.rb * kTile + (int)rank * 128 + q * 32;
   Part e;
   e.g = x.g;
-  e.width = item.half < 0 ? kTile / 2 : kTile / 4;
-  e.at = half * e.width;
-  e.col0 = x.cb * kTile + max(item.half, 0) * (kTile / 2) + e.at;
+  e.col0 = x.cb * kTile + (item.half < 0 ? half * 128 + second * 64 : item.half * 128 + half * 64);
+  e.cols = item.half >= 0 && second != 0 ? 0 : min(64, p.N - e.col0);
   e.row = (int64_t)x.lo + r0;
   e.rows = max(0, min(32, x.hi - x.lo - r0));
   return e;
 }
 
-// Scales of kAhead blocks of K from kb0 on: this lane's row of A, and B's for the warp's
-// columns where that is one.
-template <bool BY_COLUMN>
-struct Scales {
-  float a[kAhead], b[BY_COLUMN ? 1 : kAhead];
-
-  __device__ __forceinline__ void load(const F8Params& p, const Part& e, int lane, int kb0) {
-    const float* sa = p.scale_a + (e.row + lane) * p.lds_a + kb0;
-    const float* sb = p.scale_b + (int64_t)e.g * p.stride_sb + (int64_t)(e.col0 >> 7) * p.lds_b + kb0;
-    const int n = p.k_blocks - kb0;
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      a[i] = lane < e.rows && i < n ? __ldg(sa + i) : 0.0f;
-      if constexpr (!BY_COLUMN) b[i] = e.col0 < p.N && i < n ? __ldg(sb + i) : 0.0f;
-    }
+// Four scales in a row of which `n` exist (zeros behind them); volatile, so that they are
+// asked for here and not where they are used.
+__device__ __forceinline__ float4 four_scales(const float* p, bool vec, int n) {
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (vec && n >= 4) {
+    asm volatile("ld.global.nc.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
+  } else {
+    if (n > 0) asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v.x) : "l"(p));
+    if (n > 1) asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v.y) : "l"(p + 1));
+    if (n > 2) asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v.z) : "l"(p + 2));
+    if (n > 3) asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v.w) : "l"(p + 3));
   }
-};
-
-// The same of B by column into shared memory, [block][128 columns], without a register;
-// copy_async_wait and a __syncwarp come before their use.
-__device__ __forceinline__ void fetch_columns(const F8Params& p, const Part& e, int lane, int kb0, float* dst) {
-  const float* sb = p.scale_b + (int64_t)e.g * p.stride_sb + kb0;
-  const int n = p.k_blocks - kb0;
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    const int at = c * 32 + lane, col = e.col0 + at;
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      if (col < p.N && i < n)
-        copy_async_4(dst + i * 128 + at, sb + (int64_t)col * p.lds_b + i);
-      else
-        dst[i * 128 + at] = 0.0f;
-    }
-  }
+  return v;
 }
 
 // C's 32 rows of 128 bytes into the staging block, zeros outside; a __syncwarp comes
@@ -124,29 +114,83 @@ __device__ __forceinline__ void stage_c(const F8Params& p, const T* c0, int rows
   }
 }
 
-__device__ __forceinline__ void load_columns(uint32_t taddr, uint32_t (&w)[32]) { tmem_ld_32x32b_x32(taddr, w); }
-__device__ __forceinline__ void load_columns(uint32_t taddr, uint32_t (&w)[16]) { tmem_ld_32x32b_x16<0>(taddr, w); }
+
+// Shared memory by its 32-bit address.
+__device__ __forceinline__ uint32_t shared_u32(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ float shared_f32(uint32_t at) { return __uint_as_float(shared_u32(at)); }
+__device__ __forceinline__ float4 shared_f32x4(uint32_t at) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ void arrive_at(uint32_t at) {
+  asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.shared::cta.b64 st, [%0];\n\t}" ::"r"(at) : "memory");
+}
+__device__ __forceinline__ bool try_wait_at(uint32_t at, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(at), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// mbar_wait_warp.
+__device__ __forceinline__ bool wait_warp_at(uint32_t at, uint32_t parity, const WaitCtx& w) {
+  bool ok = try_wait_at(at, parity);
+  if (!ok) {
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t spins = 1;; ++spins) {
+      if (try_wait_at(at, parity)) {
+        ok = true;
+        break;
+      }
+      if ((spins & 63u) != 0u) continue;
+      if (error_raised(w)) break;
+      if (globaltimer_ns() - t0 > w.timeout_ns) {
+        record_error(w, kDevTimeout);
+        break;
+      }
+    }
+  }
+  return __all_sync(0xFFFFFFFFu, ok) != 0;
+}
+
+// Two columns at a time: half the instructions, though no faster in the FMA pipe.
+__device__ __forceinline__ void add_pair(float* sum, const uint32_t* w, float2 scale) {
+  const float2 v = __ffma2_rn(make_float2(__uint_as_float(w[0]), __uint_as_float(w[1])), scale, make_float2(sum[0], sum[1]));
+  sum[0] = v.x;
+  sum[1] = v.y;
+}
 
 // OUT: F8Result; BY_COLUMN: B has a scale for each row (a column of D).
 template <int OUT, bool BY_COLUMN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) f8_pair_kernel(const __grid_constant__ F8Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  constexpr int kStages = kStagesOf<BY_COLUMN>;
   uint8_t* sA = smem;
   uint8_t* sB = sA + kStages * kShareBytes;
-  uint8_t* staging = smem + 6 * 2 * kShareBytes;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(staging + kStagingBytes);
+  uint8_t* staging = sB + kStages * kShareBytes;
+  uint8_t* scales = staging + kStagingBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(scales + kScaleSlots * kScaleBytes);
   uint64_t* full = bars;
   uint64_t* empty = bars + kStages;
   uint64_t* tmem_full = bars + 2 * kStages;
-  uint64_t* tmem_empty = bars + 2 * kStages + 2;
-  uint64_t* stall_bar = bars + 2 * kStages + 4;
-  uint64_t* drain_bar = bars + 2 * kStages + 5;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 6);
-  // what the producer tells the MMA issuer about a stage: whether the tile is half a tile
-  int* stage_info = reinterpret_cast<int*>(bars + 2 * kStages + 7);
-  static_assert((2 * kStages + 7) * 8 + kStages * 4 <= kBarBytes, "barrier area");
+  uint64_t* tmem_empty = tmem_full + kAccs;
+  uint64_t* scale_full = tmem_empty + kAccs;
+  uint64_t* scale_empty = scale_full + kScaleSlots;
+  uint64_t* stall_bar = scale_empty + kScaleSlots;
+  uint64_t* drain_bar = stall_bar + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain_bar + 1);
+  // what the producer tells the MMA issuer about a stage: how many accumulators it fills,
+  // one of half a tile
+  int* stage_info = reinterpret_cast<int*>(drain_bar + 2);
+
+  static_assert((2 * kStages + 2 * kAccs + 2 * kScaleSlots + 3) * 8 + kStages * 4 <= kBarBytes, "barrier area");
   int* table = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + kBarBytes);
   // the whole table where it has room, else only every fourth group's first tile
   GroupTable tb{nullptr, nullptr, 1, p.col_blocks};
@@ -169,9 +213,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) f8_pair
       mbar_init(&full[lane], 1);
       mbar_init(&empty[lane], 1);
     }
-    if (lane < 2) {
+    if (lane < kAccs) {
       mbar_init(&tmem_full[lane], 1);
-      mbar_init(&tmem_empty[lane], 2 * kEpiWarpCount);
+      mbar_init(&tmem_empty[lane], kEpiWarpCount);  // half the warps of either CTA
+    }
+    if (lane < kScaleSlots) {
+      mbar_init(&scale_full[lane], kLoaders);
+      mbar_init(&scale_empty[lane], kEpiWarpCount);
     }
     if (lane == 0) {
       mbar_init(stall_bar, 1);
@@ -188,17 +236,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) f8_pair
   tc_fence_before();
   cluster_sync();
   tc_fence_after();
-  const uint32_t tmem_base = *tmem_slot;
   grid_dependency_wait();
   grid_dependents_launch();
   build_group_table<kTile>(p, tb);
-  const PairWalk walk = pair_walk(table_tiles(p, tb), num_pairs);
+  // Each role finds the walk and the accumulators for itself: what is live where the roles
+  // part is spilled in the one that is short of registers.
+  const auto find_walk = [&] { return pair_walk(table_tiles(p, tb), num_pairs); };
+  const auto find_tmem = [&] { return *const_cast<volatile uint32_t*>(tmem_slot); };
 
   if (warp < kEpiWarp0) {
     registers_down<kRegsFew>();
     if (warp == 0) {
       // ---------------------------------------------------------------- producer (both CTAs)
       if (lane == 0) {
+        const PairWalk walk = find_walk();
         const uint64_t keep = policy_evict_last();
         const uint64_t pol_b = p.b_stream ? policy_evict_first() : keep;
         int stage = 0;
@@ -221,7 +272,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) f8_pair
             }
             const uint32_t full_leader = mapa_shared(smem_u32(&full[stage]), 0);
             if (leader) {
-              stage_info[stage] = item.half >= 0;
+              stage_info[stage] = item.half < 0 ? 2 : 1;
               mbar_arrive_expect_tx(full + stage, shares * kShareBytes);
               armed |= 1u << stage;
               armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
@@ -242,31 +293,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) f8_pair
       }
     } else if (warp == 1) {
       // ---------------------------------------------------------------- MMA issuer (even CTA)
-      if (leader && lane == 0) {
-        const uint32_t idesc_whole = idesc_f8(p.a_e5m2 != 0, p.b_e5m2 != 0, kTile, kTile);
-        const uint32_t idesc_half = idesc_f8(p.a_e5m2 != 0, p.b_e5m2 != 0, kTile, kTile / 2);
+      if (leader) {
+        const uint32_t lead = elect_lead(), tmem_base = find_tmem();
+        const PairWalk walk = find_walk();
+        const uint32_t idesc = idesc_f8(p.a_e5m2 != 0, p.b_e5m2 != 0, kTile, kAccCols);
         const uint64_t a0 = smem_desc_sw128(smem_u32(sA), 16u, 1024);
         const uint64_t b0 = smem_desc_sw128(smem_u32(sB), 16u, 1024);
+        const uint32_t a_hi = (uint32_t)(a0 >> 32), b_hi = (uint32_t)(b0 >> 32);
         bool ok = true, any = false;
-        if (p.inject_stall) ok = mbar_wait(stall_bar, 0, wc);  // nothing arrives here
-        int stage = 0, it = 0;
-        uint32_t phase = 0;
+        if (p.inject_stall) ok = mbar_wait_warp(stall_bar, 0, wc);  // nothing arrives here
+        int stage = 0;
+        uint32_t it = 0, phase = 0;
         for (int t = pair; ok && t < walk.items; t += num_pairs) {
-          for (int kb = 0; kb < p.k_blocks; ++kb, ++it) {
-            const int acc = it & 1;
-            // the first use of each accumulator passes at once
-            if (!mbar_wait_cluster(&tmem_empty[acc], ((it >> 1) & 1) ^ 1u, wc) || !mbar_wait(&full[stage], phase, wc)) {
+          for (int kb = 0; ok && kb < p.k_blocks; ++kb) {
+            if (!mbar_wait_warp(&full[stage], phase, wc)) {
               ok = false;
               break;
             }
-            tc_fence_after();
-            const uint32_t idesc = stage_info[stage] != 0 ? idesc_half : idesc_whole;
-            const uint64_t ad = a0 + (uint32_t)stage * (kShareBytes >> 4), bd = b0 + (uint32_t)stage * (kShareBytes >> 4);
+            const int parts = stage_info[stage];
+            const uint32_t a_lo = (uint32_t)a0 + (uint32_t)stage * (kShareBytes >> 4);
+            uint32_t b_lo = (uint32_t)b0 + (uint32_t)stage * (kShareBytes >> 4);
+            for (int h = 0; h < parts; ++h, ++it, b_lo += 64 * kF8Block >> 4) {
+              const uint32_t acc = it & (kAccs - 1);
+              // the first use of each accumulator passes at once
+              if (!mbar_wait_warp(&tmem_empty[acc], ((it / kAccs) & 1) ^ 1u, wc)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
 #pragma unroll
-            for (int k = 0; k < kF8Block / 32; ++k) mma_f8_pair(tmem_base + acc * kTile, ad + k * 2, bd + k * 2, idesc, k != 0);
-            any = true;
-            mma_commit_pair(&empty[stage], 0x3);
-            mma_commit_pair(&tmem_full[acc], 0x3);
+              for (int k = 0; k < kF8Block / 32; ++k)
+                mma_f8_pair_lead(lead, tmem_base + acc * kAccCols, a_lo + k * 2, a_hi, b_lo + k * 2, b_hi, idesc, k != 0);
+              any = true;
+              mma_commit_pair_lead(lead, &tmem_full[acc], 0x3);
+            }
+            if (!ok) break;
+            mma_commit_pair_lead(lead, &empty[stage], 0x3);
             if (++stage == kStages) {
               stage = 0;
               phase ^= 1u;
@@ -275,8 +337,62 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) f8_pair
         }
         if (any) {
           // every MMA must have finished with both CTAs' TMEM before it is freed
-          mma_commit_pair(drain_bar, 0x1);
+          mma_commit_pair_lead(lead, drain_bar, 0x1);
           drain_wait(drain_bar, 0, 100000000ull);
+        }
+      }
+    } else {
+      // ---------------------------------------------------------------- scales (both CTAs)
+      const PairWalk walk = find_walk();
+      const int i0 = threadIdx.x - 64;
+      uint32_t chunk = 0;
+      bool ok = true;
+      for (int t = pair; ok && t < walk.items; t += num_pairs) {
+        const PairItem item = pair_item<false>(p, tb, walk, t);
+        const GroupedTile& x = item.x;
+        const int row0 = x.lo + x.rb * kTile + (int)rank * 128;
+        const int col0 = x.cb * kTile + max(item.half, 0) * (kTile / 2);
+        const int width = item.half < 0 ? kTile : kTile / 2;
+        const float* sb = p.scale_b + (int64_t)x.g * p.stride_sb;
+        for (int kb0 = 0; kb0 < p.k_blocks; kb0 += kAhead, ++chunk) {
+          const int slot = chunk % kScaleSlots, n = p.k_blocks - kb0;
+          if (!mbar_wait(&scale_empty[slot], (chunk / kScaleSlots & 1) ^ 1u, wc)) {
+            ok = false;
+            break;
+          }
+          float4* a_out = reinterpret_cast<float4*>(scales + slot * kScaleBytes);
+          float* b_out = reinterpret_cast<float*>(a_out + 128);
+          float4 a[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int row = row0 + i * kLoaders + i0;
+            a[i] = four_scales(p.scale_a + (int64_t)row * p.lds_a + kb0, p.sa_vec != 0, row < x.hi ? n : 0);
+          }
+          if constexpr (BY_COLUMN) {  // [block][column]
+            float4 v[kTile / kLoaders];
+#pragma unroll
+            for (int i = 0; i < kTile / kLoaders; ++i) {
+              const int col = col0 + i * kLoaders + i0;
+              v[i] = four_scales(sb + (int64_t)col * p.lds_b + kb0, p.sb_vec != 0,
+                                 col < p.N && i * kLoaders < width ? n : 0);
+            }
+#pragma unroll
+            for (int i = 0; i < kTile / kLoaders; ++i) {
+              float* o = b_out + i * kLoaders + i0;
+              o[0] = v[i].x;
+              o[kTile] = v[i].y;
+              o[2 * kTile] = v[i].z;
+              o[3 * kTile] = v[i].w;
+            }
+          } else if (i0 < 2) {  // one for either half's columns
+            const int col = col0 + i0 * (width / 2);
+            reinterpret_cast<float4*>(b_out)[i0] =
+                four_scales(sb + (int64_t)(col >> 7) * p.lds_b + kb0, p.sb_vec != 0, col < p.N ? n : 0);
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) a_out[i * kLoaders + i0] = a[i];
+          if (i0 == 0) *reinterpret_cast<uint32_t*>(b_out + kTile * kAhead) = width / 128;
+          mbar_arrive(&scale_full[slot]);
         }
       }
     }
@@ -286,98 +402,81 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) f8_pair
     using T = typename std::conditional<OUT == kF8ResultF32, float, uint16_t>::type;
     constexpr int kUnit = 128 / (int)sizeof(T);  // columns that 128 bytes hold
     constexpr int kElems = 16 / (int)sizeof(T);
-    const int ew = warp - kEpiWarp0, q = warp & 3, half = ew >> 2;  // quarter of the rows, half of the columns
-    uint8_t* sb = staging + ew * 4096;
-    const uint32_t tmem_mine = tmem_base + ((uint32_t)(q * 32) << 16);
-    int it = 0;
+    // quarter of the rows; which CTA's half of an accumulator's columns; which of a block's accumulators
+    const int ew = warp - kEpiWarp0, q = warp & 3, half = (ew >> 2) & 1, second = ew >> 3;
+    const PairWalk walk = find_walk();
+    const uint32_t from = find_tmem() + ((uint32_t)(q * 32) << 16) + half * (kAccCols / 2);
+    // shared memory by 32-bit addresses: the accumulators' barriers here and in the even CTA, this lane's scales
+    const uint32_t full_at = smem_u32(tmem_full), release = mapa_shared(smem_u32(tmem_empty), 0);
+    const uint32_t scales_at = smem_u32(scales);
+    uint32_t it = 0;  // accumulators so far
+    uint32_t chunk = 0;
     bool ok = true;
-    Part e{};
-    Scales<BY_COLUMN> next;
-    // the scales of this chunk of K and of the next
-    float* columns = reinterpret_cast<float*>(smem + kStages * 2 * kShareBytes + ew * 4096);
-    int buffer = 0;
-    const auto fetch = [&](int kb0) {
-      next.load(p, e, lane, kb0);
-      if constexpr (BY_COLUMN) {
-        buffer ^= kAhead * 128;
-        fetch_columns(p, e, lane, kb0, columns + buffer);
-      }
-    };
-    if (pair < walk.items) {
-      e = part_of(p, tb, walk, pair, rank, q, half);
-      fetch(0);
-    }
     for (int t = pair; ok && t < walk.items; t += num_pairs) {
-      uint64_t sums[kTile / 4];  // pairs of columns
+      float sums[64];
 #pragma unroll
-      for (int j = 0; j < kTile / 4; ++j) sums[j] = 0ull;
-      const Part me = e;
-      for (int kb0 = 0; ok && kb0 < p.k_blocks; kb0 += kAhead) {
-        float s[kAhead];
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) s[i] = BY_COLUMN ? next.a[i] : next.a[i] * next.b[BY_COLUMN ? 0 : i];
-        const float* by_column = columns + buffer;
-        if constexpr (BY_COLUMN) {
-          copy_async_wait();
-          __syncwarp();
+      for (int j = 0; j < 64; ++j) sums[j] = 0.0f;
+      for (int kb0 = 0; ok && kb0 < p.k_blocks; kb0 += kAhead, ++chunk) {
+        const uint32_t slot = chunk % kScaleSlots;
+        if (!wait_warp_at(full_at + (2 * kAccs + slot) * 8, chunk / kScaleSlots & 1, wc)) {
+          ok = false;
+          break;
         }
-        if (kb0 + kAhead < p.k_blocks) {
-          fetch(kb0 + kAhead);
-        } else if (t + num_pairs < walk.items) {
-          e = part_of(p, tb, walk, t + num_pairs, rank, q, half);
-          fetch(0);
-        }
+        uint32_t a_at = scales_at + slot * kScaleBytes, b_at = a_at + 128 * kAhead * 4;
+        const uint32_t units = shared_u32(b_at + kTile * kAhead * 4);
+        a_at += (q * 32 + lane) * kAhead * 4;
+        b_at += BY_COLUMN ? (half * (units * 64) + second * 64) * 4 : half * kAhead * 4;
         const int blocks = min(kAhead, p.k_blocks - kb0);
 #pragma unroll 1
-        for (int i = 0; i < blocks; ++i) {
-          const int acc = it & 1;
-          if (!mbar_wait_warp(&tmem_full[acc], (it >> 1) & 1, wc)) {
+        for (int i = 0; i < blocks; ++i, it += units, a_at += 4, b_at += BY_COLUMN ? kTile * 4 : 4) {
+          if (second >= (int)units) continue;
+          float scale = shared_f32(a_at);
+          if constexpr (!BY_COLUMN) scale *= shared_f32(b_at);
+          const uint32_t n = it + second, acc = n & (kAccs - 1);
+          if (!wait_warp_at(full_at + acc * 8, (n / kAccs) & 1, wc)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t from = tmem_mine + me.at + acc * kTile;
-          const float scale = s[0];
 #pragma unroll
-          for (int k = 0; k + 1 < kAhead; ++k) s[k] = s[k + 1];
-          const uint64_t scale2 = pair_of(scale, scale);
-          // two loads of kLoad columns in turn
-          uint32_t w[2][kLoad];
-          load_columns(from, w[0]);
-#pragma unroll
-          for (int c = 0; c < kTile / 2 / kLoad; ++c) {
-            tmem_ld_wait_for(w[c & 1]);
-            if (c + 1 < kTile / 2 / kLoad) {
-              load_columns(from + (c + 1) * kLoad, w[(c + 1) & 1]);
-            } else {
+          for (int c = 0; c < 64 / kLoad; ++c) {
+            uint32_t w[kLoad];
+            tmem_ld_32x32b_x16<0>(from + acc * kAccCols + c * kLoad, w);
+            tmem_ld_wait_for(w);
+            if (c + 1 == 64 / kLoad) {
               tc_fence_before();
               __syncwarp();
-              if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&tmem_empty[acc]), 0));
+              if (lane == 0) mbar_arrive_cluster_relaxed(release + acc * 8);
             }
 #pragma unroll
-            for (int j = 0; j < kLoad / 2; j += 2) {
-              uint64_t f0 = scale2, f1 = scale2;
+            for (int j = 0; j < kLoad; j += 4) {
+              float2 f0 = make_float2(scale, scale), f1 = f0;
               if constexpr (BY_COLUMN) {
-                const float4 v = *reinterpret_cast<const float4*>(by_column + i * 128 + c * kLoad + j * 2);
-                f0 = mul_pair(pair_of(v.x, v.y), scale2);
-                f1 = mul_pair(pair_of(v.z, v.w), scale2);
+                const float4 v = shared_f32x4(b_at + (c * kLoad + j) * 4);
+                f0 = __fmul2_rn(f0, make_float2(v.x, v.y));
+                f1 = __fmul2_rn(f1, make_float2(v.z, v.w));
               }
-              const uint32_t* v = w[c & 1] + 2 * j;
-              fma_pair(pair_of(__uint_as_float(v[0]), __uint_as_float(v[1])), f0, sums[c * (kLoad / 2) + j]);
-              fma_pair(pair_of(__uint_as_float(v[2]), __uint_as_float(v[3])), f1, sums[c * (kLoad / 2) + j + 1]);
+              add_pair(sums + c * kLoad + j, w + j, f0);
+              add_pair(sums + c * kLoad + j + 2, w + j + 2, f1);
             }
           }
-          ++it;
         }
+        __syncwarp();
+        if (lane == 0) arrive_at(full_at + (2 * kAccs + kScaleSlots + slot) * 8);
       }
       if (!ok) break;
-      const int cols = min(me.width, p.N - me.col0);
+      // found again rather than kept: the sums leave no registers for it
+      int t_again = t;
+      asm volatile("" : "+r"(t_again));
+      const Part me = part_of(p, tb, walk, t_again, rank, q, half, second);
+      const int cols = me.cols;
+      uint8_t* sb = staging + ew * 4096;
       float4 bias = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       if (p.bias != nullptr) bias = four_columns(p.bias + (int64_t)me.g * p.stride_bias + me.col0, lane, cols);
       T* d = static_cast<T*>(p.D) + me.row * p.ldd + me.col0;
       const T* c0 = static_cast<const T*>(p.C) + me.row * p.ldc + me.col0;
 #pragma unroll
-      for (int u = 0; u < kTile / 2 / kUnit; ++u) {
+      for (int u = 0; u < 64 / kUnit; ++u) {
         if (cols <= u * kUnit || me.rows <= 0) continue;
         if (p.C != nullptr) {
           stage_c(p, c0 + u * kUnit, me.rows, cols - u * kUnit, lane, sb);
@@ -388,7 +487,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) f8_pair
           uint4* piece = reinterpret_cast<uint4*>(sb + staged<32>(lane, i));
           float v[kElems];
 #pragma unroll
-          for (int k = 0; k < kElems / 2; ++k) halves_of(sums[(u * kUnit + i * kElems) / 2 + k], v[2 * k], v[2 * k + 1]);
+          for (int k = 0; k < kElems; ++k) v[k] = sums[u * kUnit + i * kElems + k];
           if (p.C != nullptr) {
             const uint4 old = *piece;
             const uint32_t cw[4] = {old.x, old.y, old.z, old.w};
@@ -427,7 +526,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) f8_pair
         __syncwarp();
       }
     }
-    if constexpr (BY_COLUMN) copy_async_wait();  // after an error some may be on their way
   }
 
   __syncthreads();
@@ -435,7 +533,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) f8_pair
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc_pair(tmem_base, 512);
+    tmem_dealloc_pair(find_tmem(), 512);
   }
 }
 
