@@ -28,6 +28,11 @@ struct F8Params : GroupedParams {
 constexpr int kF8PlainTile = 64;
 cudaError_t launch_f8_plain(const F8Params& p, F8Result out, int ctas, cudaStream_t stream);
 
+// Few tokens: blocks of 16, 32 and 64 of a group's, tiles of 8 to 128 output columns.  tmA
+// has boxes of few_tokens_box tokens.  Stages that fit:
+int f8_tokens_stages(int tokens, int tile_cols, int groups);
+cudaError_t launch_f8_tokens(const F8Params& p, F8Result out, int tokens, int ctas, cudaStream_t stream);
+
 // CTA pairs: tiles of 256 x 256 (kGroupedPairTile) of operands TMA can read.
 int f8_pair_clusters();
 cudaError_t launch_f8_pair(const F8Params& p, F8Result out, int clusters, cudaStream_t stream);

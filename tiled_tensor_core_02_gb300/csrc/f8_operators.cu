@@ -21,6 +21,16 @@ bool f8_maps(F8Params& p, int rows_a, int rows_b, const HostEnv& env) {
          encode_matrices(&p.tmB, u8, 1, p.B, p.K, p.N, p.ldb, p.strideB != 0 ? p.groups : 1, p.strideB, kF8Block, rows_b, sw);
 }
 
+// The few-token kernel's tiles; false where no pipeline fits.  `matrices`: how many groups
+// are likely to have rows.
+bool f8_few_tiles(F8Params& p, int tokens, int64_t matrices, const HostEnv& env) {
+  p.tile_cols = few_tile_cols(few_blocks(p.M, tokens, matrices), p.N, env.sm_count, false, 128);
+  p.col_blocks = (int)blocks_of(p.N, p.tile_cols);
+  p.stages = f8_tokens_stages(tokens, p.tile_cols, p.groups);
+  p.b_stream = p.M <= matrices * tokens;
+  return p.stages >= 2 && (blocks_of(p.M, tokens) + p.groups) * p.col_blocks <= kSizeLimit;
+}
+
 }  // namespace
 
 extern "C" {
@@ -123,6 +133,14 @@ ttc_status ttc_gemm_f8_blocks(int64_t groups, int64_t M, int64_t N, int64_t K, c
   const F8Result out = out_dtype == TTC_F32 ? kF8ResultF32 : out_dtype == TTC_BF16 ? kF8ResultBF16 : kF8ResultF16;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int64_t likely = groups < M ? groups : M;  // groups with rows, as far as the host knows
+  const int block = few_block(M, likely);
+  if (block != 0 && f8_few_tiles(p, block, likely, env) && f8_maps(p, few_tokens_box(block), p.tile_cols, env)) {
+    const int64_t tiles = (blocks_of(M, block) + likely) * p.col_blocks;
+    if (launch_f8_tokens(p, out, block, (int)(tiles < env.sm_count ? tiles : env.sm_count), s) != cudaSuccess)
+      return TTC_ERR_CUDA;
+    count_launches(1);
+    return TTC_OK;
+  }
   if (f8_maps(p, 128, 128, env)) {
     const int clusters = f8_pair_clusters();
     if (clusters <= 0) return TTC_ERR_CUDA;

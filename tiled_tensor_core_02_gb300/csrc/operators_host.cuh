@@ -95,18 +95,24 @@ inline int few_tile_cols(int64_t blocks, int64_t n, int sm_count, bool cols_cont
   return (int)c;
 }
 
+// Blocks of tokens that `rows` rows of `matrices` groups are likely to make.  Groups near
+// the mean take one block more as often as not (256 rows of 4 groups, 1088 x 1040: tiles for
+// four blocks 16.0 us, for six 11.1).
+inline int64_t few_blocks(int64_t rows, int tokens, int64_t matrices) {
+  const int64_t whole = blocks_of(blocks_of(rows, matrices), tokens) * matrices;
+  const int64_t half_more = blocks_of(2 * rows + tokens * matrices, 2 * tokens);
+  return whole > half_more ? whole : half_more;
+}
+
 // Sets up the few-token kernel's tiles and tensor maps; false where TMA cannot
 // read the operands or no pipeline fits.  `matrices`: how many weight matrices
-// are likely to be read.  Groups near the mean take one block more as often as not
-// (256 rows of 4 groups, 1088 x 1040: tiles for four blocks 16.0 us, for six 11.1).
+// are likely to be read.
 // `pair`: columns of two weight matrices lie in a stage (p.tmB is the first's map; the
 // other's, alike, is the caller's).
 inline bool few_maps(GroupedParams& p, ttc_dtype dtype, int tokens, int64_t matrices, const HostEnv& env, bool pair = false) {
   if (env.plain_loads || p.M == 0 || p.K == 0) return false;
   if (!tma_rows_ok(p.A, p.lda, 2) || !tma_rows_ok(p.B, p.ldb, 2) || !tma_stride_ok(p.groups, p.strideB, 2)) return false;
-  const int64_t whole = blocks_of(blocks_of(p.M, matrices), tokens) * matrices;
-  const int64_t half_more = blocks_of(2 * p.M + tokens * matrices, 2 * tokens);
-  p.tile_cols = few_tile_cols(whole > half_more ? whole : half_more, p.N, env.sm_count, p.b_mn != 0, pair ? 64 : 128);
+  p.tile_cols = few_tile_cols(few_blocks(p.M, tokens, matrices), p.N, env.sm_count, p.b_mn != 0, pair ? 64 : 128);
   p.col_blocks = (int)blocks_of(p.N, p.tile_cols);
   if ((blocks_of(p.M, tokens) + p.groups) * p.col_blocks > kSizeLimit) return false;
   p.b_stream = p.M <= matrices * tokens;
