@@ -3,8 +3,8 @@
 // its columns (16 to 64), `tile_cols` output columns (8 to 128) by one block of a group's
 // tokens a tile.
 //
-// A block of 128 k has sums of its own: it goes into one of four accumulators in tensor
-// memory, and the epilogue warps, a thread an output column of 16 tokens, add it to their
+// A block of 128 k has sums of its own: a stage's two go side by side into one of four
+// accumulators in tensor memory, and the epilogue warps, a thread an output column of 16 tokens, add it to their
 // sums in registers times its weights' scale and the token's.  The tokens'
 // scales come into shared memory once a tile, the weights' one a block of K and thread.
 //
@@ -21,7 +21,7 @@ namespace {
 constexpr int kKPS = 2;  // blocks of K of a stage
 constexpr int kStageK = kKPS * kF8Block;
 constexpr int kMaxStages = 16;
-constexpr int kAccs = 4;
+constexpr int kAccs = 4;  // accumulators, each with a place for either block of a stage
 constexpr int kBarBytes = 512;
 constexpr int kSmemLimit = 227 * 1024;
 // Producer, MMA issuer, two spare warps; of the epilogue four for each kPart tokens: with all
@@ -74,7 +74,7 @@ template <int BT, int OUT>
 __global__ void __launch_bounds__(kThreads<BT>, 1) f8_tokens_kernel(const __grid_constant__ F8Params p) {
   constexpr int kTokenBytes = stage_bytes_of(BT);
   constexpr int kBox = few_tokens_box(BT);
-  constexpr int kTmemCols = kAccs * BT;
+  constexpr int kTmemCols = kAccs * kKPS * BT;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int w_bytes = stage_bytes_of(p.tile_cols);
@@ -90,6 +90,7 @@ __global__ void __launch_bounds__(kThreads<BT>, 1) f8_tokens_kernel(const __grid
   uint64_t* stall_bar = tmem_empty + kAccs;
   uint64_t* drain_bar = stall_bar + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain_bar + 1);
+  static_assert(kScaleK % kKPS == 0 && kTmemCols <= 512, "chunks of scales hold whole stages");
   static_assert((2 * kMaxStages + 2 * kAccs + 2) * 8 + 4 <= kBarBytes, "barrier area");
   GroupTable tb;
   tb.offs = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + kBarBytes);
@@ -193,21 +194,23 @@ __global__ void __launch_bounds__(kThreads<BT>, 1) f8_tokens_kernel(const __grid
         }
         const uint32_t w_lo = (uint32_t)w0 + (uint32_t)(stage * stage_bytes >> 4);
         const uint32_t a_lo = (uint32_t)a0 + (uint32_t)(stage * stage_bytes >> 4);
-        const int parts = min(kKPS, p.k_blocks - ks * kKPS);
-        for (int j = 0; j < parts; ++j, ++it) {
-          const uint32_t acc = it & (kAccs - 1);
-          if (!mbar_wait_warp(&tmem_empty[acc], ((it / kAccs) & 1) ^ 1u, wc)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
+        const uint32_t acc = it & (kAccs - 1);
+        if (!mbar_wait_warp(&tmem_empty[acc], ((it / kAccs) & 1) ^ 1u, wc)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem_base + acc * (kKPS * BT);
+#pragma unroll
+        for (int k = 0; k < kF8Block / 32; ++k) mma_f8_lead(lead, d, w_lo + k * 2, w_hi, a_lo + k * 2, a_hi, idesc, k != 0);
+        if (p.k_blocks - ks * kKPS > 1) {
 #pragma unroll
           for (int k = 0; k < kF8Block / 32; ++k)
-            mma_f8_lead(lead, tmem_base + acc * BT, w_lo + j * w_kb + k * 2, w_hi, a_lo + j * kTokenKb + k * 2, a_hi, idesc, k != 0);
-          any = true;
-          mma_commit_lead(lead, &tmem_full[acc]);
+            mma_f8_lead(lead, d + BT, w_lo + w_kb + k * 2, w_hi, a_lo + kTokenKb + k * 2, a_hi, idesc, k != 0);
         }
-        if (!ok) break;
+        any = true;
+        ++it;
+        mma_commit_lead(lead, &tmem_full[acc]);
         mma_commit_lead(lead, &empty[stage]);
         if (++stage == S) {
           stage = 0;
@@ -253,27 +256,38 @@ __global__ void __launch_bounds__(kThreads<BT>, 1) f8_tokens_kernel(const __grid
         barrier_of_epilogue<kEpiThreads<BT>>();
         buffer ^= 1;
         ts += j0;
-        float next = f_ok ? __ldg(sb + kb0) : 0.0f;
-        for (int i = 0; i < n; ++i, ++it, ts += BT) {
-          const float scale = next;
-          if (f_ok && kb0 + i + 1 < p.k_blocks) next = __ldg(sb + kb0 + i + 1);
+        float next[kKPS];
+        const auto fetch = [&](int i) {
+#pragma unroll
+          for (int k = 0; k < kKPS; ++k) next[k] = f_ok && i + k < n ? __ldg(sb + kb0 + i + k) : 0.0f;
+        };
+        fetch(0);
+        for (int i = 0; i < n; i += kKPS, ++it, ts += kKPS * BT) {
+          const float scale[kKPS] = {next[0], next[1]};
+          fetch(i + kKPS);
           const uint32_t acc = it & (kAccs - 1);
           if (ok) ok = mbar_wait_warp(&tmem_full[acc], (it / kAccs) & 1, wc);
           if (!ok) continue;
           tc_fence_after();
-          uint32_t w[16];
-          tmem_ld_32x32b_x16<0>(tmem_mine + acc * BT, w);
-          tmem_ld_wait_for(w);
+          uint32_t w[kKPS][16];
+#pragma unroll
+          for (int k = 0; k < kKPS; ++k) tmem_ld_32x32b_x16<0>(tmem_mine + acc * (kKPS * BT) + k * BT, w[k]);
+          tmem_ld_wait_for(w[0]);
+          tmem_ld_wait_for(w[1]);
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&tmem_empty[acc]);
 #pragma unroll
-          for (int j = 0; j < 16; j += 4) {
-            const float4 s = *reinterpret_cast<const float4*>(ts + j);
-            sums[j] = fmaf(s.x * scale, __uint_as_float(w[j]), sums[j]);
-            sums[j + 1] = fmaf(s.y * scale, __uint_as_float(w[j + 1]), sums[j + 1]);
-            sums[j + 2] = fmaf(s.z * scale, __uint_as_float(w[j + 2]), sums[j + 2]);
-            sums[j + 3] = fmaf(s.w * scale, __uint_as_float(w[j + 3]), sums[j + 3]);
+          for (int k = 0; k < kKPS; ++k) {
+            if (i + k >= n) break;  // what lies there is of an earlier block
+#pragma unroll
+            for (int j = 0; j < 16; j += 4) {
+              const float4 s = *reinterpret_cast<const float4*>(ts + k * BT + j);
+              sums[j] = fmaf(s.x * scale[k], __uint_as_float(w[k][j]), sums[j]);
+              sums[j + 1] = fmaf(s.y * scale[k], __uint_as_float(w[k][j + 1]), sums[j + 1]);
+              sums[j + 2] = fmaf(s.z * scale[k], __uint_as_float(w[k][j + 2]), sums[j + 2]);
+              sums[j + 3] = fmaf(s.w * scale[k], __uint_as_float(w[k][j + 3]), sums[j + 3]);
+            }
           }
         }
       }
