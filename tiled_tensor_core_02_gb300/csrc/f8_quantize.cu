@@ -42,30 +42,64 @@ struct In<kF8QuantF32> {
 template <int IN>
 constexpr int kVec = 16 / (int)sizeof(typename In<IN>::T);  // elements of 16 bytes
 
-// `n` elements from src on (0 to kVec), zeros behind them; `vec`: src lies on a 16-byte
-// boundary wherever n is kVec.
+// 16 bytes of the input as they are: kVec elements.
 template <int IN>
-__device__ __forceinline__ void load_vec(const typename In<IN>::T* src, int n, bool vec, float (&f)[kVec<IN>]) {
-  if (vec && n == kVec<IN>) {
-    const uint4 w = __ldcs(reinterpret_cast<const uint4*>(src));
-    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+struct Piece {
+  uint32_t w[4];
+
+  // `n` elements from src on (0 to kVec), zeros behind them; `vec`: src lies on a 16-byte
+  // boundary wherever n is kVec.
+  __device__ __forceinline__ void load(const typename In<IN>::T* src, int n, bool vec) {
+    if (vec && n == kVec<IN>) {
+      const uint4 v = __ldcs(reinterpret_cast<const uint4*>(src));
+      w[0] = v.x;
+      w[1] = v.y;
+      w[2] = v.z;
+      w[3] = v.w;
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (IN == kF8QuantF32) {
-        f[i] = __uint_as_float(ws[i]);
-      } else {
-        f[2 * i] = In<IN>::to_float((uint16_t)(ws[i] & 0xFFFFu));
-        f[2 * i + 1] = In<IN>::to_float((uint16_t)(ws[i] >> 16));
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (IN == kF8QuantF32) {
+          w[i] = i < n ? __float_as_uint(src[i]) : 0u;
+        } else {
+          w[i] = 2 * i < n ? src[2 * i] : 0u;
+          if (2 * i + 1 < n) w[i] |= (uint32_t)src[2 * i + 1] << 16;
+        }
       }
     }
-  } else {
-#pragma unroll
-    for (int e = 0; e < kVec<IN>; ++e) f[e] = e < n ? In<IN>::to_float(src[e]) : 0.0f;
   }
-}
+  __device__ __forceinline__ float operator[](int e) const {
+    if constexpr (IN == kF8QuantF32)
+      return __uint_as_float(w[e]);
+    else
+      return In<IN>::to_float((uint16_t)(e % 2 == 0 ? w[e / 2] & 0xFFFFu : w[e / 2] >> 16));
+  }
+};
 
 // Magnitudes as unsigned integers: in order, infinity after every number and NaN behind.
-__device__ __forceinline__ uint32_t mag(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+// 16-bit ones two a word.
+template <int IN>
+__device__ __forceinline__ uint32_t mags(uint32_t w) {
+  return w & (IN == kF8QuantF32 ? 0x7FFFFFFFu : 0x7FFF7FFFu);
+}
+template <int IN>
+__device__ __forceinline__ uint32_t max_mags(uint32_t a, uint32_t b) {
+  if constexpr (IN == kF8QuantF32) return max(a, b);
+  uint32_t v;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(v) : "r"(a), "r"(b));
+  return v;
+}
+// The bits of the largest magnitude of a word as fp32, and of either of its columns (one of fp32).
+template <int IN>
+__device__ __forceinline__ uint32_t mag_of(uint32_t w, int column) {
+  if constexpr (IN == kF8QuantF32) return w;
+  return __float_as_uint(In<IN>::to_float((uint16_t)(column == 0 ? w & 0xFFFFu : w >> 16)));
+}
+template <int IN>
+__device__ __forceinline__ uint32_t top_mag(uint32_t w) {
+  if constexpr (IN == kF8QuantF32) return w;
+  return mag_of<IN>(max(w & 0xFFFFu, w >> 16), 0);
+}
 
 struct BlockScale {
   float scale, inv;
@@ -81,16 +115,17 @@ __device__ __forceinline__ BlockScale block_scale(uint32_t m) {
     r.scale = 0.0f;
     r.inv = 0.0f;
   } else {
-    r.inv = __fdiv_rn(1.0f, r.scale);
+    r.inv = __frcp_rn(r.scale);
   }
   return r;
 }
 
-// Two values to two bytes, the first in the low one.  Without an inverse 0, whatever x is.
+// Two values to two bytes, the first in the low one.  Without an inverse (a block of zeros, or
+// with a NaN or an infinity) 0.
 template <bool E5M2>
-__device__ __forceinline__ uint32_t to_f8x2(float a, float b, float inv_a, float inv_b) {
-  const float2 v = make_float2(inv_a == 0.0f ? 0.0f : __fmul_rn(a, inv_a), inv_b == 0.0f ? 0.0f : __fmul_rn(b, inv_b));
-  return __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, E5M2 ? __NV_E5M2 : __NV_E4M3);
+__device__ __forceinline__ uint32_t to_f8x2(float a, float b, float inv) {
+  const uint32_t v = __nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(a, inv), __fmul_rn(b, inv)), __NV_SATFINITE, E5M2 ? __NV_E5M2 : __NV_E4M3);
+  return inv == 0.0f ? 0u : v;
 }
 
 // ------------------------------------------------------------------ rows
@@ -109,25 +144,26 @@ __global__ void __launch_bounds__(256) f8_rows_kernel(const F8QuantParams p, int
     const int part = parts == 1 ? 0 : (int)(it - row * parts);
     const typename In<IN>::T* src = static_cast<const typename In<IN>::T*>(p.x) + row * p.ldx;
     const int c0 = part * (kAtOnce * 32 * V) + lane * V;
-    float f[kAtOnce][V];
+    Piece<IN> f[kAtOnce];
 #pragma unroll
     for (int i = 0; i < kAtOnce; ++i) {
       const int c = c0 + i * 32 * V;
-      load_vec<IN>(src + c, max(0, min(V, p.cols - c)), VEC, f[i]);
+      f[i].load(src + c, max(0, min(V, p.cols - c)), VEC);
     }
 #pragma unroll
     for (int i = 0; i < kAtOnce; ++i) {
       const int c = c0 + i * 32 * V, n = p.cols - c;
-      uint32_t m = 0u;
+      uint32_t m = mags<IN>(f[i].w[0]);
 #pragma unroll
-      for (int e = 0; e < V; ++e) m = max(m, mag(f[i][e]));
+      for (int k = 1; k < 4; ++k) m = max_mags<IN>(m, mags<IN>(f[i].w[k]));
+      m = top_mag<IN>(m);
 #pragma unroll
       for (int o = 1; o < kLanes; o <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
       const BlockScale s = block_scale<E5M2>(m);
       if (lane % kLanes == 0 && n > 0) p.scale[row * p.lds + c / kF8Block] = s.scale;
       uint32_t o[V / 2];
 #pragma unroll
-      for (int e = 0; e < V / 2; ++e) o[e] = to_f8x2<E5M2>(f[i][2 * e], f[i][2 * e + 1], s.inv, s.inv);
+      for (int e = 0; e < V / 2; ++e) o[e] = to_f8x2<E5M2>(f[i][2 * e], f[i][2 * e + 1], s.inv);
       uint8_t* dst = p.q + row * p.ldq + c;
       if (VEC && n >= V) {
         if constexpr (V == 8)
@@ -158,11 +194,12 @@ __device__ __forceinline__ int turned(int col, int piece) { return col * 128 + (
 
 // SQUARE: one scale for the tile; else (TURN) one for each of its columns.
 template <int IN, bool E5M2, bool SQUARE, bool TURN, bool VEC>
-__global__ void __launch_bounds__(256) f8_tiles_kernel(const F8QuantParams p, int tiles_x, int64_t tiles) {
+__global__ void __launch_bounds__(256, IN == kF8QuantF32 ? 2 : 4) f8_tiles_kernel(const F8QuantParams p, int tiles_x, int64_t tiles) {
   using TO = TileOf<IN>;
   constexpr int V = TO::V, R = TO::kRows;
   __shared__ __align__(16) uint8_t bytes[TURN ? kF8Block * 128 : 16];
-  __shared__ uint32_t part[8][SQUARE ? 1 : kF8Block];
+  __shared__ uint32_t part[8][SQUARE ? 1 : 4 * TO::kGroups];
+  __shared__ float inverse[SQUARE ? 1 : kF8Block];
   const int cg = threadIdx.x % TO::kGroups, rg = threadIdx.x / TO::kGroups, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   grid_dependency_wait();
   grid_dependents_launch();
@@ -173,17 +210,17 @@ __global__ void __launch_bounds__(256) f8_tiles_kernel(const F8QuantParams p, in
     const int c = col0 + cg * V, nc = max(0, min(V, p.cols - c));
     const int r0 = row0 + rg * R;
     const typename In<IN>::T* src = static_cast<const typename In<IN>::T*>(p.x) + (int64_t)r0 * p.ldx + c;
-    float f[R][V];
+    Piece<IN> f[R];
 #pragma unroll
-    for (int i = 0; i < R; ++i) load_vec<IN>(src + (int64_t)i * p.ldx, r0 + i < p.rows ? nc : 0, VEC, f[i]);
+    for (int i = 0; i < R; ++i) f[i].load(src + (int64_t)i * p.ldx, r0 + i < p.rows ? nc : 0, VEC);
     float inv[SQUARE ? 1 : V];
     if constexpr (SQUARE) {
       uint32_t m = 0u;
 #pragma unroll
       for (int i = 0; i < R; ++i)
 #pragma unroll
-        for (int e = 0; e < V; ++e) m = max(m, mag(f[i][e]));
-      m = __reduce_max_sync(0xFFFFFFFFu, m);
+        for (int k = 0; k < 4; ++k) m = max_mags<IN>(m, mags<IN>(f[i].w[k]));
+      m = __reduce_max_sync(0xFFFFFFFFu, top_mag<IN>(m));
       if (lane == 0) part[warp][0] = m;
       __syncthreads();
 #pragma unroll
@@ -192,24 +229,28 @@ __global__ void __launch_bounds__(256) f8_tiles_kernel(const F8QuantParams p, in
       inv[0] = s.inv;
       if (threadIdx.x == 0) p.scale[(TURN ? tx : ty) * p.lds + (TURN ? ty : (int64_t)tx)] = s.scale;
     } else {
-      uint32_t m[V];
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        m[e] = 0u;
+      for (int k = 0; k < 4; ++k) {
+        uint32_t m = 0u;
 #pragma unroll
-        for (int i = 0; i < R; ++i) m[e] = max(m[e], mag(f[i][e]));
-        if constexpr (TO::kGroups == 16) m[e] = max(m[e], __shfl_xor_sync(0xFFFFFFFFu, m[e], 16));
-        if (lane < TO::kGroups) part[warp][cg * V + e] = m[e];
+        for (int i = 0; i < R; ++i) m = max_mags<IN>(m, mags<IN>(f[i].w[k]));
+        if constexpr (TO::kGroups == 16) m = max_mags<IN>(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
+        if (lane < TO::kGroups) part[warp][cg * 4 + k] = m;
+      }
+      __syncthreads();
+      // a thread a column: the quotients are the costly part
+      if (threadIdx.x < kF8Block) {
+        constexpr int kPer = V / 4;  // columns of a word
+        uint32_t m = 0u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max_mags<IN>(m, part[i][threadIdx.x / kPer]);
+        const BlockScale s = block_scale<E5M2>(mag_of<IN>(m, threadIdx.x % kPer));
+        inverse[threadIdx.x] = s.inv;
+        if (col0 + (int)threadIdx.x < p.cols) p.scale[(int64_t)(col0 + (int)threadIdx.x) * p.lds + ty] = s.scale;
       }
       __syncthreads();
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m[e] = max(m[e], part[i][cg * V + e]);
-        const BlockScale s = block_scale<E5M2>(m[e]);
-        inv[e] = s.inv;
-        if (rg == 0 && e < nc) p.scale[(int64_t)(c + e) * p.lds + ty] = s.scale;
-      }
+      for (int e = 0; e < V; ++e) inv[e] = inverse[cg * V + e];
     }
     if constexpr (!TURN) {
 #pragma unroll
@@ -217,7 +258,7 @@ __global__ void __launch_bounds__(256) f8_tiles_kernel(const F8QuantParams p, in
         if (r0 + i >= p.rows) continue;
         uint32_t o[V / 2];
 #pragma unroll
-        for (int e = 0; e < V / 2; ++e) o[e] = to_f8x2<E5M2>(f[i][2 * e], f[i][2 * e + 1], inv[0], inv[0]);
+        for (int e = 0; e < V / 2; ++e) o[e] = to_f8x2<E5M2>(f[i][2 * e], f[i][2 * e + 1], inv[0]);
         uint8_t* dst = p.q + (int64_t)(r0 + i) * p.ldq + c;
         if (VEC && nc == V) {
           if constexpr (V == 8)
@@ -239,7 +280,7 @@ __global__ void __launch_bounds__(256) f8_tiles_kernel(const F8QuantParams p, in
         for (int i = 0; i < R; i += 8) {
           uint32_t o[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) o[k] = to_f8x2<E5M2>(f[i + 2 * k][e], f[i + 2 * k + 1][e], s, s);
+          for (int k = 0; k < 4; ++k) o[k] = to_f8x2<E5M2>(f[i + 2 * k][e], f[i + 2 * k + 1][e], s);
           *reinterpret_cast<uint2*>(bytes + turned(cg * V + e, (rg * R + i) / 8)) = make_uint2(o[0] | o[1] << 16, o[2] | o[3] << 16);
         }
       }
