@@ -511,9 +511,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) f8_pair
               v[4 * k + 3] += __shfl_sync(0xFFFFFFFFu, bias.w, src);
             }
           }
-          if (p.act != kActNone) {
+          if (p.act == kActGelu) {
 #pragma unroll
-            for (int k = 0; k < kElems; ++k) v[k] = act_value(p.act, v[k]);
+            for (int k = 0; k < kElems; ++k) v[k] = act_value(kActGelu, v[k]);
+          } else if (p.act == kActRelu) {
+#pragma unroll
+            for (int k = 0; k < kElems; ++k) v[k] = act_value(kActRelu, v[k]);
           }
           if constexpr (OUT == kF8ResultF32)
             *piece = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));

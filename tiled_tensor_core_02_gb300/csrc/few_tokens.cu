@@ -290,30 +290,46 @@ __global__ void __launch_bounds__(kThreads, 1) few_tokens_kernel(const __grid_co
         if constexpr (kIsGatedGrad<P>) {
           if (c > 0) load_kept(p, row0 + c, f, tokens - c, f_ok, kept);
         }
-        if (f_ok) {
+        if (!f_ok) continue;
+        if constexpr (kIsGatedForward<P>) {
+          with_act(p.act, [&](auto act) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if (c + j < tokens)
+                d[(int64_t)(c + j) * p.ldd] =
+                    round_half<BF16>(gated_act<decltype(act)::value>(__uint_as_float(w[j])) * __uint_as_float(w2[j]));
+          });
+          if (p.gate != nullptr) {
+            uint16_t* g = static_cast<uint16_t*>(p.gate) + (int64_t)(row0 + c) * p.ldp + f;
+            uint16_t* u = static_cast<uint16_t*>(p.up) + (int64_t)(row0 + c) * p.ldp + f;
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if (c + j < tokens) {
+                g[j * p.ldp] = round_half<BF16>(__uint_as_float(w[j]));
+                u[j * p.ldp] = round_half<BF16>(__uint_as_float(w2[j]));
+              }
+          }
+        } else if constexpr (kIsGatedGrad<P>) {
+          uint16_t* dg = static_cast<uint16_t*>(p.dgate) + (int64_t)(row0 + c) * p.lddp + f;
+          uint16_t* du = static_cast<uint16_t*>(p.dup) + (int64_t)(row0 + c) * p.lddp + f;
+          with_act(p.act, [&](auto act) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if (c + j < tokens) {
+                const float dh = __uint_as_float(w[j]), u = half_bits_to_float<BF16>(kept.up[j]);
+                const ActSlope a = act_slope<decltype(act)::value>(half_bits_to_float<BF16>(kept.gate[j]));
+                dg[j * p.lddp] = round_half<BF16>(dh * u * a.slope);
+                du[j * p.lddp] = round_half<BF16>(dh * a.value);
+                if (p.D != nullptr) d[(int64_t)(c + j) * p.ldd] = round_half<BF16>(a.value * u);
+              }
+          });
+        } else {
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             if (c + j < tokens) {
-              const int64_t r = c + j;
-              if constexpr (kIsGatedForward<P>) {
-                const float g = __uint_as_float(w[j]), u = __uint_as_float(w2[j]);
-                d[r * p.ldd] = round_half<BF16>(gated_act(p.act, g) * u);
-                if (p.gate != nullptr) {
-                  static_cast<uint16_t*>(p.gate)[(row0 + r) * p.ldp + f] = round_half<BF16>(g);
-                  static_cast<uint16_t*>(p.up)[(row0 + r) * p.ldp + f] = round_half<BF16>(u);
-                }
-              } else if constexpr (kIsGatedGrad<P>) {
-                const float dh = __uint_as_float(w[j]);
-                const float u = half_bits_to_float<BF16>(kept.up[j]), g = half_bits_to_float<BF16>(kept.gate[j]);
-                const ActSlope a = act_slope(p.act, g);
-                static_cast<uint16_t*>(p.dgate)[(row0 + r) * p.lddp + f] = round_half<BF16>(dh * u * a.slope);
-                static_cast<uint16_t*>(p.dup)[(row0 + r) * p.lddp + f] = round_half<BF16>(dh * a.value);
-                if (p.D != nullptr) d[r * p.ldd] = round_half<BF16>(gated_act(p.act, g) * u);
-              } else {
-                float v = p.alpha * __uint_as_float(w[j]);
-                if (p.bias != nullptr) v += bias;
-                d[r * p.ldd] = round_half<BF16>(act_value(p.act, v));
-              }
+              float v = p.alpha * __uint_as_float(w[j]);
+              if (p.bias != nullptr) v += bias;
+              d[(int64_t)(c + j) * p.ldd] = round_half<BF16>(act_value(p.act, v));
             }
           }
         }

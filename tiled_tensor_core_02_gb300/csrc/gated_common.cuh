@@ -14,11 +14,14 @@ constexpr int kActSilu = 3;  // gated blocks only
 // The logistic function.  exp overflows to infinity for v below -88.7: 0, as it should be.
 __device__ __forceinline__ float logistic(float v) { return __fdividef(1.0f, 1.0f + __expf(-v)); }
 
-__device__ __forceinline__ float gated_act(int act, float v) {
+// ACT: the activation, which a warp tells apart once for all of its values: a branch for each
+// of them cost more than the arithmetic.
+template <int ACT>
+__device__ __forceinline__ float gated_act(float v) {
   // v / (1 + exp(-v)) with the division's own limit in mind: __fdividef gives 0 for
   // denominators from 2^126 on, where the quotient is below 2^-119
-  if (act == kActSilu) return __fdividef(v, 1.0f + __expf(-v));
-  return act_value(act, v);
+  if constexpr (ACT == kActSilu) return __fdividef(v, 1.0f + __expf(-v));
+  return act_value(ACT, v);
 }
 
 // act(v) and its derivative.  SiLU: s + v s (1 - s), s the logistic function; GELU
@@ -28,23 +31,37 @@ __device__ __forceinline__ float gated_act(int act, float v) {
 struct ActSlope {
   float value, slope;
 };
-__device__ __forceinline__ ActSlope act_slope(int act, float v) {
+template <int ACT>
+__device__ __forceinline__ ActSlope act_slope(float v) {
   ActSlope r{v, 1.0f};
-  if (act == kActSilu) {
+  if constexpr (ACT == kActSilu) {
     const float s = logistic(v);
     r.value = v * s;
     r.slope = fmaf(r.value, 1.0f - s, s);
-  } else if (act == kActGelu) {
+  } else if constexpr (ACT == kActGelu) {
     const float c = fminf(fmaxf(v, -16.0f), 16.0f);
     const float q = logistic(1.5957691216057308f * fmaf(0.044715f * c, c * c, c));
     r.value = v * q;
     r.slope = fmaf(c * q * (1.0f - q), 1.5957691216057308f * fmaf(0.134145f * c, c, 1.0f), q);
     if (v != v) r.value = r.slope = v;
-  } else if (act == kActRelu) {
+  } else if constexpr (ACT == kActRelu) {
     r.value = v < 0.0f ? 0.0f : v;
     r.slope = v > 0.0f ? 1.0f : 0.0f;
   }
   return r;
+}
+
+// Calls f with the activation as a constant.
+template <typename F>
+__device__ __forceinline__ void with_act(int act, F f) {
+  if (act == kActSilu)
+    f(std::integral_constant<int, kActSilu>{});
+  else if (act == kActGelu)
+    f(std::integral_constant<int, kActGelu>{});
+  else if (act == kActRelu)
+    f(std::integral_constant<int, kActRelu>{});
+  else
+    f(std::integral_constant<int, kActNone>{});
 }
 
 // 32 staged rows of 64 16-bit columns to global memory (pitch ld), `rows` and `n` of
@@ -178,8 +195,10 @@ __device__ __forceinline__ void gated_forward_unit(const GatedParams& p, uint32_
     tmem_ld_wait();
     if (h == 1) release();
     float v[32];
+    with_act(p.act, [&](auto act) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = gated_act(p.act, __uint_as_float(g[j])) * __uint_as_float(u[j]);
+      for (int j = 0; j < 32; ++j) v[j] = gated_act<decltype(act)::value>(__uint_as_float(g[j])) * __uint_as_float(u[j]);
+    });
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       *reinterpret_cast<uint4*>(sb + staged<32>(lane, h * 4 + i)) =
@@ -225,22 +244,30 @@ __device__ __forceinline__ bool gated_grad_unit(const GatedParams& p, uint32_t a
   turn_unit(up, p.ldp, whole, rows, n, lane, sb, u);
   if (!wait()) return false;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint32_t w[32];
-    sums_32(at + h * 32, has_k, w);
-    tmem_ld_wait();
-    if (h == 1) release();
+  for (int h = 0; h < 4; ++h) {
+    uint32_t w[16];
+    if (has_k) {
+      tmem_ld_32x32b_x16<0>(at + h * 16, w);
+    } else {
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      float g0, g1, u0, u1;
-      unpack2(BF16, g[h * 16 + j], g0, g1);
-      unpack2(BF16, u[h * 16 + j], u0, u1);
-      const ActSlope a0 = act_slope(p.act, g0), a1 = act_slope(p.act, g1);
-      const float d0 = __uint_as_float(w[2 * j]), d1 = __uint_as_float(w[2 * j + 1]);
-      g[h * 16 + j] = pack2<BF16>(d0 * u0 * a0.slope, d1 * u1 * a1.slope);
-      u[h * 16 + j] = pack2<BF16>(d0 * a0.value, d1 * a1.value);
-      d[h * 16 + j] = p.D != nullptr ? pack2<BF16>(a0.value * u0, a1.value * u1) : 0u;
+      for (int j = 0; j < 16; ++j) w[j] = 0u;
     }
+    tmem_ld_wait_for(w);
+    if (h == 3) release();
+    with_act(p.act, [&](auto act) {
+      constexpr int kAct = decltype(act)::value;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float g0, g1, u0, u1;
+        unpack2(BF16, g[h * 8 + j], g0, g1);
+        unpack2(BF16, u[h * 8 + j], u0, u1);
+        const ActSlope a0 = act_slope<kAct>(g0), a1 = act_slope<kAct>(g1);
+        const float d0 = __uint_as_float(w[2 * j]), d1 = __uint_as_float(w[2 * j + 1]);
+        g[h * 8 + j] = pack2<BF16>(d0 * u0 * a0.slope, d1 * u1 * a1.slope);
+        u[h * 8 + j] = pack2<BF16>(d0 * a0.value, d1 * a1.value);
+        d[h * 8 + j] = pack2<BF16>(a0.value * u0, a1.value * u1);
+      }
+    });
   }
   stage_words(sb, lane, g);
   __syncwarp();
