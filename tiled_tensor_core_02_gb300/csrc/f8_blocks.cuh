@@ -24,8 +24,8 @@ struct F8Params : GroupedParams {
   int sa_vec, sb_vec;  // rows of scales start on 16-byte boundaries
 };
 
-// Any pitch and alignment: tiles of 64 x 64, warp-level products of fp16 copies.
-constexpr int kF8PlainTile = 64;
+// Any pitch and alignment: tiles of 128 x 128, warp-level products of fp16 copies.
+constexpr int kF8PlainTile = 128;
 cudaError_t launch_f8_plain(const F8Params& p, F8Result out, int ctas, cudaStream_t stream);
 
 // Few tokens: blocks of 16, 32 and 64 of a group's, tiles of 8 to 128 output columns.  tmA

@@ -163,7 +163,7 @@ ttc_status ttc_gemm_f8_blocks(int64_t groups, int64_t M, int64_t N, int64_t K, c
     return TTC_OK;
   }
   set_walk(p, 0, col_blocks, 4);
-  const int64_t tiles = (blocks_of(M, kF8PlainTile) + likely) * col_blocks, room = 4ll * env.sm_count;
+  const int64_t tiles = (blocks_of(M, kF8PlainTile) + likely) * col_blocks, room = env.sm_count;
   if (launch_f8_plain(p, out, (int)(tiles < room ? tiles : room), s) != cudaSuccess) return TTC_ERR_CUDA;
   count_launches(1);
   return TTC_OK;
