@@ -99,39 +99,44 @@ __device__ __forceinline__ void stage_words(uint8_t* sb, int lane, const uint32_
     *reinterpret_cast<uint4*>(sb + staged<32>(lane, i)) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
 }
 
-// The reverse of store_unit, in two steps so that both matrices' loads are on their
-// way together: rows on 16-byte boundaries and whole units into registers, in the
-// order of store_unit; then through the staging block to a row per lane.  Zeros
-// outside `rows` and `n` columns.
-__device__ __forceinline__ void fetch_unit(const uint16_t* c0, int64_t ld, bool whole, int rows, int lane, uint32_t (&w)[32]) {
+// The reverse of store_unit, in two steps so that both matrices' loads are on their way
+// together: into registers in the order of store_unit, 16 bytes a lane where rows start on
+// 16-byte boundaries and the piece lies inside (`n` columns do), else element by element, all of
+// them asked for before the first is used; then through the staging block to a row per lane.
+// Zeros outside `rows` and `n` columns.
+__device__ __forceinline__ void fetch_unit(const uint16_t* c0, int64_t ld, bool vec, int rows, int n, int lane,
+                                           uint32_t (&w)[32]) {
   const int piece = lane & 7, r0 = lane >> 3;
   const uint16_t* src = c0 + (int64_t)r0 * ld + piece * 8;
+  n -= piece * 8;
+  if (vec && n >= 8) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (whole && i * 4 + r0 < rows) v = *reinterpret_cast<const uint4*>(src + (int64_t)(i * 4) * ld);
-    w[4 * i] = v.x;
-    w[4 * i + 1] = v.y;
-    w[4 * i + 2] = v.z;
-    w[4 * i + 3] = v.w;
-  }
-}
-__device__ __forceinline__ void turn_unit(const uint16_t* c0, int64_t ld, bool whole, int rows, int n, int lane, uint8_t* sb,
-                                          uint32_t (&w)[32]) {
-  const int piece = lane & 7, r0 = lane >> 3;
-  if (whole) {
+    for (int i = 0; i < 8; ++i) {
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (i * 4 + r0 < rows) v = *reinterpret_cast<const uint4*>(src + (int64_t)(i * 4) * ld);
+      w[4 * i] = v.x;
+      w[4 * i + 1] = v.y;
+      w[4 * i + 2] = v.z;
+      w[4 * i + 3] = v.w;
+    }
+  } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      *reinterpret_cast<uint4*>(sb + staged<32>(i * 4 + r0, piece)) =
-          make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-  } else {
-#pragma unroll 1
-    for (int c = lane; c < 64; c += 32)
-#pragma unroll 1
-      for (int r = 0; r < 32; ++r)
-        *reinterpret_cast<uint16_t*>(sb + staged<32>(r, c / 8) + (c % 8) * 2) =
-            r < rows && c < n ? c0[(int64_t)r * ld + c] : (uint16_t)0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const bool in = i * 4 + r0 < rows;
+        const uint16_t* at = src + (int64_t)(i * 4) * ld + 2 * e;
+        const uint32_t lo = in && 2 * e < n ? at[0] : 0u, hi = in && 2 * e + 1 < n ? at[1] : 0u;
+        w[4 * i + e] = lo | hi << 16;
+      }
   }
+}
+__device__ __forceinline__ void turn_unit(int lane, uint8_t* sb, uint32_t (&w)[32]) {
+  const int piece = lane & 7, r0 = lane >> 3;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    *reinterpret_cast<uint4*>(sb + staged<32>(i * 4 + r0, piece)) =
+        make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
   __syncwarp();
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -235,13 +240,10 @@ __device__ __forceinline__ bool gated_grad_unit(const GatedParams& p, uint32_t a
     return true;
   }
   uint32_t g[32], u[32], d[32];
-  const bool whole = p.p_vec != 0 && n >= 64;
-  const uint16_t* gate = static_cast<const uint16_t*>(p.gate) + row * p.ldp + col;
-  const uint16_t* up = static_cast<const uint16_t*>(p.up) + row * p.ldp + col;
-  fetch_unit(gate, p.ldp, whole, rows, lane, g);
-  fetch_unit(up, p.ldp, whole, rows, lane, u);
-  turn_unit(gate, p.ldp, whole, rows, n, lane, sb, g);
-  turn_unit(up, p.ldp, whole, rows, n, lane, sb, u);
+  fetch_unit(static_cast<const uint16_t*>(p.gate) + row * p.ldp + col, p.ldp, p.p_vec != 0, rows, n, lane, g);
+  fetch_unit(static_cast<const uint16_t*>(p.up) + row * p.ldp + col, p.ldp, p.p_vec != 0, rows, n, lane, u);
+  turn_unit(lane, sb, g);
+  turn_unit(lane, sb, u);
   if (!wait()) return false;
 #pragma unroll
   for (int h = 0; h < 4; ++h) {
