@@ -120,12 +120,12 @@ __device__ __forceinline__ BlockScale block_scale(uint32_t m) {
   return r;
 }
 
-// Two values to two bytes, the first in the low one.  Without an inverse (a block of zeros, or
-// with a NaN or an infinity) 0.
+// Two values to two bytes, the first in the low one.  What comes without an inverse (of a block
+// of zeros, or with a NaN or an infinity) is no result: such a block's is 0.
 template <bool E5M2>
 __device__ __forceinline__ uint32_t to_f8x2(float a, float b, float inv) {
-  const uint32_t v = __nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(a, inv), __fmul_rn(b, inv)), __NV_SATFINITE, E5M2 ? __NV_E5M2 : __NV_E4M3);
-  return inv == 0.0f ? 0u : v;
+  const float2 v = __fmul2_rn(make_float2(a, b), make_float2(inv, inv));
+  return __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, E5M2 ? __NV_E5M2 : __NV_E4M3);
 }
 
 // ------------------------------------------------------------------ rows
@@ -150,20 +150,36 @@ __global__ void __launch_bounds__(256) f8_rows_kernel(const F8QuantParams p, int
       const int c = c0 + i * 32 * V;
       f[i].load(src + c, max(0, min(V, p.cols - c)), VEC);
     }
+    uint32_t m[kAtOnce];
 #pragma unroll
     for (int i = 0; i < kAtOnce; ++i) {
+      m[i] = mags<IN>(f[i].w[0]);
+#pragma unroll
+      for (int k = 1; k < 4; ++k) m[i] = max_mags<IN>(m[i], mags<IN>(f[i].w[k]));
+      m[i] = top_mag<IN>(m[i]);
+#pragma unroll
+      for (int o = 1; o < kLanes; o <<= 1) m[i] = max(m[i], __shfl_xor_sync(0xFFFFFFFFu, m[i], o));
+    }
+    // a lane a block: the quotients are the costly part
+    const int mine = lane % kLanes % kAtOnce;
+    uint32_t top = m[0];
+#pragma unroll
+    for (int i = 1; i < kAtOnce; ++i) top = mine == i ? m[i] : top;
+    const BlockScale s = block_scale<E5M2>(top);
+    const int block = (c0 + mine * 32 * V) / kF8Block;
+    if (lane % kLanes < kAtOnce && block * kF8Block < p.cols) p.scale[row * p.lds + block] = s.scale;
+    const bool empty = __any_sync(0xFFFFFFFFu, s.inv == 0.0f);
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const float inv = __shfl_sync(0xFFFFFFFFu, s.inv, lane / kLanes * kLanes + i);
       const int c = c0 + i * 32 * V, n = p.cols - c;
-      uint32_t m = mags<IN>(f[i].w[0]);
-#pragma unroll
-      for (int k = 1; k < 4; ++k) m = max_mags<IN>(m, mags<IN>(f[i].w[k]));
-      m = top_mag<IN>(m);
-#pragma unroll
-      for (int o = 1; o < kLanes; o <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-      const BlockScale s = block_scale<E5M2>(m);
-      if (lane % kLanes == 0 && n > 0) p.scale[row * p.lds + c / kF8Block] = s.scale;
       uint32_t o[V / 2];
 #pragma unroll
-      for (int e = 0; e < V / 2; ++e) o[e] = to_f8x2<E5M2>(f[i][2 * e], f[i][2 * e + 1], s.inv);
+      for (int e = 0; e < V / 2; ++e) o[e] = to_f8x2<E5M2>(f[i][2 * e], f[i][2 * e + 1], inv);
+      if (empty && inv == 0.0f) {
+#pragma unroll
+        for (int e = 0; e < V / 2; ++e) o[e] = 0u;
+      }
       uint8_t* dst = p.q + row * p.ldq + c;
       if (VEC && n >= V) {
         if constexpr (V == 8)
@@ -258,7 +274,7 @@ __global__ void __launch_bounds__(256, IN == kF8QuantF32 ? 2 : 4) f8_tiles_kerne
         if (r0 + i >= p.rows) continue;
         uint32_t o[V / 2];
 #pragma unroll
-        for (int e = 0; e < V / 2; ++e) o[e] = to_f8x2<E5M2>(f[i][2 * e], f[i][2 * e + 1], inv[0]);
+        for (int e = 0; e < V / 2; ++e) o[e] = inv[0] == 0.0f ? 0u : to_f8x2<E5M2>(f[i][2 * e], f[i][2 * e + 1], inv[0]);
         uint8_t* dst = p.q + (int64_t)(r0 + i) * p.ldq + c;
         if (VEC && nc == V) {
           if constexpr (V == 8)
@@ -280,7 +296,7 @@ __global__ void __launch_bounds__(256, IN == kF8QuantF32 ? 2 : 4) f8_tiles_kerne
         for (int i = 0; i < R; i += 8) {
           uint32_t o[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) o[k] = to_f8x2<E5M2>(f[i + 2 * k][e], f[i + 2 * k + 1][e], s);
+          for (int k = 0; k < 4; ++k) o[k] = s == 0.0f ? 0u : to_f8x2<E5M2>(f[i + 2 * k][e], f[i + 2 * k + 1][e], s);
           *reinterpret_cast<uint2*>(bytes + turned(cg * V + e, (rg * R + i) / 8)) = make_uint2(o[0] | o[1] << 16, o[2] | o[3] << 16);
         }
       }
