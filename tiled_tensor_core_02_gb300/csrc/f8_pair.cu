@@ -2,24 +2,26 @@
 // (kind::f8f6f4), operands by TMA.
 //
 // The scales change with every 128 of K, so the tensor cores add up one such block at
-// a time, for 128 columns each: four accumulators of tensor memory take turns, and the
-// epilogue warps add them, scaled, to the tile's sums in their registers.  Half of the
-// sixteen warps take one of a block's two accumulators, half the other; a thread has one
-// row and 64 columns, read 16 at a time.  That is what hides the way from an accumulator's
-// last MMA to its being free again (about 0.5 us, and the additions): 8192 x 14336 x 4096 with
-// GELU took 690 us by eight warps of 128 columns and these accumulators, 602 with two of 256
-// columns, 510 as it is; loads of 32 columns 594, of 8 533.  The MMAs alone take 255 us
-// with 256 columns an instruction, 313 with 128.
+// a time: each goes into one of two accumulators in tensor memory, and sixteen epilogue warps
+// add it, scaled, to the tile's sums in their registers (a thread has one row and 64 columns,
+// read 16 at a time) while the tensor cores fill the other.  What has to be short is the way
+// from an accumulator's last MMA to its being free again, two crossings between SMs and the
+// reads: 8192 x 14336 x 4096 takes 447 us, 401 without the results' way out, 255 by the MMAs
+// alone.  Eight warps of 128 columns, which read twice as long, took 751; four accumulators of
+// 128 columns 464, where an MMA of half the width costs more than half (313 us alone); loads of
+// 32 columns a fifth more, of 8 a twentieth.
 //
 // Two warps bring the scales of four blocks of K at a time into shared memory: A's by row, B's
-// one for 128 columns or one a column.  In the epilogue's own hands they took registers that
-// the sums need, and what is spilled goes to L2, nearly all of L1 being shared memory here.
-// For the same reason the four warps that load and issue hand registers over.  The MMAs are
-// issued by a converged warp: by one thread of it, which moves descriptors to uniform registers
-// each time, an accumulator took 0.38 us instead of 0.22.
+// one for 128 columns or one a column, and where the tile lies.  In the epilogue's own hands
+// they took registers that the sums need, and what is spilled goes to L2, nearly all of L1
+// being shared memory here.  For the same reason the four warps that load and issue hand
+// registers over.  The MMAs are issued by a converged warp: by one thread of it, which moves
+// descriptors to uniform registers each time, four of them took 0.38 us instead of 0.22.
 //
-// Bound by the epilogue: 0.54 us a block of K and tile, and at a tile's end 2.4 us with GELU
-// (1.3 of them its exponentials and quotients), during which the tensor cores get two blocks ahead.
+// Bound by the epilogue: 0.52 us a block of K and tile, and at a tile's end 1.9 us, with GELU
+// 3.7 (its exponentials and quotients), during which the tensor cores get two blocks ahead.
+// 8192 x 14336 x 4096: 2.15 PFLOP/s, with GELU 1.97; by columns, fp32 sums added to,
+// 4096 x 4096 x 8192 203 us.
 #include <atomic>
 #include <type_traits>
 
@@ -43,7 +45,7 @@ constexpr int kStages = 4;
 // Scales of a chunk of K: A's of 128 rows, four each, then B's.
 constexpr int kAhead = 4;       // blocks of K of a chunk
 constexpr int kScaleSlots = 2;  // chunks on their way
-constexpr int kScaleBytes = 128 * kAhead * 4 + kTile * kAhead * 4 + 16;
+constexpr int kScaleBytes = 128 * kAhead * 4 + kTile * kAhead * 4 + 32;
 constexpr int kSmemBytes =
     1024 + kStages * 2 * kShareBytes + kStagingBytes + kScaleSlots * kScaleBytes + kBarBytes + kTableInts * 4;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
@@ -52,28 +54,14 @@ static_assert((kMaxGroups + 3) / 4 + 1 <= kTableInts, "a table of every fourth g
 constexpr int kRegsLaunch = 96, kRegsFew = 64, kRegsMany = 104;
 static_assert(128 * kRegsFew + (kThreads - 128) * kRegsMany <= kThreads * kRegsLaunch, "the shares fit the launch's registers");
 constexpr int kLoad = 16;  // columns a load
-constexpr int kAccs = 4, kAccCols = 128;  // accumulators; columns of each, from either CTA's weights half of them
+constexpr int kAccs = 2, kAccCols = kTile;  // accumulators; columns of each
 
-// Where an epilogue warp's part of a tile lies: 32 rows, 64 columns (none of half a tile for
-// the warps of the second accumulator).
-struct Part {
-  int g, col0, cols;  // group; first column of D; columns inside D
-  int64_t row;
-  int rows;
+// What the loaders of scales tell the epilogue about a chunk's tile.
+struct TileInfo {
+  int parts;            // 2, of half a tile 1
+  int g, col0;          // group; first column of D
+  int row0, row_end;    // first row of the CTA, the group's last
 };
-__device__ __forceinline__ Part part_of(const F8Params& p, const GroupTable& tb, const PairWalk& walk, int t, uint32_t rank, int q,
-                                        int half, int second) {
-  const PairItem item = pair_item<false>(p, tb, walk, t);
-  const GroupedTile& x = item.x;
-  const int r0 = x.rb * kTile + (int)rank * 128 + q * 32;
-  Part e;
-  e.g = x.g;
-  e.col0 = x.cb * kTile + (item.half < 0 ? half * 128 + second * 64 : item.half * 128 + half * 64);
-  e.cols = item.half >= 0 && second != 0 ? 0 : min(64, p.N - e.col0);
-  e.row = (int64_t)x.lo + r0;
-  e.rows = max(0, min(32, x.hi - x.lo - r0));
-  return e;
-}
 
 // Four scales in a row of which `n` exist (zeros behind them); volatile, so that they are
 // asked for here and not where they are used.
@@ -186,8 +174,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) f8_pair
   uint64_t* stall_bar = scale_empty + kScaleSlots;
   uint64_t* drain_bar = stall_bar + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain_bar + 1);
-  // what the producer tells the MMA issuer about a stage: how many accumulators it fills,
-  // one of half a tile
+  // what the producer tells the MMA issuer about a stage: 2, of half a tile 1
   int* stage_info = reinterpret_cast<int*>(drain_bar + 2);
 
   static_assert((2 * kStages + 2 * kAccs + 2 * kScaleSlots + 3) * 8 + kStages * 4 <= kBarBytes, "barrier area");
@@ -215,7 +202,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) f8_pair
     }
     if (lane < kAccs) {
       mbar_init(&tmem_full[lane], 1);
-      mbar_init(&tmem_empty[lane], kEpiWarpCount);  // half the warps of either CTA
+      mbar_init(&tmem_empty[lane], 2 * kEpiWarpCount);
     }
     if (lane < kScaleSlots) {
       mbar_init(&scale_full[lane], kLoaders);
@@ -296,7 +283,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) f8_pair
       if (leader) {
         const uint32_t lead = elect_lead(), tmem_base = find_tmem();
         const PairWalk walk = find_walk();
-        const uint32_t idesc = idesc_f8(p.a_e5m2 != 0, p.b_e5m2 != 0, kTile, kAccCols);
+        const uint32_t idesc_whole = idesc_f8(p.a_e5m2 != 0, p.b_e5m2 != 0, kTile, kTile);
+        const uint32_t idesc_half = idesc_f8(p.a_e5m2 != 0, p.b_e5m2 != 0, kTile, kTile / 2);
         const uint64_t a0 = smem_desc_sw128(smem_u32(sA), 16u, 1024);
         const uint64_t b0 = smem_desc_sw128(smem_u32(sB), 16u, 1024);
         const uint32_t a_hi = (uint32_t)(a0 >> 32), b_hi = (uint32_t)(b0 >> 32);
@@ -310,24 +298,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) f8_pair
               ok = false;
               break;
             }
-            const int parts = stage_info[stage];
+            const uint32_t idesc = stage_info[stage] == 2 ? idesc_whole : idesc_half;
             const uint32_t a_lo = (uint32_t)a0 + (uint32_t)stage * (kShareBytes >> 4);
-            uint32_t b_lo = (uint32_t)b0 + (uint32_t)stage * (kShareBytes >> 4);
-            for (int h = 0; h < parts; ++h, ++it, b_lo += 64 * kF8Block >> 4) {
-              const uint32_t acc = it & (kAccs - 1);
-              // the first use of each accumulator passes at once
-              if (!mbar_wait_warp(&tmem_empty[acc], ((it / kAccs) & 1) ^ 1u, wc)) {
-                ok = false;
-                break;
-              }
-              tc_fence_after();
-#pragma unroll
-              for (int k = 0; k < kF8Block / 32; ++k)
-                mma_f8_pair_lead(lead, tmem_base + acc * kAccCols, a_lo + k * 2, a_hi, b_lo + k * 2, b_hi, idesc, k != 0);
-              any = true;
-              mma_commit_pair_lead(lead, &tmem_full[acc], 0x3);
+            const uint32_t b_lo = (uint32_t)b0 + (uint32_t)stage * (kShareBytes >> 4);
+            const uint32_t acc = it & (kAccs - 1);
+            // the first use of each accumulator passes at once
+            if (!mbar_wait_warp(&tmem_empty[acc], ((it / kAccs) & 1) ^ 1u, wc)) {
+              ok = false;
+              break;
             }
-            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < kF8Block / 32; ++k)
+              mma_f8_pair_lead(lead, tmem_base + acc * kAccCols, a_lo + k * 2, a_hi, b_lo + k * 2, b_hi, idesc, k != 0);
+            any = true;
+            ++it;
+            mma_commit_pair_lead(lead, &tmem_full[acc], 0x3);
             mma_commit_pair_lead(lead, &empty[stage], 0x3);
             if (++stage == kStages) {
               stage = 0;
@@ -391,7 +377,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) f8_pair
           }
 #pragma unroll
           for (int i = 0; i < 2; ++i) a_out[i * kLoaders + i0] = a[i];
-          if (i0 == 0) *reinterpret_cast<uint32_t*>(b_out + kTile * kAhead) = width / 128;
+          if (i0 == 0) *reinterpret_cast<TileInfo*>(b_out + kTile * kAhead) = TileInfo{width / 128, x.g, col0, row0, x.hi};
           mbar_arrive(&scale_full[slot]);
         }
       }
@@ -402,10 +388,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) f8_pair
     using T = typename std::conditional<OUT == kF8ResultF32, float, uint16_t>::type;
     constexpr int kUnit = 128 / (int)sizeof(T);  // columns that 128 bytes hold
     constexpr int kElems = 16 / (int)sizeof(T);
-    // quarter of the rows; which CTA's half of an accumulator's columns; which of a block's accumulators
+    // quarter of the rows; which CTA's weights the columns are of, and which half of those (of
+    // half a tile they have 64 columns, and the second warps nothing)
     const int ew = warp - kEpiWarp0, q = warp & 3, half = (ew >> 2) & 1, second = ew >> 3;
     const PairWalk walk = find_walk();
-    const uint32_t from = find_tmem() + ((uint32_t)(q * 32) << 16) + half * (kAccCols / 2);
+    const uint32_t from = find_tmem() + ((uint32_t)(q * 32) << 16) ;
     // shared memory by 32-bit addresses: the accumulators' barriers here and in the even CTA, this lane's scales
     const uint32_t full_at = smem_u32(tmem_full), release = mapa_shared(smem_u32(tmem_empty), 0);
     const uint32_t scales_at = smem_u32(scales);
@@ -423,17 +410,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) f8_pair
           break;
         }
         uint32_t a_at = scales_at + slot * kScaleBytes, b_at = a_at + 128 * kAhead * 4;
-        const uint32_t units = shared_u32(b_at + kTile * kAhead * 4);
+        const uint32_t parts = shared_u32(b_at + kTile * kAhead * 4);
         a_at += (q * 32 + lane) * kAhead * 4;
-        b_at += BY_COLUMN ? (half * (units * 64) + second * 64) * 4 : half * kAhead * 4;
+        b_at += BY_COLUMN ? (half * (parts * 64) + second * 64) * 4 : half * kAhead * 4;
+        const uint32_t at = from + (parts == 2 ? half * 128 + second * 64 : half * 64);
         const int blocks = min(kAhead, p.k_blocks - kb0);
 #pragma unroll 1
-        for (int i = 0; i < blocks; ++i, it += units, a_at += 4, b_at += BY_COLUMN ? kTile * 4 : 4) {
-          if (second >= (int)units) continue;
+        for (int i = 0; i < blocks; ++i, ++it, a_at += 4, b_at += BY_COLUMN ? kTile * 4 : 4) {
           float scale = shared_f32(a_at);
           if constexpr (!BY_COLUMN) scale *= shared_f32(b_at);
-          const uint32_t n = it + second, acc = n & (kAccs - 1);
-          if (!wait_warp_at(full_at + acc * 8, (n / kAccs) & 1, wc)) {
+          const uint32_t acc = it & (kAccs - 1);
+          if (!wait_warp_at(full_at + acc * 8, (it / kAccs) & 1, wc)) {
             ok = false;
             break;
           }
@@ -441,7 +428,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) f8_pair
 #pragma unroll
           for (int c = 0; c < 64 / kLoad; ++c) {
             uint32_t w[kLoad];
-            tmem_ld_32x32b_x16<0>(from + acc * kAccCols + c * kLoad, w);
+            tmem_ld_32x32b_x16<0>(at + acc * kAccCols + c * kLoad, w);
             tmem_ld_wait_for(w);
             if (c + 1 == 64 / kLoad) {
               tc_fence_before();
@@ -461,25 +448,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) f8_pair
             }
           }
         }
-        __syncwarp();
-        if (lane == 0) arrive_at(full_at + (2 * kAccs + kScaleSlots + slot) * 8);
+        if (kb0 + kAhead < p.k_blocks) {
+          __syncwarp();
+          if (lane == 0) arrive_at(full_at + (2 * kAccs + kScaleSlots + slot) * 8);
+        }
       }
       if (!ok) break;
-      // found again rather than kept: the sums leave no registers for it
-      int t_again = t;
-      asm volatile("" : "+r"(t_again));
-      const Part me = part_of(p, tb, walk, t_again, rank, q, half, second);
-      const int cols = me.cols;
+      // where the tile lies, from its last chunk
+      const uint32_t slot = (chunk - 1) % kScaleSlots;
+      const TileInfo x = *reinterpret_cast<const TileInfo*>(scales + slot * kScaleBytes + 128 * kAhead * 4 + kTile * kAhead * 4);
+      __syncwarp();
+      if (lane == 0) arrive_at(full_at + (2 * kAccs + kScaleSlots + slot) * 8);
+      const int r0 = x.row0 + q * 32, rows = max(0, min(32, x.row_end - r0));
+      const int col0 = x.col0 + (x.parts == 2 ? half * 128 + second * 64 : half * 64);
+      const int cols = x.parts == 1 && second != 0 ? 0 : min(64, p.N - col0);
       uint8_t* sb = staging + ew * 4096;
       float4 bias = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (p.bias != nullptr) bias = four_columns(p.bias + (int64_t)me.g * p.stride_bias + me.col0, lane, cols);
-      T* d = static_cast<T*>(p.D) + me.row * p.ldd + me.col0;
-      const T* c0 = static_cast<const T*>(p.C) + me.row * p.ldc + me.col0;
+      if (p.bias != nullptr) bias = four_columns(p.bias + (int64_t)x.g * p.stride_bias + col0, lane, cols);
+      T* d = static_cast<T*>(p.D) + (int64_t)r0 * p.ldd + col0;
+      const T* c0 = static_cast<const T*>(p.C) + (int64_t)r0 * p.ldc + col0;
 #pragma unroll
       for (int u = 0; u < 64 / kUnit; ++u) {
-        if (cols <= u * kUnit || me.rows <= 0) continue;
+        if (cols <= u * kUnit || rows <= 0) continue;
         if (p.C != nullptr) {
-          stage_c(p, c0 + u * kUnit, me.rows, cols - u * kUnit, lane, sb);
+          stage_c(p, c0 + u * kUnit, rows, cols - u * kUnit, lane, sb);
           __syncwarp();
         }
 #pragma unroll
@@ -525,7 +517,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) f8_pair
                                 pack2<OUT == kF8ResultBF16>(v[4], v[5]), pack2<OUT == kF8ResultBF16>(v[6], v[7]));
         }
         __syncwarp();
-        copy_out<T, 4>(p, sb, d + u * kUnit, me.rows, cols - u * kUnit, lane);
+        copy_out<T, 4>(p, sb, d + u * kUnit, rows, cols - u * kUnit, lane);
         __syncwarp();
       }
     }
