@@ -12,7 +12,13 @@
 // values (16 bytes a lane), a warp one of 32-bit values, several on their way at once.
 // Square blocks and transposed rows take a tile of 128 x 128 to a CTA, held in registers
 // between the maxima and the rounding; transposed bytes pass through shared memory so
-// that rows of 128 bytes leave.  Bound by HBM.
+// that rows of 128 bytes leave.  A block's quotients are one lane's work, handed round: done
+// by every lane they were a third of the instructions.
+//
+// Bound by HBM for rows: 8192 x 14336 bf16 56 us, 6.3 TB/s, fp32 90, 6.6; 16 x 4096 bf16 2.5.  Tiles wait
+// for their maxima between loads and stores, with four of them on an SM (fp32: two): square
+// blocks 56 us, fp32 139; transposed rows 66, fp32 114; transposed square blocks 59, fp32 126.
+// Rows off 16-byte boundaries, an element a load: 8192 x 14335 111 us, transposed 132.
 #include <cuda_fp8.h>
 
 #include "f8_blocks.cuh"
