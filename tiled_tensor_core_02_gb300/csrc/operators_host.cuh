@@ -100,6 +100,7 @@ inline int few_tile_cols(int64_t blocks, int64_t n, int sm_count, bool cols_cont
 // four blocks 16.0 us, for six 11.1).
 inline int64_t few_blocks(int64_t rows, int tokens, int64_t matrices) {
   const int64_t whole = blocks_of(blocks_of(rows, matrices), tokens) * matrices;
+  if (matrices == 1) return whole;  // no groups to differ
   const int64_t half_more = blocks_of(2 * rows + tokens * matrices, 2 * tokens);
   return whole > half_more ? whole : half_more;
 }
