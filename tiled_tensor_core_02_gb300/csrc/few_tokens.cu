@@ -19,10 +19,13 @@
 // only those in the group are loaded, in boxes of at most 32: the others would
 // come from L2 as often as there are tiles.
 //
-// Gated blocks (see gated_common.cuh) run here too: forward a stage has the same columns, 64 at
-// most, of both projections' weights, an MMA for each, and an accumulator a place for either;
-// in the gradient a thread reads its column's kept projections while the products come.
-// One token, 14336 x 4096, gated: 38.7 us, 6.1 TB/s; 24 rows of 16 groups, 1024 x 1024, 12.7.
+// Gated blocks (see gated_common.cuh) run here too.  Forward a stage has the same columns, 64 at
+// most, of both projections' weights one behind the other, so that one MMA of 128 rows takes
+// both: an MMA costs the same whatever it uses of its rows (one for each projection took 38.9 us
+// below, 12.7 and, for 64 rows of 4096 x 4096, 24.8 where this takes 22.2).  The two values of
+// an output then lie in different lanes and meet in shared memory.  In the gradient a thread
+// reads its column's kept projections while the products come.
+// One token, 14336 x 4096, gated: 36.9 us, 6.4 TB/s; 24 rows of 16 groups, 1024 x 1024, 11.1.
 //
 // Bound by HBM: 16 rows of 8 groups, 14336 x 4096 bf16 (6 groups with rows, 705
 // MB): 105 us, 6.7 TB/s; the CTA-pair kernel takes 128.
@@ -62,6 +65,8 @@ __device__ __forceinline__ GroupedTile few_tile(const GroupedParams& p, const Gr
   return x;
 }
 
+__device__ __forceinline__ void barrier_of_epilogue() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
 // 16 tokens of an output column of a gated block's gradient: what the products are
 // multiplied with comes while they are on their way.
 struct KeptTokens {
@@ -83,15 +88,76 @@ __device__ __forceinline__ uint16_t round_half(float v) {
   return (uint16_t)(pack2<BF16>(v, 0.0f) & 0xFFFFu);
 }
 
+// The epilogue of gated tiles: the lanes of tensor memory have the gate's columns, then the
+// other's.  16 tokens at a time pass through shared memory; 64 threads take eight of them.
+// After an error the walk goes on without waits: its barriers take all four warps.
+template <int BT, bool BF16>
+__device__ __forceinline__ void gated_columns(const GatedParams& p, const GroupTable& tb, int blocks, int tiles, uint32_t tmem_mine,
+                                              float* xch, uint64_t* tmem_full, uint64_t* tmem_empty, const WaitCtx& wc) {
+  const int tid = threadIdx.x - 128, lane = threadIdx.x & 31;
+  const int col = tid & 63, j0 = (tid >> 6) * 8;
+  bool ok = true;
+  int it = 0;
+  for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++it) {
+    const GroupedTile x = few_tile<BT>(p, tb, blocks, t);
+    const int f = x.cb * p.tile_cols + col;
+    const bool f_ok = col < p.tile_cols && f < p.N;
+    const int row0 = x.lo + x.rb * BT, tokens = min(BT, x.hi - row0);
+    const int acc = it & 1;
+    if (ok) ok = mbar_wait_warp(&tmem_full[acc], (it >> 1) & 1, wc);
+    tc_fence_after();
+#pragma unroll 1
+    for (int c = 0; c < BT; c += 16) {
+      uint32_t w[16];
+      tmem_ld_32x32b_x16<0>(tmem_mine + acc * BT + c, w);
+      tmem_ld_wait_for(w);
+      if (c + 16 == BT) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tmem_empty[acc]);
+      }
+      if (c > 0 || it > 0) barrier_of_epilogue();  // the values before have been read
+#pragma unroll
+      for (int j = 0; j < 16; ++j) xch[j * 128 + tid] = __uint_as_float(w[j]);
+      barrier_of_epilogue();
+      const int n = tokens - c - j0;
+      if (!ok || !f_ok || n <= 0) continue;
+      float g[8], u[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        g[j] = xch[(j0 + j) * 128 + col];
+        u[j] = xch[(j0 + j) * 128 + p.tile_cols + col];
+      }
+      const int64_t row = row0 + c + j0;
+      uint16_t* d = static_cast<uint16_t*>(p.D) + row * p.ldd + f;
+      with_act(p.act, [&](auto act) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j < n) d[j * p.ldd] = round_half<BF16>(gated_act<decltype(act)::value>(g[j]) * u[j]);
+      });
+      if (p.gate != nullptr) {
+        uint16_t* kg = static_cast<uint16_t*>(p.gate) + row * p.ldp + f;
+        uint16_t* ku = static_cast<uint16_t*>(p.up) + row * p.ldp + f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j < n) {
+            kg[j * p.ldp] = round_half<BF16>(g[j]);
+            ku[j * p.ldp] = round_half<BF16>(u[j]);
+          }
+      }
+    }
+  }
+}
+
 // P: GroupedParams, or those of a gated block; forward, a tile has the same columns of both
-// projections' weights in each stage and an accumulator for each.
+// projections' weights in each stage, the gate's first: one MMA takes both, and the epilogue's
+// threads exchange their values at the tile's end.
 template <int BT, bool BF16, typename P>
 __global__ void __launch_bounds__(kThreads, 1) few_tokens_kernel(const __grid_constant__ P p) {
   constexpr int kTokenBytes = stage_bytes_of(BT);
   constexpr int kBox = few_tokens_box(BT);
   constexpr int kMats = kIsGatedForward<P> ? 2 : 1;  // weight matrices
-  constexpr int kAcc = kMats * BT;                   // columns of an accumulator
-  constexpr int kTmemCols = 2 * kAcc;  // two accumulators: 32 to 256 columns
+  constexpr int kTmemCols = 2 * BT;  // two accumulators: 32 to 128 columns
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int w_bytes = stage_bytes_of(p.tile_cols);
@@ -147,7 +213,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_tokens_kernel(const __grid_co
   const int blocks = table_tiles(p, tb);  // of tokens, of all groups
   const int tiles = blocks * p.col_blocks;
   const int k_stages = (p.K + kStageK - 1) / kStageK;
-  const int w_blk = p.tile_cols * kBK * 2;  // weights with K contiguous: from one k-block of a stage to the next
+  const int w_rows = p.tile_cols * kBK * 2;  // weights with K contiguous: a matrix's rows of a k-block,
+  const int w_blk = kMats * w_rows;           // and from one k-block of a stage to the next
 
   if (warp == 0) {
     // ---------------------------------------------------------------- producer
@@ -184,9 +251,12 @@ __global__ void __launch_bounds__(kThreads, 1) few_tokens_kernel(const __grid_co
             if (two) tma_load_3d(w + w_blk, &p.tmB, k0 + kBK, f0, z, &full[stage], pol_w);
           }
           if constexpr (kMats == 2) {  // 64 columns at most: one box where they are contiguous
-            const int c0 = p.b_mn ? f0 : k0, c1 = p.b_mn ? k0 : f0;
-            tma_load_3d(w + w_bytes, &p.tmU, c0, c1, z, &full[stage], pol_w);
-            if (two && !p.b_mn) tma_load_3d(w + w_bytes + w_blk, &p.tmU, k0 + kBK, f0, z, &full[stage], pol_w);
+            if (p.b_mn) {
+              tma_load_3d(w + w_bytes, &p.tmU, f0, k0, z, &full[stage], pol_w);
+            } else {
+              tma_load_3d(w + w_rows, &p.tmU, k0, f0, z, &full[stage], pol_w);
+              if (two) tma_load_3d(w + w_blk + w_rows, &p.tmU, k0 + kBK, f0, z, &full[stage], pol_w);
+            }
           }
           for (int b = 0; b < boxes; ++b) {
             uint8_t* at = a + b * (kBox * kBK * 2);
@@ -220,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_tokens_kernel(const __grid_co
       const int acc = it & 1;
       if (!mbar_wait_warp(&tmem_empty[acc], ((it >> 1) & 1) ^ 1u, wc)) break;
       tc_fence_after();
-      const uint32_t d = tmem_base + acc * kAcc;
+      const uint32_t d = tmem_base + acc * BT;
       for (int ks = 0; ks < k_stages; ++ks) {
         if (!mbar_wait_warp(&full[stage], phase, wc)) {
           ok = false;
@@ -230,24 +300,19 @@ __global__ void __launch_bounds__(kThreads, 1) few_tokens_kernel(const __grid_co
         const uint64_t wd = w0 + (uint32_t)(stage * stage_bytes >> 4);
         const uint64_t ad = a0 + (uint32_t)(stage * stage_bytes >> 4);
         const uint32_t add = ks != 0;
+        if (ks < whole) {  // no condition between the MMAs: each would cost as much as one
+          const uint32_t w_lo = (uint32_t)wd, w_hi = (uint32_t)(wd >> 32), a_lo = (uint32_t)ad, a_hi = (uint32_t)(ad >> 32);
+          mma_f16_lead_lo(lead, d, w_lo, w_hi, a_lo, a_hi, idesc, add);
 #pragma unroll
-        for (int m = 0; m < kMats; ++m) {
-          const uint64_t wm = wd + (uint32_t)(m * w_bytes >> 4);
-          const uint32_t dm = d + m * BT;
-          if (ks < whole) {  // no condition between the MMAs: each would cost as much as one
-            const uint32_t w_lo = (uint32_t)wm, w_hi = (uint32_t)(wm >> 32), a_lo = (uint32_t)ad, a_hi = (uint32_t)(ad >> 32);
-            mma_f16_lead_lo(lead, dm, w_lo, w_hi, a_lo, a_hi, idesc, add);
-#pragma unroll
-            for (int k = 1; k < kStageK / kUmmaK; ++k)
-              mma_f16_lead_lo(lead, dm, w_lo + (k >> 2) * w_kb + (k & 3) * w_step, w_hi, a_lo + (k >> 2) * kTokenKb + (k & 3) * 2u,
-                              a_hi, idesc, 1u);
-          } else {
-            const int steps = (p.K - ks * kStageK + kUmmaK - 1) / kUmmaK;
+          for (int k = 1; k < kStageK / kUmmaK; ++k)
+            mma_f16_lead_lo(lead, d, w_lo + (k >> 2) * w_kb + (k & 3) * w_step, w_hi, a_lo + (k >> 2) * kTokenKb + (k & 3) * 2u,
+                            a_hi, idesc, 1u);
+        } else {
+          const int steps = (p.K - ks * kStageK + kUmmaK - 1) / kUmmaK;
 #pragma unroll 1
-            for (int k = 0; k < steps; ++k)
-              mma_f16_lead(lead, dm, wm + (k >> 2) * w_kb + (k & 3) * w_step, ad + (k >> 2) * kTokenKb + (k & 3) * 2u, idesc,
-                           add | (k != 0 ? 1u : 0u));
-          }
+          for (int k = 0; k < steps; ++k)
+            mma_f16_lead(lead, d, wd + (k >> 2) * w_kb + (k & 3) * w_step, ad + (k >> 2) * kTokenKb + (k & 3) * 2u, idesc,
+                         add | (k != 0 ? 1u : 0u));
         }
         any = true;
         mma_commit_lead(lead, &empty[stage]);
@@ -268,8 +333,13 @@ __global__ void __launch_bounds__(kThreads, 1) few_tokens_kernel(const __grid_co
     const int q = warp & 3;
     const int col = q * 32 + lane;  // of the tile
     const uint32_t tmem_mine = tmem_base + ((uint32_t)(q * 32) << 16);
+    if constexpr (kIsGatedForward<P>) {
+      // [token][gate's columns, the other's], behind the ring, where the MMAs read rows that nothing uses
+      gated_columns<BT, BF16>(p, tb, blocks, tiles, tmem_mine, reinterpret_cast<float*>(ring + S * stage_bytes), tmem_full,
+                              tmem_empty, wc);
+    }
     int it = 0;
-    for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++it) {
+    for (int t = kIsGatedForward<P> ? tiles : blockIdx.x; t < tiles; t += gridDim.x, ++it) {
       const GroupedTile x = few_tile<BT>(p, tb, blocks, t);
       const int f = x.cb * p.tile_cols + col;
       const bool f_ok = col < p.tile_cols && f < p.N;
@@ -283,9 +353,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_tokens_kernel(const __grid_co
       tc_fence_after();
 #pragma unroll 1
       for (int c = 0; c < BT; c += 16) {
-        uint32_t w[16], w2[16];
-        tmem_ld_32x32b_x16<0>(tmem_mine + acc * kAcc + c, w);
-        if constexpr (kMats == 2) tmem_ld_32x32b_x16<0>(tmem_mine + acc * kAcc + BT + c, w2);
+        uint32_t w[16];
+        tmem_ld_32x32b_x16<0>(tmem_mine + acc * BT + c, w);
         tmem_ld_wait();
         if (c + 16 == BT) {
           tc_fence_before();
@@ -296,25 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_tokens_kernel(const __grid_co
           if (c > 0) load_kept(p, row0 + c, f, tokens - c, f_ok, kept);
         }
         if (!f_ok) continue;
-        if constexpr (kIsGatedForward<P>) {
-          with_act(p.act, [&](auto act) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-              if (c + j < tokens)
-                d[(int64_t)(c + j) * p.ldd] =
-                    round_half<BF16>(gated_act<decltype(act)::value>(__uint_as_float(w[j])) * __uint_as_float(w2[j]));
-          });
-          if (p.gate != nullptr) {
-            uint16_t* g = static_cast<uint16_t*>(p.gate) + (int64_t)(row0 + c) * p.ldp + f;
-            uint16_t* u = static_cast<uint16_t*>(p.up) + (int64_t)(row0 + c) * p.ldp + f;
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-              if (c + j < tokens) {
-                g[j * p.ldp] = round_half<BF16>(__uint_as_float(w[j]));
-                u[j * p.ldp] = round_half<BF16>(__uint_as_float(w2[j]));
-              }
-          }
-        } else if constexpr (kIsGatedGrad<P>) {
+        if constexpr (kIsGatedGrad<P>) {
           uint16_t* dg = static_cast<uint16_t*>(p.dgate) + (int64_t)(row0 + c) * p.lddp + f;
           uint16_t* du = static_cast<uint16_t*>(p.dup) + (int64_t)(row0 + c) * p.lddp + f;
           with_act(p.act, [&](auto act) {
