@@ -41,9 +41,9 @@
 // products of 128 columns side by side: the even CTA stages the gate's weights, the odd one the
 // other projection's, which the pair's MMA reads as 256 columns.  In the gradient the
 // epilogue reads the kept projections of its columns before it waits for the products.
-// 8192 x 14336 x 4096 bf16: forward 1032 to 1130 us with both projections kept (1.70 to 1.87
+// 8192 x 14336 x 4096 bf16: forward 1032 to 1130 us with both projections kept (1.70 to 1.86
 // PFLOP/s, by the power cap), gradient 634 to 670 (20 us a tile for its products, 16 for its
-// epilogue, which reads and writes 1.2 GB in all; K = 512 388 us, 4 TB/s of DRAM).
+// epilogue, which reads and writes 1.2 GB in all; K = 512 388 us, 3.1 TB/s).
 //
 // Where two halves of each of the last wave's tiles find a pair, the wave takes them
 // as halves of 128 columns: half the MMA's time and half the epilogue (1120 rows of 7
