@@ -40,10 +40,10 @@ def test_waits_before_global_access(kernel):
 def test_producers_wait_for_their_loads(name):
     text = source(name)
     assert set(re.findall(r"mbar_arrive_expect_tx\((\w+) \+ \w+,", text)) == {"full"}
-    calls = list(re.finditer(r"\bdrain_ring\(\s*full\s*,", text))
+    calls = list(re.finditer(r"\bdrain_ring(?:_lanes)?\(\s*full\s*,", text))
     assert len(calls) == 1
     heads = enclosing(text, calls[0].start())
-    assert re.search(r"\(lane == 0\)", heads[0]), heads[0]  # the producer's block: no loop, no error path
+    assert re.search(r"\(lane == 0\)|^if \(warp == 0\)$", heads[0]), heads[0]  # the producer's block: no loop, no error path
     before = text[:calls[0].start()].rstrip()
     assert not before.endswith(")") or before.endswith("if (leader)")
     assert not re.search(r"if \(!ok[^{;]*\{?\s*(for[^{;]*;[^{;]*;[^{)]*\)\s*)?(if[^;{]*)?drain_", text)

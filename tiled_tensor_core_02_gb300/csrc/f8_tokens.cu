@@ -11,7 +11,7 @@
 // 58.4; a second set of epilogue warps for every other one changed nothing.)
 //
 // Bound by HBM up to 32 tokens and a few microseconds of start: 1 x 14336 x 4096 12.2 us, 16 x
-// 8192 x 8192 18.1.  With 64 tokens a tile by shared memory, which gives the MMAs 24 KB a block
+// 8192 x 8192 15.7, 1 x 4096 x 4096 8.7 (10.1 with one thread that loads).  With 64 tokens a tile by shared memory, which gives the MMAs 24 KB a block
 // of K, takes as much from TMA and hands 64 tokens' scales to every warp: 0.33 us a block,
 // 64 x 8192 x 8192 23.7 us; without the last of these 20.1.
 #include <atomic>
@@ -140,44 +140,43 @@ __global__ void __launch_bounds__(kThreads<BT>, 1) f8_tokens_kernel(const __grid
 
   if (warp == 0) {
     // ---------------------------------------------------------------- producer
-    if (lane == 0) {
-      const uint64_t keep = policy_evict_last();
-      const uint64_t pol_w = p.b_stream ? policy_evict_first() : keep;
-      int stage = 0;
-      uint32_t phase = 0, armed = 0, armed_parity = 0;
-      bool ok = true;
-      for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-        const GroupedTile x = few_tile<BT>(p, tb, blocks, t);
-        const int f0 = x.cb * p.tile_cols, t0 = x.lo + x.rb * BT;
-        const int z = p.strideB != 0 ? x.g : 0;
-        const int boxes = (min(BT, x.hi - t0) + kBox - 1) / kBox;  // of tokens
-        for (int ks = 0; ks < k_stages; ++ks) {
-          const int k0 = ks * kStageK;
-          const bool two = p.k_blocks - ks * kKPS > 1;  // both blocks of the stage
-          if (!mbar_wait(&empty[stage], phase ^ 1u, wc)) {
-            ok = false;
-            break;
-          }
-          uint8_t* w = ring + stage * stage_bytes;
-          uint8_t* a = w + w_bytes;
-          mbar_arrive_expect_tx(full + stage, (two ? 2 : 1) * (w_blk + boxes * (kBox * kF8Block)));
-          armed |= 1u << stage;
-          armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
-          tma_load_3d(w, &p.tmB, k0, f0, z, &full[stage], pol_w);
-          if (two) tma_load_3d(w + w_blk, &p.tmB, k0 + kF8Block, f0, z, &full[stage], pol_w);
-          for (int b = 0; b < boxes; ++b) {
-            uint8_t* at = a + b * (kBox * kF8Block);
-            tma_load_3d(at, &p.tmA, k0, t0 + b * kBox, 0, &full[stage], keep);
-            if (two) tma_load_3d(at + kTokenBytes / 2, &p.tmA, k0 + kF8Block, t0 + b * kBox, 0, &full[stage], keep);
-          }
-          if (++stage == S) {
-            stage = 0;
-            phase ^= 1u;
-          }
+    const uint32_t lead = elect_lead();  // a converged warp, one lane of which loads
+    const uint64_t keep = policy_evict_last();
+    const uint64_t pol_w = p.b_stream ? policy_evict_first() : keep;
+    int stage = 0;
+    uint32_t phase = 0, armed = 0, armed_parity = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+      const GroupedTile x = few_tile<BT>(p, tb, blocks, t);
+      const int f0 = x.cb * p.tile_cols, t0 = x.lo + x.rb * BT;
+      const int z = p.strideB != 0 ? x.g : 0;
+      const int boxes = (min(BT, x.hi - t0) + kBox - 1) / kBox;  // of tokens
+      for (int ks = 0; ks < k_stages; ++ks) {
+        const int k0 = ks * kStageK;
+        const bool two = p.k_blocks - ks * kKPS > 1;  // both blocks of the stage
+        if (!mbar_wait_warp(&empty[stage], phase ^ 1u, wc)) {
+          ok = false;
+          break;
+        }
+        uint8_t* w = ring + stage * stage_bytes;
+        uint8_t* a = w + w_bytes;
+        if (lead) mbar_arrive_expect_tx(full + stage, (two ? 2 : 1) * (w_blk + boxes * (kBox * kF8Block)));
+        armed |= 1u << stage;
+        armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+        tma_load_3d_lead(lead, w, &p.tmB, k0, f0, z, &full[stage], pol_w);
+        if (two) tma_load_3d_lead(lead, w + w_blk, &p.tmB, k0 + kF8Block, f0, z, &full[stage], pol_w);
+        for (int b = 0; b < boxes; ++b) {
+          uint8_t* at = a + b * (kBox * kF8Block);
+          tma_load_3d_lead(lead, at, &p.tmA, k0, t0 + b * kBox, 0, &full[stage], keep);
+          if (two) tma_load_3d_lead(lead, at + kTokenBytes / 2, &p.tmA, k0 + kF8Block, t0 + b * kBox, 0, &full[stage], keep);
+        }
+        if (++stage == S) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
-      drain_ring(full, S, armed, armed_parity);
     }
+    drain_ring_lanes(full, armed, armed_parity);
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer
     const uint32_t lead = elect_lead();

@@ -12,7 +12,8 @@
 // rows are whatever lies behind them in shared memory, and are not stored.  No
 // split of K and no partial sums between CTAs.
 //
-// One thread loads with TMA: a stage is 128 of K, as deep a ring of stages as
+// A converged warp loads with TMA (one thread on its own needs 150 clocks a load, four to six a
+// stage, as long as the stream: 1 x 4096 x 4096 14.3 us against 12.3): a stage is 128 of K, as deep a ring of stages as
 // fits shared memory (what hides HBM's latency is the bytes on the way: 100 to
 // 200 KB an SM); one warp issues tcgen05.mma into two accumulators; four warps
 // drain them, a thread an output column, a register a token.  Of a block's tokens
@@ -22,10 +23,11 @@
 // Gated blocks (see gated_common.cuh) run here too.  Forward a stage has the same columns, 64 at
 // most, of both projections' weights one behind the other, so that one MMA of 128 rows takes
 // both: an MMA costs the same whatever it uses of its rows (one for each projection took 38.9 us
-// below, 12.7 and, for 64 rows of 4096 x 4096, 24.8 where this takes 22.2).  The two values of
+// where this took 36.9, 24.8 for 22.2 with 64 rows, 4096 x 4096).  The two values of
 // an output then lie in different lanes and meet in shared memory.  In the gradient a thread
 // reads its column's kept projections while the products come.
-// One token, 14336 x 4096, gated: 36.9 us, 6.4 TB/s; 24 rows of 16 groups, 1024 x 1024, 11.1.
+// One token, gated, 14336 x 4096: 37 us, 6.4 TB/s; 4096 x 4096 15.0; 64 tokens 18.2; 24 rows of 16
+// groups, 1024 x 1024, 10.3.
 //
 // Bound by HBM: 16 rows of 8 groups, 14336 x 4096 bf16 (6 groups with rows, 705
 // MB): 105 us, 6.7 TB/s; the CTA-pair kernel takes 128.
@@ -218,59 +220,58 @@ __global__ void __launch_bounds__(kThreads, 1) few_tokens_kernel(const __grid_co
 
   if (warp == 0) {
     // ---------------------------------------------------------------- producer
-    if (lane == 0) {
-      const uint64_t keep = policy_evict_last();
-      const uint64_t pol_w = p.b_stream ? policy_evict_first() : keep;
-      int stage = 0;
-      uint32_t phase = 0, armed = 0, armed_parity = 0;
-      bool ok = true;
-      for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-        const GroupedTile x = few_tile<BT>(p, tb, blocks, t);
-        const int f0 = x.cb * p.tile_cols, t0 = x.lo + x.rb * BT;
-        const int z = p.strideB != 0 ? x.g : 0;
-        const int boxes = (min(BT, x.hi - t0) + kBox - 1) / kBox;  // of tokens
-        for (int ks = 0; ks < k_stages; ++ks) {
-          const int k0 = ks * kStageK;
-          const bool two = p.K - k0 > kBK;  // both k-blocks of the stage
-          if (!mbar_wait(&empty[stage], phase ^ 1u, wc)) {
-            ok = false;
-            break;
-          }
-          uint8_t* w = ring + stage * stage_bytes;
-          uint8_t* a = w + kMats * w_bytes;
-          // weights with their rows contiguous come in boxes of 128 of K whatever K is
-          mbar_arrive_expect_tx(&full[stage],
-                                kMats * (two || p.b_mn ? w_bytes : w_bytes / 2) + (two ? 2 : 1) * boxes * (kBox * kBK * 2));
-          armed |= 1u << stage;
-          armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+    const uint32_t lead = elect_lead();  // a converged warp, one lane of which loads
+    const uint64_t keep = policy_evict_last();
+    const uint64_t pol_w = p.b_stream ? policy_evict_first() : keep;
+    int stage = 0;
+    uint32_t phase = 0, armed = 0, armed_parity = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+      const GroupedTile x = few_tile<BT>(p, tb, blocks, t);
+      const int f0 = x.cb * p.tile_cols, t0 = x.lo + x.rb * BT;
+      const int z = p.strideB != 0 ? x.g : 0;
+      const int boxes = (min(BT, x.hi - t0) + kBox - 1) / kBox;  // of tokens
+      for (int ks = 0; ks < k_stages; ++ks) {
+        const int k0 = ks * kStageK;
+        const bool two = p.K - k0 > kBK;  // both k-blocks of the stage
+        if (!mbar_wait_warp(&empty[stage], phase ^ 1u, wc)) {
+          ok = false;
+          break;
+        }
+        uint8_t* w = ring + stage * stage_bytes;
+        uint8_t* a = w + kMats * w_bytes;
+        // weights with their rows contiguous come in boxes of 128 of K whatever K is
+        const int w_tx = kMats * (two || p.b_mn ? w_bytes : w_bytes / 2);
+        if (lead) mbar_arrive_expect_tx(&full[stage], w_tx + (two ? 2 : 1) * boxes * (kBox * kBK * 2));
+        armed |= 1u << stage;
+        armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+        if (p.b_mn) {
+          tma_load_3d_lead(lead, w, &p.tmB, f0, k0, z, &full[stage], pol_w);
+          if (p.tile_cols > 64) tma_load_3d_lead(lead, w + 64 * kStageK * 2, &p.tmB, f0 + 64, k0, z, &full[stage], pol_w);
+        } else {
+          tma_load_3d_lead(lead, w, &p.tmB, k0, f0, z, &full[stage], pol_w);
+          if (two) tma_load_3d_lead(lead, w + w_blk, &p.tmB, k0 + kBK, f0, z, &full[stage], pol_w);
+        }
+        if constexpr (kMats == 2) {  // 64 columns at most: one box where they are contiguous
           if (p.b_mn) {
-            tma_load_3d(w, &p.tmB, f0, k0, z, &full[stage], pol_w);
-            if (p.tile_cols > 64) tma_load_3d(w + 64 * kStageK * 2, &p.tmB, f0 + 64, k0, z, &full[stage], pol_w);
+            tma_load_3d_lead(lead, w + w_bytes, &p.tmU, f0, k0, z, &full[stage], pol_w);
           } else {
-            tma_load_3d(w, &p.tmB, k0, f0, z, &full[stage], pol_w);
-            if (two) tma_load_3d(w + w_blk, &p.tmB, k0 + kBK, f0, z, &full[stage], pol_w);
-          }
-          if constexpr (kMats == 2) {  // 64 columns at most: one box where they are contiguous
-            if (p.b_mn) {
-              tma_load_3d(w + w_bytes, &p.tmU, f0, k0, z, &full[stage], pol_w);
-            } else {
-              tma_load_3d(w + w_rows, &p.tmU, k0, f0, z, &full[stage], pol_w);
-              if (two) tma_load_3d(w + w_blk + w_rows, &p.tmU, k0 + kBK, f0, z, &full[stage], pol_w);
-            }
-          }
-          for (int b = 0; b < boxes; ++b) {
-            uint8_t* at = a + b * (kBox * kBK * 2);
-            tma_load_3d(at, &p.tmA, k0, t0 + b * kBox, 0, &full[stage], keep);
-            if (two) tma_load_3d(at + kTokenBytes / 2, &p.tmA, k0 + kBK, t0 + b * kBox, 0, &full[stage], keep);
-          }
-          if (++stage == S) {
-            stage = 0;
-            phase ^= 1u;
+            tma_load_3d_lead(lead, w + w_rows, &p.tmU, k0, f0, z, &full[stage], pol_w);
+            if (two) tma_load_3d_lead(lead, w + w_blk + w_rows, &p.tmU, k0 + kBK, f0, z, &full[stage], pol_w);
           }
         }
+        for (int b = 0; b < boxes; ++b) {
+          uint8_t* at = a + b * (kBox * kBK * 2);
+          tma_load_3d_lead(lead, at, &p.tmA, k0, t0 + b * kBox, 0, &full[stage], keep);
+          if (two) tma_load_3d_lead(lead, at + kTokenBytes / 2, &p.tmA, k0 + kBK, t0 + b * kBox, 0, &full[stage], keep);
+        }
+        if (++stage == S) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
-      drain_ring(full, S, armed, armed_parity);
     }
+    drain_ring_lanes(full, armed, armed_parity);
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer
     const uint32_t lead = elect_lead();
