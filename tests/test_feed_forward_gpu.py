@@ -306,7 +306,7 @@ def test_plain_loads_of_aligned_operands(knob, M):
 
 
 # few tokens, CTA pairs, plain loads
-@pytest.mark.parametrize("M,plain", [(20, False), (1300, False), (1300, True)])
+@pytest.mark.parametrize("M,plain", [(20, False), (2600, False), (2600, True)])
 def test_stalled_gated_products_time_out(knob, M, plain):
     if plain:
         knob("force_generic_load", 1)

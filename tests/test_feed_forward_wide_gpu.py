@@ -70,8 +70,9 @@ def test_f8_pitches_and_alignment(pad, shift, gap, block):
 @pytest.mark.parametrize("offsets", [[20, 90, 900, 1350], [-5, 40, 5000], [50, 50, 50], [1300, 0], [-9, -3, 1400]])
 def test_offsets_that_leave_rows_out_or_the_matrix(offsets):
     Product(offsets, 1400, 1160, 200, seed=11).verify()
-    p = Gated(offsets, 1400, 648, 72, "bf16", "row", seed=12)
+    p = Gated(offsets, 1400, 1032, 72, "bf16", "row", seed=12)
     p.verify()
+    p.verify_grad()
 
 
 def test_f8_scales():
@@ -131,6 +132,40 @@ def test_gated_group_sizes(pattern, dtype, layout):
 @pytest.mark.parametrize("n,k", [(641, 64), (1000, 63), (776, 333), (1024, 8), (648, 1000), (704, 128), (1091, 65), (904, 1)])
 def test_gated_widths(n, k, layout):
     Gated(None, 1301, n, k, "bf16", layout, seed=n + k).verify(save=n % 2 == 0)
+
+
+@pytest.mark.parametrize("layout", ["col", "row"])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("pattern", sorted(PATTERNS))
+def test_gradient_group_sizes(pattern, dtype, layout):
+    o = ends(PATTERNS[pattern])
+    Gated(o, o[-1], 1096, 136, dtype, layout, seed=len(pattern)).verify_grad(save=len(pattern) % 2 == 0)
+
+
+@pytest.mark.parametrize("layout", ["col", "row"])
+@pytest.mark.parametrize("n,k", [(1025, 64), (1000, 63), (1160, 333), (1024, 8), (1032, 1000), (1091, 65), (1096, 1)])
+def test_gradient_widths(n, k, layout):
+    p = Gated(None, 1301, n, k, "bf16", layout, seed=n + k)
+    p.verify_grad(save=n % 2 == 0)
+    p.verify_grad(in_place=True)
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("save", [False, True])
+def test_gradient_activations(dtype, act, save):
+    for o, layout in (([0, 400, 400, 1340, 1347], "col"), (None, "row")):
+        p = Gated(o, 1347, 1040, 320, dtype, layout, seed=3, scale=3.0)
+        p.verify_grad(act, save)
+        p.verify_grad(act, save, in_place=True)
+
+
+@pytest.mark.parametrize("layout", ["col", "row"])
+@pytest.mark.parametrize("pad,shift,gap", [((8, 16, 24, 8), 0, 64), ((8, 8, 8, 8), 8, 8), ((8, 8, 1, 3), 0, 0), ((8, 8, 8, 4), 0, 0)])
+def test_gradient_pitches_and_alignment(pad, shift, gap, layout):
+    p = Gated([0, 500, 500, 1399, 1400], 1400, 1032, 264, "bf16", layout, seed=9, pad=pad, shift=shift, gap=gap)
+    p.verify_grad("gelu_tanh")
+    p.verify_grad("silu", in_place=True)
 
 
 @pytest.mark.parametrize("n", [1, 8, 40, 64, 100, 128, 136])

@@ -95,15 +95,14 @@ bool map_up(GatedForward& p, ttc_dtype dtype, int box_rows) {
 bool map_up(GatedGrad&, ttc_dtype, int) { return true; }
 
 // Block of tokens of the few-token kernel, 0 for CTA pairs: as ttc_gemm_grouped chooses it, and
-// forward with more rows too wherever blocks of 64 make one wave of tiles (128 x 4096 x 4096
-// 22.4 us against 23.7, with the weights' columns contiguous 20.4 against 24.1; 100 x 1000 x 1000
-// 10.1 against 11.4; 512 rows of 4 groups, 512 x 2048, 12.7 against 14.1; 192 x 1024 x 4096 the
-// other way, 21.9 against 21.4).  In the gradient that came out on either side (100 rows, 4096 x
-// 4096 23.4 against 24.6, 1024 x 1024 13.1 against 11.9).
-int gated_few_block(int64_t rows, int64_t n, int64_t groups, bool forward, int sm_count) {
+// with more rows too wherever blocks of 64 make one wave of tiles of `width` columns (100 x 4096 x
+// 4096 18.9 us against 23.7, the gradient 20.2 against 24.2, with the block's values 21.9; 100 x
+// 1000 x 1000 9.3 against 11.4, 13.0 against 13.8; 512 x 1024 x 1024, where it loses most, 8.8
+// against 9.9, 12.1 against 11.9 and 13.5 against 12.4).
+int gated_few_block(int64_t rows, int64_t n, int64_t groups, int width, int sm_count) {
   const int block = few_block(rows, groups);
-  if (block != 0 || !forward) return block;
-  return few_blocks(rows, 64, groups) * blocks_of(n, 64) <= sm_count ? 64 : 0;
+  if (block != 0) return block;
+  return few_blocks(rows, 64, groups) * blocks_of(n, width) <= sm_count ? 64 : 0;
 }
 
 // Launches the kernel for these operands.
@@ -112,7 +111,7 @@ ttc_status launch_gated(P& p, ttc_dtype dtype, const HostEnv& env, cudaStream_t 
   constexpr bool kForward = kIsGatedForward<P>;
   const bool bf16 = dtype == TTC_BF16;
   const int64_t groups = p.groups < p.M ? p.groups : p.M;  // that have rows, as far as the host knows
-  const int block = gated_few_block(p.M, p.N, groups, kForward, env.sm_count);
+  const int block = gated_few_block(p.M, p.N, groups, kForward ? 64 : 128, env.sm_count);
   if (block != 0 && few_maps(p, dtype, block, groups, env, kForward) && map_up(p, dtype, p.tile_cols)) {
     const int64_t tiles = (blocks_of(p.M, block) + groups) * p.col_blocks;
     if (launch_few_tokens(bf16, block, p, (int)(tiles < env.sm_count ? tiles : env.sm_count), stream) != cudaSuccess)
