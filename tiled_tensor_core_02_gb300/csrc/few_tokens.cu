@@ -12,8 +12,10 @@
 // rows are whatever lies behind them in shared memory, and are not stored.  No
 // split of K and no partial sums between CTAs.
 //
-// A converged warp loads with TMA (one thread on its own needs 150 clocks a load, four to six a
-// stage, as long as the stream: 1 x 4096 x 4096 14.3 us against 12.3): a stage is 128 of K, as deep a ring of stages as
+// A converged warp loads with TMA (one thread on its own needs 150 clocks a load, four a stage,
+// as long as the stream: 1 x 4096 x 4096 14.3 us against 12.3), of gated tiles, whose stages take
+// six, one the weights and one the tokens (13.7 against 15.0; otherwise the MMAs' issue is
+// as slow, and a second warp costs 2 %): a stage is 128 of K, as deep a ring of stages as
 // fits shared memory (what hides HBM's latency is the bytes on the way: 100 to
 // 200 KB an SM); one warp issues tcgen05.mma into two accumulators; four warps
 // drain them, a thread an output column, a register a token.  Of a block's tokens
@@ -26,8 +28,8 @@
 // where this took 36.9, 24.8 for 22.2 with 64 rows, 4096 x 4096).  The two values of
 // an output then lie in different lanes and meet in shared memory.  In the gradient a thread
 // reads its column's kept projections while the products come.
-// One token, gated, 14336 x 4096: 37 us, 6.4 TB/s; 4096 x 4096 15.0; 64 tokens 18.2; 24 rows of 16
-// groups, 1024 x 1024, 10.3.
+// One token, gated, 14336 x 4096: 37 us, 6.4 TB/s; 4096 x 4096 13.7; 64 tokens 16.4; 24 rows of 16
+// groups, 1024 x 1024, 9.8.
 //
 // Bound by HBM: 16 rows of 8 groups, 14336 x 4096 bf16 (6 groups with rows, 705
 // MB): 105 us, 6.7 TB/s; the CTA-pair kernel takes 128.
@@ -43,7 +45,7 @@ constexpr int kStageK = 128;
 constexpr int kMaxStages = 16;
 constexpr int kBarBytes = 512;
 constexpr int kSmemLimit = 227 * 1024;
-constexpr int kThreads = 256;  // producer, MMA issuer, two spare warps, four of the epilogue
+constexpr int kThreads = 256;  // producer, MMA issuer, gated tiles' tokens, a spare warp, four of the epilogue
 
 __host__ __device__ constexpr int stage_bytes_of(int rows) { return rows * kStageK * 2; }
 
@@ -185,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_tokens_kernel(const __grid_co
   const WaitCtx wc{p.err, p.timeout_ns};
   if (warp == 0) {
     if (lane < S) {
-      mbar_init(&full[lane], 1);
+      mbar_init(&full[lane], kMats);  // of gated tiles the weights' loader and the tokens'
       mbar_init(&empty[lane], 1);
     }
     if (lane < 2) {
@@ -218,6 +220,21 @@ __global__ void __launch_bounds__(kThreads, 1) few_tokens_kernel(const __grid_co
   const int w_rows = p.tile_cols * kBK * 2;  // weights with K contiguous: a matrix's rows of a k-block,
   const int w_blk = kMats * w_rows;           // and from one k-block of a stage to the next
 
+  // a stage's tokens: those of the group, in boxes
+  const auto load_tokens = [&](uint32_t lead, const GroupedTile& x, int stage, int k0, uint64_t policy) {
+    const int t0 = x.lo + x.rb * BT, boxes = (min(BT, x.hi - t0) + kBox - 1) / kBox;
+    uint8_t* a = ring + stage * stage_bytes + kMats * w_bytes;
+    for (int b = 0; b < boxes; ++b) {
+      uint8_t* at = a + b * (kBox * kBK * 2);
+      tma_load_3d_lead(lead, at, &p.tmA, k0, t0 + b * kBox, 0, &full[stage], policy);
+      if (p.K - k0 > kBK) tma_load_3d_lead(lead, at + kTokenBytes / 2, &p.tmA, k0 + kBK, t0 + b * kBox, 0, &full[stage], policy);
+    }
+  };
+  const auto token_tx = [&](const GroupedTile& x, int k0) {
+    const int boxes = (min(BT, x.hi - x.lo - x.rb * BT) + kBox - 1) / kBox;
+    return (p.K - k0 > kBK ? 2 : 1) * boxes * (kBox * kBK * 2);
+  };
+
   if (warp == 0) {
     // ---------------------------------------------------------------- producer
     const uint32_t lead = elect_lead();  // a converged warp, one lane of which loads
@@ -228,9 +245,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_tokens_kernel(const __grid_co
     bool ok = true;
     for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
       const GroupedTile x = few_tile<BT>(p, tb, blocks, t);
-      const int f0 = x.cb * p.tile_cols, t0 = x.lo + x.rb * BT;
+      const int f0 = x.cb * p.tile_cols;
       const int z = p.strideB != 0 ? x.g : 0;
-      const int boxes = (min(BT, x.hi - t0) + kBox - 1) / kBox;  // of tokens
       for (int ks = 0; ks < k_stages; ++ks) {
         const int k0 = ks * kStageK;
         const bool two = p.K - k0 > kBK;  // both k-blocks of the stage
@@ -239,10 +255,9 @@ __global__ void __launch_bounds__(kThreads, 1) few_tokens_kernel(const __grid_co
           break;
         }
         uint8_t* w = ring + stage * stage_bytes;
-        uint8_t* a = w + kMats * w_bytes;
         // weights with their rows contiguous come in boxes of 128 of K whatever K is
         const int w_tx = kMats * (two || p.b_mn ? w_bytes : w_bytes / 2);
-        if (lead) mbar_arrive_expect_tx(&full[stage], w_tx + (two ? 2 : 1) * boxes * (kBox * kBK * 2));
+        if (lead) mbar_arrive_expect_tx(&full[stage], w_tx + (kMats == 1 ? token_tx(x, k0) : 0));
         armed |= 1u << stage;
         armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
         if (p.b_mn) {
@@ -260,11 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_tokens_kernel(const __grid_co
             if (two) tma_load_3d_lead(lead, w + w_blk + w_rows, &p.tmU, k0 + kBK, f0, z, &full[stage], pol_w);
           }
         }
-        for (int b = 0; b < boxes; ++b) {
-          uint8_t* at = a + b * (kBox * kBK * 2);
-          tma_load_3d_lead(lead, at, &p.tmA, k0, t0 + b * kBox, 0, &full[stage], keep);
-          if (two) tma_load_3d_lead(lead, at + kTokenBytes / 2, &p.tmA, k0 + kBK, t0 + b * kBox, 0, &full[stage], keep);
-        }
+        if constexpr (kMats == 1) load_tokens(lead, x, stage, k0, keep);
         if (++stage == S) {
           stage = 0;
           phase ^= 1u;
@@ -329,6 +340,31 @@ __global__ void __launch_bounds__(kThreads, 1) few_tokens_kernel(const __grid_co
       mma_commit_lead(lead, drain_bar);
       drain_wait(drain_bar, 0, 100000000ull);
     }
+  } else if (kMats == 2 && warp == 2) {
+    // ---------------------------------------------------------------- tokens of gated tiles
+    const uint32_t lead = elect_lead();
+    const uint64_t keep = policy_evict_last();
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+      const GroupedTile x = few_tile<BT>(p, tb, blocks, t);
+      for (int ks = 0; ks < k_stages; ++ks) {
+        if (!mbar_wait_warp(&empty[stage], phase ^ 1u, wc)) {
+          ok = false;
+          break;
+        }
+        if (lead) mbar_arrive_expect_tx(&full[stage], token_tx(x, ks * kStageK));
+        load_tokens(lead, x, stage, ks * kStageK, keep);
+        if (++stage == S) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    // the producer waits for the stages that both have loaded; after an error this warp may be
+    // a few ahead, and pauses as the odd CTA of a pair does
+    drain_odd_cta(wc);
   } else if (warp >= 4) {
     // ---------------------------------------------------------------- epilogue
     const int q = warp & 3;
