@@ -6,7 +6,7 @@
 // add it, scaled, to the tile's sums in their registers (a thread has one row and 64 columns,
 // read 16 at a time) while the tensor cores fill the other.  What has to be short is the way
 // from an accumulator's last MMA to its being free again, two crossings between SMs and the
-// reads: 8192 x 14336 x 4096 takes 447 us, 401 without the results' way out, 255 by the MMAs
+// reads: 8192 x 14336 x 4096 takes 441 us, 401 without the results' way out, 255 by the MMAs
 // alone.  Eight warps of 128 columns, which read twice as long, took 751; four accumulators of
 // 128 columns 464, where an MMA of half the width costs more than half (313 us alone); loads of
 // 32 columns a fifth more, of 8 a twentieth.
@@ -16,11 +16,13 @@
 // they took registers that the sums need, and what is spilled goes to L2, nearly all of L1
 // being shared memory here.  For the same reason the four warps that load and issue hand
 // registers over.  The MMAs are issued by a converged warp: by one thread of it, which moves
-// descriptors to uniform registers each time, four of them took 0.38 us instead of 0.22.
+// descriptors to uniform registers each time, four of them took 0.38 us instead of 0.22.  One
+// commit after a block's MMAs says both that its accumulator is full and that its operands' place
+// is free (two, and loads by a single thread: 447 us).
 //
 // Bound by the epilogue: 0.52 us a block of K and tile, and at a tile's end 1.9 us, with GELU
 // 3.7 (its exponentials and quotients), during which the tensor cores get two blocks ahead.
-// 8192 x 14336 x 4096: 2.15 PFLOP/s, with GELU 1.97; by columns, fp32 sums added to,
+// 8192 x 14336 x 4096: 2.18 PFLOP/s, with GELU 2.01; by columns, fp32 sums added to,
 // 4096 x 4096 x 8192 203 us.
 #include <atomic>
 #include <type_traits>
@@ -166,9 +168,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) f8_pair
   uint8_t* scales = staging + kStagingBytes;
   uint64_t* bars = reinterpret_cast<uint64_t*>(scales + kScaleSlots * kScaleBytes);
   uint64_t* full = bars;
-  uint64_t* empty = bars + kStages;
-  uint64_t* tmem_full = bars + 2 * kStages;
-  uint64_t* tmem_empty = tmem_full + kAccs;
+  uint64_t* done = bars + kStages;  // a stage's MMAs: its accumulator is full and its place free
+  uint64_t* tmem_empty = done + kStages;
   uint64_t* scale_full = tmem_empty + kAccs;
   uint64_t* scale_empty = scale_full + kScaleSlots;
   uint64_t* stall_bar = scale_empty + kScaleSlots;
@@ -198,10 +199,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) f8_pair
   if (warp == 0) {
     if (lane < kStages) {
       mbar_init(&full[lane], 1);
-      mbar_init(&empty[lane], 1);
+      mbar_init(&done[lane], 1);
     }
     if (lane < kAccs) {
-      mbar_init(&tmem_full[lane], 1);
       mbar_init(&tmem_empty[lane], 2 * kEpiWarpCount);
     }
     if (lane < kScaleSlots) {
@@ -235,49 +235,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) f8_pair
     registers_down<kRegsFew>();
     if (warp == 0) {
       // ---------------------------------------------------------------- producer (both CTAs)
-      if (lane == 0) {
-        const PairWalk walk = find_walk();
-        const uint64_t keep = policy_evict_last();
-        const uint64_t pol_b = p.b_stream ? policy_evict_first() : keep;
-        int stage = 0;
-        uint32_t phase = 0, armed = 0, armed_parity = 0;  // stages armed on `full` (even CTA)
-        bool ok = true;
-        for (int t = pair; ok && t < walk.items; t += num_pairs) {
-          const PairItem item = pair_item<false>(p, tb, walk, t);
-          const GroupedTile& x = item.x;
-          // of half a tile the MMA reads 64 columns, the first of the 128 that are loaded
-          const int n0 = x.cb * kTile + (item.half < 0 ? (int)rank * 128 : item.half * 128 + (int)rank * 64);
-          const int m0 = x.lo + x.rb * kTile + (int)rank * 128;
-          // whether this CTA's, and the other's, rows of A hold any of the group
-          const bool a_on = m0 < x.hi;
-          const int shares = (x.lo + x.rb * kTile + 128 < x.hi ? 2 : 1) + 2;
-          const int zb = p.strideB != 0 ? x.g : 0;
-          for (int kb = 0; kb < p.k_blocks; ++kb) {
-            if (!mbar_wait(&empty[stage], phase ^ 1u, wc)) {
-              ok = false;
-              break;
-            }
-            const uint32_t full_leader = mapa_shared(smem_u32(&full[stage]), 0);
-            if (leader) {
+      const uint32_t lead = elect_lead();  // a converged warp, one lane of which loads
+      const PairWalk walk = find_walk();
+      const uint64_t keep = policy_evict_last();
+      const uint64_t pol_b = p.b_stream ? policy_evict_first() : keep;
+      int stage = 0;
+      uint32_t phase = 0, armed = 0, armed_parity = 0;  // stages armed on `full` (even CTA)
+      bool ok = true;
+      for (int t = pair; ok && t < walk.items; t += num_pairs) {
+        const PairItem item = pair_item<false>(p, tb, walk, t);
+        const GroupedTile& x = item.x;
+        // of half a tile the MMA reads 64 columns, the first of the 128 that are loaded
+        const int n0 = x.cb * kTile + (item.half < 0 ? (int)rank * 128 : item.half * 128 + (int)rank * 64);
+        const int m0 = x.lo + x.rb * kTile + (int)rank * 128;
+        // whether this CTA's, and the other's, rows of A hold any of the group
+        const bool a_on = m0 < x.hi;
+        const int shares = (x.lo + x.rb * kTile + 128 < x.hi ? 2 : 1) + 2;
+        const int zb = p.strideB != 0 ? x.g : 0;
+        for (int kb = 0; kb < p.k_blocks; ++kb) {
+          if (!mbar_wait_warp(&done[stage], phase ^ 1u, wc)) {
+            ok = false;
+            break;
+          }
+          const uint32_t full_leader = mapa_shared(smem_u32(&full[stage]), 0);
+          if (leader) {
+            if (lead) {
               stage_info[stage] = item.half < 0 ? 2 : 1;
               mbar_arrive_expect_tx(full + stage, shares * kShareBytes);
-              armed |= 1u << stage;
-              armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
             }
-            if (a_on) tma_load_3d_pair(sA + stage * kShareBytes, &p.tmA, kb * kF8Block, m0, 0, full_leader, keep);
-            tma_load_3d_pair(sB + stage * kShareBytes, &p.tmB, kb * kF8Block, n0, zb, full_leader, pol_b);
-            if (++stage == kStages) {
-              stage = 0;
-              phase ^= 1u;
-            }
+            armed |= 1u << stage;
+            armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+          }
+          if (a_on) tma_load_3d_pair_lead(lead, sA + stage * kShareBytes, &p.tmA, kb * kF8Block, m0, 0, full_leader, keep);
+          tma_load_3d_pair_lead(lead, sB + stage * kShareBytes, &p.tmB, kb * kF8Block, n0, zb, full_leader, pol_b);
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
           }
         }
-        // a stage completes once both CTAs' loads for it have landed
-        if (leader)
-          drain_ring(full, kStages, armed, armed_parity);
-        else
-          drain_odd_cta(wc);
       }
+      // a stage completes once both CTAs' loads for it have landed
+      if (leader)
+        drain_ring_lanes(full, armed, armed_parity);
+      else
+        drain_odd_cta(wc);
     } else if (warp == 1) {
       // ---------------------------------------------------------------- MMA issuer (even CTA)
       if (leader) {
@@ -313,8 +314,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) f8_pair
               mma_f8_pair_lead(lead, tmem_base + acc * kAccCols, a_lo + k * 2, a_hi, b_lo + k * 2, b_hi, idesc, k != 0);
             any = true;
             ++it;
-            mma_commit_pair_lead(lead, &tmem_full[acc], 0x3);
-            mma_commit_pair_lead(lead, &empty[stage], 0x3);
+            mma_commit_pair_lead(lead, &done[stage], 0x3);
             if (++stage == kStages) {
               stage = 0;
               phase ^= 1u;
@@ -394,7 +394,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) f8_pair
     const PairWalk walk = find_walk();
     const uint32_t from = find_tmem() + ((uint32_t)(q * 32) << 16) ;
     // shared memory by 32-bit addresses: the accumulators' barriers here and in the even CTA, this lane's scales
-    const uint32_t full_at = smem_u32(tmem_full), release = mapa_shared(smem_u32(tmem_empty), 0);
+    const uint32_t full_at = smem_u32(done), release = mapa_shared(smem_u32(tmem_empty), 0);
     const uint32_t scales_at = smem_u32(scales);
     uint32_t it = 0;  // accumulators so far
     uint32_t chunk = 0;
@@ -405,7 +405,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) f8_pair
       for (int j = 0; j < 64; ++j) sums[j] = 0.0f;
       for (int kb0 = 0; ok && kb0 < p.k_blocks; kb0 += kAhead, ++chunk) {
         const uint32_t slot = chunk % kScaleSlots;
-        if (!wait_warp_at(full_at + (2 * kAccs + slot) * 8, chunk / kScaleSlots & 1, wc)) {
+        if (!wait_warp_at(full_at + (kStages + kAccs + slot) * 8, chunk / kScaleSlots & 1, wc)) {
           ok = false;
           break;
         }
@@ -420,7 +420,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) f8_pair
           float scale = shared_f32(a_at);
           if constexpr (!BY_COLUMN) scale *= shared_f32(b_at);
           const uint32_t acc = it & (kAccs - 1);
-          if (!wait_warp_at(full_at + acc * 8, (it / kAccs) & 1, wc)) {
+          if (!wait_warp_at(full_at + (it % kStages) * 8, (it / kStages) & 1, wc)) {
             ok = false;
             break;
           }
@@ -450,7 +450,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) f8_pair
         }
         if (kb0 + kAhead < p.k_blocks) {
           __syncwarp();
-          if (lane == 0) arrive_at(full_at + (2 * kAccs + kScaleSlots + slot) * 8);
+          if (lane == 0) arrive_at(full_at + (kStages + kAccs + kScaleSlots + slot) * 8);
         }
       }
       if (!ok) break;
@@ -458,7 +458,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) f8_pair
       const uint32_t slot = (chunk - 1) % kScaleSlots;
       const TileInfo x = *reinterpret_cast<const TileInfo*>(scales + slot * kScaleBytes + 128 * kAhead * 4 + kTile * kAhead * 4);
       __syncwarp();
-      if (lane == 0) arrive_at(full_at + (2 * kAccs + kScaleSlots + slot) * 8);
+      if (lane == 0) arrive_at(full_at + (kStages + kAccs + kScaleSlots + slot) * 8);
       const int r0 = x.row0 + q * 32, rows = max(0, min(32, x.row_end - r0));
       const int col0 = x.col0 + (x.parts == 2 ? half * 128 + second * 64 : half * 64);
       const int cols = x.parts == 1 && second != 0 ? 0 : min(64, p.N - col0);

@@ -489,6 +489,17 @@ __device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* m
       : "memory");
 }
 
+// The same by one lane of a converged warp.
+__device__ __forceinline__ void tma_load_3d_pair_lead(uint32_t lead, void* dst, const CUtensorMap* m, int32_t c0, int32_t c1,
+                                                      int32_t c2, uint32_t bar_cluster, uint64_t cache_hint) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %7, 0;\n\t"
+      "@e cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4}], [%5], %6;\n\t}" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(c2), "r"(bar_cluster), "l"(cache_hint), "r"(lead)
+      : "memory");
+}
+
 // im2col TMA load for a CTA pair (completion on the leader's barrier): the
 // map fixes the box, `pixels` consecutive output pixels x `channels`
 // channels of an NHWC tensor.  (c, w, h, n) is the first pixel's window
