@@ -10,10 +10,10 @@
 // ahead.  (An accumulator for each block: 4099 rows of 64 groups, 1536 x 2048 65.6 us against
 // 58.4; a second set of epilogue warps for every other one changed nothing.)
 //
-// Bound by HBM up to 32 tokens and a few microseconds of start: 1 x 14336 x 4096 12.2 us, 16 x
-// 8192 x 8192 15.7, 1 x 4096 x 4096 8.7 (10.1 with one thread that loads).  With 64 tokens a tile by shared memory, which gives the MMAs 24 KB a block
-// of K, takes as much from TMA and hands 64 tokens' scales to every warp: 0.33 us a block,
-// 64 x 8192 x 8192 23.7 us; without the last of these 20.1.
+// Bound by HBM up to 32 tokens and a few microseconds of start: 1 x 14336 x 4096 12.3 us, 16 x
+// 8192 x 8192 16.0, 1 x 4096 x 4096 8.7 (10.1 with one thread that loads).  With 64 tokens a tile
+// by shared memory, which gives the MMAs 24 KB a block of K, takes as much from TMA and hands 64
+// tokens' scales to every warp: 0.31 us a block, 64 x 8192 x 8192 21.1 us.
 #include <atomic>
 
 #include "f8_blocks.cuh"
@@ -75,7 +75,22 @@ __device__ __forceinline__ void store_result(void* d, int64_t i, float v) {
     static_cast<uint16_t*>(d)[i] = (uint16_t)(pack2<OUT == kF8ResultBF16>(v, 0.0f) & 0xFFFFu);
 }
 
-template <int BT, int OUT>
+// Two tokens at a time: half the instructions, 2 % of 64 x 8192 x 8192.
+__device__ __forceinline__ void add_pair(float* sum, const uint32_t* w, float2 token_scale, float scale) {
+  const float2 v = __ffma2_rn(__fmul2_rn(token_scale, make_float2(scale, scale)),
+                              make_float2(__uint_as_float(w[0]), __uint_as_float(w[1])), make_float2(sum[0], sum[1]));
+  sum[0] = v.x;
+  sum[1] = v.y;
+}
+
+// Blocks of K whose weights' scales a thread reads at a time.  A column's own scales are
+// 4 bytes of a line for each thread and block: four at a time took 500 rows of 16 groups,
+// 4096 x 4096, from 82 us to 58, where one for 128 columns, the same for all threads, lost 2 %
+// by the registers.
+template <bool BY_COLUMN>
+constexpr int kFetch = BY_COLUMN ? 4 : kKPS;
+
+template <int BT, int OUT, bool BY_COLUMN>
 __global__ void __launch_bounds__(kThreads<BT>, 1) f8_tokens_kernel(const __grid_constant__ F8Params p) {
   constexpr int kTokenBytes = stage_bytes_of(BT);
   constexpr int kBox = few_tokens_box(BT);
@@ -260,15 +275,33 @@ __global__ void __launch_bounds__(kThreads<BT>, 1) f8_tokens_kernel(const __grid
         barrier_of_epilogue<kEpiThreads<BT>>();
         buffer ^= 1;
         ts += j0;
-        float next[kKPS];
+        // the weights' scales, a stage's or, of a column's own, two stages' ahead
+        float next[kFetch<BY_COLUMN>], now[kFetch<BY_COLUMN>];
         const auto fetch = [&](int i) {
+          const float* at = sb + kb0 + i;
+          if constexpr (BY_COLUMN) {
+            if (p.sb_vec && f_ok && i + 4 <= n) {
+              const float4 v = __ldg(reinterpret_cast<const float4*>(at));
+              next[0] = v.x;
+              next[1] = v.y;
+              next[2] = v.z;
+              next[3] = v.w;
+              return;
+            }
+          }
 #pragma unroll
-          for (int k = 0; k < kKPS; ++k) next[k] = f_ok && i + k < n ? __ldg(sb + kb0 + i + k) : 0.0f;
+          for (int k = 0; k < kFetch<BY_COLUMN>; ++k) next[k] = f_ok && i + k < n ? __ldg(at + k) : 0.0f;
         };
         fetch(0);
         for (int i = 0; i < n; i += kKPS, ++it, ts += kKPS * BT) {
-          const float scale[kKPS] = {next[0], next[1]};
-          fetch(i + kKPS);
+          const int in_fetch = i % kFetch<BY_COLUMN>;
+          if (in_fetch == 0) {
+#pragma unroll
+            for (int k = 0; k < kFetch<BY_COLUMN>; ++k) now[k] = next[k];
+            fetch(i + kFetch<BY_COLUMN>);
+          }
+          const float scale[kKPS] = {in_fetch == 0 ? now[0] : now[kFetch<BY_COLUMN> - 2],
+                                     in_fetch == 0 ? now[1] : now[kFetch<BY_COLUMN> - 1]};
           const uint32_t acc = it & (kAccs - 1);
           if (ok) ok = mbar_wait_warp(&tmem_full[acc], (it / kAccs) & 1, wc);
           if (!ok) continue;
@@ -287,10 +320,8 @@ __global__ void __launch_bounds__(kThreads<BT>, 1) f8_tokens_kernel(const __grid
 #pragma unroll
             for (int j = 0; j < 16; j += 4) {
               const float4 s = *reinterpret_cast<const float4*>(ts + k * BT + j);
-              sums[j] = fmaf(s.x * scale[k], __uint_as_float(w[k][j]), sums[j]);
-              sums[j + 1] = fmaf(s.y * scale[k], __uint_as_float(w[k][j + 1]), sums[j + 1]);
-              sums[j + 2] = fmaf(s.z * scale[k], __uint_as_float(w[k][j + 2]), sums[j + 2]);
-              sums[j + 3] = fmaf(s.w * scale[k], __uint_as_float(w[k][j + 3]), sums[j + 3]);
+              add_pair(sums + j, w[k] + j, make_float2(s.x, s.y), scale[k]);
+              add_pair(sums + j + 2, w[k] + j + 2, make_float2(s.z, s.w), scale[k]);
             }
           }
         }
@@ -316,7 +347,7 @@ __global__ void __launch_bounds__(kThreads<BT>, 1) f8_tokens_kernel(const __grid
   }
 }
 
-template <int BT, int OUT>
+template <int BT, int OUT, bool BY_COLUMN>
 cudaError_t launch(const F8Params& p, int ctas, cudaStream_t stream) {
   static std::atomic<bool> done[64];
   int dev = 0;
@@ -324,7 +355,7 @@ cudaError_t launch(const F8Params& p, int ctas, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!done[dev].load()) {
-    e = cudaFuncSetAttribute(f8_tokens_kernel<BT, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+    e = cudaFuncSetAttribute(f8_tokens_kernel<BT, OUT, BY_COLUMN>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
     if (e != cudaSuccess) return e;
     done[dev].store(true);
   }
@@ -335,16 +366,17 @@ cudaError_t launch(const F8Params& p, int ctas, cudaStream_t stream) {
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   add_pdl_attribute(cfg, attr);
-  e = cudaLaunchKernelEx(&cfg, f8_tokens_kernel<BT, OUT>, p);
+  e = cudaLaunchKernelEx(&cfg, f8_tokens_kernel<BT, OUT, BY_COLUMN>, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <int BT>
 cudaError_t launch_out(const F8Params& p, F8Result out, int ctas, cudaStream_t stream) {
+  const bool by_column = p.b_shift == 0;
   switch (out) {
-    case kF8ResultF16: return launch<BT, kF8ResultF16>(p, ctas, stream);
-    case kF8ResultBF16: return launch<BT, kF8ResultBF16>(p, ctas, stream);
-    case kF8ResultF32: return launch<BT, kF8ResultF32>(p, ctas, stream);
+    case kF8ResultF16: return by_column ? launch<BT, kF8ResultF16, true>(p, ctas, stream) : launch<BT, kF8ResultF16, false>(p, ctas, stream);
+    case kF8ResultBF16: return by_column ? launch<BT, kF8ResultBF16, true>(p, ctas, stream) : launch<BT, kF8ResultBF16, false>(p, ctas, stream);
+    case kF8ResultF32: return by_column ? launch<BT, kF8ResultF32, true>(p, ctas, stream) : launch<BT, kF8ResultF32, false>(p, ctas, stream);
   }
   return cudaErrorInvalidValue;
 }
