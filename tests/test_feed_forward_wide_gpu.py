@@ -221,3 +221,36 @@ def test_the_same_call_gives_the_same_bits(rows, n):
     for _ in range(10):
         assert all(torch.equal(x, y) for x, y in zip(first, ttc.gemm_gated(a, w[:n].t(), w[n:].t(), pre=True)))
         assert torch.equal(f8, ttc.gemm_f8_blocks(qa, sa, qw, sw))
+
+
+@pytest.mark.parametrize("rows,n", [(40, 136), (300, 264), (2000, 1160)])
+@pytest.mark.parametrize("block", [1, 128])
+def test_groups_that_share_weights(rows, n, block):
+    """Weights and scales expanded over the groups, stride 0, give what copies of them give."""
+    gen = generator(31)
+    groups, k = 3, 264
+    cut = torch.tensor([0, rows // 4, rows // 2, rows - 1], dtype=torch.int32, device="cuda")
+    a = torch.randn((rows, k), generator=gen, device="cuda").bfloat16()
+    w = torch.randn((2 * n, k), generator=gen, device="cuda").bfloat16() / 16
+    one = [w[:n].t()[None].expand(groups, k, n), w[n:].t()[None].expand(groups, k, n)]
+    many = [x.transpose(1, 2).contiguous().transpose(1, 2) for x in one]
+    outs = [torch.zeros((rows, n), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    pres = [torch.zeros((rows, 2 * n), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    for x, out, pre in zip((one, many), outs, pres):
+        ttc.gemm_gated(a, *x, out, offsets=cut, pre=pre)
+    assert torch.equal(*outs) and torch.equal(*pres) and outs[0][:-1].abs().sum() > 0
+    dy = torch.randn((rows, k), generator=gen, device="cuda").bfloat16()
+    grads = [torch.zeros_like(pres[0]) for _ in range(2)]
+    for x, d in zip((one[0], many[0]), grads):
+        ttc.gemm_gated_grad(dy, x, pres[0], d, offsets=cut)
+    assert torch.equal(*grads)
+    qa, sa = ttc.quantize_blocks(a)
+    qw, sw = ttc.quantize_blocks(w[:n], block_rows=block)
+    shared = [t[None].expand(groups, *t.shape) for t in (qw, sw)]
+    # rows on 16-byte boundaries, as the quantizer leaves them
+    copy = torch.empty((groups, n, qw.stride(0)), dtype=torch.uint8, device="cuda")[..., :k].view(qw.dtype)
+    copy.view(torch.uint8).copy_(shared[0].view(torch.uint8))
+    outs = [torch.zeros((rows, n), device="cuda") for _ in range(2)]
+    ttc.gemm_f8_blocks(qa, sa, *shared, outs[0], offsets=cut)
+    ttc.gemm_f8_blocks(qa, sa, copy, shared[1].contiguous(), outs[1], offsets=cut)
+    assert torch.equal(*outs) and outs[0][:-1].abs().sum() > 0
