@@ -23,9 +23,9 @@ bool f8_maps(F8Params& p, int rows_a, int rows_b, const HostEnv& env) {
 
 // Block of tokens of the few-token kernel, 0 for CTA pairs: as for 16-bit operands up to 64
 // rows a group, and with more wherever blocks of 64 make one wave of tiles, whose narrow
-// tiles keep all SMs at work (rows x 4096 x 4096: 65 to 256 13.9 us against 18.9 to 20.8;
+// tiles keep all SMs at work (rows x 4096 x 4096: 65 to 256 12.4 to 12.7 us against 18.9 to 20.8;
 // 128 x 8192 x 8192 24.2 against 35.6, 256 x 1024 x 4096 13.8 against 18.5; two waves, 320 x
-// 4096 x 4096, 24.1 against 20.8; 1024 rows of 8 groups, 4096 x 4096, four waves, 45.8 against 41.1).
+// 4096 x 4096, 24.1 against 20.8; 1024 rows of 8 groups, 4096 x 4096, four waves, 50.9 against 41.5).
 int f8_few_block(int64_t rows, int64_t n, int64_t groups, int sm_count) {
   const int block = few_block(rows, groups);
   if (block != 0) return block;
