@@ -50,6 +50,37 @@ def test_gated_unsupported(kw):
     assert gated(**kw) == UNSUPPORTED
 
 
+# Outputs in the rows of an input's buffer, beside it: of 80 columns A (or the weights) takes the first 48 (32)
+# and an output the next 32.
+WIDE = dict(lda=80, ldd=80)
+ROWS = dict(layout=R, ldb=80, ldd=80, strideB=48 * 80)
+BESIDE_GATED = [dict(WIDE, D=P + 2 * 48), dict(KEPT, lda=80, gate=P + 2 * 48, up=P * 12, ldp=80), dict(ROWS, D=P * 3 + 2 * 32),
+                dict(ROWS, D=P * 4 + 2 * 48), dict(ROWS, D=P * 4 + 2 * (48 * 80 + 40)),
+                dict(D=P * 3 + 2 * 32 * 48, strideB=1 << 20), dict(groups=1, offsets=None, strideB=7, D=P * 4 + 2 * 32 * 48)]
+BESIDE_GRAD = [dict(WIDE, D=P + 2 * 48), dict(lda=128, lddp=128, dgate=P + 2 * 48, dup=P + 2 * 88), dict(ROWS, D=P * 3 + 2 * 32),
+               dict(ROWS, lddp=80, dup=P * 3 + 2 * 33, dgate=P * 14)]
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="calls that are taken would run on these addresses")
+@pytest.mark.parametrize("call,kw", [(0, kw) for kw in BESIDE_GATED] + [(1, kw) for kw in BESIDE_GRAD])
+def test_outputs_beside_inputs_are_taken(call, kw):
+    assert (grad if call else gated)(**kw) == 3  # as far as the missing GPU
+
+
+@pytest.mark.parametrize("kw", [dict(WIDE, D=P + 2 * 47), dict(WIDE, D=P + 2 * 49), dict(WIDE, ldd=81, D=P + 2 * 48),
+                                dict(WIDE, D=P - 2 * 31), dict(ROWS, D=P * 3 + 2 * 31), dict(ROWS, D=P * 4 + 2 * 49),
+                                dict(ROWS, strideB=48 * 80 + 1, D=P * 4 + 2 * 32 + 2 * 80 * 47), dict(ROWS, strideB=1, D=P * 3 + 2 * 32),
+                                dict(D=P * 3 + 2 * 32 * 48 - 2, strideB=1 << 20), dict(D=P * 3 + 2 * 3 * (1 << 20), strideB=1 << 20)])
+def test_gated_beside_and_over(kw):
+    assert gated(**kw) == INVALID
+
+
+@pytest.mark.parametrize("kw", [dict(WIDE, D=P + 2 * 47), dict(lda=128, lddp=128, dgate=P + 2 * 48, dup=P + 2 * 97),
+                                dict(ROWS, lddp=80, dup=P * 3 + 2 * 49, dgate=P * 14), dict(ROWS, D=P * 3 + 2 * 31)])
+def test_grad_beside_and_over(kw):
+    assert grad(**kw) == INVALID
+
+
 def test_gated_empty():
     for kw in (dict(groups=0), dict(M=0), dict(N=0), dict(M=0, A=None, Bg=None, Bu=None, D=None, offsets=None)):
         assert gated(**kw) == 0

@@ -8,35 +8,36 @@ namespace {
 
 bool is_gated_act(ttc_act a) { return is_act(a) || a == TTC_ACT_SILU; }
 
-// A matrix of M rows and N columns.
-struct Rows {
+// A matrix of 16-bit elements.
+struct Mat {
   const void* p;
-  int64_t ld;
+  int64_t ld, rows, cols;
 };
-int64_t rows_bytes(int64_t M, int64_t ld, int64_t N) { return span_bytes(1, 0, M, ld, N, 2); }
-bool overlap(Rows a, Rows b, int64_t M, int64_t N) {
-  return a.p != nullptr && b.p != nullptr && byte_ranges_overlap(a.p, rows_bytes(M, a.ld, N), b.p, rows_bytes(M, b.ld, N));
-}
+int64_t bytes_of(const Mat& a) { return span_bytes(1, 0, a.rows, a.ld, a.cols, 2); }
 // Two matrices of the same pitch may lie side by side in one buffer: then their
 // spans overlap, their elements do not.
-bool side_by_side(Rows a, Rows b, int64_t N) {
+bool side_by_side(const Mat& a, const Mat& b) {
   if (a.ld != b.ld) return false;
   const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-  const uint64_t apart = (x < y ? y - x : x - y) % (uint64_t)(2 * a.ld);
-  return apart >= (uint64_t)(2 * N) && (uint64_t)(2 * a.ld) - apart >= (uint64_t)(2 * N);
+  const uint64_t pitch = (uint64_t)(2 * a.ld);
+  const uint64_t apart = y >= x ? (y - x) % pitch : (pitch - (x - y) % pitch) % pitch;  // from a's columns on to b's
+  return apart >= (uint64_t)(2 * a.cols) && pitch - apart >= (uint64_t)(2 * b.cols);
 }
-bool clash(Rows a, Rows b, int64_t M, int64_t N) { return overlap(a, b, M, N) && !side_by_side(a, b, N); }
+bool clash(const Mat& a, const Mat& b) {
+  return a.p != nullptr && b.p != nullptr && byte_ranges_overlap(a.p, bytes_of(a), b.p, bytes_of(b)) && !side_by_side(a, b);
+}
 
 // What both calls refuse of their products' operands; TTC_OK with `nothing` set for
-// an empty result.  The reads of A and B end inside a_bytes and b_bytes.
+// an empty result.  A and one group's B as they are read, and how many of B; none with K == 0.
 struct Products {
   bool nothing;
-  int64_t a_bytes, b_bytes;
+  Mat a, b;
+  int64_t mats, stride;
 };
 ttc_status check_products(int64_t groups, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const int32_t* offsets,
                           const void* B, int64_t ldb, int64_t strideB, ttc_layout layoutB, ttc_act act, ttc_dtype dtype,
                           Products& out) {
-  out = Products{false, 0, 0};
+  out = Products{};
   if (groups < 0 || M < 0 || N < 0 || K < 0 || strideB < 0) return TTC_ERR_INVALID_ARG;
   if (layoutB != TTC_ROW_MAJOR && layoutB != TTC_COL_MAJOR) return TTC_ERR_INVALID_ARG;
   if (!is_gated_act(act) || !is_dtype(dtype)) return TTC_ERR_INVALID_ARG;
@@ -54,19 +55,26 @@ ttc_status check_products(int64_t groups, int64_t M, int64_t N, int64_t K, const
     return TTC_ERR_UNSUPPORTED;
   if ((blocks_of(M, kGroupedPlainTile) + groups) * blocks_of(N, kGatedPlainCols) > kSizeLimit) return TTC_ERR_UNSUPPORTED;
   if (K > 0) {
-    const int64_t b_rows = layoutB == TTC_ROW_MAJOR ? K : N, b_cols = layoutB == TTC_ROW_MAJOR ? N : K;
-    out.a_bytes = rows_bytes(M, lda, K);
-    out.b_bytes = span_bytes(groups, strideB, b_rows, ldb, b_cols, 2);
+    out.a = Mat{A, lda, M, K};
+    out.b = layoutB == TTC_ROW_MAJOR ? Mat{B, ldb, K, N} : Mat{B, ldb, N, K};
+    out.mats = strideB != 0 ? groups : 1;
+    out.stride = strideB;
   }
   return TTC_OK;
 }
 
-// Whether an output may be written while A and B (of `b_bytes`) are read.
-bool hits_operands(Rows d, int64_t M, int64_t N, const Products& o, const void* A, const void* B, const void* U) {
-  if (d.p == nullptr || o.a_bytes == 0) return false;
-  const int64_t bytes = rows_bytes(M, d.ld, N);
-  return byte_ranges_overlap(d.p, bytes, A, o.a_bytes) || byte_ranges_overlap(d.p, bytes, B, o.b_bytes) ||
-         (U != nullptr && byte_ranges_overlap(d.p, bytes, U, o.b_bytes));
+// Whether an output touches what is read while it is written: A, a group's B, or of the forward
+// pass its U, laid out as B.
+bool hits_operands(const Mat& d, const Products& o, const void* U) {
+  if (d.p == nullptr || o.mats == 0) return false;
+  if (clash(d, o.a)) return true;
+  const int64_t all = span_bytes(o.mats, o.stride, o.b.rows, o.b.ld, o.b.cols, 2);
+  for (const void* w : {o.b.p, U}) {
+    if (w == nullptr || !byte_ranges_overlap(d.p, bytes_of(d), w, all)) continue;
+    for (int64_t g = 0; g < o.mats; ++g)
+      if (clash(d, Mat{static_cast<const uint16_t*>(w) + g * o.stride, o.b.ld, o.b.rows, o.b.cols})) return true;
+  }
+  return false;
 }
 
 bool rows_on_16(const void* p, int64_t ld) { return aligned(p, 16) && ld % 8 == 0; }
@@ -153,9 +161,9 @@ ttc_status ttc_gemm_gated(int64_t groups, int64_t M, int64_t N, int64_t K, const
   if (D == nullptr || ldd < N || !aligned(D, 2) || (K > 0 && (Bup == nullptr || !aligned(Bup, 2)))) return TTC_ERR_INVALID_ARG;
   if (save && (gate == nullptr || up == nullptr || ldp < N || !aligned(gate, 2) || !aligned(up, 2))) return TTC_ERR_INVALID_ARG;
   if (ldd > kSizeLimit || (save && ldp > kSizeLimit)) return TTC_ERR_UNSUPPORTED;
-  const Rows d{D, ldd}, g{gate, ldp}, u{up, ldp};
-  if (hits_operands(d, M, N, o, A, Bgate, Bup) || hits_operands(g, M, N, o, A, Bgate, Bup) ||
-      hits_operands(u, M, N, o, A, Bgate, Bup) || clash(d, g, M, N) || clash(d, u, M, N) || clash(g, u, M, N))
+  const Mat d{D, ldd, M, N}, g{gate, ldp, M, N}, u{up, ldp, M, N};
+  if (hits_operands(d, o, Bup) || hits_operands(g, o, Bup) || hits_operands(u, o, Bup) || clash(d, g) || clash(d, u) ||
+      clash(g, u))
     return TTC_ERR_INVALID_ARG;
 
   HostEnv env;
@@ -185,13 +193,12 @@ ttc_status ttc_gemm_gated_grad(int64_t groups, int64_t M, int64_t N, int64_t K, 
     return TTC_ERR_INVALID_ARG;
   if (!aligned(gate, 2) || !aligned(up, 2) || !aligned(dgate, 2) || !aligned(dup, 2) || !aligned(D, 2)) return TTC_ERR_INVALID_ARG;
   if (ldp > kSizeLimit || lddp > kSizeLimit || (D != nullptr && ldd > kSizeLimit)) return TTC_ERR_UNSUPPORTED;
-  const Rows g{gate, ldp}, u{up, ldp}, dg{dgate, lddp}, du{dup, lddp}, d{D, ldd};
+  const Mat g{gate, ldp, M, N}, u{up, ldp, M, N}, dg{dgate, lddp, M, N}, du{dup, lddp, M, N}, d{D, ldd, M, N};
   const bool in_place = gate == dgate && up == dup && ldp == lddp;
-  if (hits_operands(dg, M, N, o, A, B, nullptr) || hits_operands(du, M, N, o, A, B, nullptr) ||
-      hits_operands(d, M, N, o, A, B, nullptr) || clash(dg, du, M, N) || clash(d, g, M, N) || clash(d, u, M, N) ||
-      clash(d, dg, M, N) || clash(d, du, M, N))
+  if (hits_operands(dg, o, nullptr) || hits_operands(du, o, nullptr) || hits_operands(d, o, nullptr) || clash(dg, du) ||
+      clash(d, g) || clash(d, u) || clash(d, dg) || clash(d, du))
     return TTC_ERR_INVALID_ARG;
-  if (!in_place && (clash(dg, g, M, N) || clash(dg, u, M, N) || clash(du, g, M, N) || clash(du, u, M, N)))
+  if (!in_place && (clash(dg, g) || clash(dg, u) || clash(du, g) || clash(du, u)))
     return TTC_ERR_INVALID_ARG;
 
   HostEnv env;
