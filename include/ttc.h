@@ -313,8 +313,9 @@ size_t ttc_gemm_i8_scaled_workspace_size(int64_t M, int64_t N, int64_t K,
  * notes apply).  Operands TMA can read (see ttc_gemm_grouped) run faster.
  * TTC_ERR_INVALID_ARG: negative sizes or strides, pitches below the extent, NULL
  * or misaligned pointers (one of gate and up NULL among them), an output
- * overlapping an input or another output (side by side in rows of one pitch is
- * no overlap), offsets NULL with groups > 1, an unknown enum value.
+ * overlapping an input, the offsets among them, or another output (side by side
+ * in rows of one pitch is no overlap), offsets NULL with groups > 1, an unknown
+ * enum value.
  * TTC_ERR_UNSUPPORTED: TTC_I8 or TTC_F32, more than 1024 groups, sizes beyond
  * 2^31 - 2^24.  groups, M or N == 0 is a no-op; K == 0 gives products of zeros.
  */
@@ -399,9 +400,9 @@ ttc_status ttc_quantize_blocks(int64_t rows, int64_t cols, const void* X, int64_
  * Asynchronous on `stream`; allocates nothing; may be captured (ttc_gemm's notes
  * apply).  Rows of A and B on 16-byte boundaries run faster.
  * TTC_ERR_INVALID_ARG: negative sizes or strides, pitches below the extent, NULL or
- * misaligned pointers, D overlapping an input other than C in place, offsets NULL
- * with groups > 1, another block_rows_b, an unknown enum value or act (TTC_ACT_SILU
- * among them).  TTC_ERR_UNSUPPORTED: other types, more than 1024 groups, sizes
+ * misaligned pointers, D overlapping an input (offsets among them) other than C in
+ * place, offsets NULL with groups > 1, another block_rows_b, an unknown enum value or
+ * act (TTC_ACT_SILU among them).  TTC_ERR_UNSUPPORTED: other types, more than 1024 groups, sizes
  * beyond 2^31 - 2^24.  groups, M or N == 0 is a no-op; K == 0 gives act(C + bias_g).
  */
 ttc_status ttc_gemm_f8_blocks(int64_t groups, int64_t M, int64_t N, int64_t K,

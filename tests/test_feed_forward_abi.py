@@ -165,6 +165,32 @@ def test_f8_unsupported(kw):
     assert f8(**kw) == UNSUPPORTED
 
 
+# The offsets of the four groups (20 bytes at P * 9) are an input too: written while tiles are being dealt out,
+# parts of the grid would disagree about them.
+END = P * 9 + 20
+
+
+@pytest.mark.parametrize("call,kw", [
+    (gated, dict(D=END - 2)), (gated, dict(D=P * 9 + 2 - 64 * 32 * 2)), (gated, dict(ldd=80, D=END - 2 - 160)),
+    (gated, dict(K=0, D=P * 9)), (gated, dict(KEPT, gate=END - 2, up=P * 10)), (gated, dict(KEPT, up=P * 9 + 2 - 64 * 64 * 2 + 64)),
+    (gated, dict(groups=1, D=P * 9 + 6)), (grad, dict(D=END - 2)), (grad, dict(dgate=END - 2, dup=P * 10)),
+    (grad, dict(dup=END - 2, dgate=P * 10)), (grad, dict(gate=P * 9, up=P * 9 + 64, dgate=P * 9, dup=P * 9 + 64)),
+    (f8, dict(D=END - 2)), (f8, dict(D=P * 9 + 2 - 64 * 160 * 2)), (f8, dict(K=0, D=P * 9)), (f8, dict(out=F32, D=END - 4)),
+    (f8, dict(Cp=P * 9, D=P * 9)),
+])
+def test_results_over_offsets(call, kw):
+    assert call(**kw) == INVALID
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="calls that are taken would run on these addresses")
+@pytest.mark.parametrize("call,kw", [
+    (gated, dict(D=END)), (gated, dict(D=P * 9 - 64 * 32 * 2)), (gated, dict(ldd=80, D=END - 160)), (gated, dict(groups=1, D=P * 9 + 8)),
+    (grad, dict(D=END)), (f8, dict(D=END)), (f8, dict(D=P * 9 - 64 * 160 * 2)),
+])
+def test_results_beside_offsets(call, kw):
+    assert call(**kw) == 3  # as far as the missing GPU
+
+
 def test_f8_empty():
     assert f8(groups=0) == 0 and f8(M=0) == 0 and f8(N=0, A=None, B=None, D=None) == 0
 

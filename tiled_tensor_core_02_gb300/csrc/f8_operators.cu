@@ -109,6 +109,7 @@ ttc_status ttc_gemm_f8_blocks(int64_t groups, int64_t M, int64_t N, int64_t K, c
     return TTC_ERR_INVALID_ARG;
   if (C != nullptr && !(C == D && ldc == ldd) && byte_ranges_overlap(D, d_bytes, C, span_bytes(1, 0, M, ldc, N, esize)))
     return TTC_ERR_INVALID_ARG;
+  if (offsets != nullptr && byte_ranges_overlap(D, d_bytes, offsets, (groups + 1) * 4)) return TTC_ERR_INVALID_ARG;
   if (bias != nullptr && byte_ranges_overlap(D, d_bytes, bias, span_bytes(groups, strideBias, 1, N, N, 4)))
     return TTC_ERR_INVALID_ARG;
 

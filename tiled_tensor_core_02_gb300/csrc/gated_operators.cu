@@ -29,9 +29,10 @@ bool clash(const Mat& a, const Mat& b) {
 
 // What both calls refuse of their products' operands; TTC_OK with `nothing` set for
 // an empty result.  A and one group's B as they are read, and how many of B; none with K == 0.
+// The offsets are one row of 16-bit elements.
 struct Products {
   bool nothing;
-  Mat a, b;
+  Mat offsets, a, b;
   int64_t mats, stride;
 };
 ttc_status check_products(int64_t groups, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const int32_t* offsets,
@@ -54,6 +55,7 @@ ttc_status check_products(int64_t groups, int64_t M, int64_t N, int64_t K, const
       strideB > kStrideLimit)
     return TTC_ERR_UNSUPPORTED;
   if ((blocks_of(M, kGroupedPlainTile) + groups) * blocks_of(N, kGatedPlainCols) > kSizeLimit) return TTC_ERR_UNSUPPORTED;
+  out.offsets = Mat{offsets, 0, 1, 2 * (groups + 1)};
   if (K > 0) {
     out.a = Mat{A, lda, M, K};
     out.b = layoutB == TTC_ROW_MAJOR ? Mat{B, ldb, K, N} : Mat{B, ldb, N, K};
@@ -63,10 +65,12 @@ ttc_status check_products(int64_t groups, int64_t M, int64_t N, int64_t K, const
   return TTC_OK;
 }
 
-// Whether an output touches what is read while it is written: A, a group's B, or of the forward
-// pass its U, laid out as B.
+// Whether an output touches what is read while it is written: the offsets (which CTAs that work on
+// one tile each read for themselves), A, a group's B, or of the forward pass its U, laid out as B.
 bool hits_operands(const Mat& d, const Products& o, const void* U) {
-  if (d.p == nullptr || o.mats == 0) return false;
+  if (d.p == nullptr) return false;
+  if (clash(d, Mat{o.offsets.p, d.ld, o.offsets.rows, o.offsets.cols})) return true;  // a single row has any pitch
+  if (o.mats == 0) return false;
   if (clash(d, o.a)) return true;
   const int64_t all = span_bytes(o.mats, o.stride, o.b.rows, o.b.ld, o.b.cols, 2);
   for (const void* w : {o.b.p, U}) {
