@@ -20,8 +20,9 @@ plus `gemm(...)`, `gemm_grouped(...)`, `gemm_grouped_wgrad(...)`,
 `gemm_gated_grad(...)`, `quantize_blocks(...)` and `gemm_f8_blocks(...)`,
 convenience wrappers on torch tensors that read the layouts and leading
 dimensions off the tensors' strides.
-Their work goes to `stream`, an address, or to the current stream; the caller
-orders it behind its inputs, and what reads a result on another stream behind it.
+Their work goes to `stream`, an address, or to the current stream of the operands' device,
+which need not be the current device; the caller orders it behind its inputs, and what
+reads a result on another stream behind it.
 """
 from __future__ import annotations
 
@@ -280,6 +281,16 @@ def _stream_of(stream, device):
     return torch.cuda.current_stream(device).cuda_stream if stream is None else stream
 
 
+def _call(f, device, *args):
+    """f(*args) with the operands' device as the current one, which is where the library works."""
+    import torch
+
+    if device.index == torch.cuda.current_device():
+        return f(*args)
+    with torch.cuda.device(device):
+        return f(*args)
+
+
 def _scratch(shape, dtype, device, stream):
     """A new tensor for work on `stream` (an address, or None: the current one).
 
@@ -343,8 +354,8 @@ def gemm(a, b, c=None, out=None, *, alpha=1.0, beta=0.0, bias=None, act="none", 
             raise ValueError(f"{name} must be on {a.device}")
     bptr = bias.data_ptr() if bias is not None else None
     stream = _stream_of(stream, a.device)
-    st = ttc_gemm(M, N, K, a.data_ptr(), lda, la, b.data_ptr(), ldb, lb, cptr, ldc, out.data_ptr(),
-                  ldd, float(alpha), float(beta), bptr, ACT[act], DTYPE[dt], stream)
+    st = _call(ttc_gemm, a.device, M, N, K, a.data_ptr(), lda, la, b.data_ptr(), ldb, lb, cptr, ldc, out.data_ptr(),
+               ldd, float(alpha), float(beta), bptr, ACT[act], DTYPE[dt], stream)
     if check and st != 0:
         raise TTCError(st)
     return out
@@ -383,9 +394,10 @@ def _check_offsets(offsets, groups, device):
         raise ValueError("offsets must be groups + 1 contiguous int32")
 
 
-def _finish(status, what, check):
+def _finish(f, device, check, *args):
+    status = _call(f, device, *args)
     if check and status != 0:
-        raise TTCError(status, what)
+        raise TTCError(status, f.__name__)
 
 
 def _half(t, what):
@@ -426,9 +438,9 @@ def gemm_grouped(a, b, offsets, out=None, *, alpha=1.0, bias=None, act="none", s
             raise ValueError("bias must be groups x N, its rows contiguous")
         stride_bias = bias.stride(0)
     stream = _stream_of(stream, a.device)
-    _finish(ttc_gemm_grouped(groups, M, N, K, a.data_ptr(), lda, offsets.data_ptr(), b.data_ptr(), ldb, b.stride(0), lb,
-                             out.data_ptr(), ldd, float(alpha), None if bias is None else bias.data_ptr(), stride_bias,
-                             ACT[act], DTYPE[dt], stream), "ttc_gemm_grouped", check)
+    _finish(ttc_gemm_grouped, a.device, check, groups, M, N, K, a.data_ptr(), lda, offsets.data_ptr(), b.data_ptr(),
+            ldb, b.stride(0), lb, out.data_ptr(), ldd, float(alpha), None if bias is None else bias.data_ptr(),
+            stride_bias, ACT[act], DTYPE[dt], stream)
     return out
 
 
@@ -458,10 +470,9 @@ def gemm_grouped_wgrad(a, b, offsets, c=None, out=None, *, alpha=1.0, beta=0.0, 
     stride_c, ldc = (0, max(N, 1)) if c is None else _group_pitch(c, "c")
     odt = "f32" if out.dtype == torch.float32 else dt
     stream = _stream_of(stream, a.device)
-    _finish(ttc_gemm_grouped_wgrad(groups, M, N, K, a.data_ptr(), lda, b.data_ptr(), ldb, offsets.data_ptr(),
-                                   None if c is None else c.data_ptr(), ldc, stride_c, out.data_ptr(), ldd, stride_d,
-                                   float(alpha), float(beta), DTYPE[dt], DTYPE[odt], stream),
-            "ttc_gemm_grouped_wgrad", check)
+    _finish(ttc_gemm_grouped_wgrad, a.device, check, groups, M, N, K, a.data_ptr(), lda, b.data_ptr(), ldb,
+            offsets.data_ptr(), None if c is None else c.data_ptr(), ldc, stride_c, out.data_ptr(), ldd, stride_d,
+            float(alpha), float(beta), DTYPE[dt], DTYPE[odt], stream)
     return out
 
 
@@ -486,8 +497,8 @@ def quantize_rows(x, out=None, scale=None, *, stream=None, check=True):
     ldq = _row_pitch(out, "out")
     dt = {torch.float16: "f16", torch.bfloat16: "bf16", torch.float32: "f32"}[x.dtype]
     stream = _stream_of(stream, x.device)
-    _finish(ttc_quantize_rows(rows, cols, x.data_ptr(), ldx, DTYPE[dt], out.data_ptr(), ldq, scale.data_ptr(), stream),
-            "ttc_quantize_rows", check)
+    _finish(ttc_quantize_rows, x.device, check, rows, cols, x.data_ptr(), ldx, DTYPE[dt], out.data_ptr(), ldq,
+            scale.data_ptr(), stream)
     return out, scale
 
 
@@ -522,14 +533,14 @@ def gemm_i8_scaled(a, scale_a, b, scale_b, out=None, *, out_dtype=None, bias=Non
         raise ValueError(f"workspace must be on {a.device} and contiguous")
     stream = _stream_of(stream, a.device)
     if workspace is None:
-        need = ttc_gemm_i8_scaled_workspace_size(M, N, K, a.data_ptr(), lda, b.data_ptr(), ldb, out.data_ptr(), ldd, odt)
+        need = _call(ttc_gemm_i8_scaled_workspace_size, a.device, M, N, K, a.data_ptr(), lda, b.data_ptr(), ldb, out.data_ptr(),
+                     ldd, odt)
         if need:
             workspace = _scratch((need,), torch.uint8, a.device, stream)
-    _finish(ttc_gemm_i8_scaled(M, N, K, a.data_ptr(), lda, scale_a.data_ptr(), b.data_ptr(), ldb, scale_b.data_ptr(),
-                               out.data_ptr(), ldd, None if bias is None else bias.data_ptr(), ACT[act], odt,
-                               None if workspace is None else workspace.data_ptr(),
-                               0 if workspace is None else workspace.numel() * workspace.element_size(), stream),
-            "ttc_gemm_i8_scaled", check)
+    _finish(ttc_gemm_i8_scaled, a.device, check, M, N, K, a.data_ptr(), lda, scale_a.data_ptr(), b.data_ptr(), ldb,
+            scale_b.data_ptr(), out.data_ptr(), ldd, None if bias is None else bias.data_ptr(), ACT[act], odt,
+            None if workspace is None else workspace.data_ptr(),
+            0 if workspace is None else workspace.numel() * workspace.element_size(), stream)
     return out
 
 
@@ -592,9 +603,9 @@ def gemm_gated(a, b_gate, b_up, out=None, *, offsets=None, pre=None, act="silu",
     ldd = _row_pitch(out, "out")
     gate, up, ldp = (None, None, 0) if pre is None else _half_of(pre, N, "pre")
     stream = _stream_of(stream, a.device)
-    _finish(ttc_gemm_gated(1 if groups is None else groups, M, N, K, a.data_ptr(), lda,
-                           None if offsets is None else offsets.data_ptr(), b_gate.data_ptr(), b_up.data_ptr(), ldb, stride_b,
-                           layout, out.data_ptr(), ldd, gate, up, ldp, ACT[act], DTYPE[dt], stream), "ttc_gemm_gated", check)
+    _finish(ttc_gemm_gated, a.device, check, 1 if groups is None else groups, M, N, K, a.data_ptr(), lda,
+            None if offsets is None else offsets.data_ptr(), b_gate.data_ptr(), b_up.data_ptr(), ldb, stride_b, layout,
+            out.data_ptr(), ldd, gate, up, ldp, ACT[act], DTYPE[dt], stream)
     return (out, pre) if new else out
 
 
@@ -623,10 +634,9 @@ def gemm_gated_grad(a, b, pre, dpre=None, out=None, *, offsets=None, act="silu",
     dgate, dup, lddp = _half_of(dpre, N, "dpre")
     ldd = N if out is None else _row_pitch(out, "out")
     stream = _stream_of(stream, a.device)
-    _finish(ttc_gemm_gated_grad(1 if groups is None else groups, M, N, K, a.data_ptr(), lda,
-                                None if offsets is None else offsets.data_ptr(), b.data_ptr(), ldb, stride_b, layout, gate, up,
-                                ldp, dgate, dup, lddp, None if out is None else out.data_ptr(), ldd, ACT[act], DTYPE[dt],
-                                stream), "ttc_gemm_gated_grad", check)
+    _finish(ttc_gemm_gated_grad, a.device, check, 1 if groups is None else groups, M, N, K, a.data_ptr(), lda,
+            None if offsets is None else offsets.data_ptr(), b.data_ptr(), ldb, stride_b, layout, gate, up, ldp, dgate,
+            dup, lddp, None if out is None else out.data_ptr(), ldd, ACT[act], DTYPE[dt], stream)
     return dpre
 
 
@@ -667,8 +677,8 @@ def quantize_blocks(x, out=None, scale=None, *, block_rows=1, transpose=False, d
     ldq, lds = _row_pitch(out, "out"), _row_pitch(scale, "scale")
     dt = {torch.float16: "f16", torch.bfloat16: "bf16", torch.float32: "f32"}[x.dtype]
     stream = _stream_of(stream, x.device)
-    _finish(ttc_quantize_blocks(rows, cols, x.data_ptr(), ldx, DTYPE[dt], block_rows, int(transpose), out.data_ptr(), ldq,
-                                DTYPE[q_dtype], scale.data_ptr(), lds, stream), "ttc_quantize_blocks", check)
+    _finish(ttc_quantize_blocks, x.device, check, rows, cols, x.data_ptr(), ldx, DTYPE[dt], block_rows, int(transpose),
+            out.data_ptr(), ldq, DTYPE[q_dtype], scale.data_ptr(), lds, stream)
     return out, scale
 
 
@@ -718,10 +728,9 @@ def gemm_f8_blocks(a, scale_a, b, scale_b, out=None, *, offsets=None, c=None, ou
         (stride_b, ldb), (stride_sb, lds_b) = _group_pitch(b, "b"), _group_pitch(scale_b, "scale_b")
     odt = DTYPE[{torch.float16: "f16", torch.bfloat16: "bf16", torch.float32: "f32"}[out.dtype]]
     stream = _stream_of(stream, a.device)
-    _finish(ttc_gemm_f8_blocks(1 if groups is None else groups, M, N, K, a.data_ptr(), lda, DTYPE[ta], scale_a.data_ptr(), lds_a,
-                               None if offsets is None else offsets.data_ptr(), b.data_ptr(), ldb, stride_b, DTYPE[tb],
-                               scale_b.data_ptr(), lds_b, stride_sb, block_rows, None if c is None else c.data_ptr(), ldc,
-                               out.data_ptr(), ldd, None if bias is None else bias.data_ptr(),
-                               0 if groups is None or bias is None else bias.stride(0), ACT[act], odt, stream),
-            "ttc_gemm_f8_blocks", check)
+    _finish(ttc_gemm_f8_blocks, a.device, check, 1 if groups is None else groups, M, N, K, a.data_ptr(), lda, DTYPE[ta],
+            scale_a.data_ptr(), lds_a, None if offsets is None else offsets.data_ptr(), b.data_ptr(), ldb, stride_b,
+            DTYPE[tb], scale_b.data_ptr(), lds_b, stride_sb, block_rows, None if c is None else c.data_ptr(), ldc,
+            out.data_ptr(), ldd, None if bias is None else bias.data_ptr(),
+            0 if groups is None or bias is None else bias.stride(0), ACT[act], odt, stream)
     return out
