@@ -388,9 +388,11 @@ ttc_status ttc_quantize_blocks(int64_t rows, int64_t cols, const void* X, int64_
  * M x ceil(K / 128) with pitch ldsa, scaleB_g ceil(N / block_rows_b) x ceil(K / 128)
  * with pitch ldsb, block_rows_b 1 or 128, all fp32 of any value (zero, negative
  * and NaN among them).  B_g, scaleB_g and bias_g are strideB, strideSB and
- * strideBias elements apart.  The sum over a block is the tensor cores' fp32 sum;
- * the two scales' product, its product with that sum, the sum over the blocks, C,
- * bias and activation are fp32, rounded to nearest.  C (pitch ldc, or NULL) and D
+ * strideBias elements apart.  All of it is fp32.  The sum over a block is the tensor
+ * cores'; the two scales' product is rounded to nearest, and one fused multiply-add
+ * a block, rounded to nearest, adds the block's sum times that product to the sum of the
+ * blocks before it; C and bias are added after the last one, each rounded to nearest.
+ * GELU is within 2^-20 of its argument's magnitude.  C (pitch ldc, or NULL) and D
  * have the type out_dtype: TTC_F16, TTC_BF16 or TTC_F32; C may be D itself with
  * the same pitch, which adds up micro-batches in place.  bias_g is fp32[N]; bias
  * may be NULL.

@@ -5,8 +5,9 @@
 //   P_b[i, j] = sum of A[i, k] B_g[j, k] over the k of block b (128 of them),
 //
 // r = 1 or 128 rows of B a scale.  Rows are grouped as in ttc_gemm_grouped, or all one
-// group's (offsets null).  P_b is the tensor cores' fp32 sum; scales, the sum over the
-// blocks, C, bias and the activation are fp32, rounded to nearest.
+// group's (offsets null).  P_b is the tensor cores' fp32 sum; the scales' product is rounded to
+// nearest, one fused multiply-add a block, in order, adds P_b times it to the sum; C, bias and the
+// activation are fp32.
 #pragma once
 #include "grouped.cuh"
 

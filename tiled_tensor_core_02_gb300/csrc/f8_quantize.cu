@@ -17,7 +17,9 @@
 //
 // Bound by HBM for rows: 8192 x 14336 bf16 56 us, 6.3 TB/s, fp32 90, 6.6; 16 x 4096 bf16 2.5.  Tiles wait
 // for their maxima between loads and stores, with four of them on an SM (fp32: two): square
-// blocks 56 us, fp32 139; transposed rows 66, fp32 114; transposed square blocks 59, fp32 126.
+// blocks 56 us, fp32 139; transposed rows 66, fp32 114; transposed square blocks 59, fp32 125.  fp32 square
+// blocks keep HBM 42 % busy where transposed rows have 55: twice the stores (4 bytes a lane) and a fifth
+// more instructions at two tiles an SM.
 // Rows off 16-byte boundaries, an element a load: 8192 x 14335 111 us, transposed 132.
 #include <cuda_fp8.h>
 

@@ -10,9 +10,10 @@
 // ahead.  (An accumulator for each block: 4099 rows of 64 groups, 1536 x 2048 65.6 us against
 // 58.4; a second set of epilogue warps for every other one changed nothing.)
 //
-// Bound by HBM up to 32 tokens and a few microseconds of start: 1 x 14336 x 4096 12.3 us, 16 x
-// 8192 x 8192 16.0, 1 x 4096 x 4096 8.7 (10.1 with one thread that loads).  With 64 tokens a tile
-// by shared memory, which gives the MMAs 24 KB a block of K, takes as much from TMA and hands 64
+// Up to 32 tokens bound by HBM on wide layers, behind a few microseconds of start: 1 x 14336 x 4096
+// 12.3 us, 16 x 8192 x 8192 16.0; on narrower ones by a tile's stages, which follow one another, 0.31 us
+// each: 1 x 4096 x K 4.4, 6.0, 8.7 and 13.8 us for K = 1024, 2048, 4096 and 8192, the weights' bytes
+// 0.6 to 4.9 (with one thread that loads 10.1 for K = 4096).  With 64 tokens a tile by shared memory, which gives the MMAs 24 KB a block of K, takes as much from TMA and hands 64
 // tokens' scales to every warp: 0.31 us a block, 64 x 8192 x 8192 21.1 us.
 #include <atomic>
 

@@ -47,7 +47,9 @@
 //
 // Where two halves of each of the last wave's tiles find a pair, the wave takes them
 // as halves of 128 columns: half the MMA's time and half the epilogue (1120 rows of 7
-// groups, 896 x 2944 20.7 -> 17.6 us; long walks at capped clocks gain nothing).
+// groups, 896 x 2944 20.7 -> 17.6 us; long walks at capped clocks gain nothing).  A gated
+// forward tile's half saves half of the MMAs and stores; its epilogue reads and computes 64 columns
+// a warp all the same, the second 32 of them for nothing.
 //
 // Results leave through a 4 KB block of shared memory per epilogue warp, 32 rows
 // of 128 bytes: written a row per lane, read back and stored four whole rows an
